@@ -338,6 +338,103 @@ int t2s_gemm_f64_smem32(int64_t M, int64_t N, int64_t K, const double *A, const 
 int t2s_vector_add_f32(int64_t n, const float *x, const float *y, float *z,
                        t2s_stream_t stream);
 
+/*
+ * Feed-forward operators of a transformer block, on 16-bit types (bfloat16 or binary16 inputs
+ * and outputs, uint16_t bit patterns): a linear layer, a gated pair of projections, and their
+ * gradients. Not on the pages; their products run on the tensor cores like t2s_gemm_bf16_f32.
+ *
+ *   linear           Z = X W + b,  Y = act(Z) + R
+ *   linear_backward  dZ = dY * act'(Z),  dX = dZ W^T,  dW = X^T dZ,  db = sum over rows of dZ
+ *                    (the gradient of R is dY itself)
+ *   gated            G = X Wg,  U = X Wu,  H = act(G) * U
+ *   gated_backward   dG = dH * U * act'(G),  dU = dH * act(G),
+ *                    dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU
+ *
+ * X is M x K (M rows, one per token), the weights take K inputs to N outputs. act is one of
+ *   T2S_ACT_NONE z, T2S_ACT_RELU max(z, 0), T2S_ACT_SILU z / (1 + e^-z),
+ *   T2S_ACT_GELU z (1 + erf(z / sqrt 2)) / 2,
+ *   T2S_ACT_GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
+ * Sums, activations and db are FP32 (the sums' order is the library's, the same in every call
+ * of the same sizes and alignment); every output is rounded to 16 bits once. dZ, dG and dU are
+ * rounded to 16 bits where they enter the products of a gradient.
+ *
+ * Layout: each matrix has its own row stride (ld, in elements, at least its row length and at
+ * most T2S_MAX_DIM), so views of larger matrices are taken as they are. Weights and their
+ * gradients are K x N (w_order T2S_W_KN) or N x K (T2S_W_NK). Every pointer must be 2-byte
+ * aligned. Rows that all start on 16-byte boundaries (pointer and 2 ld multiples of 16) are
+ * read in place; other operands are first copied into the workspace.
+ *
+ * Optional arguments are NULL: bias, R; Z, or G and U, where the forward pass need not keep
+ * them; in the gradients each output that is not wanted (dX, dW, db, ...). X is then only
+ * needed for the weights' gradients, W for dX, and Z for an act other than T2S_ACT_NONE.
+ * Y may be R (with ldy = ldr). Any other output equal to another argument is rejected;
+ * partial overlap is not detected.
+ *
+ * Lengths of 0: no output values means nothing to do; a sum over no values is 0 (K = 0 gives
+ * Y = act(b) + R, M = 0 gives dW = 0 and db = 0, N = 0 gives dX = 0).
+ *
+ * workspace: a DEVICE buffer, 256-byte aligned, owned by the caller and untouched until the
+ * stream has run the call, of t2s_<operator>_workspace_size(M, N, K, aligned) bytes; `aligned`
+ * nonzero says that X and the weights (in linear_backward also dY) are read in place. It may be NULL where that is
+ * 0. Too small a workspace for the call: T2S_ERR_WORKSPACE. Otherwise the common contract and
+ * return codes at the top apply (asynchronous on `stream`, no allocation).
+ */
+#define T2S_ACT_NONE 0
+#define T2S_ACT_RELU 1
+#define T2S_ACT_SILU 2
+#define T2S_ACT_GELU 3
+#define T2S_ACT_GELU_TANH 4
+#define T2S_W_KN 0
+#define T2S_W_NK 1
+
+size_t t2s_linear_workspace_size(int64_t M, int64_t N, int64_t K, int aligned);
+size_t t2s_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, int aligned);
+size_t t2s_gated_workspace_size(int64_t M, int64_t N, int64_t K, int aligned);
+size_t t2s_gated_backward_workspace_size(int64_t M, int64_t N, int64_t K, int aligned);
+
+int t2s_linear_bf16(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_t ldx,
+                    const uint16_t *W, int64_t ldw, int w_order, const uint16_t *bias,
+                    const uint16_t *R, int64_t ldr, int act, uint16_t *Y, int64_t ldy,
+                    uint16_t *Z, int64_t ldz, void *workspace, size_t workspace_bytes,
+                    t2s_stream_t stream);
+int t2s_linear_f16(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_t ldx,
+                   const uint16_t *W, int64_t ldw, int w_order, const uint16_t *bias,
+                   const uint16_t *R, int64_t ldr, int act, uint16_t *Y, int64_t ldy,
+                   uint16_t *Z, int64_t ldz, void *workspace, size_t workspace_bytes,
+                   t2s_stream_t stream);
+int t2s_linear_backward_bf16(int64_t M, int64_t N, int64_t K, const uint16_t *dY, int64_t lddy,
+                             const uint16_t *X, int64_t ldx, const uint16_t *W, int64_t ldw,
+                             int w_order, const uint16_t *Z, int64_t ldz, int act, uint16_t *dX,
+                             int64_t lddx, uint16_t *dW, int64_t lddw, uint16_t *db,
+                             void *workspace, size_t workspace_bytes, t2s_stream_t stream);
+int t2s_linear_backward_f16(int64_t M, int64_t N, int64_t K, const uint16_t *dY, int64_t lddy,
+                            const uint16_t *X, int64_t ldx, const uint16_t *W, int64_t ldw,
+                            int w_order, const uint16_t *Z, int64_t ldz, int act, uint16_t *dX,
+                            int64_t lddx, uint16_t *dW, int64_t lddw, uint16_t *db,
+                            void *workspace, size_t workspace_bytes, t2s_stream_t stream);
+int t2s_gated_bf16(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_t ldx,
+                   const uint16_t *Wg, int64_t ldwg, const uint16_t *Wu, int64_t ldwu, int w_order,
+                   int act, uint16_t *H, int64_t ldh, uint16_t *G, int64_t ldg, uint16_t *U,
+                   int64_t ldu, void *workspace, size_t workspace_bytes, t2s_stream_t stream);
+int t2s_gated_f16(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_t ldx,
+                  const uint16_t *Wg, int64_t ldwg, const uint16_t *Wu, int64_t ldwu, int w_order,
+                  int act, uint16_t *H, int64_t ldh, uint16_t *G, int64_t ldg, uint16_t *U,
+                  int64_t ldu, void *workspace, size_t workspace_bytes, t2s_stream_t stream);
+int t2s_gated_backward_bf16(int64_t M, int64_t N, int64_t K, const uint16_t *dH, int64_t lddh,
+                            const uint16_t *X, int64_t ldx, const uint16_t *Wg, int64_t ldwg,
+                            const uint16_t *Wu, int64_t ldwu, int w_order, const uint16_t *G,
+                            int64_t ldg, const uint16_t *U, int64_t ldu, int act, uint16_t *dX,
+                            int64_t lddx, uint16_t *dWg, int64_t lddwg, uint16_t *dWu,
+                            int64_t lddwu, void *workspace, size_t workspace_bytes,
+                            t2s_stream_t stream);
+int t2s_gated_backward_f16(int64_t M, int64_t N, int64_t K, const uint16_t *dH, int64_t lddh,
+                           const uint16_t *X, int64_t ldx, const uint16_t *Wg, int64_t ldwg,
+                           const uint16_t *Wu, int64_t ldwu, int w_order, const uint16_t *G,
+                           int64_t ldg, const uint16_t *U, int64_t ldu, int act, uint16_t *dX,
+                           int64_t lddx, uint16_t *dWg, int64_t lddwg, uint16_t *dWu,
+                           int64_t lddwu, void *workspace, size_t workspace_bytes,
+                           t2s_stream_t stream);
+
 /* Static description of a return code. Never NULL. */
 const char *t2s_status_string(int status);
 

@@ -25,9 +25,16 @@ T2S_ERR_WORKSPACE = 4
 T2S_ERR_TOO_LARGE = 5
 T2S_TF32X3_NOALLOC_MAX_SCRATCH = 32 << 20
 T2S_MAX_DIM = 1 << 30
+T2S_ACT_NONE, T2S_ACT_RELU, T2S_ACT_SILU, T2S_ACT_GELU, T2S_ACT_GELU_TANH = range(5)
+T2S_W_KN, T2S_W_NK = 0, 1
 
 #: Every function the header declares, with (argtypes, restype).
 _i64, _p, _i, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_MAT, _TAIL = [_p, _i64], [_p, _sz, _p]  # pointer, row stride; workspace, its bytes, stream
+_LINEAR = [_i64] * 3 + 2 * _MAT + [_i, _p] + _MAT + [_i] + 2 * _MAT + _TAIL
+_LINEAR_BACKWARD = [_i64] * 3 + 3 * _MAT + [_i] + _MAT + [_i] + 2 * _MAT + [_p] + _TAIL
+_GATED = [_i64] * 3 + 3 * _MAT + [_i, _i] + 3 * _MAT + _TAIL
+_GATED_BACKWARD = [_i64] * 3 + 4 * _MAT + [_i] + 2 * _MAT + [_i] + 3 * _MAT + _TAIL
 SIGNATURES = {
     "t2s_gemm_f32": ([_i64, _i64, _i64, _p, _p, _p, _p], _i),
     "t2s_gemm_f32_host": ([_i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p], _i),
@@ -50,6 +57,18 @@ SIGNATURES = {
     "t2s_gemm_f16_f32_workspace_size": ([_i64, _i64, _i64], _sz),
     "t2s_gemm_f16_f32": ([_i64, _i64, _i64, _p, _p, _p, _p, _sz, _p], _i),
     "t2s_vector_add_f32": ([_i64, _p, _p, _p, _p], _i),
+    "t2s_linear_workspace_size": ([_i64, _i64, _i64, _i], _sz),
+    "t2s_linear_backward_workspace_size": ([_i64, _i64, _i64, _i], _sz),
+    "t2s_gated_workspace_size": ([_i64, _i64, _i64, _i], _sz),
+    "t2s_gated_backward_workspace_size": ([_i64, _i64, _i64, _i], _sz),
+    "t2s_linear_bf16": (_LINEAR, _i),
+    "t2s_linear_f16": (_LINEAR, _i),
+    "t2s_linear_backward_bf16": (_LINEAR_BACKWARD, _i),
+    "t2s_linear_backward_f16": (_LINEAR_BACKWARD, _i),
+    "t2s_gated_bf16": (_GATED, _i),
+    "t2s_gated_f16": (_GATED, _i),
+    "t2s_gated_backward_bf16": (_GATED_BACKWARD, _i),
+    "t2s_gated_backward_f16": (_GATED_BACKWARD, _i),
     "t2s_status_string": ([_i], ctypes.c_char_p),
     "t2s_device_status": ([_p], _i),
     "t2s_last_cuda_error": ([], _i),
@@ -173,6 +192,54 @@ def t2s_gemm_f16_f32(M, N, K, A, B, C, workspace, workspace_bytes, stream=0) -> 
 
 def t2s_vector_add_f32(n, x, y, z, stream=0) -> int:
     return lib().t2s_vector_add_f32(n, x, y, z, stream)
+
+
+def t2s_linear_workspace_size(M, N, K, aligned=0) -> int:
+    return lib().t2s_linear_workspace_size(M, N, K, aligned)
+
+
+def t2s_linear_backward_workspace_size(M, N, K, aligned=0) -> int:
+    return lib().t2s_linear_backward_workspace_size(M, N, K, aligned)
+
+
+def t2s_gated_workspace_size(M, N, K, aligned=0) -> int:
+    return lib().t2s_gated_workspace_size(M, N, K, aligned)
+
+
+def t2s_gated_backward_workspace_size(M, N, K, aligned=0) -> int:
+    return lib().t2s_gated_backward_workspace_size(M, N, K, aligned)
+
+
+def t2s_linear_bf16(*args) -> int:
+    return lib().t2s_linear_bf16(*args)
+
+
+def t2s_linear_f16(*args) -> int:
+    return lib().t2s_linear_f16(*args)
+
+
+def t2s_linear_backward_bf16(*args) -> int:
+    return lib().t2s_linear_backward_bf16(*args)
+
+
+def t2s_linear_backward_f16(*args) -> int:
+    return lib().t2s_linear_backward_f16(*args)
+
+
+def t2s_gated_bf16(*args) -> int:
+    return lib().t2s_gated_bf16(*args)
+
+
+def t2s_gated_f16(*args) -> int:
+    return lib().t2s_gated_f16(*args)
+
+
+def t2s_gated_backward_bf16(*args) -> int:
+    return lib().t2s_gated_backward_bf16(*args)
+
+
+def t2s_gated_backward_f16(*args) -> int:
+    return lib().t2s_gated_backward_f16(*args)
 
 
 def t2s_status_string(status: int) -> str:

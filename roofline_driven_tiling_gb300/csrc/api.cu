@@ -119,6 +119,8 @@ __global__ void wait_selftest_kernel(unsigned* status, uint64_t limit_ns) {
 
 void set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<int>(e); }
 
+cudaError_t device_status_word(unsigned** out) { return status_word(out); }
+
 int gemm_f32_block(int64_t M, int64_t N, int64_t K, const float* A, const float* B, float* C,
                    t2s_stream_t stream, int concurrent) {
   Problem p{};

@@ -1,0 +1,70 @@
+// ff_internal.h -- the feed-forward operators (linear, gated and their gradients) between their C
+// entry points (ff_api.cu) and the kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "t2s_internal.h"
+
+namespace t2s {
+namespace ff {
+
+// 16-bit element types.
+enum Kind : int { kBf16 = 1, kF16 = 0 };
+
+// A product operand of `extent` x K values: `k_major` stores them as `extent` rows of K
+// (contiguous along the sum), otherwise as K rows of `extent`. `ld` elements per row.
+struct Operand {
+  const uint16_t* p = nullptr;
+  int64_t ld = 0;
+  bool k_major = true;
+};
+
+struct Matrix {
+  uint16_t* p = nullptr;  // nullptr: absent
+  int64_t ld = 0;
+};
+
+// What follows a product's sums (one of the three forms).
+enum Form : int {
+  kLinear = 0,  // S = A B            Z = S + bias, Y = act(Z) + R
+  kGated = 1,   // S = A B, S2 = A B2  Z = S, Z2 = S2, Y = act(S) * S2
+  kJoined = 2,  // S = A B + A2 B2    Y = S
+};
+
+// One product M x N over K with its epilogue. B and B2 are N x K operands.
+struct Task {
+  Form form = kLinear;
+  int64_t M = 0, N = 0, K = 0;
+  Operand A, A2, B, B2;
+  const uint16_t* bias = nullptr;
+  Matrix R, Y, Z, Z2;
+  int act = 0;
+};
+
+struct Context {
+  Kind kind;
+  cudaStream_t stream;
+  unsigned* status;
+};
+
+inline bool aligned16(const void* p, int64_t ld) {
+  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2)) & 15u) == 0;
+}
+
+cudaError_t run_simple(const Context& c, const Task& t);
+
+// dZ = dY * act'(Z) (Z absent: act none, dZ not wanted) and, unless db is nullptr, its column
+// sums. `partials` holds db_partial_rows(M, N) x N floats.
+int64_t db_partial_rows(int64_t M, int64_t N);
+cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dY,
+                             int64_t lddy, const uint16_t* Z, int64_t ldz, uint16_t* dZ,
+                             int64_t lddz, uint16_t* db, float* partials);
+// dG = dH * U * act'(G), dU = dH * act(G).
+cudaError_t run_gated_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dH,
+                               int64_t lddh, const uint16_t* G, int64_t ldg, const uint16_t* U,
+                               int64_t ldu, uint16_t* dG, uint16_t* dU, int64_t ldd);
+
+}  // namespace ff
+}  // namespace t2s

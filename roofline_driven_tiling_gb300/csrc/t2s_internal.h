@@ -92,5 +92,7 @@ cudaError_t launch_store_probe(int64_t M, int64_t N, float* C, int mode, float v
                                cudaStream_t stream, int64_t* bytes);
 // Records a CUDA error for t2s_last_cuda_error() on this host thread.
 void set_last_cuda_error(cudaError_t e);
+// Device address of the current device's status word.
+cudaError_t device_status_word(unsigned** out);
 
 }  // namespace t2s
