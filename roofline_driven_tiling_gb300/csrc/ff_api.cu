@@ -80,6 +80,36 @@ struct Workspace {
   }
 };
 
+// Whether the tensor cores' copies can read a matrix where it lies: all its rows on 16-byte
+// boundaries (one row: only its start).
+bool in_place(const void* p, int64_t rows, int64_t ld) { return aligned16(p, rows <= 1 ? 8 : ld); }
+
+size_t copy_bytes(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return rows == 0 || cols == 0 || in_place(p, rows, ld) ? 0 : plane_bytes(rows, cols);
+}
+
+// The rows x cols matrix `o` as it can be read: itself, or a copy in the workspace.
+cudaError_t readable(const Context& c, Workspace* ws, int64_t rows, int64_t cols, Operand* o) {
+  if (rows == 0 || cols == 0) return cudaSuccess;
+  if (in_place(o->p, rows, o->ld)) {
+    if (rows <= 1) o->ld = up8(cols);
+    return cudaSuccess;
+  }
+  uint16_t* copy = static_cast<uint16_t*>(ws->take(plane_bytes(rows, cols)));
+  const cudaError_t e = run_copy(c, rows, cols, o->p, o->ld, copy, up8(cols));
+  o->p = copy;
+  o->ld = up8(cols);
+  return e;
+}
+
+cudaError_t readable_weight(const Context& c, Workspace* ws, int64_t K, int64_t N, int w_order, Operand* o) {
+  return w_order == T2S_W_KN ? readable(c, ws, K, N, o) : readable(c, ws, N, K, o);
+}
+
+size_t weight_copy_bytes(const void* p, int64_t K, int64_t N, int64_t ld, int w_order) {
+  return w_order == T2S_W_KN ? copy_bytes(p, K, N, ld) : copy_bytes(p, N, K, ld);
+}
+
 int check_workspace(const void* p, size_t have, size_t need) {
   if (need == 0) return T2S_OK;
   if (p == nullptr || have < need || (reinterpret_cast<uintptr_t>(p) & 255u) != 0) return T2S_ERR_WORKSPACE;
@@ -108,8 +138,6 @@ Task weight_gradient(int64_t M, int64_t N, int64_t K, Operand x, Operand d, int 
 int linear(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const uint16_t* W,
            int64_t ldw, int w_order, const uint16_t* bias, const uint16_t* R, int64_t ldr, int act, uint16_t* Y,
            int64_t ldy, uint16_t* Z, int64_t ldz, void* workspace, size_t workspace_bytes, t2s_stream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (bad_size(M) || bad_size(N) || bad_size(K) || bad_flags(w_order, act)) return T2S_ERR_INVALID;
   const Arg x{X, ldx, M, K}, w = weight_arg(W, ldw, K, N, w_order), r{R, ldr, M, N}, y{Y, ldy, M, N};
   // Y may be R itself: every value of R is read by the thread block that then writes it.
@@ -119,6 +147,9 @@ int linear(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_
     return T2S_ERR_INVALID;
   if (M == 0 || N == 0) return T2S_OK;
   if (Y == nullptr) return T2S_ERR_INVALID;
+  const int rc = check_workspace(workspace, workspace_bytes,
+                                 copy_bytes(X, M, K, ldx) + weight_copy_bytes(W, K, N, ldw, w_order));
+  if (rc != T2S_OK) return rc;
   Context c{kind, reinterpret_cast<cudaStream_t>(stream), nullptr};
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
@@ -131,7 +162,10 @@ int linear(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_
   t.act = act;
   t.Y = {Y, ldy};
   t.Z = {Z, ldz};
-  return done(run_simple(c, t));
+  Workspace ws{static_cast<uint8_t*>(workspace)};
+  if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
+  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
+  return done(run_pair(c, &t, 1));
 }
 
 int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* X,
@@ -148,19 +182,22 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   if ((dW != nullptr && bad_matrix(x, N > 0)) || (dX != nullptr && bad_matrix(w, M > 0)) ||
       (act != T2S_ACT_NONE && bad_matrix(z, true)))
     return T2S_ERR_INVALID;
-  const bool plane = act != T2S_ACT_NONE;
+  const bool products = dX != nullptr || dW != nullptr;
+  const bool plane = products && (act != T2S_ACT_NONE || !in_place(dY, M, lddy));
   const int64_t ldd = up8(N);
-  const size_t need = (plane ? plane_bytes(M, N) : 0) + (db ? up256(static_cast<size_t>(db_partial_rows(M, N)) * N * 4) : 0);
+  const size_t sums = db != nullptr ? up256(static_cast<size_t>(db_partial_rows(M, N)) * N * 4) : 0;
+  const size_t need = (plane ? plane_bytes(M, N) : 0) + sums + (dW != nullptr ? copy_bytes(X, M, K, ldx) : 0) +
+                      (dX != nullptr ? weight_copy_bytes(W, K, N, ldw, w_order) : 0);
   const int rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != T2S_OK) return rc;
   Context c{kind, reinterpret_cast<cudaStream_t>(stream), nullptr};
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
-  Operand d{dY, lddy, true};
+  Operand d{dY, M <= 1 ? ldd : lddy, true};
   if (M > 0 && N > 0 && (plane || db != nullptr)) {
     uint16_t* dz = plane ? static_cast<uint16_t*>(ws.take(plane_bytes(M, N))) : nullptr;
-    float* partials = db ? static_cast<float*>(ws.take(static_cast<size_t>(db_partial_rows(M, N)) * N * 4)) : nullptr;
+    float* partials = db ? static_cast<float*>(ws.take(sums)) : nullptr;
     e = run_act_backward(c, M, N, act, dY, lddy, Z, ldz, dz, ldd, db, partials);
     if (e != cudaSuccess) return done(e);
     if (plane) d = {dz, ldd, true};
@@ -168,32 +205,37 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
     e = cudaMemsetAsync(db, 0, static_cast<size_t>(N) * 2, c.stream);
     if (e != cudaSuccess) return done(e);
   }
+  Task tasks[2];
+  int n = 0;
   if (dX != nullptr && M > 0 && K > 0) {
-    Task t;
+    Task& t = tasks[n++];
     t.M = M, t.N = K, t.K = N;
     t.A = d;
     t.B = weight_backward(W, ldw, w_order);
     t.Y = {dX, lddx};
-    if ((e = run_simple(c, t)) != cudaSuccess) return done(e);
+    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
   }
   if (dW != nullptr && K > 0 && N > 0) {
-    if ((e = run_simple(c, weight_gradient(M, N, K, {X, ldx, false}, d, w_order, {dW, lddw}))) != cudaSuccess)
-      return done(e);
+    Operand x{X, ldx, false};
+    if ((e = readable(c, &ws, M, K, &x)) != cudaSuccess) return done(e);
+    tasks[n++] = weight_gradient(M, N, K, x, d, w_order, {dW, lddw});
   }
-  return T2S_OK;
+  return done(run_pair(c, tasks, n));
 }
 
 int gated(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const uint16_t* Wg,
           int64_t ldwg, const uint16_t* Wu, int64_t ldwu, int w_order, int act, uint16_t* H, int64_t ldh, uint16_t* G,
           int64_t ldg, uint16_t* U, int64_t ldu, void* workspace, size_t workspace_bytes, t2s_stream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (bad_size(M) || bad_size(N) || bad_size(K) || bad_flags(w_order, act)) return T2S_ERR_INVALID;
   if (bad_arguments({{X, ldx, M, K}, weight_arg(Wg, ldwg, K, N, w_order), weight_arg(Wu, ldwu, K, N, w_order)}, {},
                     {{H, ldh, M, N}, {G, ldg, M, N}, {U, ldu, M, N}}))
     return T2S_ERR_INVALID;
   if (M == 0 || N == 0) return T2S_OK;
   if (H == nullptr) return T2S_ERR_INVALID;
+  const int rc = check_workspace(workspace, workspace_bytes,
+                                 copy_bytes(X, M, K, ldx) + weight_copy_bytes(Wg, K, N, ldwg, w_order) +
+                                     weight_copy_bytes(Wu, K, N, ldwu, w_order));
+  if (rc != T2S_OK) return rc;
   Context c{kind, reinterpret_cast<cudaStream_t>(stream), nullptr};
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
@@ -207,7 +249,11 @@ int gated(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t
   t.Y = {H, ldh};
   t.Z = {G, ldg};
   t.Z2 = {U, ldu};
-  return done(run_simple(c, t));
+  Workspace ws{static_cast<uint8_t*>(workspace)};
+  if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
+  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
+  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B2)) != cudaSuccess) return done(e);
+  return done(run_pair(c, &t, 1));
 }
 
 int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* dH, int64_t lddh, const uint16_t* X,
@@ -226,21 +272,26 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
   if ((dw && bad_matrix(x, N > 0)) || (dX != nullptr && M > 0 && (bad_matrix(wg, true) || bad_matrix(wu, true))))
     return T2S_ERR_INVALID;
   const int64_t ldd = up8(N);
-  const int rc = check_workspace(workspace, workspace_bytes, 2 * plane_bytes(M, N));
+  size_t need = 2 * plane_bytes(M, N);
+  if (dw) need += copy_bytes(X, M, K, ldx);
+  if (dX != nullptr) need += weight_copy_bytes(Wg, K, N, ldwg, w_order) + weight_copy_bytes(Wu, K, N, ldwu, w_order);
+  const int rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != T2S_OK) return rc;
   Context c{kind, reinterpret_cast<cudaStream_t>(stream), nullptr};
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
   uint16_t *dG = nullptr, *dU = nullptr;
-  if (M > 0 && N > 0) {
+  if (M > 0 && N > 0 && (dw || dX != nullptr)) {
     dG = static_cast<uint16_t*>(ws.take(plane_bytes(M, N)));
     dU = static_cast<uint16_t*>(ws.take(plane_bytes(M, N)));
     e = run_gated_backward(c, M, N, act, dH, lddh, G, ldg, U, ldu, dG, dU, ldd);
     if (e != cudaSuccess) return done(e);
   }
+  Task tasks[3];
+  int n = 0;
   if (dX != nullptr && M > 0 && K > 0) {
-    Task t;
+    Task& t = tasks[n++];
     t.form = kJoined;
     t.M = M, t.N = K, t.K = N;
     t.A = {dG, ldd, true};
@@ -248,19 +299,16 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
     t.B = weight_backward(Wg, ldwg, w_order);
     t.B2 = weight_backward(Wu, ldwu, w_order);
     t.Y = {dX, lddx};
-    if ((e = run_simple(c, t)) != cudaSuccess) return done(e);
+    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
+    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B2)) != cudaSuccess) return done(e);
   }
-  if (K > 0 && N > 0) {
-    if (dWg != nullptr &&
-        (e = run_simple(c, weight_gradient(M, N, K, {X, ldx, false}, {dG, ldd, false}, w_order, {dWg, lddwg}))) !=
-            cudaSuccess)
-      return done(e);
-    if (dWu != nullptr &&
-        (e = run_simple(c, weight_gradient(M, N, K, {X, ldx, false}, {dU, ldd, false}, w_order, {dWu, lddwu}))) !=
-            cudaSuccess)
-      return done(e);
+  if (dw && K > 0 && N > 0) {
+    Operand x{X, ldx, false};
+    if ((e = readable(c, &ws, M, K, &x)) != cudaSuccess) return done(e);
+    if (dWg != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dG, ldd, false}, w_order, {dWg, lddwg});
+    if (dWu != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dU, ldd, false}, w_order, {dWu, lddwu});
   }
-  return T2S_OK;
+  return done(run_pair(c, tasks, n));
 }
 
 bool bad_sizes(int64_t M, int64_t N, int64_t K) { return bad_size(M) || bad_size(N) || bad_size(K); }

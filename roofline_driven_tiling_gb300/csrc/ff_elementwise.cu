@@ -70,7 +70,31 @@ __global__ void __launch_bounds__(kThreads)
   });
 }
 
+// Copies of operands whose rows are not 16-byte aligned: 8 values per thread, written as one word.
+__global__ void __launch_bounds__(kThreads) copy_kernel(int64_t rows, int64_t cols, const uint16_t* __restrict__ src,
+                                                        int64_t ld, uint16_t* __restrict__ dst, int64_t ldd) {
+  const int64_t per_row = ldd / 8, total = rows * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : static_cast<uint16_t>(0);
+    *reinterpret_cast<uint4*>(dst + r * ldd + c) =
+        make_uint4(v[0] | (uint32_t(v[1]) << 16), v[2] | (uint32_t(v[3]) << 16), v[4] | (uint32_t(v[5]) << 16),
+                   v[6] | (uint32_t(v[7]) << 16));
+  }
+}
+
 }  // namespace
+
+cudaError_t run_copy(const Context& c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld, uint16_t* dst,
+                     int64_t ldd) {
+  const int64_t blocks = (rows * (ldd / 8) + kThreads - 1) / kThreads;
+  copy_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kThreads, 0, c.stream>>>(rows, cols, src, ld,
+                                                                                              dst, ldd);
+  return cudaGetLastError();
+}
 
 // Chunks of at least 64 rows, at most 128 of them.
 int64_t db_partial_rows(int64_t M, int64_t) {

@@ -53,7 +53,13 @@ inline bool aligned16(const void* p, int64_t ld) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2)) & 15u) == 0;
 }
 
-cudaError_t run_simple(const Context& c, const Task& t);
+// Up to three products in one launch, all of the gated form or none. Operands must be readable
+// in place (aligned16), and rows of a single-row operand given a stride that is.
+cudaError_t run_pair(const Context& c, const Task* tasks, int n);
+
+// dst (rows x cols, ldd per row) = src.
+cudaError_t run_copy(const Context& c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld, uint16_t* dst,
+                     int64_t ldd);
 
 // dZ = dY * act'(Z) (Z absent: act none, dZ not wanted) and, unless db is nullptr, its column
 // sums. `partials` holds db_partial_rows(M, N) x N floats.

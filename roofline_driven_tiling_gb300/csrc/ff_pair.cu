@@ -1,0 +1,563 @@
+// ff_pair.cu -- the products of the feed-forward operators on pairs of SMs (tcgen05 .cta_group::2).
+//
+// One persistent launch takes the tiles of up to three products (a gradient's dX and weight
+// gradients run together, so that one product's last round is filled by the next one's tiles).
+// A tile is 256 rows x up to 256 sums, computed by a cluster of two CTAs on two SMs: each
+// stages its 128 rows of A and half of the columns of B (one 64-deep K block per ring slot), rank 0
+// issues the MMAs, and each CTA's TMEM holds the sums of its 128 rows.
+//
+// Operands are read where they lie, whatever their order: rows along K (K-major boxes of 64
+// values x rows) or K rows of outputs (MN-major boxes of 64 outputs x 64 K rows), both in
+// 128-byte swizzle. That covers X W, dZ W^T and X^T dZ for weights of either order.
+//
+// The gated product needs no wider machinery: rank 0 stages 128 columns of Wg and rank 1 the same
+// 128 columns of Wu, so the lower half of the accumulator's columns holds G, the upper half U.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "ff_internal.h"
+#include "ff_math.cuh"
+#include "t2s_device.cuh"
+#include "t2s_tmap.h"
+#include "tc_gemm.cuh"
+
+namespace t2s {
+namespace ff {
+namespace {
+
+constexpr int kRows = 128;    // A rows of one CTA
+constexpr int kBK = 64;       // K block: 128-byte rows
+constexpr int kStages = 6;    // ring slots of 32 KB
+constexpr int kMaxN = 256;    // widest MMA
+constexpr int kABytes = kRows * kBK * 2;
+constexpr int kBBytes = kMaxN / 2 * kBK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kBoxBytes = 64 * kBK * 2;  // 64 outputs x 64 K rows of an MN-major operand
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kUnit = 32;                        // columns an epilogue warp takes at a time
+constexpr int kUnitBytes = 32 * kUnit * 2;       // 32 rows of 64 bytes
+constexpr int kStagingBytes = kEpiWarps * 2 * kUnitBytes;
+constexpr int kBiasBytes = kEpiWarps * kUnit * 4;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kStagingBytes + kBiasBytes;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
+constexpr int kMaxProblems = 3;
+
+struct PairProblem {
+  CUtensorMap a[2], b[2], y, z, z2;
+  const uint16_t* bias;
+  const uint16_t* R;
+  uint16_t *Y, *Z, *Z2;
+  int64_t ldr, ldy, ldz, ldz2;
+  int M, N;
+  int nkb, nkb_first;  // K blocks, and how many of them come from a[0], b[0]
+  int tiles_m, tiles_n;
+  int bn;       // columns of Y in a tile
+  int mma_n;    // sums per row in a tile (gated: 2 bn)
+  uint32_t idesc;
+  uint32_t stage_tx;  // bytes that both CTAs copy per K block
+  int a_k_major, b_k_major, b_boxes;
+  int y_tma, z_tma, z2_tma, r_wide;
+  int act;
+};
+
+struct PairParams {
+  PairProblem p[kMaxProblems];
+  int first[kMaxProblems + 1];  // first tile of each problem; the last entry is the tile count
+  unsigned* status;
+};
+
+// A matrix descriptor without its address: K-major 128-byte-swizzled rows (8-row groups 1024
+// bytes apart), or MN-major atoms (64 outputs x 8 K rows; the next 64 outputs one box further,
+// the next 8 K rows 1024 bytes further). `step` is the advance of 16 K values.
+struct OperandForm {
+  uint64_t base;
+  uint32_t step;
+};
+__device__ __forceinline__ OperandForm operand_form(bool k_major) {
+  OperandForm f;
+  f.base = (static_cast<uint64_t>(k_major ? 1 : kBoxBytes >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+  f.step = (k_major ? 32 : 16 * 128) >> 4;
+  return f;
+}
+__device__ __forceinline__ uint64_t with_address(const OperandForm& f, uint32_t addr) {
+  return f.base | static_cast<uint64_t>((addr & 0x3ffffu) >> 4);
+}
+
+// Column groups of 8 tile rows sweep the columns together, so that the tiles in flight share A
+// and B in the L2 cache.
+__device__ __forceinline__ void tile_at(const PairProblem& p, int t, int& m0, int& n0) {
+  tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, p.bn, m0, n0);
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr));
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in a 32 x 64-byte box (64-byte swizzle).
+__device__ __forceinline__ uint32_t unit_chunk(int r, int c) {
+  return static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(c ^ ((r >> 1) & 3)) << 4);
+}
+
+// One epilogue warp's two staging boxes, taken in turn.
+struct Staging {
+  uint32_t base;
+  uint32_t count;
+  int lane;
+
+  // The next box, free of the TMA store that last used it.
+  __device__ __forceinline__ uint32_t next() {
+    const uint32_t at = base + (count++ & 1u) * kUnitBytes;
+    if (lane == 0) bulk_wait_read_but_one();
+    __syncwarp();
+    return at;
+  }
+};
+
+// Stores a warp's 32 x 32 outputs at (m, n) from its box, each lane having written its own row:
+// by TMA, or (rows not 16-byte aligned) one row of 32 values per instruction.
+__device__ __forceinline__ void store_unit(const CUtensorMap* map, bool tma, uint32_t box, uint16_t* p, int64_t ld,
+                                           int m, int n, int M, int N, int lane) {
+  if (tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, box, n, m);
+    return;
+  }
+  __syncwarp();
+  const int rows = min(32, M - m);
+  for (int r = 0; r < rows; ++r) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + unit_chunk(r, lane >> 3) + (lane & 7) * 2));
+    if (n + lane < N) p[static_cast<int64_t>(m + r) * ld + n + lane] = v;
+  }
+  __syncwarp();
+  // The TMA-store count that next() waits by: an empty group stands for this box.
+  if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// The residual's 32 x 32 values at (m, n) into the box, zeros outside the matrix.
+__device__ __forceinline__ void load_unit(uint32_t box, const uint16_t* p, int64_t ld, bool wide, int m, int n, int M,
+                                          int N, int lane) {
+  if (wide && n + kUnit <= N) {
+    // Four lanes per row of 64 bytes.
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (m + r < M)
+        v[i] = *reinterpret_cast<const uint4*>(p + static_cast<int64_t>(m + r) * ld + n + (lane & 3) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      st_shared_v4(box + unit_chunk(8 * i + (lane >> 2), lane & 3), v[i].x, v[i].y, v[i].z, v[i].w);
+  } else {
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      uint16_t v = 0;
+      if (m + r < M && n + lane < N) v = p[static_cast<int64_t>(m + r) * ld + n + lane];
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + unit_chunk(r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
+    }
+  }
+  __syncwarp();
+}
+
+// A lane's row of 32 values, rounded, into the box.
+template <int KIND>
+__device__ __forceinline__ void put_row(uint32_t box, int lane, const float (&v)[kUnit]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(box + unit_chunk(lane, c), pack_f32<KIND>(v[8 * c], v[8 * c + 1]),
+                 pack_f32<KIND>(v[8 * c + 2], v[8 * c + 3]), pack_f32<KIND>(v[8 * c + 4], v[8 * c + 5]),
+                 pack_f32<KIND>(v[8 * c + 6], v[8 * c + 7]));
+}
+
+// The accumulator's 32 columns from `taddr` on, one row per lane.
+__device__ __forceinline__ void load_sums(uint32_t taddr, bool any, float (&s)[kUnit]) {
+  uint32_t r[kUnit];
+  tc::tmem_ld32(taddr, r);
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) s[i] = any ? __uint_as_float(r[i]) : 0.0f;
+}
+
+// Roles as in tc_gemm.cuh: warp 0 copies, warp 1 issues the MMAs (rank 0 only), warps 2..9 are the
+// epilogue. full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
+// that gives up a bounded wait records it and stops, and the others' own waits end the same way.
+template <int KIND, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_constant__ PairParams params) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = base + kStages * kStageBytes;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  const uint32_t acc_full = bars + 16u * kStages, acc_empty = acc_full + 16u, mma_done = acc_empty + 16u;
+  const uint32_t slot = mma_done + 8u;
+  const uint32_t staging = bars + 1024u;
+  unsigned* const status = params.status;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile0 = static_cast<int>(cluster_id_x()), tile_step = static_cast<int>(cluster_count_x());
+  const int tiles = params.first[kMaxProblems];
+  auto problem_of = [&](int t) { return t < params.first[1] ? 0 : t < params.first[2] ? 1 : 2; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + 8u * b, 1);
+      mbar_init(acc_empty + 8u * b, 2 * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    mbar_fence_init();
+  }
+  if (warp == 1) tc::tmem_alloc<2>(slot, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's copies and commits arrive on these barriers
+  tc::tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = tile0; ok && t < tiles; t += tile_step) {
+        const int pi = problem_of(t);
+        const PairProblem& p = params.p[pi];
+        int m0, n0;
+        tile_at(p, t - params.first[pi], m0, n0);
+        m0 += rank * kRows;
+        // Gated: the same columns of this rank's weight; otherwise this rank's half of them.
+        if (!GATED) n0 += rank * (p.mma_n / 2);
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!mbar_wait_bounded(empty(s), phase ^ 1u, status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+          const int part = kb >= p.nkb_first ? 1 : 0;
+          const int k0 = (kb - (part ? p.nkb_first : 0)) * kBK;
+          const CUtensorMap* ma = &p.a[part];
+          const CUtensorMap* mb = &p.b[GATED ? rank : part];
+          const uint32_t bar = tc::map_to_rank(full(s), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), p.stage_tx);
+          if (p.a_k_major) {
+            tc::tma_load_2d_pair(st, ma, k0, m0, bar);
+          } else {
+            tc::tma_load_2d_pair(st, ma, m0, k0, bar);
+            tc::tma_load_2d_pair(st + kBoxBytes, ma, m0 + 64, k0, bar);
+          }
+          if (p.b_k_major) {
+            tc::tma_load_2d_pair(st + kABytes, mb, k0, n0, bar);
+          } else {
+            tc::tma_load_2d_pair(st + kABytes, mb, n0, k0, bar);
+            if (p.b_boxes > 1) tc::tma_load_2d_pair(st + kABytes + kBoxBytes, mb, n0 + 64, k0, bar);
+          }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every slot's copies have landed and been read before the CTA may go.
+      for (int i = 0; ok && i < kStages; ++i) {
+        ok = mbar_wait_bounded(empty(s), phase ^ 1u, status);
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int s = 0, use = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = tile0; ok && t < tiles; t += tile_step, ++use) {
+        const PairProblem& p = params.p[problem_of(t)];
+        const OperandForm fa = operand_form(p.a_k_major), fb = operand_form(p.b_k_major);
+        const uint32_t idesc = p.idesc;
+        const int nkb = p.nkb, b = use & 1;
+        const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
+        if (!mbar_wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status)) break;
+        tc::tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait_bounded(full(s), phase, status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+          const uint64_t da = with_address(fa, st), db = with_address(fb, st + kABytes);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k)
+            tc::mma_issue<1, 2>(acc, da + k * fa.step, db + k * fb.step, idesc, (kb | k) != 0 ? 1u : 0u);
+          tc::mma_commit_pair(empty(s));
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc::mma_commit_pair(acc_full + 8u * b);
+      }
+      // Every MMA issued above ends before TMEM is released.
+      tc::mma_commit<2>(mma_done);
+      mbar_wait_bounded(mma_done, 0u, status);
+    }
+    __syncwarp();
+  } else {
+    const int e = warp - 2, q = warp & 3, half = e >> 2;
+    Staging boxes{staging + static_cast<uint32_t>(e) * 2u * kUnitBytes, 0u, lane};
+    const uint32_t bias_row = staging + kStagingBytes + static_cast<uint32_t>(e) * kUnit * 4u;
+    int use = 0;
+    for (int t = tile0; t < tiles; t += tile_step, ++use) {
+      const int pi = problem_of(t);
+      const PairProblem& p = params.p[pi];
+      int m0, n0;
+      tile_at(p, t - params.first[pi], m0, n0);
+      const int b = use & 1, m = m0 + rank * kRows + 32 * q;
+      const bool done = mbar_wait_bounded(acc_full + 8u * b, (use >> 1) & 1u, status);
+      if (!__all_sync(0xffffffffu, done)) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b) * kMaxN;
+      const bool any = p.nkb > 0;
+      // The two warps of a row quarter take every other group of 32 columns.
+      for (int c = half * kUnit; c < p.bn; c += 2 * kUnit) {
+        const int n = n0 + c;
+        if (n >= p.N || m >= p.M) continue;  // the same for the whole warp
+        float v[kUnit];
+        load_sums(acc + static_cast<uint32_t>(c), any, v);
+        if constexpr (GATED) {
+          float u[kUnit];
+          load_sums(acc + static_cast<uint32_t>(p.bn + c), any, u);
+          if (p.Z != nullptr) {
+            const uint32_t box = boxes.next();
+            put_row<KIND>(box, lane, v);
+            store_unit(&p.z, p.z_tma, box, p.Z, p.ldz, m, n, p.M, p.N, lane);
+          }
+          if (p.Z2 != nullptr) {
+            const uint32_t box = boxes.next();
+            put_row<KIND>(box, lane, u);
+            store_unit(&p.z2, p.z2_tma, box, p.Z2, p.ldz2, m, n, p.M, p.N, lane);
+          }
+          with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] = act_value<decltype(a)::value>(v[i]) * u[i];
+          });
+          const uint32_t box = boxes.next();
+          put_row<KIND>(box, lane, v);
+          store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
+        } else {
+          if (p.bias != nullptr) {
+            const float mine = n + lane < p.N ? to_f32<KIND>(p.bias[n + lane]) : 0.0f;
+            __syncwarp();
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_row + 4u * lane), "f"(mine) : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kUnit; i += 4) {
+              const float4 x = lds128(bias_row + 4u * i);
+              v[i] += x.x;
+              v[i + 1] += x.y;
+              v[i + 2] += x.z;
+              v[i + 3] += x.w;
+            }
+          }
+          if (p.Z != nullptr) {
+            const uint32_t box = boxes.next();
+            put_row<KIND>(box, lane, v);
+            store_unit(&p.z, p.z_tma, box, p.Z, p.ldz, m, n, p.M, p.N, lane);
+          }
+          with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+          });
+          const uint32_t box = boxes.next();
+          if (p.R != nullptr) {
+            load_unit(box, p.R, p.ldr, p.r_wide, m, n, p.M, p.N, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[4];
+              ld_shared_v4(box + unit_chunk(lane, i), r);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 x = to_f32x2<KIND>(r[j]);
+                v[8 * i + 2 * j] += x.x;
+                v[8 * i + 2 * j + 1] += x.y;
+              }
+            }
+          }
+          put_row<KIND>(box, lane, v);
+          store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_empty + 8u * b, 0));
+    }
+    if (lane == 0) bulk_wait_all();  // the stores read this CTA's shared memory
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA goes while the other may use its memory, barriers or TMEM
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc<2>(tmem, kTmemCols);
+  }
+}
+
+// Resident clusters of a kernel on the current device, looked up once.
+template <int KIND, bool GATED>
+cudaError_t resident_clusters(int* out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    auto kern = ff_pair_kernel<KIND, GATED>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
+      return e;
+    int sms = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    known[dev].store(n, std::memory_order_release);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+cudaError_t operand_map(CUtensorMap* m, const Operand& o, int64_t extent, int64_t K, uint32_t box_extent) {
+  return o.k_major ? encode_tmap_16bit_2d(m, o.p, K, extent, o.ld, kBK, box_extent, CU_TENSOR_MAP_SWIZZLE_128B)
+                   : encode_tmap_16bit_2d(m, o.p, extent, K, o.ld, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The store map of an output, where its rows allow one: on 16-byte boundaries and of whole 16-byte
+// words (a store clipped at an odd width still writes the whole of its last 16 bytes).
+cudaError_t output_map(CUtensorMap* m, int* usable, const Matrix& o, int64_t M, int64_t N) {
+  *usable = 0;
+  if (o.p == nullptr || N % 8 != 0 || !aligned16(o.p, o.ld)) return cudaSuccess;
+  *usable = 1;
+  return encode_tmap_16bit_2d(m, o.p, N, M, o.ld, kUnit, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int KIND>
+cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
+  const bool gated = t.form == kGated;
+  cudaError_t e = cudaSuccess;
+  p->M = static_cast<int>(t.M);
+  p->N = static_cast<int>(t.N);
+  p->mma_n = mma_n;
+  p->bn = gated ? mma_n / 2 : mma_n;
+  p->tiles_m = static_cast<int>((t.M + 2 * kRows - 1) / (2 * kRows));
+  p->tiles_n = static_cast<int>((t.N + p->bn - 1) / p->bn);
+  const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
+  p->nkb_first = blocks;
+  p->nkb = t.form == kJoined ? 2 * blocks : blocks;
+  p->a_k_major = t.A.k_major;
+  p->b_k_major = t.B.k_major;
+  p->b_boxes = (mma_n / 2 + 63) / 64;
+  const uint32_t b_bytes = p->b_k_major ? static_cast<uint32_t>(mma_n / 2) * kBK * 2
+                                        : static_cast<uint32_t>(p->b_boxes) * kBoxBytes;
+  p->stage_tx = 2 * (kABytes + b_bytes);
+  // D FP32, A and B of the 16-bit type, their orders, N and M = 256.
+  const uint32_t fmt = KIND == kBf16 ? 1u : 0u;
+  p->idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p->a_k_major ? 0u : 1u) << 15) |
+             ((p->b_k_major ? 0u : 1u) << 16) | (static_cast<uint32_t>(mma_n >> 3) << 17) |
+             (static_cast<uint32_t>(2 * kRows >> 4) << 24);
+  p->bias = t.bias;
+  p->R = t.R.p;
+  p->ldr = t.R.ld;
+  p->r_wide = t.R.p != nullptr && aligned16(t.R.p, t.R.ld);
+  p->Y = t.Y.p;
+  p->ldy = t.Y.ld;
+  p->Z = t.Z.p;
+  p->ldz = t.Z.ld;
+  p->Z2 = t.Z2.p;
+  p->ldz2 = t.Z2.ld;
+  p->act = t.act;
+  if (blocks > 0) {
+    const uint32_t half = static_cast<uint32_t>(mma_n / 2);
+    if ((e = operand_map(&p->a[0], t.A, t.M, t.K, kRows)) != cudaSuccess) return e;
+    if ((e = operand_map(&p->b[0], t.B, t.N, t.K, half)) != cudaSuccess) return e;
+    if (t.form == kJoined && (e = operand_map(&p->a[1], t.A2, t.M, t.K, kRows)) != cudaSuccess) return e;
+    if (t.form != kLinear && (e = operand_map(&p->b[1], t.B2, t.N, t.K, half)) != cudaSuccess) return e;
+  }
+  if ((e = output_map(&p->y, &p->y_tma, t.Y, t.M, t.N)) != cudaSuccess) return e;
+  if ((e = output_map(&p->z, &p->z_tma, t.Z, t.M, t.N)) != cudaSuccess) return e;
+  return output_map(&p->z2, &p->z2_tma, t.Z2, t.M, t.N);
+}
+
+template <int KIND, bool GATED>
+cudaError_t launch(const Context& c, const Task* tasks, int n) {
+  int resident = 0;
+  cudaError_t e = resident_clusters<KIND, GATED>(&resident);
+  if (e != cudaSuccess) return e;
+  PairParams params;
+  memset(&params, 0, sizeof(params));
+  params.status = c.status;
+  int64_t tiles = 0;
+  for (int i = 0; i < kMaxProblems; ++i) {
+    params.first[i] = static_cast<int>(tiles);
+    if (i < n) {
+      if ((e = fill<KIND>(&params.p[i], tasks[i], kMaxN)) != cudaSuccess) return e;
+      tiles += static_cast<int64_t>(params.p[i].tiles_m) * params.p[i].tiles_n;
+      if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    }
+  }
+  params.first[kMaxProblems] = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ff_pair_kernel<KIND, GATED>, params);
+}
+
+}  // namespace
+
+cudaError_t run_pair(const Context& c, const Task* tasks, int n) {
+  if (n == 0) return cudaSuccess;
+  const bool gated = tasks[0].form == kGated;
+  if (c.kind == kBf16) return gated ? launch<kBf16, true>(c, tasks, n) : launch<kBf16, false>(c, tasks, n);
+  return gated ? launch<kF16, true>(c, tasks, n) : launch<kF16, false>(c, tasks, n);
+}
+
+}  // namespace ff
+}  // namespace t2s

@@ -64,8 +64,8 @@ def _rows(t, name, like, shape=None):
     if shape is not None and (rows, cols) != shape:
         raise ValueError("%s must be %d x %d, got %d x %d" % (name, *shape, rows, cols))
     ld, step = t.stride()
-    if rows <= 1:
-        ld = cols
+    if rows <= 1:  # its stride is never used: one that keeps the row in place
+        ld = (cols + 7) // 8 * 8
     if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
     return t.data_ptr(), ld
@@ -81,9 +81,9 @@ def _weight(t, name, like, shape=None):
         raise ValueError("%s must be %d x %d, got %d x %d" % (name, *shape, k, n))
     a, b = t.stride()
     if b == 1 and (a >= n or k <= 1):
-        return t.data_ptr(), max(a, n), T2S_W_KN
+        return t.data_ptr(), a if k > 1 else (n + 7) // 8 * 8, T2S_W_KN
     if a == 1 and (b >= k or n <= 1):
-        return t.data_ptr(), max(b, k), T2S_W_NK
+        return t.data_ptr(), b if n > 1 else (k + 7) // 8 * 8, T2S_W_NK
     raise ValueError("%s must be row-major or the transpose of a row-major tensor" % name)
 
 

@@ -231,8 +231,11 @@ def test_gated_backward(m, k, n):
         mk.check_canaries()
 
 
-@pytest.mark.parametrize("pad,shift", [(8, 8), (24, 0), (3, 0), (0, 1), (5, 3)])
-@pytest.mark.parametrize("m,k,n", [(1, 256, 136), (20, 72, 264), (300, 136, 200)])
+@pytest.mark.parametrize("m,k,n,pad,shift", [
+    (m, k, n, pad, shift) for m, k, n in [(1, 256, 136), (20, 72, 264), (300, 136, 200)]
+    for pad, shift in [(8, 8), (24, 0), (3, 0), (0, 1), (5, 3)]] + [
+    # Odd widths inside rows that are 16-byte aligned: what lies behind them is not theirs.
+    (1, 253, 133, 3, 0), (20, 69, 261, 3, 8), (300, 133, 197, 3, 0), (45, 70, 262, 10, 0)])
 def test_strides_and_offsets(m, k, n, pad, shift):
     """Views of larger tensors: rows that stay 16-byte aligned and rows that do not."""
     for wt in (False, True):
