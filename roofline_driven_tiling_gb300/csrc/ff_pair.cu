@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "ff_device.cuh"
 #include "ff_internal.h"
 #include "ff_math.cuh"
 #include "t2s_device.cuh"
@@ -38,7 +39,7 @@ constexpr int kBBytes = kMaxN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kBoxBytes = 64 * kBK * 2;  // 64 outputs x 64 K rows of an MN-major operand
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kUnit = 32;                        // columns an epilogue warp takes at a time
 constexpr int kUnitBytes = 32 * kUnit * 2;       // 32 rows of 64 bytes
 constexpr int kStagingBytes = kEpiWarps * 2 * kUnitBytes;
@@ -189,8 +190,35 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, bool any, float (&s)[k
   for (int i = 0; i < kUnit; ++i) s[i] = any ? __uint_as_float(r[i]) : 0.0f;
 }
 
-// Roles as in tc_gemm.cuh: warp 0 copies, warp 1 issues the MMAs (rank 0 only), warps 2..9 are the
-// epilogue. full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
+// A copying thread's walk over the ring's slots.
+struct Ring {
+  uint32_t first, bars;  // its part of slot 0; the full barriers, then the empty ones
+  uint32_t st, s = 0, phase = 1;
+
+  __device__ __forceinline__ Ring(uint32_t first_, uint32_t bars_) : first(first_), bars(bars_), st(first_) {}
+
+  // `blocks` K blocks from k = 0 on, each into the next slot once that is free.
+  template <class F>
+  __device__ __forceinline__ bool copy(int blocks, bool expects, uint32_t bytes, uint32_t bar0, unsigned* status,
+                                       F&& issue) {
+#pragma unroll 1
+    for (int k0 = 0; k0 < blocks * kBK; k0 += kBK) {
+      if (!wait_bounded(bars + 8u * (kStages + s), phase, status)) return false;
+      if (expects) mbar_arrive_expect_tx(bars + 8u * s, bytes);
+      issue(st, k0, bar0 + 8u * s);
+      st += kStageBytes;
+      if (++s == kStages) {
+        s = 0;
+        st = first;
+        phase ^= 1u;
+      }
+    }
+    return true;
+  }
+};
+
+// Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 are the
+// epilogue (warp 3 only holds TMEM). full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
 // that gives up a bounded wait records it and stops, and the others' own waits end the same way.
 template <int KIND, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_constant__ PairParams params) {
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
     mbar_init(mma_done, 1);
     mbar_fence_init();
   }
-  if (warp == 1) tc::tmem_alloc<2>(slot, kTmemCols);
+  if (warp == 3) tc::tmem_alloc<2>(slot, kTmemCols);
   tc::tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // the peer's copies and commits arrive on these barriers
@@ -230,63 +258,56 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
+    // Copies of A (warp 0) and of B (warp 2): one thread each, so that neither's instructions
+    // between two copies hold up the other's.
     if (lane == 0) {
-      int s = 0;
-      uint32_t phase = 0;
+      const bool is_a = warp == 0;
+      Ring ring(base + (is_a ? 0 : kABytes), bars);
+      const uint32_t bar0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
+      const bool expects = is_a && rank == 0;
       bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         const int pi = problem_of(t);
         const PairProblem& p = params.p[pi];
         int m0, n0;
         tile_at(p, t - params.first[pi], m0, n0);
-        m0 += rank * kRows;
         // Gated: the same columns of this rank's weight; otherwise this rank's half of them.
-        if (!GATED) n0 += rank * (p.mma_n / 2);
-        for (int kb = 0; kb < p.nkb; ++kb) {
-          if (!mbar_wait_bounded(empty(s), phase ^ 1u, status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
-          const int part = kb >= p.nkb_first ? 1 : 0;
-          const int k0 = (kb - (part ? p.nkb_first : 0)) * kBK;
-          const CUtensorMap* ma = &p.a[part];
-          const CUtensorMap* mb = &p.b[GATED ? rank : part];
-          const uint32_t bar = tc::map_to_rank(full(s), 0);
-          if (rank == 0) mbar_arrive_expect_tx(full(s), p.stage_tx);
-          if (p.a_k_major) {
-            tc::tma_load_2d_pair(st, ma, k0, m0, bar);
+        const int at = is_a ? m0 + rank * kRows : GATED ? n0 : n0 + rank * (p.mma_n / 2);
+        const bool k_major = is_a ? p.a_k_major : p.b_k_major;
+        const int boxes = is_a ? kRows / 64 : p.b_boxes;
+        const uint32_t bytes = p.stage_tx;
+        int blocks = p.nkb_first, left = p.nkb - blocks;
+        const CUtensorMap* map = is_a ? &p.a[0] : &p.b[GATED ? rank : 0];
+        while (ok) {
+          if (k_major) {
+            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+              tc::tma_load_2d_pair(st, map, k0, at, bar);
+            });
+          } else if (boxes > 1) {
+            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+              tc::tma_load_2d_pair(st, map, at, k0, bar);
+              tc::tma_load_2d_pair(st + kBoxBytes, map, at + 64, k0, bar);
+            });
           } else {
-            tc::tma_load_2d_pair(st, ma, m0, k0, bar);
-            tc::tma_load_2d_pair(st + kBoxBytes, ma, m0 + 64, k0, bar);
+            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+              tc::tma_load_2d_pair(st, map, at, k0, bar);
+            });
           }
-          if (p.b_k_major) {
-            tc::tma_load_2d_pair(st + kABytes, mb, k0, n0, bar);
-          } else {
-            tc::tma_load_2d_pair(st + kABytes, mb, n0, k0, bar);
-            if (p.b_boxes > 1) tc::tma_load_2d_pair(st + kABytes + kBoxBytes, mb, n0 + 64, k0, bar);
-          }
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1u;
-          }
+          if (left == 0) break;
+          blocks = left;
+          left = 0;
+          map = is_a ? &p.a[1] : &p.b[1];
         }
       }
       // Every slot's copies have landed and been read before the CTA may go.
-      for (int i = 0; ok && i < kStages; ++i) {
-        ok = mbar_wait_bounded(empty(s), phase ^ 1u, status);
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1u;
-        }
-      }
+      if (ok) ring.copy(kStages, false, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       int s = 0, use = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, st = base;
       bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step, ++use) {
         const PairProblem& p = params.p[problem_of(t)];
@@ -294,22 +315,27 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         const uint32_t idesc = p.idesc;
         const int nkb = p.nkb, b = use & 1;
         const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
-        if (!mbar_wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status)) break;
+        if (!wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status)) break;
         tc::tc_fence_after();
+        uint32_t accumulate = 0;
+#pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_bounded(full(s), phase, status)) {
+          const uint64_t da = with_address(fa, st), db = with_address(fb, st + kABytes);
+          if (!wait_bounded(full(s), phase, status)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
-          const uint64_t da = with_address(fa, st), db = with_address(fb, st + kABytes);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            tc::mma_issue<1, 2>(acc, da + k * fa.step, db + k * fb.step, idesc, (kb | k) != 0 ? 1u : 0u);
+          for (int k = 0; k < kBK / 16; ++k) {
+            tc::mma_issue<1, 2>(acc, da + k * fa.step, db + k * fb.step, idesc, accumulate);
+            accumulate = 1;
+          }
           tc::mma_commit_pair(empty(s));
+          st += kStageBytes;
           if (++s == kStages) {
             s = 0;
+            st = base;
             phase ^= 1u;
           }
         }
@@ -317,11 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       }
       // Every MMA issued above ends before TMEM is released.
       tc::mma_commit<2>(mma_done);
-      mbar_wait_bounded(mma_done, 0u, status);
+      wait_bounded(mma_done, 0u, status);
     }
     __syncwarp();
-  } else {
-    const int e = warp - 2, q = warp & 3, half = e >> 2;
+  } else if (warp >= 4) {
+    const int e = warp - 4, q = warp & 3, half = e >> 2;
     Staging boxes{staging + static_cast<uint32_t>(e) * 2u * kUnitBytes, 0u, lane};
     const uint32_t bias_row = staging + kStagingBytes + static_cast<uint32_t>(e) * kUnit * 4u;
     int use = 0;
@@ -331,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       int m0, n0;
       tile_at(p, t - params.first[pi], m0, n0);
       const int b = use & 1, m = m0 + rank * kRows + 32 * q;
-      const bool done = mbar_wait_bounded(acc_full + 8u * b, (use >> 1) & 1u, status);
+      const bool done = wait_bounded(acc_full + 8u * b, (use >> 1) & 1u, status);
       if (!__all_sync(0xffffffffu, done)) break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b) * kMaxN;
@@ -415,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   tc::tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // neither CTA goes while the other may use its memory, barriers or TMEM
-  if (warp == 1) {
+  if (warp == 3) {
     tc::tc_fence_after();
     tc::tmem_dealloc<2>(tmem, kTmemCols);
   }
