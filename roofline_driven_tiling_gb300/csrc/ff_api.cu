@@ -165,7 +165,7 @@ int linear(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_
   Workspace ws{static_cast<uint8_t*>(workspace)};
   if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
   if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
-  return done(run_pair(c, &t, 1));
+  return done(run_products(c, &t, 1));
 }
 
 int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* X,
@@ -220,7 +220,7 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
     if ((e = readable(c, &ws, M, K, &x)) != cudaSuccess) return done(e);
     tasks[n++] = weight_gradient(M, N, K, x, d, w_order, {dW, lddw});
   }
-  return done(run_pair(c, tasks, n));
+  return done(run_products(c, tasks, n));
 }
 
 int gated(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const uint16_t* Wg,
@@ -253,7 +253,7 @@ int gated(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t
   if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
   if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
   if ((e = readable_weight(c, &ws, K, N, w_order, &t.B2)) != cudaSuccess) return done(e);
-  return done(run_pair(c, &t, 1));
+  return done(run_products(c, &t, 1));
 }
 
 int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* dH, int64_t lddh, const uint16_t* X,
@@ -308,7 +308,7 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
     if (dWg != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dG, ldd, false}, w_order, {dWg, lddwg});
     if (dWu != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dU, ldd, false}, w_order, {dWu, lddwu});
   }
-  return done(run_pair(c, tasks, n));
+  return done(run_products(c, tasks, n));
 }
 
 bool bad_sizes(int64_t M, int64_t N, int64_t K) { return bad_size(M) || bad_size(N) || bad_size(K); }

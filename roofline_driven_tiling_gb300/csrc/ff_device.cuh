@@ -1,7 +1,9 @@
 // ff_device.cuh -- device helpers of the feed-forward kernels beside t2s_device.cuh.
 #pragma once
 
+#include "ff_internal.h"
 #include "t2s_device.cuh"
+#include "t2s_tmap.h"
 
 namespace t2s {
 namespace ff {
@@ -28,6 +30,34 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsi
     if (ok != 0) return true;
   }
   return wait_long(bar, parity, status);
+}
+
+constexpr int kBK = 64;                  // K block: 128-byte rows of 16-bit values
+constexpr int kBoxBytes = 64 * kBK * 2;  // 64 outputs x 64 K rows of an MN-major operand
+
+// A matrix descriptor without its address: K-major 128-byte-swizzled rows (8-row groups 1024
+// bytes apart), or MN-major atoms (64 outputs x 8 K rows; the next 64 outputs one box further,
+// the next 8 K rows 1024 bytes further). `step` is the advance of 16 K values.
+struct OperandForm {
+  uint64_t base;
+  uint32_t step;
+};
+__device__ __forceinline__ OperandForm operand_form(bool k_major) {
+  OperandForm f;
+  f.base = (static_cast<uint64_t>(k_major ? 1 : kBoxBytes >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+  f.step = (k_major ? 32 : 16 * 128) >> 4;
+  return f;
+}
+__device__ __forceinline__ uint64_t with_address(const OperandForm& f, uint32_t addr) {
+  return f.base | static_cast<uint64_t>((addr & 0x3ffffu) >> 4);
+}
+
+// The tensor map of an operand of `extent` x K values, in boxes of box_extent x 64 (K-major) or of
+// 64 K rows x 64 (MN-major).
+inline cudaError_t operand_map(CUtensorMap* m, const Operand& o, int64_t extent, int64_t K, uint32_t box_extent) {
+  return o.k_major ? encode_tmap_16bit_2d(m, o.p, K, extent, o.ld, kBK, box_extent, CU_TENSOR_MAP_SWIZZLE_128B)
+                   : encode_tmap_16bit_2d(m, o.p, extent, K, o.ld, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace ff

@@ -57,6 +57,19 @@ inline bool aligned16(const void* p, int64_t ld) {
 // in place (aligned16), and rows of a single-row operand given a stride that is.
 cudaError_t run_pair(const Context& c, const Task* tasks, int n);
 
+// How ff_rows.cu takes a product: rows of X per tile, CTAs along K, ring slots.
+struct RowsPlan {
+  int tm = 0, splits = 1, stages = 0, smem_bytes = 0;
+  uint32_t stage_bytes = 0, tmem_cols = 0;
+  int64_t ctas = 0;
+};
+RowsPlan plan_rows(const Task& t, int sms);
+// One product with its sum split over a cluster; operands as for run_pair.
+cudaError_t run_rows(const Context& c, const Task& t, const RowsPlan& plan);
+
+// Up to three products, none or all of them of the gated form, each by the kernel that suits its sizes.
+cudaError_t run_products(const Context& c, const Task* tasks, int n);
+
 // dst (rows x cols, ldd per row) = src.
 cudaError_t run_copy(const Context& c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld, uint16_t* dst,
                      int64_t ldd);

@@ -31,13 +31,11 @@ namespace ff {
 namespace {
 
 constexpr int kRows = 128;    // A rows of one CTA
-constexpr int kBK = 64;       // K block: 128-byte rows
 constexpr int kStages = 6;    // ring slots of 32 KB
 constexpr int kMaxN = 256;    // widest MMA
 constexpr int kABytes = kRows * kBK * 2;
 constexpr int kBBytes = kMaxN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kBoxBytes = 64 * kBK * 2;  // 64 outputs x 64 K rows of an MN-major operand
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kUnit = 32;                        // columns an epilogue warp takes at a time
@@ -72,24 +70,6 @@ struct PairParams {
   int first[kMaxProblems + 1];  // first tile of each problem; the last entry is the tile count
   unsigned* status;
 };
-
-// A matrix descriptor without its address: K-major 128-byte-swizzled rows (8-row groups 1024
-// bytes apart), or MN-major atoms (64 outputs x 8 K rows; the next 64 outputs one box further,
-// the next 8 K rows 1024 bytes further). `step` is the advance of 16 K values.
-struct OperandForm {
-  uint64_t base;
-  uint32_t step;
-};
-__device__ __forceinline__ OperandForm operand_form(bool k_major) {
-  OperandForm f;
-  f.base = (static_cast<uint64_t>(k_major ? 1 : kBoxBytes >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-           (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-  f.step = (k_major ? 32 : 16 * 128) >> 4;
-  return f;
-}
-__device__ __forceinline__ uint64_t with_address(const OperandForm& f, uint32_t addr) {
-  return f.base | static_cast<uint64_t>((addr & 0x3ffffu) >> 4);
-}
 
 // Column groups of 8 tile rows sweep the columns together, so that the tiles in flight share A
 // and B in the L2 cache.
@@ -480,11 +460,6 @@ cudaError_t resident_clusters(int* out) {
   }
   *out = n;
   return cudaSuccess;
-}
-
-cudaError_t operand_map(CUtensorMap* m, const Operand& o, int64_t extent, int64_t K, uint32_t box_extent) {
-  return o.k_major ? encode_tmap_16bit_2d(m, o.p, K, extent, o.ld, kBK, box_extent, CU_TENSOR_MAP_SWIZZLE_128B)
-                   : encode_tmap_16bit_2d(m, o.p, extent, K, o.ld, 64, kBK, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The store map of an output, where its rows allow one: on 16-byte boundaries and of whole 16-byte
