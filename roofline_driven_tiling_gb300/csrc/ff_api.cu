@@ -88,23 +88,32 @@ size_t copy_bytes(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   return rows == 0 || cols == 0 || in_place(p, rows, ld) ? 0 : plane_bytes(rows, cols);
 }
 
-// The rows x cols matrix `o` as it can be read: itself, or a copy in the workspace.
-cudaError_t readable(const Context& c, Workspace* ws, int64_t rows, int64_t cols, Operand* o) {
-  if (rows == 0 || cols == 0) return cudaSuccess;
-  if (in_place(o->p, rows, o->ld)) {
-    if (rows <= 1) o->ld = up8(cols);
-    return cudaSuccess;
-  }
-  uint16_t* copy = static_cast<uint16_t*>(ws->take(plane_bytes(rows, cols)));
-  const cudaError_t e = run_copy(c, rows, cols, o->p, o->ld, copy, up8(cols));
-  o->p = copy;
-  o->ld = up8(cols);
-  return e;
-}
+// The operands of a call that are copied into the workspace first, in one launch.
+struct Copies {
+  Workspace* ws;
+  Copy list[kMaxCopies];
+  int n = 0;
 
-cudaError_t readable_weight(const Context& c, Workspace* ws, int64_t K, int64_t N, int w_order, Operand* o) {
-  return w_order == T2S_W_KN ? readable(c, ws, K, N, o) : readable(c, ws, N, K, o);
-}
+  // The rows x cols matrix `o` as it can be read: itself, or a copy.
+  void read(int64_t rows, int64_t cols, Operand* o) {
+    if (rows == 0 || cols == 0) return;
+    if (in_place(o->p, rows, o->ld)) {
+      if (rows <= 1) o->ld = up8(cols);
+      return;
+    }
+    uint16_t* copy = static_cast<uint16_t*>(ws->take(plane_bytes(rows, cols)));
+    list[n++] = {o->p, o->ld, rows, cols, copy};
+    o->p = copy;
+    o->ld = up8(cols);
+  }
+  void read_weight(int64_t K, int64_t N, int w_order, Operand* o) {
+    if (w_order == T2S_W_KN) {
+      read(K, N, o);
+    } else {
+      read(N, K, o);
+    }
+  }
+};
 
 size_t weight_copy_bytes(const void* p, int64_t K, int64_t N, int64_t ld, int w_order) {
   return w_order == T2S_W_KN ? copy_bytes(p, K, N, ld) : copy_bytes(p, N, K, ld);
@@ -163,8 +172,10 @@ int linear(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_
   t.Y = {Y, ldy};
   t.Z = {Z, ldz};
   Workspace ws{static_cast<uint8_t*>(workspace)};
-  if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
-  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
+  Copies copies{&ws};
+  copies.read(M, K, &t.A);
+  copies.read_weight(K, N, w_order, &t.B);
+  if ((e = run_copies(c, copies.list, copies.n)) != cudaSuccess) return done(e);
   return done(run_products(c, &t, 1));
 }
 
@@ -194,6 +205,7 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
+  Copies copies{&ws};
   Operand d{dY, M <= 1 ? ldd : lddy, true};
   if (M > 0 && N > 0 && (plane || db != nullptr)) {
     uint16_t* dz = plane ? static_cast<uint16_t*>(ws.take(plane_bytes(M, N))) : nullptr;
@@ -213,13 +225,14 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
     t.A = d;
     t.B = weight_backward(W, ldw, w_order);
     t.Y = {dX, lddx};
-    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
+    copies.read_weight(K, N, w_order, &t.B);
   }
   if (dW != nullptr && K > 0 && N > 0) {
     Operand x{X, ldx, false};
-    if ((e = readable(c, &ws, M, K, &x)) != cudaSuccess) return done(e);
+    copies.read(M, K, &x);
     tasks[n++] = weight_gradient(M, N, K, x, d, w_order, {dW, lddw});
   }
+  if ((e = run_copies(c, copies.list, copies.n)) != cudaSuccess) return done(e);
   return done(run_products(c, tasks, n));
 }
 
@@ -250,9 +263,11 @@ int gated(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t
   t.Z = {G, ldg};
   t.Z2 = {U, ldu};
   Workspace ws{static_cast<uint8_t*>(workspace)};
-  if ((e = readable(c, &ws, M, K, &t.A)) != cudaSuccess) return done(e);
-  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
-  if ((e = readable_weight(c, &ws, K, N, w_order, &t.B2)) != cudaSuccess) return done(e);
+  Copies copies{&ws};
+  copies.read(M, K, &t.A);
+  copies.read_weight(K, N, w_order, &t.B);
+  copies.read_weight(K, N, w_order, &t.B2);
+  if ((e = run_copies(c, copies.list, copies.n)) != cudaSuccess) return done(e);
   return done(run_products(c, &t, 1));
 }
 
@@ -281,6 +296,7 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
   cudaError_t e = device_status_word(&c.status);
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
+  Copies copies{&ws};
   uint16_t *dG = nullptr, *dU = nullptr;
   if (M > 0 && N > 0 && (dw || dX != nullptr)) {
     dG = static_cast<uint16_t*>(ws.take(plane_bytes(M, N)));
@@ -299,15 +315,16 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
     t.B = weight_backward(Wg, ldwg, w_order);
     t.B2 = weight_backward(Wu, ldwu, w_order);
     t.Y = {dX, lddx};
-    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B)) != cudaSuccess) return done(e);
-    if ((e = readable_weight(c, &ws, K, N, w_order, &t.B2)) != cudaSuccess) return done(e);
+    copies.read_weight(K, N, w_order, &t.B);
+    copies.read_weight(K, N, w_order, &t.B2);
   }
   if (dw && K > 0 && N > 0) {
     Operand x{X, ldx, false};
-    if ((e = readable(c, &ws, M, K, &x)) != cudaSuccess) return done(e);
+    copies.read(M, K, &x);
     if (dWg != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dG, ldd, false}, w_order, {dWg, lddwg});
     if (dWu != nullptr) tasks[n++] = weight_gradient(M, N, K, x, {dU, ldd, false}, w_order, {dWu, lddwu});
   }
+  if ((e = run_copies(c, copies.list, copies.n)) != cudaSuccess) return done(e);
   return done(run_products(c, tasks, n));
 }
 

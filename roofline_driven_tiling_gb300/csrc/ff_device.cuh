@@ -32,6 +32,38 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, unsi
   return wait_long(bar, parity, status);
 }
 
+// A kernel launched by launch_early may start while the ones before it on its stream still run:
+// what it does before wait_for_earlier_kernels touches no global memory. From then on the next kernel's
+// start-up may overlap this one's work in the same way.
+__device__ __forceinline__ void wait_for_earlier_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+struct LaunchShape {
+  dim3 grid;
+  int threads, cluster, smem;
+};
+
+template <class... P, class... A>
+cudaError_t launch_early(cudaStream_t stream, const LaunchShape& shape, void (*kernel)(P...), const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(shape.cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = shape.grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(shape.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(shape.smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = shape.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 constexpr int kBK = 64;                  // K block: 128-byte rows of 16-bit values
 constexpr int kBoxBytes = 64 * kBK * 2;  // 64 outputs x 64 K rows of an MN-major operand
 
@@ -52,6 +84,34 @@ __device__ __forceinline__ OperandForm operand_form(bool k_major) {
 __device__ __forceinline__ uint64_t with_address(const OperandForm& f, uint32_t addr) {
   return f.base | static_cast<uint64_t>((addr & 0x3ffffu) >> 4);
 }
+
+// A copying thread's walk over a ring of shared-memory slots.
+struct Ring {
+  uint32_t first, stride, full, empty, slots;  // its part of slot 0, slot size, barriers of slot 0
+  uint32_t st, s = 0, phase = 1;
+
+  __device__ __forceinline__ Ring(uint32_t first_, uint32_t stride_, uint32_t full_, uint32_t empty_, uint32_t slots_)
+      : first(first_), stride(stride_), full(full_), empty(empty_), slots(slots_), st(first_) {}
+
+  // K blocks [kb0, kb1), each into the next slot once that is free: issue(slot, k, barrier offset
+  // from `bar0` by slot). `expect` bytes are announced on the slot's full barrier if not 0.
+  template <class F>
+  __device__ __forceinline__ bool copy(int kb0, int kb1, uint32_t expect, uint32_t bar0, unsigned* status, F&& issue) {
+#pragma unroll 1
+    for (int k0 = kb0 * kBK; k0 < kb1 * kBK; k0 += kBK) {
+      if (!wait_bounded(empty + 8u * s, phase, status)) return false;
+      if (expect != 0) mbar_arrive_expect_tx(full + 8u * s, expect);
+      issue(st, k0, bar0 + 8u * s);
+      st += stride;
+      if (++s == slots) {
+        s = 0;
+        st = first;
+        phase ^= 1u;
+      }
+    }
+    return true;
+  }
+};
 
 // The tensor map of an operand of `extent` x K values, in boxes of box_extent x 64 (K-major) or of
 // 64 K rows x 64 (MN-major).

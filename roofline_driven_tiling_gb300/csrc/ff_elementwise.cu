@@ -1,15 +1,22 @@
-// ff_elementwise.cu -- the elementwise halves of the feed-forward operators' gradients.
+// ff_elementwise.cu -- the elementwise halves of the feed-forward operators' gradients, and copies of
+// operands that the tensor cores' copies cannot read in place.
 //
 //   linear: dZ = dY * act'(Z), db = sum over rows of dZ
 //   gated:  dG = dH * U * act'(G), dU = dH * act(G)
 //
 // dZ, dG and dU are rounded to the 16-bit type: they are the tensor-core operands of the weight
-// and input gradients. db sums the FP32 values before that rounding.
+// and input gradients. db sums the FP32 values before that rounding, in an order that depends on
+// the sizes alone. Bound by memory: every value is read or written once, 16 bytes per access
+// where rows allow it.
+//
+// Inputs are read with plain loads (no __restrict__): these kernels may start before the one that
+// writes them has ended (wait_for_earlier_kernels), which read-only loads do not allow for.
 #include <cuda_runtime.h>
 
 #include <cstdint>
 #include <type_traits>
 
+#include "ff_device.cuh"
 #include "ff_internal.h"
 #include "ff_math.cuh"
 
@@ -18,82 +25,185 @@ namespace ff {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kVec = 8;        // values of a thread in a row: 16 bytes
+constexpr int kGroups = 32;    // threads along a row: 256 columns of a block
+constexpr int kLanes = kThreads / kGroups;  // rows a block takes at a time
 
-// One thread per column, block row y takes the rows of one chunk: partials[y][n].
-template <int KIND>
-__global__ void __launch_bounds__(kThreads)
-    act_backward_kernel(int64_t M, int64_t N, int64_t chunk, int act, const uint16_t* __restrict__ dY,
-                        int64_t lddy, const uint16_t* __restrict__ Z, int64_t ldz,
-                        uint16_t* __restrict__ dZ, int64_t lddz, float* __restrict__ partials) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (n >= N) return;
-  const int64_t m0 = blockIdx.y * chunk, m1 = m0 + chunk < M ? m0 + chunk : M;
-  float sum = 0.0f;
-  with_act(act, [&](auto a) {
-    for (int64_t m = m0; m < m1; ++m) {
-      float value, slope = 1.0f;
-      if (decltype(a)::value != T2S_ACT_NONE)
-        act_value_slope<decltype(a)::value>(to_f32<KIND>(Z[m * ldz + n]), value, slope);
-      const float d = to_f32<KIND>(dY[m * lddy + n]) * slope;
-      sum += d;
-      if (dZ != nullptr) dZ[m * lddz + n] = from_f32<KIND>(d);
-    }
-  });
-  if (partials != nullptr) partials[static_cast<int64_t>(blockIdx.y) * N + n] = sum;
-}
+struct Source {
+  const uint16_t* p;
+  int64_t ld;
+  int wide;  // rows on 16-byte boundaries
+};
 
-template <int KIND>
-__global__ void __launch_bounds__(kThreads)
-    db_sum_kernel(int64_t rows, int64_t N, const float* __restrict__ partials, uint16_t* __restrict__ db) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (n >= N) return;
-  float sum = 0.0f;
-  for (int64_t r = 0; r < rows; ++r) sum += partials[r * N + n];
-  db[n] = from_f32<KIND>(sum);
-}
-
-template <int KIND>
-__global__ void __launch_bounds__(kThreads)
-    gated_backward_kernel(int64_t M, int64_t N, int act, const uint16_t* __restrict__ dH, int64_t lddh,
-                          const uint16_t* __restrict__ G, int64_t ldg, const uint16_t* __restrict__ U,
-                          int64_t ldu, uint16_t* __restrict__ dG, uint16_t* __restrict__ dU, int64_t ldd) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (n >= N) return;
-  with_act(act, [&](auto a) {
-    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-      float value, slope;
-      act_value_slope<decltype(a)::value>(to_f32<KIND>(G[m * ldg + n]), value, slope);
-      const float d = to_f32<KIND>(dH[m * lddh + n]);
-      dG[m * ldd + n] = from_f32<KIND>(d * to_f32<KIND>(U[m * ldu + n]) * slope);
-      dU[m * ldd + n] = from_f32<KIND>(d * value);
-    }
-  });
-}
-
-// Copies of operands whose rows are not 16-byte aligned: 8 values per thread, written as one word.
-__global__ void __launch_bounds__(kThreads) copy_kernel(int64_t rows, int64_t cols, const uint16_t* __restrict__ src,
-                                                        int64_t ld, uint16_t* __restrict__ dst, int64_t ldd) {
-  const int64_t per_row = ldd / 8, total = rows * per_row;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-    uint16_t v[8];
+// Eight values of a row from column c on as four words, zeros beyond `cols`.
+__device__ __forceinline__ uint4 load8(const Source& s, int64_t r, int64_t c, int64_t cols) {
+  const uint16_t* p = s.p + r * s.ld + c;
+  if (s.wide && c + kVec <= cols) return *reinterpret_cast<const uint4*>(p);
+  uint32_t v[kVec];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? src[r * ld + c + j] : static_cast<uint16_t>(0);
-    *reinterpret_cast<uint4*>(dst + r * ldd + c) =
-        make_uint4(v[0] | (uint32_t(v[1]) << 16), v[2] | (uint32_t(v[3]) << 16), v[4] | (uint32_t(v[5]) << 16),
-                   v[6] | (uint32_t(v[7]) << 16));
+  for (int i = 0; i < kVec; ++i) v[i] = c + i < cols ? p[i] : 0u;
+  return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
+template <int KIND>
+__device__ __forceinline__ void widen(const uint4& w, float (&v)[kVec]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = to_f32x2<KIND>(u[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 
+template <int KIND>
+__device__ __forceinline__ uint4 narrow(const float (&v)[kVec]) {
+  return make_uint4(pack_f32<KIND>(v[0], v[1]), pack_f32<KIND>(v[2], v[3]), pack_f32<KIND>(v[4], v[5]),
+                    pack_f32<KIND>(v[6], v[7]));
+}
+
+// Block (x, y): 256 columns, the rows of chunk y, eight at a time; dZ's rows are 16-byte aligned and
+// padded to whole words. partials[y] receives the chunk's column sums.
+template <int KIND, int ACT>
+__global__ void __launch_bounds__(kThreads)
+    act_backward_kernel(int64_t M, int64_t N, int64_t chunk, Source dy, Source z, uint16_t* dZ, int64_t lddz,
+                        float* partials) {
+  wait_for_earlier_kernels();
+  const int group = threadIdx.x % kGroups, row = threadIdx.x / kGroups;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * kGroups + group) * kVec;
+  const int64_t m1 = min((blockIdx.y + 1) * chunk, M);
+  float sum[kVec] = {};
+  if (c < N) {
+#pragma unroll 4
+    for (int64_t m = blockIdx.y * chunk + row; m < m1; m += kLanes) {
+      float d[kVec];
+      widen<KIND>(load8(dy, m, c, N), d);
+      if constexpr (ACT != T2S_ACT_NONE) {
+        float x[kVec];
+        widen<KIND>(load8(z, m, c, N), x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          float value, slope;
+          act_value_slope<ACT>(x[i], value, slope);
+          d[i] *= slope;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum[i] += d[i];
+      if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + m * lddz + c) = narrow<KIND>(d);
+    }
+  }
+  if (partials == nullptr) return;
+  __shared__ float sums[kLanes][kGroups * kVec + kGroups];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) sums[row][i * (kGroups + 1) + group] = sum[i];
+  __syncthreads();
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * kGroups * kVec + threadIdx.x;
+  if (n >= N) return;
+  float total = 0.0f;
+#pragma unroll
+  for (int r = 0; r < kLanes; ++r) total += sums[r][(threadIdx.x % kVec) * (kGroups + 1) + threadIdx.x / kVec];
+  partials[blockIdx.y * N + n] = total;
+}
+
+// 32 columns per block, the partial sums' rows over its eight warps.
+template <int KIND>
+__global__ void __launch_bounds__(kThreads) db_sum_kernel(int64_t rows, int64_t N, const float* partials, uint16_t* db) {
+  wait_for_earlier_kernels();
+  __shared__ float sums[kThreads / 32][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float sum = 0.0f;
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t r = warp; r < rows; r += kThreads / 32) sum += partials[r * N + n];
+  }
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || n >= N) return;
+  float total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += sums[w][lane];
+  db[n] = from_f32<KIND>(total);
+}
+
+// One thread per eight values.
+template <int KIND, int ACT>
+__global__ void __launch_bounds__(kThreads)
+    gated_backward_kernel(int64_t M, int64_t N, Source dh, Source g, Source u, uint16_t* dG, uint16_t* dU,
+                          int64_t ldd) {
+  wait_for_earlier_kernels();
+  const int64_t per_row = ldd / kVec, total = M * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / per_row, c = (i - m * per_row) * kVec;
+    const uint4 wd = load8(dh, m, c, N), wg = load8(g, m, c, N), wu = load8(u, m, c, N);
+    float d[kVec], x[kVec], y[kVec];
+    widen<KIND>(wd, d);
+    widen<KIND>(wg, x);
+    widen<KIND>(wu, y);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      float value, slope;
+      act_value_slope<ACT>(x[j], value, slope);
+      x[j] = d[j] * y[j] * slope;
+      y[j] = d[j] * value;
+    }
+    *reinterpret_cast<uint4*>(dG + m * ldd + c) = narrow<KIND>(x);
+    *reinterpret_cast<uint4*>(dU + m * ldd + c) = narrow<KIND>(y);
+  }
+}
+
+struct CopyJobs {
+  Copy job[kMaxCopies];
+  unsigned first[kMaxCopies + 1];  // first block of each
+};
+
+// Eight values per thread, written as one word.
+__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyJobs jobs) {
+  wait_for_earlier_kernels();
+  int j = 0;
+  while (blockIdx.x >= jobs.first[j + 1]) ++j;
+  const Copy& c = jobs.job[j];
+  const int64_t ldd = (c.cols + kVec - 1) / kVec * kVec, per_row = ldd / kVec, total = c.rows * per_row;
+  const int64_t step = static_cast<int64_t>(jobs.first[j + 1] - jobs.first[j]) * kThreads;
+  const Source s{c.src, c.ld, 0};
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - jobs.first[j]) * kThreads + threadIdx.x; i < total; i += step) {
+    const int64_t r = i / per_row, col = (i - r * per_row) * kVec;
+    *reinterpret_cast<uint4*>(c.dst + r * ldd + col) = load8(s, r, col, c.cols);
+  }
+}
+
+Source source(const uint16_t* p, int64_t ld) { return {p, ld, aligned16(p, ld) ? 1 : 0}; }
+
+template <class F>
+cudaError_t for_act(int act, F&& f) {
+  switch (act) {
+    case T2S_ACT_RELU: return f(std::integral_constant<int, T2S_ACT_RELU>{});
+    case T2S_ACT_SILU: return f(std::integral_constant<int, T2S_ACT_SILU>{});
+    case T2S_ACT_GELU: return f(std::integral_constant<int, T2S_ACT_GELU>{});
+    case T2S_ACT_GELU_TANH: return f(std::integral_constant<int, T2S_ACT_GELU_TANH>{});
+    default: return f(std::integral_constant<int, T2S_ACT_NONE>{});
+  }
+}
+
+unsigned capped(int64_t blocks, int64_t most) { return static_cast<unsigned>(blocks < most ? blocks : most); }
+
 }  // namespace
 
-cudaError_t run_copy(const Context& c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld, uint16_t* dst,
-                     int64_t ldd) {
-  const int64_t blocks = (rows * (ldd / 8) + kThreads - 1) / kThreads;
-  copy_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), kThreads, 0, c.stream>>>(rows, cols, src, ld,
-                                                                                              dst, ldd);
-  return cudaGetLastError();
+cudaError_t run_copies(const Context& c, const Copy* copies, int n) {
+  if (n == 0) return cudaSuccess;
+  CopyJobs jobs = {};
+  unsigned blocks = 0;
+  for (int i = 0; i < kMaxCopies; ++i) {
+    jobs.first[i] = blocks;
+    if (i < n) {
+      jobs.job[i] = copies[i];
+      blocks += capped((copies[i].rows * ((copies[i].cols + kVec - 1) / kVec) + kThreads - 1) / kThreads, 2048);
+    }
+  }
+  jobs.first[kMaxCopies] = blocks;
+  return launch_early(c.stream, {dim3(blocks), kThreads, 1, 0}, copy_kernel, jobs);
 }
 
 // Chunks of at least 64 rows, at most 128 of them.
@@ -106,31 +216,30 @@ cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, co
                              int64_t lddy, const uint16_t* Z, int64_t ldz, uint16_t* dZ,
                              int64_t lddz, uint16_t* db, float* partials) {
   const int64_t rows = db_partial_rows(M, N), chunk = (M + rows - 1) / rows;
-  const dim3 grid(static_cast<unsigned>((N + kThreads - 1) / kThreads), static_cast<unsigned>(rows));
+  const int64_t columns = kGroups * kVec;
+  const LaunchShape shape{dim3(static_cast<unsigned>((N + columns - 1) / columns), static_cast<unsigned>(rows)), kThreads, 1, 0};
   float* parts = db != nullptr ? partials : nullptr;
-  if (c.kind == kBf16)
-    act_backward_kernel<kBf16><<<grid, kThreads, 0, c.stream>>>(M, N, chunk, act, dY, lddy, Z, ldz, dZ, lddz, parts);
-  else
-    act_backward_kernel<kF16><<<grid, kThreads, 0, c.stream>>>(M, N, chunk, act, dY, lddy, Z, ldz, dZ, lddz, parts);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = for_act(act, [&](auto a) {
+    constexpr int kAct = decltype(a)::value;
+    return launch_early(c.stream, shape,
+                        c.kind == kBf16 ? act_backward_kernel<kBf16, kAct> : act_backward_kernel<kF16, kAct>, M, N,
+                        chunk, source(dY, lddy), source(Z, ldz), dZ, lddz, parts);
+  });
   if (e != cudaSuccess || db == nullptr) return e;
-  if (c.kind == kBf16)
-    db_sum_kernel<kBf16><<<grid.x, kThreads, 0, c.stream>>>(rows, N, parts, db);
-  else
-    db_sum_kernel<kF16><<<grid.x, kThreads, 0, c.stream>>>(rows, N, parts, db);
-  return cudaGetLastError();
+  return launch_early(c.stream, {dim3(static_cast<unsigned>((N + 31) / 32)), kThreads, 1, 0},
+                      c.kind == kBf16 ? db_sum_kernel<kBf16> : db_sum_kernel<kF16>, rows, N, parts, db);
 }
 
 cudaError_t run_gated_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dH,
                                int64_t lddh, const uint16_t* G, int64_t ldg, const uint16_t* U,
                                int64_t ldu, uint16_t* dG, uint16_t* dU, int64_t ldd) {
-  const dim3 grid(static_cast<unsigned>((N + kThreads - 1) / kThreads),
-                  static_cast<unsigned>(M < 65535 ? M : 65535));
-  if (c.kind == kBf16)
-    gated_backward_kernel<kBf16><<<grid, kThreads, 0, c.stream>>>(M, N, act, dH, lddh, G, ldg, U, ldu, dG, dU, ldd);
-  else
-    gated_backward_kernel<kF16><<<grid, kThreads, 0, c.stream>>>(M, N, act, dH, lddh, G, ldg, U, ldu, dG, dU, ldd);
-  return cudaGetLastError();
+  const LaunchShape shape{dim3(capped((M * (ldd / kVec) + kThreads - 1) / kThreads, 1 << 20)), kThreads, 1, 0};
+  return for_act(act, [&](auto a) {
+    constexpr int kAct = decltype(a)::value;
+    return launch_early(c.stream, shape,
+                        c.kind == kBf16 ? gated_backward_kernel<kBf16, kAct> : gated_backward_kernel<kF16, kAct>, M, N,
+                        source(dH, lddh), source(G, ldg), source(U, ldu), dG, dU, ldd);
+  });
 }
 
 }  // namespace ff

@@ -70,9 +70,14 @@ cudaError_t run_rows(const Context& c, const Task& t, const RowsPlan& plan);
 // Up to three products, none or all of them of the gated form, each by the kernel that suits its sizes.
 cudaError_t run_products(const Context& c, const Task* tasks, int n);
 
-// dst (rows x cols, ldd per row) = src.
-cudaError_t run_copy(const Context& c, int64_t rows, int64_t cols, const uint16_t* src, int64_t ld, uint16_t* dst,
-                     int64_t ldd);
+// dst = src, rows x cols, dst's rows padded to whole 16-byte words. Up to three copies in one launch.
+struct Copy {
+  const uint16_t* src;
+  int64_t ld, rows, cols;
+  uint16_t* dst;
+};
+constexpr int kMaxCopies = 3;
+cudaError_t run_copies(const Context& c, const Copy* copies, int n);
 
 // dZ = dY * act'(Z) (Z absent: act none, dZ not wanted) and, unless db is nullptr, its column
 // sums. `partials` holds db_partial_rows(M, N) x N floats.

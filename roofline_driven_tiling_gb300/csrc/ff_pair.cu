@@ -170,33 +170,6 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, bool any, float (&s)[k
   for (int i = 0; i < kUnit; ++i) s[i] = any ? __uint_as_float(r[i]) : 0.0f;
 }
 
-// A copying thread's walk over the ring's slots.
-struct Ring {
-  uint32_t first, bars;  // its part of slot 0; the full barriers, then the empty ones
-  uint32_t st, s = 0, phase = 1;
-
-  __device__ __forceinline__ Ring(uint32_t first_, uint32_t bars_) : first(first_), bars(bars_), st(first_) {}
-
-  // `blocks` K blocks from k = 0 on, each into the next slot once that is free.
-  template <class F>
-  __device__ __forceinline__ bool copy(int blocks, bool expects, uint32_t bytes, uint32_t bar0, unsigned* status,
-                                       F&& issue) {
-#pragma unroll 1
-    for (int k0 = 0; k0 < blocks * kBK; k0 += kBK) {
-      if (!wait_bounded(bars + 8u * (kStages + s), phase, status)) return false;
-      if (expects) mbar_arrive_expect_tx(bars + 8u * s, bytes);
-      issue(st, k0, bar0 + 8u * s);
-      st += kStageBytes;
-      if (++s == kStages) {
-        s = 0;
-        st = first;
-        phase ^= 1u;
-      }
-    }
-    return true;
-  }
-};
-
 // Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 are the
 // epilogue (warp 3 only holds TMEM). full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
 // that gives up a bounded wait records it and stops, and the others' own waits end the same way.
@@ -234,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   tc::tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // the peer's copies and commits arrive on these barriers
+  wait_for_earlier_kernels();
   tc::tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
@@ -243,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
     // between two copies hold up the other's.
     if (lane == 0) {
       const bool is_a = warp == 0;
-      Ring ring(base + (is_a ? 0 : kABytes), bars);
+      Ring ring(base + (is_a ? 0 : kABytes), kStageBytes, full(0), empty(0), kStages);
       const uint32_t bar0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
       const bool expects = is_a && rank == 0;
       bool ok = true;
@@ -261,16 +235,16 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         const CUtensorMap* map = is_a ? &p.a[0] : &p.b[GATED ? rank : 0];
         while (ok) {
           if (k_major) {
-            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, k0, at, bar);
             });
           } else if (boxes > 1) {
-            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
               tc::tma_load_2d_pair(st + kBoxBytes, map, at + 64, k0, bar);
             });
           } else {
-            ok = ring.copy(blocks, expects, bytes, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
             });
           }
@@ -281,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         }
       }
       // Every slot's copies have landed and been read before the CTA may go.
-      if (ok) ring.copy(kStages, false, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
+      if (ok) ring.copy(0, kStages, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -536,19 +510,8 @@ cudaError_t launch(const Context& c, const Task* tasks, int n) {
     }
   }
   params.first[kMaxProblems] = static_cast<int>(tiles);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ff_pair_kernel<KIND, GATED>, params);
+  const LaunchShape shape{dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident))), kThreads, 2, kSmemBytes};
+  return launch_early(c.stream, shape, ff_pair_kernel<KIND, GATED>, params);
 }
 
 }  // namespace
