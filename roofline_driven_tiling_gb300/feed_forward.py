@@ -22,12 +22,16 @@ from __future__ import annotations
 import torch
 
 from . import binding
-from .binding import T2S_OK, T2S_W_KN, T2S_W_NK, T2SError
+from .binding import T2S_ERR_WORKSPACE, T2S_OK, T2S_W_KN, T2S_W_NK, T2SError
 
 ACTS = {"none": binding.T2S_ACT_NONE, "relu": binding.T2S_ACT_RELU, "silu": binding.T2S_ACT_SILU,
         "gelu": binding.T2S_ACT_GELU, "gelu_tanh": binding.T2S_ACT_GELU_TANH}
 _SUFFIX = {torch.bfloat16: "_bf16", torch.float16: "_f16"}
 _FUNCTIONS = {}
+# A single token's call lasts a few microseconds on the device: what surrounds the launch is kept short.
+_Tensor, _empty, _current_device = torch.Tensor, torch.empty, torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _function(name: str, dtype):
@@ -39,90 +43,106 @@ def _function(name: str, dtype):
 
 
 def _first(t, name):
-    """Checks the tensor that sets the type and device of a call."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _SUFFIX:
+    """Type and device of a call, set by its first tensor."""
+    if not isinstance(t, _Tensor) or t.dtype not in _SUFFIX or not t.is_cuda:
         raise TypeError("%s must be a bfloat16 or float16 CUDA tensor" % name)
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError("%s must be on the current CUDA device" % name)
-    return t.dtype, t.get_device()
+    return t.dtype, t.device
 
 
-def _typed(t, name, like):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != like.dtype:
-        raise TypeError("%s must be a %s CUDA tensor" % (name, like.dtype))
-    if t.get_device() != like.get_device():
-        raise ValueError("%s must be on the device of the other tensors" % name)
+def _refuse(t, name, dtype, device):
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or not t.is_cuda:
+        raise TypeError("%s must be a %s CUDA tensor" % (name, dtype))
+    raise ValueError("%s must be on the device of the other tensors" % name)
 
 
-def _rows(t, name, like, shape=None):
+def _matrix(t, name, dtype, device, shape=None):
     """Pointer and row stride of a matrix with contiguous rows."""
-    if t is not like:
-        _typed(t, name, like)
-    if t.dim() != 2:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device:
+        _refuse(t, name, dtype, device)
+    size, stride = t.shape, t.stride()
+    if len(size) != 2:
         raise ValueError("%s must be 2-D" % name)
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError("%s must be %d x %d, got %d x %d" % (name, *shape, rows, cols))
-    ld, step = t.stride()
+    if shape is not None and size != shape:
+        raise ValueError("%s must be %d x %d, got %d x %d" % (name, *shape, *size))
+    rows, cols = size
+    ld, step = stride
     if rows <= 1:  # its stride is never used: one that keeps the row in place
-        ld = (cols + 7) // 8 * 8
+        ld = cols + 7 & -8
     if (step != 1 and cols > 1) or ld < cols:
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
     return t.data_ptr(), ld
 
 
-def _weight(t, name, like, shape=None):
-    """Pointer, row stride and order (T2S_W_KN or T2S_W_NK) of an inputs x outputs weight."""
-    _typed(t, name, like)
-    if t.dim() != 2:
+def _weight(t, name, dtype, device, k, n=None):
+    """Pointer, row stride, order (T2S_W_KN or T2S_W_NK) and outputs of an inputs x outputs weight."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device:
+        _refuse(t, name, dtype, device)
+    size = t.shape
+    if len(size) != 2:
         raise ValueError("%s must be 2-D" % name)
-    k, n = t.shape
-    if shape is not None and (k, n) != shape:
-        raise ValueError("%s must be %d x %d, got %d x %d" % (name, *shape, k, n))
+    if size[0] != k or (n is not None and size[1] != n):
+        raise ValueError("shape mismatch: %s %s for %d inputs%s" % (
+            name, tuple(size), k, "" if n is None else " and %d outputs" % n))
+    n = size[1]
     a, b = t.stride()
     if b == 1 and (a >= n or k <= 1):
-        return t.data_ptr(), a if k > 1 else (n + 7) // 8 * 8, T2S_W_KN
+        return t.data_ptr(), a if k > 1 else n + 7 & -8, T2S_W_KN, n
     if a == 1 and (b >= k or n <= 1):
-        return t.data_ptr(), b if n > 1 else (k + 7) // 8 * 8, T2S_W_NK
+        return t.data_ptr(), b if n > 1 else k + 7 & -8, T2S_W_NK, n
     raise ValueError("%s must be row-major or the transpose of a row-major tensor" % name)
 
 
-def _vector(t, name, like, n):
-    _typed(t, name, like)
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _gradient(t, name, dtype, device, k, n, order):
+    """Pointer and row stride of a weight's gradient, which has the weight's order."""
+    if order == T2S_W_KN:
+        return _matrix(t, name, dtype, device, (k, n))
+    if not isinstance(t, _Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    return _matrix(t.t(), name + ".t()", dtype, device, (n, k))
+
+
+def _vector(t, name, dtype, device, n):
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device:
+        _refuse(t, name, dtype, device)
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d values" % (name, n))
     return t.data_ptr()
 
 
 def _act(act):
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
-    return ACTS[act]
+    return code
 
 
-class _Call:
-    """Where a call runs: its stream, and allocations that belong to that stream."""
+def _new(shape, dtype, device, stream):
+    """A tensor of the pool of the call's stream (None: the current one), so that the reuse of its
+    memory is ordered there."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return _empty(shape, dtype=dtype, device=device)
 
-    def __init__(self, device, stream):
-        current = torch.cuda.current_stream(device).cuda_stream
-        self.device, self.stream = device, current if stream is None else stream
-        self.other = stream is not None and stream != current
 
-    def empty(self, shape, dtype):
-        if self.other:  # memory of that stream's pool, so that its reuse is ordered there
-            with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=self.device)):
-                return torch.empty(shape, dtype=dtype, device=self.device)
-        return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def workspace(self, given, need):
-        """Pointer and size of the caller's workspace, or of a new one (kept by the third)."""
-        if given is None:
-            if not need:
-                return None, 0, None
-            given = self.empty(need, torch.uint8)
-        elif not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous():
+def _run(name, dtype, device, sizes, args, workspace, need, stream):
+    """One call of a C entry point. `need` gives the workspace's bytes, asked for where the call
+    has none of its own and wants one."""
+    f = _FUNCTIONS.get((name, dtype)) or _function(name, dtype)
+    at = _raw_stream(device.index) if stream is None else stream
+    if workspace is not None:
+        if not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
-        return given.data_ptr(), given.numel() * given.element_size(), given
+        rc = f(*sizes, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), at)
+    else:
+        rc = f(*sizes, *args, None, 0, at)
+        if rc == T2S_ERR_WORKSPACE:
+            workspace = _new(need(), torch.uint8, device, stream)
+            rc = f(*sizes, *args, workspace.data_ptr(), workspace.numel(), at)
+    if rc != T2S_OK:
+        raise T2SError(rc, name + _SUFFIX[dtype])
 
 
 def _in_place(*matrices) -> int:
@@ -133,36 +153,24 @@ def _in_place(*matrices) -> int:
     return 0 if bits & 15 else 1
 
 
-def _wanted(out, make):
-    """An optional output: False is not wanted, None is allocated."""
-    return None if out is False else make() if out is None else out
-
-
 def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, workspace=None, stream=None):
     """act(x @ w + bias) + residual; ``preact`` (a tensor of the output's shape) receives
     x @ w + bias, which ``linear_backward`` needs for an activation."""
     dtype, device = _first(x, "x")
-    xp, ldx = _rows(x, "x", x)
+    xp, ldx = _matrix(x, "x", dtype, device)
     M, K = x.shape
-    wp, ldw, order = _weight(w, "w", x)
-    if w.shape[0] != K:
-        raise ValueError("shape mismatch: x %s, w %s" % (tuple(x.shape), tuple(w.shape)))
-    N = w.shape[1]
-    call = _Call(device, stream)
-    bp = None if bias is None else _vector(bias, "bias", x, N)
-    rp, ldr = (None, N) if residual is None else _rows(residual, "residual", x, (M, N))
-    zp, ldz = (None, N) if preact is None else _rows(preact, "preact", x, (M, N))
+    wp, ldw, order, N = _weight(w, "w", dtype, device, K)
+    bp = None if bias is None else _vector(bias, "bias", dtype, device, N)
+    rp, ldr = (None, N) if residual is None else _matrix(residual, "residual", dtype, device, (M, N))
+    zp, ldz = (None, N) if preact is None else _matrix(preact, "preact", dtype, device, (M, N))
+    code = _act(act)
     if out is None:
-        out, ldy = call.empty((M, N), dtype), N
-        yp = out.data_ptr()
+        out = _new((M, N), dtype, device, stream)
+        yp, ldy = out.data_ptr(), N
     else:
-        yp, ldy = _rows(out, "out", x, (M, N))
-    need = 0 if _in_place((xp, ldx), (wp, ldw)) else binding.lib().t2s_linear_workspace_size(M, N, K, 0)
-    ws, size, keep = call.workspace(workspace, need)
-    rc = _function("t2s_linear", dtype)(M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, _act(act), yp, ldy, zp, ldz,
-                                        ws, size, call.stream)
-    if rc != T2S_OK:
-        raise T2SError(rc, "t2s_linear" + _SUFFIX[dtype])
+        yp, ldy = _matrix(out, "out", dtype, device, (M, N))
+    _run("t2s_linear", dtype, device, (M, N, K), (xp, ldx, wp, ldw, order, bp, rp, ldr, code, yp, ldy, zp, ldz),
+         workspace, lambda: binding.t2s_linear_workspace_size(M, N, K, 0), stream)
     return out
 
 
@@ -171,74 +179,70 @@ def linear_backward(dy, x, w, preact=None, act="none", dx=None, dw=None, db=Fals
     None (allocated here), a tensor that receives it, or False (not computed). ``preact`` is
     what ``linear`` left there, needed for an ``act`` other than "none"."""
     dtype, device = _first(dy, "dy")
-    yp, ldy = _rows(dy, "dy", dy)
+    yp, ldy = _matrix(dy, "dy", dtype, device)
     M, N = dy.shape
-    xp, ldx = _rows(x, "x", dy)
+    xp, ldx = _matrix(x, "x", dtype, device)
     K = x.shape[1]
     if x.shape[0] != M:
         raise ValueError("shape mismatch: dy %s, x %s" % (tuple(dy.shape), tuple(x.shape)))
-    wp, ldw, order = _weight(w, "w", dy, (K, N))
+    wp, ldw, order, _ = _weight(w, "w", dtype, device, K, N)
     code = _act(act)
-    if code != binding.T2S_ACT_NONE and preact is None:
-        raise ValueError("act %r needs the pre-activations" % act)
-    zp, ldz = (None, N) if preact is None or code == binding.T2S_ACT_NONE else _rows(preact, "preact", dy, (M, N))
-    call = _Call(device, stream)
-    dx = _wanted(dx, lambda: call.empty((M, K), dtype))
-    dw = _wanted(dw, lambda: call.empty((K, N), dtype) if order == T2S_W_KN else call.empty((N, K), dtype).t())
-    db = _wanted(db, lambda: call.empty((N,), dtype))
-    dxp, lddx = (None, K) if dx is None else _rows(dx, "dx", dy, (M, K))
-    dwp, lddw = (None, max(K, N)) if dw is None else _gradient(dw, "dw", dy, (K, N), order)
-    dbp = None if db is None else _vector(db, "db", dy, N)
-    need = binding.lib().t2s_linear_backward_workspace_size(M, N, K, _in_place((xp, ldx), (wp, ldw), (yp, ldy)))
-    ws, size, keep = call.workspace(workspace, need)
-    rc = _function("t2s_linear_backward", dtype)(M, N, K, yp, ldy, xp, ldx, wp, ldw, order, zp, ldz, code, dxp, lddx,
-                                                 dwp, lddw, dbp, ws, size, call.stream)
-    if rc != T2S_OK:
-        raise T2SError(rc, "t2s_linear_backward" + _SUFFIX[dtype])
-    return dx, dw, db
+    zp, ldz = None, N
+    if code != binding.T2S_ACT_NONE:
+        if preact is None:
+            raise ValueError("act %r needs the pre-activations" % act)
+        zp, ldz = _matrix(preact, "preact", dtype, device, (M, N))
+    dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, K), stream)
+    dw, dwp, lddw = _weight_output(dw, "dw", dtype, device, K, N, order, stream)
+    if db is None:
+        db = _new((N,), dtype, device, stream)
+    dbp = None if db is False else _vector(db, "db", dtype, device, N)
+    _run("t2s_linear_backward", dtype, device, (M, N, K),
+         (yp, ldy, xp, ldx, wp, ldw, order, zp, ldz, code, dxp, lddx, dwp, lddw, dbp), workspace,
+         lambda: binding.t2s_linear_backward_workspace_size(M, N, K, _in_place((xp, ldx), (wp, ldw), (yp, ldy))), stream)
+    return dx, dw, None if db is False else db
 
 
-def _gradient(t, name, like, shape, order):
-    """Pointer and row stride of a weight's gradient, which has the weight's order."""
-    if order == T2S_W_KN:
-        return _rows(t, name, like, shape)
-    _typed(t, name, like)
-    if t.dim() != 2:
-        raise ValueError("%s must be 2-D" % name)
-    return _rows(t.t(), name + ".t()", like, (shape[1], shape[0]))
+def _output(t, name, dtype, device, shape, stream):
+    """An output, its pointer and row stride: given, allocated (None) or not wanted (False)."""
+    if t is None:
+        t = _new(shape, dtype, device, stream)
+    elif t is False:
+        return None, None, shape[1]
+    return (t, *_matrix(t, name, dtype, device, shape))
+
+
+def _weight_output(t, name, dtype, device, k, n, order, stream):
+    if t is None:
+        t = _new((k, n), dtype, device, stream) if order == T2S_W_KN else _new((n, k), dtype, device, stream).t()
+    elif t is False:
+        return None, None, max(k, n)
+    return (t, *_gradient(t, name, dtype, device, k, n, order))
 
 
 def gated_linear(x, w_gate, w_up, act="silu", out=None, preact=None, workspace=None, stream=None):
     """act(x @ w_gate) * (x @ w_up); ``preact``, a pair of tensors of the output's shape,
     receives x @ w_gate and x @ w_up, which ``gated_linear_backward`` needs."""
     dtype, device = _first(x, "x")
-    xp, ldx = _rows(x, "x", x)
+    xp, ldx = _matrix(x, "x", dtype, device)
     M, K = x.shape
-    gp, ldg, order = _weight(w_gate, "w_gate", x)
-    if w_gate.shape[0] != K:
-        raise ValueError("shape mismatch: x %s, w_gate %s" % (tuple(x.shape), tuple(w_gate.shape)))
-    N = w_gate.shape[1]
-    up, ldu, order_up = _weight(w_up, "w_up", x, (K, N))
+    gp, ldg, order, N = _weight(w_gate, "w_gate", dtype, device, K)
+    up, ldu, order_up, _ = _weight(w_up, "w_up", dtype, device, K, N)
     if order != order_up:
         raise ValueError("w_gate and w_up must have the same order")
-    call = _Call(device, stream)
-    if out is None:
-        out, ldh = call.empty((M, N), dtype), N
-        hp = out.data_ptr()
-    else:
-        hp, ldh = _rows(out, "out", x, (M, N))
     zg, ldzg, zu, ldzu = None, N, None, N
     if preact is not None:
-        zg, ldzg = _rows(preact[0], "preact[0]", x, (M, N))
-        zu, ldzu = _rows(preact[1], "preact[1]", x, (M, N))
-    need = 0
-    if not _in_place((xp, ldx), (gp, ldg), (up, ldu)):
-        need = binding.lib().t2s_gated_workspace_size(M, N, K, 0)
-    ws, size, keep = call.workspace(workspace, need)
-    rc = _function("t2s_gated", dtype)(M, N, K, xp, ldx, gp, ldg, up, ldu, order, _act(act), hp, ldh, zg, ldzg, zu,
-                                       ldzu, ws, size, call.stream)
-    if rc != T2S_OK:
-        raise T2SError(rc, "t2s_gated" + _SUFFIX[dtype])
+        zg, ldzg = _matrix(preact[0], "preact[0]", dtype, device, (M, N))
+        zu, ldzu = _matrix(preact[1], "preact[1]", dtype, device, (M, N))
+    code = _act(act)
+    if out is None:
+        out = _new((M, N), dtype, device, stream)
+        hp, ldh = out.data_ptr(), N
+    else:
+        hp, ldh = _matrix(out, "out", dtype, device, (M, N))
+    _run("t2s_gated", dtype, device, (M, N, K),
+         (xp, ldx, gp, ldg, up, ldu, order, code, hp, ldh, zg, ldzg, zu, ldzu), workspace,
+         lambda: binding.t2s_gated_workspace_size(M, N, K, 0), stream)
     return out
 
 
@@ -247,32 +251,24 @@ def gated_linear_backward(dh, x, w_gate, w_up, preact, act="silu", dx=None, dw_g
     """(dx, dw_gate, dw_up) of ``gated_linear``; ``preact`` is the pair that it left there. Each
     output is None (allocated here), a tensor that receives it, or False (not computed)."""
     dtype, device = _first(dh, "dh")
-    hp, ldh = _rows(dh, "dh", dh)
+    hp, ldh = _matrix(dh, "dh", dtype, device)
     M, N = dh.shape
-    xp, ldx = _rows(x, "x", dh)
+    xp, ldx = _matrix(x, "x", dtype, device)
     K = x.shape[1]
     if x.shape[0] != M:
         raise ValueError("shape mismatch: dh %s, x %s" % (tuple(dh.shape), tuple(x.shape)))
-    gp, ldg, order = _weight(w_gate, "w_gate", dh, (K, N))
-    up, ldu, order_up = _weight(w_up, "w_up", dh, (K, N))
+    gp, ldg, order, _ = _weight(w_gate, "w_gate", dtype, device, K, N)
+    up, ldu, order_up, _ = _weight(w_up, "w_up", dtype, device, K, N)
     if order != order_up:
         raise ValueError("w_gate and w_up must have the same order")
-    zg, ldzg = _rows(preact[0], "preact[0]", dh, (M, N))
-    zu, ldzu = _rows(preact[1], "preact[1]", dh, (M, N))
-    call = _Call(device, stream)
-
-    def weight_like():
-        return call.empty((K, N), dtype) if order == T2S_W_KN else call.empty((N, K), dtype).t()
-
-    dx = _wanted(dx, lambda: call.empty((M, K), dtype))
-    dw_gate, dw_up = _wanted(dw_gate, weight_like), _wanted(dw_up, weight_like)
-    dxp, lddx = (None, K) if dx is None else _rows(dx, "dx", dh, (M, K))
-    dgp, lddg = (None, max(K, N)) if dw_gate is None else _gradient(dw_gate, "dw_gate", dh, (K, N), order)
-    dup, lddu = (None, max(K, N)) if dw_up is None else _gradient(dw_up, "dw_up", dh, (K, N), order)
-    need = binding.lib().t2s_gated_backward_workspace_size(M, N, K, _in_place((xp, ldx), (gp, ldg), (up, ldu)))
-    ws, size, keep = call.workspace(workspace, need)
-    rc = _function("t2s_gated_backward", dtype)(M, N, K, hp, ldh, xp, ldx, gp, ldg, up, ldu, order, zg, ldzg, zu, ldzu,
-                                                _act(act), dxp, lddx, dgp, lddg, dup, lddu, ws, size, call.stream)
-    if rc != T2S_OK:
-        raise T2SError(rc, "t2s_gated_backward" + _SUFFIX[dtype])
+    zg, ldzg = _matrix(preact[0], "preact[0]", dtype, device, (M, N))
+    zu, ldzu = _matrix(preact[1], "preact[1]", dtype, device, (M, N))
+    code = _act(act)
+    dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, K), stream)
+    dw_gate, dgp, lddg = _weight_output(dw_gate, "dw_gate", dtype, device, K, N, order, stream)
+    dw_up, dup, lddu = _weight_output(dw_up, "dw_up", dtype, device, K, N, order, stream)
+    _run("t2s_gated_backward", dtype, device, (M, N, K),
+         (hp, ldh, xp, ldx, gp, ldg, up, ldu, order, zg, ldzg, zu, ldzu, code, dxp, lddx, dgp, lddg, dup, lddu),
+         workspace,
+         lambda: binding.t2s_gated_backward_workspace_size(M, N, K, _in_place((xp, ldx), (gp, ldg), (up, ldu))), stream)
     return dx, dw_gate, dw_up
