@@ -85,7 +85,59 @@ __device__ __forceinline__ uint64_t with_address(const OperandForm& f, uint32_t 
   return f.base | static_cast<uint64_t>((addr & 0x3ffffu) >> 4);
 }
 
-// A copying thread's walk over a ring of shared-memory slots.
+// The MMAs of one 64-deep K block (four of K = 16) by one elected thread of a converged warp:
+// D (+)= A B^T from the descriptors `a` and `b`, which advance by the forms' steps; accumulate = 0
+// starts D from the first product. Issued by a single diverged thread instead, the four took 264 cycles
+// (every descriptor is moved to uniform registers), about as long as the widest ones compute.
+template <int G>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint32_t a_step, uint64_t b, uint32_t b_step,
+                                          uint32_t idesc, uint32_t accumulate) {
+  if constexpr (G == 2) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b, sa, sb;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "cvt.u64.u32 sa, %2;\n\tcvt.u64.u32 sb, %4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %3, %5, p;\n\t"
+        "add.u64 a, %1, sa;\n\tadd.u64 b, %3, sb;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t}" ::"r"(d),
+        "l"(a), "r"(a_step), "l"(b), "r"(b_step), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b, sa, sb;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "cvt.u64.u32 sa, %2;\n\tcvt.u64.u32 sb, %4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %3, %5, p;\n\t"
+        "add.u64 a, %1, sa;\n\tadd.u64 b, %3, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u64 a, a, sa;\n\tadd.u64 b, b, sb;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t}" ::"r"(d),
+        "l"(a), "r"(a_step), "l"(b), "r"(b_step), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// A copying warp's walk over a ring of shared-memory slots. The warp stays converged (its
+// addresses and counters live in uniform registers); one elected lane announces and copies.
 struct Ring {
   uint32_t first, stride, full, empty, slots;  // its part of slot 0, slot size, barriers of slot 0
   uint32_t st, s = 0, phase = 1;
@@ -99,9 +151,12 @@ struct Ring {
   __device__ __forceinline__ bool copy(int kb0, int kb1, uint32_t expect, uint32_t bar0, unsigned* status, F&& issue) {
 #pragma unroll 1
     for (int k0 = kb0 * kBK; k0 < kb1 * kBK; k0 += kBK) {
-      if (!wait_bounded(empty + 8u * s, phase, status)) return false;
-      if (expect != 0) mbar_arrive_expect_tx(full + 8u * s, expect);
-      issue(st, k0, bar0 + 8u * s);
+      if (!__all_sync(0xffffffffu, wait_bounded(empty + 8u * s, phase, status))) return false;
+      if (elect_one()) {
+        if (expect != 0) mbar_arrive_expect_tx(full + 8u * s, expect);
+        issue(st, k0, bar0 + 8u * s);
+      }
+      __syncwarp();
       st += stride;
       if (++s == slots) {
         s = 0;

@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
   if (warp == 0 || warp == 2) {
-    // Copies of A (warp 0) and of B (warp 2): one thread each, so that neither's instructions
+    // Copies of A (warp 0) and of B (warp 2): a warp each, so that neither's instructions
     // between two copies hold up the other's.
-    if (lane == 0) {
+    {
       const bool is_a = warp == 0;
       Ring ring(base + (is_a ? 0 : kABytes), kStageBytes, full(0), empty(0), kStages);
       const uint32_t bar0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
@@ -257,9 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       // Every slot's copies have landed and been read before the CTA may go.
       if (ok) ring.copy(0, kStages, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int s = 0, use = 0;
       uint32_t phase = 0, st = base;
       bool ok = true;
@@ -269,23 +268,19 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         const uint32_t idesc = p.idesc;
         const int nkb = p.nkb, b = use & 1;
         const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
-        if (!wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status)) break;
+        if (!__all_sync(0xffffffffu, wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status))) break;
         tc::tc_fence_after();
-        uint32_t accumulate = 0;
 #pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
           const uint64_t da = with_address(fa, st), db = with_address(fb, st + kABytes);
-          if (!wait_bounded(full(s), phase, status)) {
+          if (!__all_sync(0xffffffffu, wait_bounded(full(s), phase, status))) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            tc::mma_issue<1, 2>(acc, da + k * fa.step, db + k * fb.step, idesc, accumulate);
-            accumulate = 1;
-          }
-          tc::mma_commit_pair(empty(s));
+          mma_block<2>(acc, da, fa.step, db, fb.step, idesc, kb);
+          if (elect_one()) tc::mma_commit_pair(empty(s));
+          __syncwarp();
           st += kStageBytes;
           if (++s == kStages) {
             s = 0;
@@ -293,13 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
             phase ^= 1u;
           }
         }
-        if (ok) tc::mma_commit_pair(acc_full + 8u * b);
+        if (ok && elect_one()) tc::mma_commit_pair(acc_full + 8u * b);
+        __syncwarp();
       }
       // Every MMA issued above ends before TMEM is released.
-      tc::mma_commit<2>(mma_done);
+      if (elect_one()) tc::mma_commit<2>(mma_done);
+      __syncwarp();
       wait_bounded(mma_done, 0u, status);
     }
-    __syncwarp();
   } else if (warp >= 4) {
     const int e = warp - 4, q = warp & 3, half = e >> 2;
     Staging boxes{staging + static_cast<uint32_t>(e) * 2u * kUnitBytes, 0u, lane};

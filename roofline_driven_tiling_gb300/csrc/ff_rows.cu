@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
   constexpr uint32_t kXOffset = kWeights * kWeightBytes;
 
   if (warp == 0 || warp == 2) {
-    if (lane == 0) {
+    {
       const bool is_w = warp == 0, k_major = p.w_k_major, x_k_major = p.x_k_major;
       const int first = p.nkb_first, x_boxes = p.x_boxes;
       const uint32_t expect = is_w ? p.stage_bytes : 0u;
@@ -160,26 +160,20 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
         if (!ok) break;
       }
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       int s = 0;
-      uint32_t phase = 0, st = base, accumulate = 0;
+      uint32_t phase = 0, st = base;
       const OperandForm fw = operand_form(p.w_k_major), fx = operand_form(p.x_k_major);
 #pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_bounded(full(s), phase, status)) break;
+        if (!__all_sync(0xffffffffu, wait_bounded(full(s), phase, status))) break;
         tc::tc_fence_after();
         const uint64_t dw = with_address(fw, st), dx = with_address(fx, st + kXOffset);
-#pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) {
-          tc::mma_issue<1, 1>(tmem, dw + k * fw.step, dx + k * fx.step, p.idesc, accumulate);
-          if (GATED)
-            tc::mma_issue<1, 1>(tmem + p.tm, dw + (kWeightBytes >> 4) + k * fw.step, dx + k * fx.step, p.idesc,
-                                accumulate);
-          accumulate = 1;
-        }
-        tc::mma_commit<1>(empty(s));
+        mma_block<1>(tmem, dw, fw.step, dx, fx.step, p.idesc, kb - kb0);
+        if (GATED) mma_block<1>(tmem + p.tm, dw + (kWeightBytes >> 4), fw.step, dx, fx.step, p.idesc, kb - kb0);
+        if (elect_one()) tc::mma_commit<1>(empty(s));
+        __syncwarp();
         st += p.stage_bytes;
         if (++s == S) {
           s = 0;
@@ -187,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
           phase ^= 1u;
         }
       }
-      tc::mma_commit<1>(done);
+      if (elect_one()) tc::mma_commit<1>(done);
     }
     __syncwarp();
   }
