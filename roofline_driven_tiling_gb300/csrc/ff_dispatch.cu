@@ -1,4 +1,5 @@
-// ff_dispatch.cu -- which kernel takes a product of the feed-forward operators.
+// ff_dispatch.cu -- which kernel takes a product of the feed-forward operators: the one whose own
+// estimate of the time (plan_rows, pair_width) is shorter.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -27,10 +28,6 @@ cudaError_t sm_count(int* out) {
   return cudaSuccess;
 }
 
-bool takes_rows(const Task& t, const RowsPlan& plan, int sms) {
-  return t.M <= 256;
-}
-
 }  // namespace
 
 cudaError_t run_products(const Context& c, const Task* tasks, int n) {
@@ -38,16 +35,19 @@ cudaError_t run_products(const Context& c, const Task* tasks, int n) {
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   Task rest[3];
-  int left = 0;
+  int widths[3], left = 0;
   for (int i = 0; i < n; ++i) {
+    double pair_cost = 0.0;
+    const int width = pair_width(tasks[i], sms / 2, &pair_cost);
     const RowsPlan plan = plan_rows(tasks[i], sms);
-    if (takes_rows(tasks[i], plan, sms)) {
+    if (plan.cost < pair_cost) {
       if ((e = run_rows(c, tasks[i], plan)) != cudaSuccess) return e;
     } else {
+      widths[left] = width;
       rest[left++] = tasks[i];
     }
   }
-  return run_pair(c, rest, left);
+  return run_pair(c, rest, widths, left);
 }
 
 }  // namespace ff

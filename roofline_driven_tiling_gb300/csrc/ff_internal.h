@@ -53,15 +53,18 @@ inline bool aligned16(const void* p, int64_t ld) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2)) & 15u) == 0;
 }
 
+// Sums per row of a tile that ff_pair.cu takes for a product on `pairs` pairs of SMs, and its
+// expected time in microseconds.
+int pair_width(const Task& t, int pairs, double* cost);
 // Up to three products in one launch, all of the gated form or none. Operands must be readable
 // in place (aligned16), and rows of a single-row operand given a stride that is.
-cudaError_t run_pair(const Context& c, const Task* tasks, int n);
+cudaError_t run_pair(const Context& c, const Task* tasks, const int* widths, int n);
 
 // How ff_rows.cu takes a product: rows of X per tile, CTAs along K, ring slots.
 struct RowsPlan {
   int tm = 0, splits = 1, stages = 0, smem_bytes = 0;
   uint32_t stage_bytes = 0, tmem_cols = 0;
-  int64_t ctas = 0;
+  double cost = 0.0;  // expected time in microseconds
 };
 RowsPlan plan_rows(const Task& t, int sms);
 // One product with its sum split over a cluster; operands as for run_pair.

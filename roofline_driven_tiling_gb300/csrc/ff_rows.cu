@@ -80,6 +80,70 @@ __device__ __forceinline__ void store4(uint16_t* p, int left, const float (&v)[4
   }
 }
 
+// Adds the S CTAs' partial sums, applies the epilogue and stores: the rows of X in turn over the
+// cluster's warps, four outputs per lane, several rows' loads (distributed shared memory and the
+// residual answer after hundreds of cycles) before the first row's arithmetic.
+template <int KIND, bool GATED, int S>
+__device__ __forceinline__ void finish(const RowsParams& p, uint32_t base, int rank, int n0, int m0) {
+  constexpr int kWeights = GATED ? 2 : 1;
+  constexpr int kUnroll = S * kWeights <= 2 ? 4 : S * kWeights <= 4 ? 2 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = n0 + 4 * lane, left = p.N - n, rows = min(p.tm, p.M - m0);
+  float bias[4] = {};
+  if (p.bias != nullptr && left > 0) load4<KIND>(p.bias + n, left, bias);
+  uint32_t from[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) from[i] = S > 1 ? tc::map_to_rank(base + 16u * lane, i) : base + 16u * lane;
+  constexpr int kStep = kWarps * S;
+  for (int c0 = warp * S + rank; c0 < rows; c0 += kUnroll * kStep) {
+    float4 parts[kUnroll][kWeights][S];
+    float r[kUnroll][4] = {};
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int c = min(c0 + j * kStep, rows - 1);
+      if (p.R != nullptr && left > 0) load4<KIND>(p.R + (m0 + static_cast<int64_t>(c)) * p.ldr + n, left, r[j]);
+#pragma unroll
+      for (int g = 0; g < kWeights; ++g)
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const uint32_t at = from[i] + static_cast<uint32_t>(g * p.tm + c) * (kTileN * 4u);
+          parts[j][g][i] = S > 1 ? ld_cluster_v4(at) : lds128(at);
+        }
+    }
+    float v[kUnroll][kWeights][4], y[kUnroll][4];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+      for (int g = 0; g < kWeights; ++g) {
+        float* x = v[j][g];
+        x[0] = parts[j][g][0].x, x[1] = parts[j][g][0].y, x[2] = parts[j][g][0].z, x[3] = parts[j][g][0].w;
+#pragma unroll
+        for (int i = 1; i < S; ++i)
+          x[0] += parts[j][g][i].x, x[1] += parts[j][g][i].y, x[2] += parts[j][g][i].z, x[3] += parts[j][g][i].w;
+        if (g == 0) x[0] += bias[0], x[1] += bias[1], x[2] += bias[2], x[3] += bias[3];
+      }
+    with_act(p.act, [&](auto a) {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = act_value<decltype(a)::value>(v[j][0][i]);
+          y[j][i] = GATED ? x * v[j][kWeights - 1][i] : x + r[j][i];
+        }
+    });
+    if (left <= 0) continue;
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int c = c0 + j * kStep;
+      if (c >= rows) break;
+      const int64_t m = m0 + static_cast<int64_t>(c);
+      if (p.Z != nullptr) store4<KIND>(p.Z + m * p.ldz + n, left, v[j][0]);
+      if (GATED && p.Z2 != nullptr) store4<KIND>(p.Z2 + m * p.ldz2 + n, left, v[j][kWeights - 1]);
+      store4<KIND>(p.Y + m * p.ldy + n, left, y[j]);
+    }
+  }
+}
+
 // Warp 0 copies the weight's blocks, warp 2 those of X (and of the gated form's second weight),
 // warp 1 issues the MMAs; then all eight warps read TMEM and finish the outputs. full[s] / empty[s]
 // per ring slot. A role that gives up a bounded wait records it and stops; every thread still
@@ -211,51 +275,11 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
     __syncthreads();
   }
 
-  // Rows of X in turn over the cluster's warps; four outputs per lane.
-  const int n = n0 + 4 * lane, left = p.N - n;
-  const int rows = min(p.tm, p.M - m0);
-  float bias[4] = {};
-  if (p.bias != nullptr && left > 0) load4<KIND>(p.bias + n, left, bias);
-  for (int c = warp * p.splits + rank; c < rows; c += kWarps * p.splits) {
-    const int64_t m = m0 + c;
-    float r[4] = {}, v[4] = {}, u[4] = {};
-    if (p.R != nullptr && left > 0) load4<KIND>(p.R + m * p.ldr + n, left, r);
-    const uint32_t at = base + static_cast<uint32_t>(c) * (kTileN * 4u) + 16u * lane;
-    const uint32_t at_u = at + static_cast<uint32_t>(p.tm) * (kTileN * 4u);
-    if (p.splits > 1) {
-      float4 parts[kMaxSplits], parts_u[GATED ? kMaxSplits : 1];
-#pragma unroll
-      for (int i = 0; i < kMaxSplits; ++i)
-        if (i < p.splits) {
-          parts[i] = ld_cluster_v4(tc::map_to_rank(at, i));
-          if (GATED) parts_u[i] = ld_cluster_v4(tc::map_to_rank(at_u, i));
-        }
-#pragma unroll
-      for (int i = 0; i < kMaxSplits; ++i)
-        if (i < p.splits) {
-          v[0] += parts[i].x, v[1] += parts[i].y, v[2] += parts[i].z, v[3] += parts[i].w;
-          if (GATED) u[0] += parts_u[i].x, u[1] += parts_u[i].y, u[2] += parts_u[i].z, u[3] += parts_u[i].w;
-        }
-    } else {
-      const float4 a = lds128(at);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      if (GATED) {
-        const float4 b = lds128(at_u);
-        u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
-      }
-    }
-    if (left <= 0) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += bias[i];
-    if (p.Z != nullptr) store4<KIND>(p.Z + m * p.ldz + n, left, v);
-    if (GATED && p.Z2 != nullptr) store4<KIND>(p.Z2 + m * p.ldz2 + n, left, u);
-    with_act(p.act, [&](auto a) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
-    });
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = GATED ? v[i] * u[i] : v[i] + r[i];
-    store4<KIND>(p.Y + m * p.ldy + n, left, v);
+  switch (p.splits) {
+    case 1: finish<KIND, GATED, 1>(p, base, rank, n0, m0); break;
+    case 2: finish<KIND, GATED, 2>(p, base, rank, n0, m0); break;
+    case 4: finish<KIND, GATED, 4>(p, base, rank, n0, m0); break;
+    default: finish<KIND, GATED, 8>(p, base, rank, n0, m0); break;
   }
 
   // No CTA's partial sums go while another may read them.
@@ -327,40 +351,72 @@ cudaError_t launch(const Context& c, const Task& t, const RowsPlan& plan) {
 
 }  // namespace
 
+// The time that a product takes this way with tiles of `tm` rows of X and `splits` CTAs along K, in
+// microseconds, up to what all ways share. Fitted to 30 products of 1 to 1024 rows (within 15 %):
+// a K block of 16 KB of weights takes a CTA 0.15 us, more once X's tile outweighs the weight's
+// (0.165 at 128 rows, 0.24 at 256), the gated form's two weights 0.22 to 0.25; the partial sums' way through shared
+// memory 17 ns a row (gated: 25); a cluster's two barriers 0.6 us. All SMs together take in at most
+// 16 TB/s.
+static double rows_cost(bool gated, int tm, int splits, int64_t tiles, int64_t blocks, int sms, bool* fits) {
+  // Clusters of 4 reach 95 % of the SMs and clusters of 8 79 % with CTAs that fill them (144 and 120
+  // of 152).
+  const int reach = splits <= 2 ? sms : splits == 4 ? sms * 95 / 100 : sms * 79 / 100;
+  const int64_t ctas = tiles * splits, waves = (ctas + reach - 1) / reach;
+  *fits = waves == 1;
+  double block = tm <= 64 ? 0.15 : tm <= 128 ? 0.15 + (tm - 64) * 0.00023 : 0.165 + (tm - 128) * 0.00059;
+  if (gated) block = 0.22 + tm * 0.00025;
+  const double per_cta = static_cast<double>((blocks + splits - 1) / splits) * block + tm * (gated ? 0.025 : 0.017);
+  const double bytes = static_cast<double>(tiles) * static_cast<double>(blocks) *
+                       ((gated ? 2 : 1) * kWeightBytes + tm * kBK * 2);
+  const double time = static_cast<double>(waves) * per_cta;
+  return (time > bytes / 16e6 ? time : bytes / 16e6) + (splits > 1 ? 0.6 : 0.0) + 4.0;
+}
+
 RowsPlan plan_rows(const Task& t, int sms) {
   RowsPlan plan;
-  const int weights = t.form == kGated ? 2 : 1;
-  // Rows of X per tile: equal shares of M, at most 256 sums per TMEM lane.
-  const int64_t most = 256 / weights;
-  const int64_t tiles_m = (t.M + most - 1) / most;
-  plan.tm = static_cast<int>(((t.M + tiles_m - 1) / tiles_m + 15) / 16 * 16);
-  const int64_t tiles = ((t.N + kTileN - 1) / kTileN) * ((t.M + plan.tm - 1) / plan.tm);
+  const bool gated = t.form == kGated;
+  const int weights = gated ? 2 : 1;
   const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
-  // As many splits of K as leave two blocks to each CTA and one CTA to an SM. Of the SMs, clusters of
-  // 4 reach 95 % and clusters of 8 79 % with CTAs that fill them (144 and 120 of 152).
-  plan.splits = 1;
-  for (int s = 2; s <= kMaxSplits; s *= 2) {
-    const int64_t reach = s <= 2 ? sms : s == 4 ? sms * 95 / 100 : sms * 79 / 100;
-    if (tiles * s <= reach && blocks >= 2 * s) plan.splits = s;
+  const int64_t tiles_n = (t.N + kTileN - 1) / kTileN;
+  // Equal shares of M per tile, at most 256 sums per TMEM lane, and no tiles under 32 rows but one.
+  const int64_t fewest = (t.M * weights + 255) / 256, most = (t.M + 31) / 32;
+  bool one_wave = false;
+  plan.cost = 0.0;
+  for (int64_t tiles_m = fewest; tiles_m <= most || tiles_m == fewest; tiles_m += tiles_m < 16 ? 1 : tiles_m / 8) {
+    const int tm = static_cast<int>(((t.M + tiles_m - 1) / tiles_m + 15) / 16 * 16);
+    const int64_t tiles = tiles_n * ((t.M + tm - 1) / tm);
+    if (tiles_m > fewest && tiles > 2 * sms) break;
+    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+      if (splits > 1 && (blocks < 2 * splits || tiles * splits > sms)) break;
+      bool fits = false;
+      const double cost = rows_cost(gated, tm, splits, tiles, blocks, sms, &fits);
+      if (plan.cost == 0.0 || cost < plan.cost) {
+        plan.cost = cost;
+        plan.tm = tm;
+        plan.splits = splits;
+        one_wave = fits;
+      }
+    }
   }
-  const int64_t ctas = tiles * plan.splits;
-  plan.ctas = ctas;
   const int x_bytes = t.A.k_major ? plan.tm * kBK * 2 : (plan.tm + 63) / 64 * kBoxBytes;
   plan.stage_bytes = static_cast<uint32_t>(weights * kWeightBytes + x_bytes);
   plan.tmem_cols = 32;
   while (plan.tmem_cols < static_cast<uint32_t>(weights * plan.tm)) plan.tmem_cols *= 2;
-  // One CTA per SM takes a deep ring, two share the SM's memory. The partial sums lie over the
-  // ring, so it holds at least those.
+  // Half of an SM's memory where that holds six slots (then the next call's CTAs can be set up beside
+  // these: linear 8x8192x4096 13.1 us against 14.0 with all of it) or more CTAs are to come; otherwise
+  // a ring over all of it (64x4096x4096: 8.7 against 9.0, 128x4096x4096 10.2 against 11.6).
+  const int half = 112 * 1024, whole = 200 * 1024, stage = static_cast<int>(plan.stage_bytes);
+  const int budget = !one_wave || 6 * stage <= half ? half : whole;
+  // The partial sums lie over the ring, so it holds at least those.
   const int partials = weights * plan.tm * kTileN * 4;
-  const int budget = (ctas > sms ? 112 : 200) * 1024;
   const int64_t per_cta = (blocks + plan.splits - 1) / plan.splits;
-  int stages = static_cast<int>(budget / plan.stage_bytes);
+  int stages = budget / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages > per_cta) stages = static_cast<int>(per_cta);
-  const int least = (partials + static_cast<int>(plan.stage_bytes) - 1) / static_cast<int>(plan.stage_bytes);
+  const int least = (partials + stage - 1) / stage;
   if (stages < least) stages = least;
   plan.stages = stages;
-  plan.smem_bytes = stages * static_cast<int>(plan.stage_bytes) + 1024 + 512;
+  plan.smem_bytes = stages * stage + 1024 + 512;
   // CTAs that share an SM must find TMEM for all of them, or clusters could wait for each other's:
   // shared memory in the proportion of TMEM (and never so little that a CTA fits beside a kernel
   // that fills the rest) keeps the sum of their columns at most 512.
