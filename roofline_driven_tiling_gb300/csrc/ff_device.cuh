@@ -125,6 +125,13 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint32_t a_ste
   }
 }
 
+// Arrives on an mbarrier given by its shared::cluster address, possibly another CTA's. Ordered
+// within the CTA only: for TMEM reads, which the tcgen05 fences order, not for memory (a release at cluster
+// scope waits for every store in flight, about a microsecond).
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;

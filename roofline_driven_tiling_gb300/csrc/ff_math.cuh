@@ -56,20 +56,49 @@ __device__ __forceinline__ uint16_t from_f32(float v) {
 constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// z s(v) with the logistic s, as a quotient: e^-v overflowing to infinity gives the limit 0.
-__device__ __forceinline__ float times_logistic(float z, float v) {
-  return __fdividef(z, 1.0f + __expf(-v));
+// 2^x and 1 / x by the hardware's approximations (2 and 1 ulp; results under 2^-126 become 0). The
+// epilogues' arithmetic is bound by instructions, and these are one each.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// act(z): relu max(z, 0) (a NaN passes), silu z s(z), gelu z (1 + erf(z / sqrt 2)) / 2,
+constexpr float kLog2E = 1.4426950408889634f;
+
+// The logistic function of v from w = -v log2(e): 2^w overflowing to infinity gives the limit 0.
+__device__ __forceinline__ float logistic_of(float w) { return reciprocal_approx(1.0f + exp2_approx(w)); }
+
+// P(-|x|), the normal distribution's tail, = erfc(|x| / sqrt 2) / 2 by Abramowitz and Stegun's formula
+// 7.1.26 (a polynomial of degree 5 in 1 / (1 + p |x| / sqrt 2) times e^(-x^2 / 2), off by at most
+// 7.5e-8 in P). erff in its place made the epilogue of 2048^3 with gelu the longer half of the kernel.
+__device__ __forceinline__ float normal_tail(float x) {
+  const float t = reciprocal_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+  float q = 0.5f * 1.061405429f;
+  q = fmaf(q, t, 0.5f * -1.453152027f);
+  q = fmaf(q, t, 0.5f * 1.421413741f);
+  q = fmaf(q, t, 0.5f * -0.284496736f);
+  q = fmaf(q, t, 0.5f * 0.254829592f);
+  return q * t * exp2_approx((-0.5f * kLog2E) * x * x);
+}
+
+// act(z): relu max(z, 0) (a NaN passes), silu z s(z), gelu z P(z) = z (1 + erf(z / sqrt 2)) / 2,
 // gelu_tanh z (1 + tanh u) / 2 = z s(2 u) with u = c (z + a z^3).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == T2S_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if constexpr (ACT == T2S_ACT_SILU) return times_logistic(z, z);
-  if constexpr (ACT == T2S_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == T2S_ACT_SILU) return z * logistic_of(-kLog2E * z);
+  if constexpr (ACT == T2S_ACT_GELU) {
+    const float q = normal_tail(z);
+    return z * (z > 0.0f ? 1.0f - q : q);
+  }
   if constexpr (ACT == T2S_ACT_GELU_TANH)
-    return times_logistic(z, (2.0f * kGeluC) * (z + kGeluA * z * z * z));
+    return z * logistic_of(z * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, z * z, -2.0f * kLog2E * kGeluC));
   return z;
 }
 
@@ -87,15 +116,14 @@ __device__ __forceinline__ void act_value_slope(float z, float& value, float& sl
     value = act_value<ACT>(z);
     const float x = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;  // a NaN stays
     if constexpr (ACT == T2S_ACT_SILU) {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-x));
+      const float s = logistic_of(-kLog2E * x);
       slope = s * (1.0f + x * (1.0f - s));
     } else if constexpr (ACT == T2S_ACT_GELU) {
       // P(x) + x p(x) with the normal distribution P and its density p.
-      slope = 0.5f * (1.0f + erff(x * 0.70710678118654752f)) +
-              x * (0.39894228040143268f * __expf(-0.5f * x * x));
+      const float q = normal_tail(x);
+      slope = (x > 0.0f ? 1.0f - q : q) + x * (0.39894228040143268f * exp2_approx((-0.5f * kLog2E) * x * x));
     } else {
-      const float u2 = (2.0f * kGeluC) * (x + kGeluA * x * x * x);
-      const float s = __fdividef(1.0f, 1.0f + __expf(-u2));
+      const float s = logistic_of(x * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, x * x, -2.0f * kLog2E * kGeluC));
       slope = s + x * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * x * x);
     }
   }

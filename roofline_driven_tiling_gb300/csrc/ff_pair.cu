@@ -43,6 +43,7 @@ constexpr int kUnitBytes = 32 * kUnit * 2;       // 32 rows of 64 bytes
 constexpr int kStagingBytes = kEpiWarps * 2 * kUnitBytes;
 constexpr int kBiasBytes = kEpiWarps * kUnit * 4;
 constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kStagingBytes + kBiasBytes;
+static_assert(kMaxN / (2 * kUnit) == 4, "column groups of an epilogue warp");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
 constexpr int kMaxProblems = 3;
@@ -125,32 +126,40 @@ __device__ __forceinline__ void store_unit(const CUtensorMap* map, bool tma, uin
   if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The residual's 32 x 32 values at (m, n) into the box, zeros outside the matrix.
-__device__ __forceinline__ void load_unit(uint32_t box, const uint16_t* p, int64_t ld, bool wide, int m, int n, int M,
-                                          int N, int lane) {
-  if (wide && n + kUnit <= N) {
-    // Four lanes per row of 64 bytes.
-    uint4 v[4];
+// The residual's 32 x 32 values at (m, n), zeros outside the matrix: fetched four lanes to a row of 64
+// bytes, some time before they are placed in the box; or (rows not 16-byte aligned, or cut by the
+// matrix's edge) read into the box value by value.
+struct Residual {
+  uint4 v[4];
+  bool fetched;
+
+  __device__ __forceinline__ void fetch(const PairProblem& p, int m, int n, int lane) {
+    fetched = p.R != nullptr && p.r_wide && n + kUnit <= p.N && m < p.M;
+    if (!fetched) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
+      const int r = m + 8 * i + (lane >> 2);
       v[i] = make_uint4(0, 0, 0, 0);
-      if (m + r < M)
-        v[i] = *reinterpret_cast<const uint4*>(p + static_cast<int64_t>(m + r) * ld + n + (lane & 3) * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      st_shared_v4(box + unit_chunk(8 * i + (lane >> 2), lane & 3), v[i].x, v[i].y, v[i].z, v[i].w);
-  } else {
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      uint16_t v = 0;
-      if (m + r < M && n + lane < N) v = p[static_cast<int64_t>(m + r) * ld + n + lane];
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + unit_chunk(r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
+      if (r < p.M) v[i] = *reinterpret_cast<const uint4*>(p.R + static_cast<int64_t>(r) * p.ldr + n + (lane & 3) * 8);
     }
   }
-  __syncwarp();
-}
+  __device__ __forceinline__ void place(const PairProblem& p, uint32_t box, int m, int n, int lane) const {
+    if (fetched) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(box + unit_chunk(8 * i + (lane >> 2), lane & 3), v[i].x, v[i].y, v[i].z, v[i].w);
+    } else {
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        uint16_t x = 0;
+        if (m + r < p.M && n + lane < p.N) x = p.R[static_cast<int64_t>(m + r) * p.ldr + n + lane];
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + unit_chunk(r, lane >> 3) + (lane & 7) * 2), "h"(x)
+                     : "memory");
+      }
+    }
+    __syncwarp();
+  }
+};
 
 // A lane's row of 32 values, rounded, into the box.
 template <int KIND>
@@ -307,6 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       int m0, n0;
       tile_at(p, t - params.first[pi], m0, n0);
       const int b = use & 1, m = m0 + rank * kRows + 32 * q;
+      // What the epilogue reads from memory is on its way before the sums are there: the bias of
+      // this warp's columns (lane i has column i of each group of 32) and the first residual box.
+      Residual residual;
+      float bias[kMaxN / (2 * kUnit)] = {};
+      if (!GATED) {
+        residual.fetch(p, m, n0 + half * kUnit, lane);
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int i = 0; i < kMaxN / (2 * kUnit); ++i) {
+            const int c = (2 * i + half) * kUnit + lane;
+            if (c < p.bn && n0 + c < p.N) bias[i] = to_f32<KIND>(p.bias[n0 + c]);
+          }
+        }
+      }
       const bool done = wait_bounded(acc_full + 8u * b, (use >> 1) & 1u, status);
       if (!__all_sync(0xffffffffu, done)) break;
       tc::tc_fence_after();
@@ -340,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
         } else {
           if (p.bias != nullptr) {
-            const float mine = n + lane < p.N ? to_f32<KIND>(p.bias[n + lane]) : 0.0f;
+            const int i = c / (2 * kUnit);
+            const float mine = i == 0 ? bias[0] : i == 1 ? bias[1] : i == 2 ? bias[2] : bias[3];
             __syncwarp();
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_row + 4u * lane), "f"(mine) : "memory");
             __syncwarp();
@@ -364,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           });
           const uint32_t box = boxes.next();
           if (p.R != nullptr) {
-            load_unit(box, p.R, p.ldr, p.r_wide, m, n, p.M, p.N, lane);
+            residual.place(p, box, m, n, lane);
+            if (c + 2 * kUnit < p.bn) residual.fetch(p, m, n + 2 * kUnit, lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t r[4];
@@ -383,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_empty + 8u * b, 0));
+      if (lane == 0) arrive_remote(tc::map_to_rank(acc_empty + 8u * b, 0));
     }
     if (lane == 0) bulk_wait_all();  // the stores read this CTA's shared memory
   }
