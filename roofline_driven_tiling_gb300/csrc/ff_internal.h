@@ -82,12 +82,11 @@ struct Copy {
 constexpr int kMaxCopies = 3;
 cudaError_t run_copies(const Context& c, const Copy* copies, int n);
 
-// dZ = dY * act'(Z) (Z absent: act none, dZ not wanted) and, unless db is nullptr, its column
-// sums. `partials` holds db_partial_rows(M, N) x N floats.
-int64_t db_partial_rows(int64_t M, int64_t N);
+// dZ = dY * act'(Z) (not stored if dZ is nullptr; Z is not read for act none) and, unless db is
+// nullptr, its column sums.
 cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dY,
                              int64_t lddy, const uint16_t* Z, int64_t ldz, uint16_t* dZ,
-                             int64_t lddz, uint16_t* db, float* partials);
+                             int64_t lddz, uint16_t* db);
 // dG = dH * U * act'(G), dU = dH * act(G).
 cudaError_t run_gated_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dH,
                                int64_t lddh, const uint16_t* G, int64_t ldg, const uint16_t* U,

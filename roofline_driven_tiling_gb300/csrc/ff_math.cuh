@@ -77,14 +77,15 @@ __device__ __forceinline__ float logistic_of(float w) { return reciprocal_approx
 // P(-|x|), the normal distribution's tail, = erfc(|x| / sqrt 2) / 2 by Abramowitz and Stegun's formula
 // 7.1.26 (a polynomial of degree 5 in 1 / (1 + p |x| / sqrt 2) times e^(-x^2 / 2), off by at most
 // 7.5e-8 in P). erff in its place made the epilogue of 2048^3 with gelu the longer half of the kernel.
-__device__ __forceinline__ float normal_tail(float x) {
+// `e` is e^(-x^2 / 2).
+__device__ __forceinline__ float normal_tail(float x, float e) {
   const float t = reciprocal_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
   float q = 0.5f * 1.061405429f;
   q = fmaf(q, t, 0.5f * -1.453152027f);
   q = fmaf(q, t, 0.5f * 1.421413741f);
   q = fmaf(q, t, 0.5f * -0.284496736f);
   q = fmaf(q, t, 0.5f * 0.254829592f);
-  return q * t * exp2_approx((-0.5f * kLog2E) * x * x);
+  return q * t * e;
 }
 
 // act(z): relu max(z, 0) (a NaN passes), silu z s(z), gelu z P(z) = z (1 + erf(z / sqrt 2)) / 2,
@@ -94,7 +95,7 @@ __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == T2S_ACT_RELU) return z < 0.0f ? 0.0f : z;
   if constexpr (ACT == T2S_ACT_SILU) return z * logistic_of(-kLog2E * z);
   if constexpr (ACT == T2S_ACT_GELU) {
-    const float q = normal_tail(z);
+    const float q = normal_tail(z, exp2_approx((-0.5f * kLog2E) * z * z));
     return z * (z > 0.0f ? 1.0f - q : q);
   }
   if constexpr (ACT == T2S_ACT_GELU_TANH)
@@ -102,8 +103,15 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
-// Both act(z) and act'(z). From |z| = 100 on every slope here is exactly 0 or 1 in FP32 (e^100
-// overflows), so z is clamped there before products that would be 0 times infinity.
+// z within [-100, 100]; a NaN stays.
+__device__ __forceinline__ float within_100(float z) {
+  float x;
+  asm("max.NaN.f32 %0, %1, 0fC2C80000;\n\tmin.NaN.f32 %0, %0, 0f42C80000;" : "=f"(x) : "f"(z));
+  return x;
+}
+
+// Both act(z) and act'(z) from one exponential. From |z| = 100 on every slope here is exactly 0 or 1
+// in FP32 (e^100 overflows), so slopes take z clamped there: no product is 0 times infinity.
 template <int ACT>
 __device__ __forceinline__ void act_value_slope(float z, float& value, float& slope) {
   if constexpr (ACT == T2S_ACT_NONE) {
@@ -113,18 +121,23 @@ __device__ __forceinline__ void act_value_slope(float z, float& value, float& sl
     value = z < 0.0f ? 0.0f : z;
     slope = z <= 0.0f ? 0.0f : 1.0f;
   } else {
-    value = act_value<ACT>(z);
-    const float x = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;  // a NaN stays
+    const float x = within_100(z), x2 = x * x;
     if constexpr (ACT == T2S_ACT_SILU) {
+      // s + x s (1 - s)
       const float s = logistic_of(-kLog2E * x);
-      slope = s * (1.0f + x * (1.0f - s));
+      slope = fmaf(x, fmaf(-s, s, s), s);
+      value = z * s;
     } else if constexpr (ACT == T2S_ACT_GELU) {
       // P(x) + x p(x) with the normal distribution P and its density p.
-      const float q = normal_tail(x);
-      slope = (x > 0.0f ? 1.0f - q : q) + x * (0.39894228040143268f * exp2_approx((-0.5f * kLog2E) * x * x));
+      const float e = exp2_approx((-0.5f * kLog2E) * x2), q = normal_tail(x, e);
+      const float d = x > 0.0f ? 1.0f - q : q;
+      slope = fmaf(0.39894228040143268f * x, e, d);
+      value = z * d;
     } else {
-      const float s = logistic_of(x * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, x * x, -2.0f * kLog2E * kGeluC));
-      slope = s + x * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * x * x);
+      // s + x s (1 - s) v' with v = 2 c (x + a x^3)
+      const float s = logistic_of(x * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, x2, -2.0f * kLog2E * kGeluC));
+      slope = fmaf(x * fmaf(-s, s, s), fmaf(6.0f * kGeluC * kGeluA, x2, 2.0f * kGeluC), s);
+      value = z * s;
     }
   }
 }

@@ -22,14 +22,15 @@ from __future__ import annotations
 import torch
 
 from . import binding
-from .binding import T2S_ERR_WORKSPACE, T2S_OK, T2S_W_KN, T2S_W_NK, T2SError
+from .binding import T2S_OK, T2S_W_KN, T2S_W_NK, T2SError
 
 ACTS = {"none": binding.T2S_ACT_NONE, "relu": binding.T2S_ACT_RELU, "silu": binding.T2S_ACT_SILU,
         "gelu": binding.T2S_ACT_GELU, "gelu_tanh": binding.T2S_ACT_GELU_TANH}
 _SUFFIX = {torch.bfloat16: "_bf16", torch.float16: "_f16"}
 _FUNCTIONS = {}
 # A single token's call lasts a few microseconds on the device: what surrounds the launch is kept short.
-_Tensor, _empty, _current_device = torch.Tensor, torch.empty, torch.cuda.current_device
+_Tensor, _empty, _strided = torch.Tensor, torch.empty, torch.empty_strided
+_current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -128,29 +129,21 @@ def _new(shape, dtype, device, stream):
 
 
 def _run(name, dtype, device, sizes, args, workspace, need, stream):
-    """One call of a C entry point. `need` gives the workspace's bytes, asked for where the call
-    has none of its own and wants one."""
+    """One call of a C entry point; `need`: the bytes of the workspace that is allocated for it
+    where it is given none."""
     f = _FUNCTIONS.get((name, dtype)) or _function(name, dtype)
     at = _raw_stream(device.index) if stream is None else stream
     if workspace is not None:
         if not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
         rc = f(*sizes, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), at)
+    elif need:
+        workspace = _new(need, torch.uint8, device, stream)
+        rc = f(*sizes, *args, workspace.data_ptr(), need, at)
     else:
         rc = f(*sizes, *args, None, 0, at)
-        if rc == T2S_ERR_WORKSPACE:
-            workspace = _new(need(), torch.uint8, device, stream)
-            rc = f(*sizes, *args, workspace.data_ptr(), workspace.numel(), at)
     if rc != T2S_OK:
         raise T2SError(rc, name + _SUFFIX[dtype])
-
-
-def _in_place(*matrices) -> int:
-    """1 if every (pointer, row stride) starts all its rows on 16-byte boundaries."""
-    bits = 0
-    for p, ld in matrices:
-        bits |= p | 2 * ld
-    return 0 if bits & 15 else 1
 
 
 def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, workspace=None, stream=None):
@@ -169,8 +162,10 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, wo
         yp, ldy = out.data_ptr(), N
     else:
         yp, ldy = _matrix(out, "out", dtype, device, (M, N))
+    # Rows that all start on 16-byte boundaries are read in place and need no workspace.
+    need = binding.t2s_linear_workspace_size(M, N, K, 0) if (xp | wp | 2 * (ldx | ldw)) & 15 else 0
     _run("t2s_linear", dtype, device, (M, N, K), (xp, ldx, wp, ldw, order, bp, rp, ldr, code, yp, ldy, zp, ldz),
-         workspace, lambda: binding.t2s_linear_workspace_size(M, N, K, 0), stream)
+         workspace, need, stream)
     return out
 
 
@@ -199,7 +194,8 @@ def linear_backward(dy, x, w, preact=None, act="none", dx=None, dw=None, db=Fals
     dbp = None if db is False else _vector(db, "db", dtype, device, N)
     _run("t2s_linear_backward", dtype, device, (M, N, K),
          (yp, ldy, xp, ldx, wp, ldw, order, zp, ldz, code, dxp, lddx, dwp, lddw, dbp), workspace,
-         lambda: binding.t2s_linear_backward_workspace_size(M, N, K, _in_place((xp, ldx), (wp, ldw), (yp, ldy))), stream)
+         0 if workspace is not None else binding.t2s_linear_backward_workspace_size(
+             M, N, K, 0 if (xp | wp | yp | 2 * (ldx | ldw | ldy)) & 15 else 1), stream)
     return dx, dw, None if db is False else db
 
 
@@ -207,15 +203,23 @@ def _output(t, name, dtype, device, shape, stream):
     """An output, its pointer and row stride: given, allocated (None) or not wanted (False)."""
     if t is None:
         t = _new(shape, dtype, device, stream)
-    elif t is False:
+        return t, t.data_ptr(), shape[1]
+    if t is False:
         return None, None, shape[1]
     return (t, *_matrix(t, name, dtype, device, shape))
 
 
 def _weight_output(t, name, dtype, device, k, n, order, stream):
     if t is None:
-        t = _new((k, n), dtype, device, stream) if order == T2S_W_KN else _new((n, k), dtype, device, stream).t()
-    elif t is False:
+        if order == T2S_W_KN:
+            t = _new((k, n), dtype, device, stream)
+            return t, t.data_ptr(), n
+        if stream is None:
+            t = _strided((k, n), (1, k), dtype=dtype, device=device)
+        else:
+            t = _new((n, k), dtype, device, stream).t()
+        return t, t.data_ptr(), k
+    if t is False:
         return None, None, max(k, n)
     return (t, *_gradient(t, name, dtype, device, k, n, order))
 
@@ -242,7 +246,7 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, preact=None, workspace=N
         hp, ldh = _matrix(out, "out", dtype, device, (M, N))
     _run("t2s_gated", dtype, device, (M, N, K),
          (xp, ldx, gp, ldg, up, ldu, order, code, hp, ldh, zg, ldzg, zu, ldzu), workspace,
-         lambda: binding.t2s_gated_workspace_size(M, N, K, 0), stream)
+         binding.t2s_gated_workspace_size(M, N, K, 0) if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 0, stream)
     return out
 
 
@@ -270,5 +274,6 @@ def gated_linear_backward(dh, x, w_gate, w_up, preact, act="silu", dx=None, dw_g
     _run("t2s_gated_backward", dtype, device, (M, N, K),
          (hp, ldh, xp, ldx, gp, ldg, up, ldu, order, zg, ldzg, zu, ldzu, code, dxp, lddx, dgp, lddg, dup, lddu),
          workspace,
-         lambda: binding.t2s_gated_backward_workspace_size(M, N, K, _in_place((xp, ldx), (gp, ldg), (up, ldu))), stream)
+         0 if workspace is not None else binding.t2s_gated_backward_workspace_size(
+             M, N, K, 0 if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 1), stream)
     return dx, dw_gate, dw_up
