@@ -45,21 +45,27 @@ __device__ __forceinline__ uint4 load8(const Source& s, int64_t r, int64_t c, in
   return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
+constexpr int kPairs = kVec / 2;
+
 template <int KIND>
-__device__ __forceinline__ void widen(const uint4& w, float (&v)[kVec]) {
+__device__ __forceinline__ void widen(const uint4& w, uint64_t (&v)[kPairs]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPairs; ++i) {
     const float2 f = to_f32x2<KIND>(u[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    v[i] = pack2(f.x, f.y);
   }
 }
 
 template <int KIND>
-__device__ __forceinline__ uint4 narrow(const float (&v)[kVec]) {
-  return make_uint4(pack_f32<KIND>(v[0], v[1]), pack_f32<KIND>(v[2], v[3]), pack_f32<KIND>(v[4], v[5]),
-                    pack_f32<KIND>(v[6], v[7]));
+__device__ __forceinline__ uint4 narrow(const uint64_t (&v)[kPairs]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 f = halves(v[i]);
+    u[i] = pack_f32<KIND>(f.x, f.y);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // kGroups threads along a row. Block (x, y): 8 kGroups columns y, y + gridDim.y, ..., the rows of
@@ -67,7 +73,7 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[kVec]) {
 // 16-byte aligned and padded to whole words. With db the chunks are a cluster's CTAs: each leaves its
 // column sums in its shared memory, and the first adds them in rank order.
 template <int KIND, int ACT, int kGroups>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     act_backward_kernel(int64_t M, int64_t N, int64_t chunk, Source dy, Source z, uint16_t* dZ, int64_t lddz,
                         uint16_t* db) {
   constexpr int kColumns = kGroups * kVec, kLanes = kThreads / kGroups;
@@ -79,30 +85,50 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * kColumns; c0 < N;
        c0 += static_cast<int64_t>(gridDim.y) * kColumns) {
     const int64_t c = c0 + group * kVec;
-    float sum[kVec] = {};
-    if (c < N) {
-#pragma unroll 4
-      for (int64_t m = blockIdx.x * chunk + row; m < m1; m += kLanes) {
-        float d[kVec];
-        widen<KIND>(load8(dy, m, c, N), d);
-        if constexpr (ACT != T2S_ACT_NONE) {
-          float x[kVec];
-          widen<KIND>(load8(z, m, c, N), x);
+    uint64_t sum[kPairs] = {};
+    auto take = [&](int64_t m, const uint4& wy, const uint4& wz) {
+      uint64_t d[kPairs];
+      widen<KIND>(wy, d);
+      if constexpr (ACT != T2S_ACT_NONE) {
+        uint64_t x[kPairs];
+        widen<KIND>(wz, x);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            float value, slope;
-            act_value_slope<ACT>(x[i], value, slope);
-            d[i] *= slope;
-          }
+        for (int i = 0; i < kPairs; ++i) {
+          uint64_t value, slope;
+          act_pair_slope<ACT>(x[i], value, slope);
+          d[i] = mul2(d[i], slope);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) sum[i] = add2(sum[i], d[i]);
+      if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + m * lddz + c) = narrow<KIND>(d);
+    };
+    int64_t m = blockIdx.x * chunk + row;
+    if (dy.wide && (ACT == T2S_ACT_NONE || z.wide) && c + kVec <= N) {
+      // Two rows' loads before the first row's arithmetic, four blocks to an SM (4096^2 with gelu
+      // 16.6 us, floor 9.9; four rows and three blocks 19.2).
+      constexpr int kAhead = 2;
+      for (; m + (kAhead - 1) * kLanes < m1; m += kAhead * kLanes) {
+        uint4 wy[kAhead], wz[kAhead] = {};
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          wy[j] = *reinterpret_cast<const uint4*>(dy.p + (m + j * kLanes) * dy.ld + c);
+          if (ACT != T2S_ACT_NONE) wz[j] = *reinterpret_cast<const uint4*>(z.p + (m + j * kLanes) * z.ld + c);
         }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum[i] += d[i];
-        if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + m * lddz + c) = narrow<KIND>(d);
+        for (int j = 0; j < kAhead; ++j) take(m + j * kLanes, wy[j], wz[j]);
       }
     }
+    if (c < N)
+      for (; m < m1; m += kLanes)
+        take(m, load8(dy, m, c, N), ACT != T2S_ACT_NONE ? load8(z, m, c, N) : make_uint4(0, 0, 0, 0));
     if (db == nullptr) continue;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) sums[row][group * kVec + i] = sum[i];
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 f = halves(sum[i]);
+      sums[row][group * kVec + 2 * i] = f.x;
+      sums[row][group * kVec + 2 * i + 1] = f.y;
+    }
     __syncthreads();
     if (threadIdx.x < kColumns) {
       float total = 0.0f;
@@ -141,16 +167,16 @@ __global__ void __launch_bounds__(kThreads)
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
     const int64_t m = i / per_row, c = (i - m * per_row) * kVec;
     const uint4 wd = load8(dh, m, c, N), wg = load8(g, m, c, N), wu = load8(u, m, c, N);
-    float d[kVec], x[kVec], y[kVec];
+    uint64_t d[kPairs], x[kPairs], y[kPairs];
     widen<KIND>(wd, d);
     widen<KIND>(wg, x);
     widen<KIND>(wu, y);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      float value, slope;
-      act_value_slope<ACT>(x[j], value, slope);
-      x[j] = d[j] * y[j] * slope;
-      y[j] = d[j] * value;
+    for (int j = 0; j < kPairs; ++j) {
+      uint64_t value, slope;
+      act_pair_slope<ACT>(x[j], value, slope);
+      x[j] = mul2(mul2(d[j], y[j]), slope);
+      y[j] = mul2(d[j], value);
     }
     *reinterpret_cast<uint4*>(dG + m * ldd + c) = narrow<KIND>(x);
     *reinterpret_cast<uint4*>(dU + m * ldd + c) = narrow<KIND>(y);

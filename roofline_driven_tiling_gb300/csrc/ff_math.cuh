@@ -71,35 +71,81 @@ __device__ __forceinline__ float reciprocal_approx(float x) {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-// The logistic function of v from w = -v log2(e): 2^w overflowing to infinity gives the limit 0.
-__device__ __forceinline__ float logistic_of(float w) { return reciprocal_approx(1.0f + exp2_approx(w)); }
+// Two FP32 values in a 64-bit register, for the packed instructions: half the issue slots of the
+// epilogues' additions, products and polynomials.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float x) { return pack2(x, x); }
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t exp2_of(uint64_t v) {
+  const float2 x = halves(v);
+  return pack2(exp2_approx(x.x), exp2_approx(x.y));
+}
+__device__ __forceinline__ uint64_t reciprocal_of(uint64_t v) {
+  const float2 x = halves(v);
+  return pack2(reciprocal_approx(x.x), reciprocal_approx(x.y));
+}
+// max(x, 0); a NaN stays.
+__device__ __forceinline__ uint64_t positive_of(uint64_t v) {
+  float2 x = halves(v);
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x.x));
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(x.y));
+  return pack2(x.x, x.y);
+}
 
 // P(-|x|), the normal distribution's tail, = erfc(|x| / sqrt 2) / 2 by Abramowitz and Stegun's formula
 // 7.1.26 (a polynomial of degree 5 in 1 / (1 + p |x| / sqrt 2) times e^(-x^2 / 2), off by at most
-// 7.5e-8 in P). erff in its place made the epilogue of 2048^3 with gelu the longer half of the kernel.
-// `e` is e^(-x^2 / 2).
-__device__ __forceinline__ float normal_tail(float x, float e) {
-  const float t = reciprocal_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
-  float q = 0.5f * 1.061405429f;
-  q = fmaf(q, t, 0.5f * -1.453152027f);
-  q = fmaf(q, t, 0.5f * 1.421413741f);
-  q = fmaf(q, t, 0.5f * -0.284496736f);
-  q = fmaf(q, t, 0.5f * 0.254829592f);
-  return q * t * e;
+// 7.5e-8 in P), for 0 <= ax = |x| and e = e^(-x^2 / 2). erff in its place made the epilogue of 2048^3 with
+// gelu the longer half of the kernel.
+__device__ __forceinline__ uint64_t normal_tail(uint64_t ax, uint64_t e) {
+  const uint64_t t = reciprocal_of(fma2(ax, both(0.3275911f * 0.70710678118654752f), both(1.0f)));
+  uint64_t q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * -0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  return mul2(mul2(q, t), e);
 }
 
-// act(z): relu max(z, 0) (a NaN passes), silu z s(z), gelu z P(z) = z (1 + erf(z / sqrt 2)) / 2,
-// gelu_tanh z (1 + tanh u) / 2 = z s(2 u) with u = c (z + a z^3).
+// act(z) of two values: relu max(z, 0), silu z s(z), gelu z P(z) = z (1 + erf(z / sqrt 2)) / 2 =
+// max(z, 0) - |z| P(-|z|), gelu_tanh z (1 + tanh u) / 2 = z s(2 u) with u = c (z + a z^3). A NaN stays.
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == T2S_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if constexpr (ACT == T2S_ACT_SILU) return z * logistic_of(-kLog2E * z);
+__device__ __forceinline__ uint64_t act_pair(uint64_t z) {
+  if constexpr (ACT == T2S_ACT_RELU) return positive_of(z);
+  if constexpr (ACT == T2S_ACT_SILU)
+    return mul2(z, reciprocal_of(add2(exp2_of(mul2(z, both(-kLog2E))), both(1.0f))));
   if constexpr (ACT == T2S_ACT_GELU) {
-    const float q = normal_tail(z, exp2_approx((-0.5f * kLog2E) * z * z));
-    return z * (z > 0.0f ? 1.0f - q : q);
+    // Beyond 100 the tail is 0, and |z| need not grow to meet it.
+    const float2 x = halves(z);
+    const uint64_t ax = pack2(fminf(fabsf(x.x), 100.0f), fminf(fabsf(x.y), 100.0f));
+    const uint64_t q = normal_tail(ax, exp2_of(mul2(mul2(ax, ax), both(-0.5f * kLog2E))));
+    return fma2(mul2(ax, both(-1.0f)), q, positive_of(z));
   }
-  if constexpr (ACT == T2S_ACT_GELU_TANH)
-    return z * logistic_of(z * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, z * z, -2.0f * kLog2E * kGeluC));
+  if constexpr (ACT == T2S_ACT_GELU_TANH) {
+    const uint64_t w = mul2(z, fma2(mul2(z, z), both(-2.0f * kLog2E * kGeluC * kGeluA), both(-2.0f * kLog2E * kGeluC)));
+    return mul2(z, reciprocal_of(add2(exp2_of(w), both(1.0f))));
+  }
   return z;
 }
 
@@ -110,34 +156,38 @@ __device__ __forceinline__ float within_100(float z) {
   return x;
 }
 
-// Both act(z) and act'(z) from one exponential. From |z| = 100 on every slope here is exactly 0 or 1
-// in FP32 (e^100 overflows), so slopes take z clamped there: no product is 0 times infinity.
+// Both act(z) and act'(z) of two values, from one exponential each. From |z| = 100 on every slope
+// here is exactly 0 or 1 in FP32 (e^100 overflows), so slopes take z clamped there: no product is 0 times infinity.
 template <int ACT>
-__device__ __forceinline__ void act_value_slope(float z, float& value, float& slope) {
+__device__ __forceinline__ void act_pair_slope(uint64_t z, uint64_t& value, uint64_t& slope) {
+  const float2 f = halves(z);
   if constexpr (ACT == T2S_ACT_NONE) {
     value = z;
-    slope = 1.0f;
+    slope = both(1.0f);
   } else if constexpr (ACT == T2S_ACT_RELU) {
-    value = z < 0.0f ? 0.0f : z;
-    slope = z <= 0.0f ? 0.0f : 1.0f;
+    value = positive_of(z);
+    slope = pack2(f.x <= 0.0f ? 0.0f : 1.0f, f.y <= 0.0f ? 0.0f : 1.0f);
   } else {
-    const float x = within_100(z), x2 = x * x;
-    if constexpr (ACT == T2S_ACT_SILU) {
-      // s + x s (1 - s)
-      const float s = logistic_of(-kLog2E * x);
-      slope = fmaf(x, fmaf(-s, s, s), s);
-      value = z * s;
-    } else if constexpr (ACT == T2S_ACT_GELU) {
+    const uint64_t x = pack2(within_100(f.x), within_100(f.y)), x2 = mul2(x, x), one = both(1.0f);
+    if constexpr (ACT == T2S_ACT_GELU) {
       // P(x) + x p(x) with the normal distribution P and its density p.
-      const float e = exp2_approx((-0.5f * kLog2E) * x2), q = normal_tail(x, e);
-      const float d = x > 0.0f ? 1.0f - q : q;
-      slope = fmaf(0.39894228040143268f * x, e, d);
-      value = z * d;
+      const float2 c = halves(x);
+      const uint64_t e = exp2_of(mul2(x2, both(-0.5f * kLog2E)));
+      const uint64_t q = normal_tail(pack2(fabsf(c.x), fabsf(c.y)), e);
+      const float2 tail = halves(q), rest = halves(fma2(q, both(-1.0f), one));
+      const uint64_t d = pack2(c.x > 0.0f ? rest.x : tail.x, c.y > 0.0f ? rest.y : tail.y);
+      slope = fma2(mul2(x, both(0.39894228040143268f)), e, d);
+      value = mul2(z, d);
     } else {
-      // s + x s (1 - s) v' with v = 2 c (x + a x^3)
-      const float s = logistic_of(x * fmaf(-2.0f * kLog2E * kGeluC * kGeluA, x2, -2.0f * kLog2E * kGeluC));
-      slope = fmaf(x * fmaf(-s, s, s), fmaf(6.0f * kGeluC * kGeluA, x2, 2.0f * kGeluC), s);
-      value = z * s;
+      // s(v) + x s (1 - s) v' with v = x (silu) or 2 c (x + a x^3) (gelu_tanh)
+      constexpr bool kSilu = ACT == T2S_ACT_SILU;
+      const uint64_t w = kSilu ? mul2(x, both(-kLog2E))
+                               : mul2(x, fma2(x2, both(-2.0f * kLog2E * kGeluC * kGeluA), both(-2.0f * kLog2E * kGeluC)));
+      const uint64_t s = reciprocal_of(add2(exp2_of(w), one));
+      const uint64_t bell = mul2(x, fma2(mul2(s, both(-1.0f)), s, s));
+      slope = kSilu ? add2(bell, s)
+                    : fma2(bell, fma2(x2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC)), s);
+      value = mul2(z, s);
     }
   }
 }

@@ -163,20 +163,26 @@ struct Residual {
 
 // A lane's row of 32 values, rounded, into the box.
 template <int KIND>
-__device__ __forceinline__ void put_row(uint32_t box, int lane, const float (&v)[kUnit]) {
+__device__ __forceinline__ void put_row(uint32_t box, int lane, const uint64_t (&v)[kUnit / 2]) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    st_shared_v4(box + unit_chunk(lane, c), pack_f32<KIND>(v[8 * c], v[8 * c + 1]),
-                 pack_f32<KIND>(v[8 * c + 2], v[8 * c + 3]), pack_f32<KIND>(v[8 * c + 4], v[8 * c + 5]),
-                 pack_f32<KIND>(v[8 * c + 6], v[8 * c + 7]));
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = halves(v[4 * c + i]);
+      w[i] = pack_f32<KIND>(f.x, f.y);
+    }
+    st_shared_v4(box + unit_chunk(lane, c), w[0], w[1], w[2], w[3]);
+  }
 }
 
 // The accumulator's 32 columns from `taddr` on, one row per lane.
-__device__ __forceinline__ void load_sums(uint32_t taddr, bool any, float (&s)[kUnit]) {
+__device__ __forceinline__ void load_sums(uint32_t taddr, bool any, uint64_t (&s)[kUnit / 2]) {
   uint32_t r[kUnit];
   tc::tmem_ld32(taddr, r);
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) s[i] = any ? __uint_as_float(r[i]) : 0.0f;
+  for (int i = 0; i < kUnit / 2; ++i)
+    s[i] = any ? pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0ull;
 }
 
 // Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 are the
@@ -212,6 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
     mbar_init(mma_done, 1);
     mbar_fence_init();
   }
+  if (warp == 0 && elect_one()) tma_prefetch_desc(&params.p[0].a[0]);
+  if (warp == 2 && elect_one()) tma_prefetch_desc(&params.p[0].b[GATED ? rank : 0]);
   if (warp == 3) tc::tmem_alloc<2>(slot, kTmemCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -339,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       for (int c = half * kUnit; c < p.bn; c += 2 * kUnit) {
         const int n = n0 + c;
         if (n >= p.N || m >= p.M) continue;  // the same for the whole warp
-        float v[kUnit];
+        uint64_t v[kUnit / 2];
         load_sums(acc + static_cast<uint32_t>(c), any, v);
         if constexpr (GATED) {
-          float u[kUnit];
+          uint64_t u[kUnit / 2];
           load_sums(acc + static_cast<uint32_t>(p.bn + c), any, u);
           if (p.Z != nullptr) {
             const uint32_t box = boxes.next();
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           }
           with_act(p.act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] = act_value<decltype(a)::value>(v[i]) * u[i];
+            for (int i = 0; i < kUnit / 2; ++i) v[i] = mul2(act_pair<decltype(a)::value>(v[i]), u[i]);
           });
           const uint32_t box = boxes.next();
           put_row<KIND>(box, lane, v);
@@ -370,11 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kUnit; i += 4) {
-              const float4 x = lds128(bias_row + 4u * i);
-              v[i] += x.x;
-              v[i + 1] += x.y;
-              v[i + 2] += x.z;
-              v[i + 3] += x.w;
+              uint64_t lo, hi;
+              lds128_pairs(bias_row + 4u * i, lo, hi);
+              v[i / 2] = add2(v[i / 2], lo);
+              v[i / 2 + 1] = add2(v[i / 2 + 1], hi);
             }
           }
           if (p.Z != nullptr) {
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           }
           with_act(p.act, [&](auto a) {
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+            for (int i = 0; i < kUnit / 2; ++i) v[i] = act_pair<decltype(a)::value>(v[i]);
           });
           const uint32_t box = boxes.next();
           if (p.R != nullptr) {
@@ -397,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const float2 x = to_f32x2<KIND>(r[j]);
-                v[8 * i + 2 * j] += x.x;
-                v[8 * i + 2 * j + 1] += x.y;
+                v[4 * i + j] = add2(v[4 * i + j], pack2(x.x, x.y));
               }
             }
           }

@@ -126,9 +126,10 @@ __device__ __forceinline__ void finish(const RowsParams& p, uint32_t base, int r
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = act_value<decltype(a)::value>(v[j][0][i]);
-          y[j][i] = GATED ? x * v[j][kWeights - 1][i] : x + r[j][i];
+        for (int i = 0; i < 4; i += 2) {
+          const float2 x = halves(act_pair<decltype(a)::value>(pack2(v[j][0][i], v[j][0][i + 1])));
+          y[j][i] = GATED ? x.x * v[j][kWeights - 1][i] : x.x + r[j][i];
+          y[j][i + 1] = GATED ? x.y * v[j][kWeights - 1][i + 1] : x.y + r[j][i + 1];
         }
     });
     if (left <= 0) continue;
@@ -173,6 +174,8 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
     mbar_init(done, 1);
     mbar_fence_init();
   }
+  if (warp == 0 && elect_one()) tma_prefetch_desc(&p.w[0]);
+  if (warp == 2 && elect_one()) tma_prefetch_desc(&p.x[0]);
   if (warp == 3) tc::tmem_alloc<1>(slot, p.tmem_cols);
   tc::tc_fence_before();
   __syncthreads();
@@ -398,6 +401,8 @@ RowsPlan plan_rows(const Task& t, int sms) {
       }
     }
   }
+  // More tiles than the grid's second dimension holds: not this way.
+  if ((t.M + plan.tm - 1) / plan.tm > 65535) plan.cost = 1e30;
   const int x_bytes = t.A.k_major ? plan.tm * kBK * 2 : (plan.tm + 63) / 64 * kBoxBytes;
   plan.stage_bytes = static_cast<uint32_t>(weights * kWeightBytes + x_bytes);
   plan.tmem_cols = 32;

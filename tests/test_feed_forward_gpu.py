@@ -518,3 +518,15 @@ def test_refusals():
         t2s.linear(x, w, out=r, preact=r)
     with pytest.raises(t2s.binding.T2SError):
         t2s.linear_backward(r, x, w, r, act="silu", workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
+
+
+def test_many_rows():
+    """More rows than a grid's second dimension has tiles, one output per row."""
+    m, k, n = (1 << 24) + 1000, 8, 1
+    mk = Maker(16, BF16)
+    x, w, b = mk.normal(m, k), mk.normal(k, 8)[:, :n], mk.vector(n)
+    y, bar, _, _ = linear_want(x, w, b, None, "relu", BF16)
+    within(t2s.linear(x, w, b, act="relu"), y, bar, "y")
+    dx, _, _ = t2s.linear_backward(x[:, :n], x, w, dw=False)
+    zero = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    within(dx, *product_bar(zero, x[:, :n].double(), w.double().t(), BF16), "dx")
