@@ -29,7 +29,7 @@ ACTS = {"none": binding.T2S_ACT_NONE, "relu": binding.T2S_ACT_RELU, "silu": bind
 _SUFFIX = {torch.bfloat16: "_bf16", torch.float16: "_f16"}
 _FUNCTIONS = {}
 # A single token's call lasts a few microseconds on the device: what surrounds the launch is kept short.
-_Tensor, _empty, _strided = torch.Tensor, torch.empty, torch.empty_strided
+_Tensor, _strided = torch.Tensor, torch.empty_strided
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -44,12 +44,14 @@ def _function(name: str, dtype):
 
 
 def _first(t, name):
-    """Type and device of a call, set by its first tensor."""
+    """Type and device of a call, set by its first tensor, and the tensor's pointer, row stride and sizes."""
     if not isinstance(t, _Tensor) or t.dtype not in _SUFFIX or not t.is_cuda:
         raise TypeError("%s must be a bfloat16 or float16 CUDA tensor" % name)
-    if t.get_device() != _current_device():
+    device = t.device
+    if device.index != _current_device():
         raise ValueError("%s must be on the current CUDA device" % name)
-    return t.dtype, t.device
+    dtype = t.dtype
+    return (dtype, device, *_matrix(t, name, dtype, device), *t.shape)
 
 
 def _refuse(t, name, dtype, device):
@@ -119,53 +121,49 @@ def _act(act):
     return code
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, strides, dtype, device, stream):
     """A tensor of the pool of the call's stream (None: the current one), so that the reuse of its
     memory is ordered there."""
     if stream is None:
-        return _empty(shape, dtype=dtype, device=device)
+        return _strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-        return _empty(shape, dtype=dtype, device=device)
+        return _strided(shape, strides, dtype=dtype, device=device)
 
 
-def _run(name, dtype, device, sizes, args, workspace, need, stream):
-    """One call of a C entry point; `need`: the bytes of the workspace that is allocated for it
-    where it is given none."""
-    f = _FUNCTIONS.get((name, dtype)) or _function(name, dtype)
-    at = _raw_stream(device.index) if stream is None else stream
-    if workspace is not None:
-        if not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous CUDA tensor")
-        rc = f(*sizes, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), at)
-    elif need:
-        workspace = _new(need, torch.uint8, device, stream)
-        rc = f(*sizes, *args, workspace.data_ptr(), need, at)
-    else:
-        rc = f(*sizes, *args, None, 0, at)
-    if rc != T2S_OK:
-        raise T2SError(rc, name + _SUFFIX[dtype])
+def _workspace(given, need, device, stream):
+    """The workspace of a call (kept by the caller until it has been enqueued), its pointer and bytes."""
+    if given is None:
+        if not need:
+            return None, None, 0
+        given = _new((need,), (1,), torch.uint8, device, stream)
+        return given, given.data_ptr(), need
+    if not isinstance(given, _Tensor) or not given.is_cuda or not given.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
 def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, workspace=None, stream=None):
     """act(x @ w + bias) + residual; ``preact`` (a tensor of the output's shape) receives
     x @ w + bias, which ``linear_backward`` needs for an activation."""
-    dtype, device = _first(x, "x")
-    xp, ldx = _matrix(x, "x", dtype, device)
-    M, K = x.shape
+    dtype, device, xp, ldx, M, K = _first(x, "x")
     wp, ldw, order, N = _weight(w, "w", dtype, device, K)
     bp = None if bias is None else _vector(bias, "bias", dtype, device, N)
     rp, ldr = (None, N) if residual is None else _matrix(residual, "residual", dtype, device, (M, N))
     zp, ldz = (None, N) if preact is None else _matrix(preact, "preact", dtype, device, (M, N))
     code = _act(act)
     if out is None:
-        out = _new((M, N), dtype, device, stream)
+        out = _new((M, N), (N, 1), dtype, device, stream)
         yp, ldy = out.data_ptr(), N
     else:
         yp, ldy = _matrix(out, "out", dtype, device, (M, N))
     # Rows that all start on 16-byte boundaries are read in place and need no workspace.
     need = binding.t2s_linear_workspace_size(M, N, K, 0) if (xp | wp | 2 * (ldx | ldw)) & 15 else 0
-    _run("t2s_linear", dtype, device, (M, N, K), (xp, ldx, wp, ldw, order, bp, rp, ldr, code, yp, ldy, zp, ldz),
-         workspace, need, stream)
+    keep, ws, size = _workspace(workspace, need, device, stream)
+    f = _FUNCTIONS.get(("t2s_linear", dtype)) or _function("t2s_linear", dtype)
+    rc = f(M, N, K, xp, ldx, wp, ldw, order, bp, rp, ldr, code, yp, ldy, zp, ldz, ws, size,
+           _raw_stream(device.index) if stream is None else stream)
+    if rc != T2S_OK:
+        raise T2SError(rc, "t2s_linear" + _SUFFIX[dtype])
     return out
 
 
@@ -173,9 +171,7 @@ def linear_backward(dy, x, w, preact=None, act="none", dx=None, dw=None, db=Fals
     """(dx, dw, db) of ``linear``; the residual's gradient is dy itself. Each of dx, dw, db is
     None (allocated here), a tensor that receives it, or False (not computed). ``preact`` is
     what ``linear`` left there, needed for an ``act`` other than "none"."""
-    dtype, device = _first(dy, "dy")
-    yp, ldy = _matrix(dy, "dy", dtype, device)
-    M, N = dy.shape
+    dtype, device, yp, ldy, M, N = _first(dy, "dy")
     xp, ldx = _matrix(x, "x", dtype, device)
     K = x.shape[1]
     if x.shape[0] != M:
@@ -190,19 +186,23 @@ def linear_backward(dy, x, w, preact=None, act="none", dx=None, dw=None, db=Fals
     dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, K), stream)
     dw, dwp, lddw = _weight_output(dw, "dw", dtype, device, K, N, order, stream)
     if db is None:
-        db = _new((N,), dtype, device, stream)
+        db = _new((N,), (1,), dtype, device, stream)
     dbp = None if db is False else _vector(db, "db", dtype, device, N)
-    _run("t2s_linear_backward", dtype, device, (M, N, K),
-         (yp, ldy, xp, ldx, wp, ldw, order, zp, ldz, code, dxp, lddx, dwp, lddw, dbp), workspace,
-         0 if workspace is not None else binding.t2s_linear_backward_workspace_size(
-             M, N, K, 0 if (xp | wp | yp | 2 * (ldx | ldw | ldy)) & 15 else 1), stream)
+    need = 0 if workspace is not None else binding.t2s_linear_backward_workspace_size(
+        M, N, K, 0 if (xp | wp | yp | 2 * (ldx | ldw | ldy)) & 15 else 1)
+    keep, ws, size = _workspace(workspace, need, device, stream)
+    f = _FUNCTIONS.get(("t2s_linear_backward", dtype)) or _function("t2s_linear_backward", dtype)
+    rc = f(M, N, K, yp, ldy, xp, ldx, wp, ldw, order, zp, ldz, code, dxp, lddx, dwp, lddw, dbp, ws, size,
+           _raw_stream(device.index) if stream is None else stream)
+    if rc != T2S_OK:
+        raise T2SError(rc, "t2s_linear_backward" + _SUFFIX[dtype])
     return dx, dw, None if db is False else db
 
 
 def _output(t, name, dtype, device, shape, stream):
     """An output, its pointer and row stride: given, allocated (None) or not wanted (False)."""
     if t is None:
-        t = _new(shape, dtype, device, stream)
+        t = _new(shape, (shape[1], 1), dtype, device, stream)
         return t, t.data_ptr(), shape[1]
     if t is False:
         return None, None, shape[1]
@@ -211,14 +211,9 @@ def _output(t, name, dtype, device, shape, stream):
 
 def _weight_output(t, name, dtype, device, k, n, order, stream):
     if t is None:
-        if order == T2S_W_KN:
-            t = _new((k, n), dtype, device, stream)
-            return t, t.data_ptr(), n
-        if stream is None:
-            t = _strided((k, n), (1, k), dtype=dtype, device=device)
-        else:
-            t = _new((n, k), dtype, device, stream).t()
-        return t, t.data_ptr(), k
+        kn = order == T2S_W_KN
+        t = _new((k, n), (n, 1) if kn else (1, k), dtype, device, stream)
+        return t, t.data_ptr(), n if kn else k
     if t is False:
         return None, None, max(k, n)
     return (t, *_gradient(t, name, dtype, device, k, n, order))
@@ -227,9 +222,7 @@ def _weight_output(t, name, dtype, device, k, n, order, stream):
 def gated_linear(x, w_gate, w_up, act="silu", out=None, preact=None, workspace=None, stream=None):
     """act(x @ w_gate) * (x @ w_up); ``preact``, a pair of tensors of the output's shape,
     receives x @ w_gate and x @ w_up, which ``gated_linear_backward`` needs."""
-    dtype, device = _first(x, "x")
-    xp, ldx = _matrix(x, "x", dtype, device)
-    M, K = x.shape
+    dtype, device, xp, ldx, M, K = _first(x, "x")
     gp, ldg, order, N = _weight(w_gate, "w_gate", dtype, device, K)
     up, ldu, order_up, _ = _weight(w_up, "w_up", dtype, device, K, N)
     if order != order_up:
@@ -240,13 +233,17 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, preact=None, workspace=N
         zu, ldzu = _matrix(preact[1], "preact[1]", dtype, device, (M, N))
     code = _act(act)
     if out is None:
-        out = _new((M, N), dtype, device, stream)
+        out = _new((M, N), (N, 1), dtype, device, stream)
         hp, ldh = out.data_ptr(), N
     else:
         hp, ldh = _matrix(out, "out", dtype, device, (M, N))
-    _run("t2s_gated", dtype, device, (M, N, K),
-         (xp, ldx, gp, ldg, up, ldu, order, code, hp, ldh, zg, ldzg, zu, ldzu), workspace,
-         binding.t2s_gated_workspace_size(M, N, K, 0) if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 0, stream)
+    need = binding.t2s_gated_workspace_size(M, N, K, 0) if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 0
+    keep, ws, size = _workspace(workspace, need, device, stream)
+    f = _FUNCTIONS.get(("t2s_gated", dtype)) or _function("t2s_gated", dtype)
+    rc = f(M, N, K, xp, ldx, gp, ldg, up, ldu, order, code, hp, ldh, zg, ldzg, zu, ldzu, ws, size,
+           _raw_stream(device.index) if stream is None else stream)
+    if rc != T2S_OK:
+        raise T2SError(rc, "t2s_gated" + _SUFFIX[dtype])
     return out
 
 
@@ -254,9 +251,7 @@ def gated_linear_backward(dh, x, w_gate, w_up, preact, act="silu", dx=None, dw_g
                           workspace=None, stream=None):
     """(dx, dw_gate, dw_up) of ``gated_linear``; ``preact`` is the pair that it left there. Each
     output is None (allocated here), a tensor that receives it, or False (not computed)."""
-    dtype, device = _first(dh, "dh")
-    hp, ldh = _matrix(dh, "dh", dtype, device)
-    M, N = dh.shape
+    dtype, device, hp, ldh, M, N = _first(dh, "dh")
     xp, ldx = _matrix(x, "x", dtype, device)
     K = x.shape[1]
     if x.shape[0] != M:
@@ -271,9 +266,12 @@ def gated_linear_backward(dh, x, w_gate, w_up, preact, act="silu", dx=None, dw_g
     dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, K), stream)
     dw_gate, dgp, lddg = _weight_output(dw_gate, "dw_gate", dtype, device, K, N, order, stream)
     dw_up, dup, lddu = _weight_output(dw_up, "dw_up", dtype, device, K, N, order, stream)
-    _run("t2s_gated_backward", dtype, device, (M, N, K),
-         (hp, ldh, xp, ldx, gp, ldg, up, ldu, order, zg, ldzg, zu, ldzu, code, dxp, lddx, dgp, lddg, dup, lddu),
-         workspace,
-         0 if workspace is not None else binding.t2s_gated_backward_workspace_size(
-             M, N, K, 0 if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 1), stream)
+    need = 0 if workspace is not None else binding.t2s_gated_backward_workspace_size(
+        M, N, K, 0 if (xp | gp | up | 2 * (ldx | ldg | ldu)) & 15 else 1)
+    keep, ws, size = _workspace(workspace, need, device, stream)
+    f = _FUNCTIONS.get(("t2s_gated_backward", dtype)) or _function("t2s_gated_backward", dtype)
+    rc = f(M, N, K, hp, ldh, xp, ldx, gp, ldg, up, ldu, order, zg, ldzg, zu, ldzu, code, dxp, lddx, dgp, lddg, dup,
+           lddu, ws, size, _raw_stream(device.index) if stream is None else stream)
+    if rc != T2S_OK:
+        raise T2SError(rc, "t2s_gated_backward" + _SUFFIX[dtype])
     return dx, dw_gate, dw_up
