@@ -43,6 +43,8 @@ struct Task {
   int act = 0;
 };
 
+constexpr int kMaxProblems = 3;  // products of one launch
+
 struct Context {
   Kind kind;
   cudaStream_t stream;
@@ -60,15 +62,20 @@ int pair_width(const Task& t, int pairs, double* cost);
 // in place (aligned16), and rows of a single-row operand given a stride that is.
 cudaError_t run_pair(const Context& c, const Task* tasks, const int* widths, int n);
 
-// How ff_rows.cu takes a product: rows of X per tile, CTAs along K, ring slots.
-struct RowsPlan {
-  int tm = 0, splits = 1, stages = 0, smem_bytes = 0;
+// How ff_rows.cu takes up to three products in one launch: CTAs along K, and for each product the
+// rows of X per tile and the ring slots. `cost` is the expected time in microseconds.
+struct RowsTile {
+  int tm = 0, stages = 0;
   uint32_t stage_bytes = 0, tmem_cols = 0;
-  double cost = 0.0;  // expected time in microseconds
 };
-RowsPlan plan_rows(const Task& t, int sms);
-// One product with its sum split over a cluster; operands as for run_pair.
-cudaError_t run_rows(const Context& c, const Task& t, const RowsPlan& plan);
+struct RowsPlan {
+  int splits = 1, smem_bytes = 0;
+  RowsTile tile[kMaxProblems];
+  double cost = 0.0;
+};
+RowsPlan plan_rows(const Task* tasks, int n, int sms);
+// Products with their sums split over clusters; operands as for run_pair.
+cudaError_t run_rows(const Context& c, const Task* tasks, const RowsPlan& plan, int n);
 
 // Up to three products, none or all of them of the gated form, each by the kernel that suits its sizes.
 cudaError_t run_products(const Context& c, const Task* tasks, int n);

@@ -46,7 +46,6 @@ constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kStagingBytes +
 static_assert(kMaxN / (2 * kUnit) == 4, "column groups of an epilogue warp");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
-constexpr int kMaxProblems = 3;
 
 struct PairProblem {
   CUtensorMap a[2], b[2], y, z, z2;

@@ -32,20 +32,26 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSplits = 8;
 constexpr int kMaxStages = 12;
 
-struct RowsParams {
+struct RowsProblem {
   CUtensorMap w[2], x[2];
   const uint16_t* bias;
   const uint16_t* R;
   uint16_t *Y, *Z, *Z2;
   int64_t ldr, ldy, ldz, ldz2;
-  unsigned* status;
   int M, N;
   int nkb, nkb_first;  // K blocks, and how many of them come from w[0], x[0]
   int tm;              // rows of X in a tile: the MMA's N
-  int splits, stages;
+  int tiles_n, stages;
   int w_k_major, x_k_major, x_boxes;
   int act;
   uint32_t idesc, stage_bytes, tmem_cols;
+};
+
+struct RowsParams {
+  RowsProblem p[kMaxProblems];
+  int first[kMaxProblems];  // first tile of each problem (one past the last tile where there is none)
+  int splits;
+  unsigned* status;
 };
 
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
@@ -84,7 +90,7 @@ __device__ __forceinline__ void store4(uint16_t* p, int left, const float (&v)[4
 // cluster's warps, four outputs per lane, several rows' loads (distributed shared memory and the
 // residual answer after hundreds of cycles) before the first row's arithmetic.
 template <int KIND, bool GATED, int S>
-__device__ __forceinline__ void finish(const RowsParams& p, uint32_t base, int rank, int n0, int m0) {
+__device__ __forceinline__ void finish(const RowsProblem& p, uint32_t base, int rank, int n0, int m0) {
   constexpr int kWeights = GATED ? 2 : 1;
   constexpr int kUnroll = S * kWeights <= 2 ? 4 : S * kWeights <= 4 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,21 +156,25 @@ __device__ __forceinline__ void finish(const RowsParams& p, uint32_t base, int r
 // per ring slot. A role that gives up a bounded wait records it and stops; every thread still
 // reaches the cluster barriers.
 template <int KIND, bool GATED>
-__global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant__ RowsParams params) {
   extern __shared__ uint8_t smem_raw[];
+  const int splits = params.splits, cluster = static_cast<int>(blockIdx.x) / splits;
+  const int pi = cluster < params.first[1] ? 0 : cluster < params.first[2] ? 1 : 2;
+  const RowsProblem& p = params.p[pi];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int S = p.stages;
   const uint32_t bars = base + S * p.stage_bytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
   const uint32_t done = bars + 16u * kMaxStages, slot = done + 8u;
-  unsigned* const status = p.status;
+  unsigned* const status = params.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int n0 = static_cast<int>(blockIdx.x / p.splits) * kTileN, m0 = static_cast<int>(blockIdx.y) * p.tm;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = cluster - params.first[pi];
+  const int n0 = tile % p.tiles_n * kTileN, m0 = tile / p.tiles_n * p.tm;
   // This CTA's K blocks.
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / p.splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / p.splits);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / splits);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -272,13 +282,13 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
                    : "memory");
   }
   tc::tc_fence_before();
-  if (p.splits > 1) {
+  if (splits > 1) {
     cluster_sync_all();
   } else {
     __syncthreads();
   }
 
-  switch (p.splits) {
+  switch (splits) {
     case 1: finish<KIND, GATED, 1>(p, base, rank, n0, m0); break;
     case 2: finish<KIND, GATED, 2>(p, base, rank, n0, m0); break;
     case 4: finish<KIND, GATED, 4>(p, base, rank, n0, m0); break;
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
   }
 
   // No CTA's partial sums go while another may read them.
-  if (p.splits > 1) {
+  if (splits > 1) {
     cluster_sync_all();
   } else {
     __syncthreads();
@@ -297,8 +307,44 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
   }
 }
 
+template <int KIND>
+cudaError_t fill(RowsProblem* p, const Task& t, const RowsTile& tile) {
+  cudaError_t e = cudaSuccess;
+  p->M = static_cast<int>(t.M);
+  p->N = static_cast<int>(t.N);
+  p->tm = tile.tm;
+  p->tiles_n = static_cast<int>((t.N + kTileN - 1) / kTileN);
+  p->stages = tile.stages;
+  p->stage_bytes = tile.stage_bytes;
+  p->tmem_cols = tile.tmem_cols;
+  const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
+  p->nkb_first = blocks;
+  p->nkb = t.form == kJoined ? 2 * blocks : blocks;
+  p->w_k_major = t.B.k_major;
+  p->x_k_major = t.A.k_major;
+  p->x_boxes = (tile.tm + 63) / 64;
+  const uint32_t fmt = KIND == kBf16 ? 1u : 0u;
+  // D FP32, both operands of the 16-bit type, their orders, N = tm, M = 128.
+  p->idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p->w_k_major ? 0u : 1u) << 15) |
+             ((p->x_k_major ? 0u : 1u) << 16) | (static_cast<uint32_t>(tile.tm >> 3) << 17) |
+             (static_cast<uint32_t>(kTileN >> 4) << 24);
+  p->bias = t.bias;
+  p->R = t.R.p, p->ldr = t.R.ld;
+  p->Y = t.Y.p, p->ldy = t.Y.ld;
+  p->Z = t.Z.p, p->ldz = t.Z.ld;
+  p->Z2 = t.Z2.p, p->ldz2 = t.Z2.ld;
+  p->act = t.act;
+  if (blocks == 0) return cudaSuccess;
+  const uint32_t tm = static_cast<uint32_t>(tile.tm);
+  if ((e = operand_map(&p->w[0], t.B, t.N, t.K, kTileN)) != cudaSuccess) return e;
+  if ((e = operand_map(&p->x[0], t.A, t.M, t.K, tm)) != cudaSuccess) return e;
+  if (t.form != kLinear && (e = operand_map(&p->w[1], t.B2, t.N, t.K, kTileN)) != cudaSuccess) return e;
+  if (t.form == kJoined && (e = operand_map(&p->x[1], t.A2, t.M, t.K, tm)) != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
 template <int KIND, bool GATED>
-cudaError_t launch(const Context& c, const Task& t, const RowsPlan& plan) {
+cudaError_t launch(const Context& c, const Task* tasks, const RowsPlan& plan, int n) {
   constexpr int kMaxDevices = 64;
   constexpr int kMaxSmem = 227 * 1024;
   static std::atomic<bool> prepared[kMaxDevices];
@@ -312,129 +358,148 @@ cudaError_t launch(const Context& c, const Task& t, const RowsPlan& plan) {
       return e;
     prepared[dev].store(true, std::memory_order_release);
   }
-  RowsParams p;
-  memset(&p, 0, sizeof(p));
-  p.status = c.status;
-  p.M = static_cast<int>(t.M);
-  p.N = static_cast<int>(t.N);
-  p.tm = plan.tm;
-  p.splits = plan.splits;
-  p.stages = plan.stages;
-  p.stage_bytes = plan.stage_bytes;
-  p.tmem_cols = plan.tmem_cols;
-  const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
-  p.nkb_first = blocks;
-  p.nkb = t.form == kJoined ? 2 * blocks : blocks;
-  p.w_k_major = t.B.k_major;
-  p.x_k_major = t.A.k_major;
-  p.x_boxes = (plan.tm + 63) / 64;
-  const uint32_t fmt = KIND == kBf16 ? 1u : 0u;
-  // D FP32, both operands of the 16-bit type, their orders, N = tm, M = 128.
-  p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p.w_k_major ? 0u : 1u) << 15) |
-            ((p.x_k_major ? 0u : 1u) << 16) | (static_cast<uint32_t>(plan.tm >> 3) << 17) |
-            (static_cast<uint32_t>(kTileN >> 4) << 24);
-  p.bias = t.bias;
-  p.R = t.R.p, p.ldr = t.R.ld;
-  p.Y = t.Y.p, p.ldy = t.Y.ld;
-  p.Z = t.Z.p, p.ldz = t.Z.ld;
-  p.Z2 = t.Z2.p, p.ldz2 = t.Z2.ld;
-  p.act = t.act;
-  if (blocks > 0) {
-    const uint32_t tm = static_cast<uint32_t>(plan.tm);
-    if ((e = operand_map(&p.w[0], t.B, t.N, t.K, kTileN)) != cudaSuccess) return e;
-    if ((e = operand_map(&p.x[0], t.A, t.M, t.K, tm)) != cudaSuccess) return e;
-    if (t.form != kLinear && (e = operand_map(&p.w[1], t.B2, t.N, t.K, kTileN)) != cudaSuccess) return e;
-    if (t.form == kJoined && (e = operand_map(&p.x[1], t.A2, t.M, t.K, tm)) != cudaSuccess) return e;
+  RowsParams params;
+  memset(&params, 0, sizeof(params));
+  params.status = c.status;
+  params.splits = plan.splits;
+  int64_t tiles = 0;
+  for (int i = 0; i < kMaxProblems; ++i) {
+    params.first[i] = static_cast<int>(tiles);
+    if (i >= n) continue;
+    if ((e = fill<KIND>(&params.p[i], tasks[i], plan.tile[i])) != cudaSuccess) return e;
+    tiles += static_cast<int64_t>(params.p[i].tiles_n) * ((tasks[i].M + plan.tile[i].tm - 1) / plan.tile[i].tm);
+    if (tiles * plan.splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
   }
-  const LaunchShape shape{dim3(static_cast<unsigned>((t.N + kTileN - 1) / kTileN) * plan.splits,
-                               static_cast<unsigned>((t.M + plan.tm - 1) / plan.tm)),
-                          kThreads, plan.splits, plan.smem_bytes};
-  return launch_early(c.stream, shape, kern, p);
+  const LaunchShape shape{dim3(static_cast<unsigned>(tiles * plan.splits)), kThreads, plan.splits, plan.smem_bytes};
+  return launch_early(c.stream, shape, kern, params);
 }
+
+// What a product takes this way in tiles of `tm` rows of X with `splits` CTAs along K, in microseconds.
+// Fitted to 30 products of 1 to 1024 rows (within 15 %): a K block of 16 KB of weights takes a CTA 0.15
+// us, more once X's tile outweighs the weight's (0.165 at 128 rows, 0.24 at 256), the gated form's two
+// weights 0.22 to 0.25; the partial sums' way through shared memory 17 ns a row (gated: 25).
+struct Cost {
+  int64_t ctas;
+  double per_cta;  // one CTA's time
+  double feed;     // all SMs together take in at most 16 TB/s
+};
+Cost cost_of(const Task& t, int tm, int splits) {
+  const bool gated = t.form == kGated;
+  const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
+  const int64_t tiles = (t.N + kTileN - 1) / kTileN * ((t.M + tm - 1) / tm);
+  double block = tm <= 64 ? 0.15 : tm <= 128 ? 0.15 + (tm - 64) * 0.00023 : 0.165 + (tm - 128) * 0.00059;
+  if (gated) block = 0.22 + tm * 0.00025;
+  Cost c;
+  c.ctas = tiles * splits;
+  c.per_cta = static_cast<double>((blocks + splits - 1) / splits) * block + tm * (gated ? 0.025 : 0.017);
+  c.feed = static_cast<double>(tiles) * static_cast<double>(blocks) *
+           ((gated ? 2 : 1) * kWeightBytes + tm * kBK * 2) / 16e6;
+  return c;
+}
+
+// SMs that clusters of `splits` CTAs reach when a CTA fills an SM: measured 152, 152, 144 and 120 of 152.
+int reach_of(int splits, int sms) { return splits <= 2 ? sms : splits == 4 ? sms * 95 / 100 : sms * 79 / 100; }
 
 }  // namespace
 
-// The time that a product takes this way with tiles of `tm` rows of X and `splits` CTAs along K, in
-// microseconds, up to what all ways share. Fitted to 30 products of 1 to 1024 rows (within 15 %):
-// a K block of 16 KB of weights takes a CTA 0.15 us, more once X's tile outweighs the weight's
-// (0.165 at 128 rows, 0.24 at 256), the gated form's two weights 0.22 to 0.25; the partial sums' way through shared
-// memory 17 ns a row (gated: 25); a cluster's two barriers 0.6 us. All SMs together take in at most
-// 16 TB/s.
-static double rows_cost(bool gated, int tm, int splits, int64_t tiles, int64_t blocks, int sms, bool* fits) {
-  // Clusters of 4 reach 95 % of the SMs and clusters of 8 79 % with CTAs that fill them (144 and 120
-  // of 152).
-  const int reach = splits <= 2 ? sms : splits == 4 ? sms * 95 / 100 : sms * 79 / 100;
-  const int64_t ctas = tiles * splits, waves = (ctas + reach - 1) / reach;
-  *fits = waves == 1;
-  double block = tm <= 64 ? 0.15 : tm <= 128 ? 0.15 + (tm - 64) * 0.00023 : 0.165 + (tm - 128) * 0.00059;
-  if (gated) block = 0.22 + tm * 0.00025;
-  const double per_cta = static_cast<double>((blocks + splits - 1) / splits) * block + tm * (gated ? 0.025 : 0.017);
-  const double bytes = static_cast<double>(tiles) * static_cast<double>(blocks) *
-                       ((gated ? 2 : 1) * kWeightBytes + tm * kBK * 2);
-  const double time = static_cast<double>(waves) * per_cta;
-  return (time > bytes / 16e6 ? time : bytes / 16e6) + (splits > 1 ? 0.6 : 0.0) + 4.0;
-}
-
-RowsPlan plan_rows(const Task& t, int sms) {
+RowsPlan plan_rows(const Task* tasks, int n, int sms) {
   RowsPlan plan;
-  const bool gated = t.form == kGated;
-  const int weights = gated ? 2 : 1;
-  const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
-  const int64_t tiles_n = (t.N + kTileN - 1) / kTileN;
-  // Equal shares of M per tile, at most 256 sums per TMEM lane, and no tiles under 32 rows but one.
-  const int64_t fewest = (t.M * weights + 255) / 256, most = (t.M + 31) / 32;
-  bool one_wave = false;
   plan.cost = 0.0;
-  for (int64_t tiles_m = fewest; tiles_m <= most || tiles_m == fewest; tiles_m += tiles_m < 16 ? 1 : tiles_m / 8) {
-    const int tm = static_cast<int>(((t.M + tiles_m - 1) / tiles_m + 15) / 16 * 16);
-    const int64_t tiles = tiles_n * ((t.M + tm - 1) / tm);
-    if (tiles_m > fewest && tiles > 2 * sms) break;
-    for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
-      if (splits > 1 && (blocks < 2 * splits || tiles * splits > sms)) break;
-      bool fits = false;
-      const double cost = rows_cost(gated, tm, splits, tiles, blocks, sms, &fits);
-      if (plan.cost == 0.0 || cost < plan.cost) {
-        plan.cost = cost;
-        plan.tm = tm;
-        plan.splits = splits;
-        one_wave = fits;
+  bool one_wave = false;
+  for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+    const int reach = reach_of(splits, sms);
+    int tm[kMaxProblems] = {};
+    int64_t ctas = 0;
+    double longest = 0.0, work = 0.0, feed = 0.0;
+    for (int i = 0; i < n; ++i) {
+      const Task& t = tasks[i];
+      const int weights = t.form == kGated ? 2 : 1;
+      const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
+      if (splits > 1 && blocks < 2 * splits) {
+        longest = -1.0;  // fewer than two blocks to a CTA
+        break;
       }
+      // Equal shares of M: the fewest tiles that hold 256 sums per TMEM lane, or tiles of fewer rows.
+      const int64_t fewest = (t.M * weights + 255) / 256;
+      double best = 0.0;
+      Cost chosen = {};
+      for (const int rows : {256, 192, 128, 96, 64, 32}) {
+        int64_t tiles_m = (t.M + rows - 1) / rows;
+        if (tiles_m < fewest) tiles_m = fewest;
+        const int candidate = static_cast<int>(((t.M + tiles_m - 1) / tiles_m + 15) / 16 * 16);
+        if (candidate == tm[i]) continue;
+        const Cost c = cost_of(t, candidate, splits);
+        // Alone a product's waves count; among others, the SMs' time it takes.
+        const double waves = n == 1 ? static_cast<double>((c.ctas + reach - 1) / reach)
+                                    : 0.5 + static_cast<double>(c.ctas) / reach;
+        double time = waves * c.per_cta;
+        if (time < c.feed) time = c.feed;
+        if (best == 0.0 || time < best) {
+          best = time;
+          chosen = c;
+          tm[i] = candidate;
+        }
+      }
+      ctas += chosen.ctas;
+      if (longest < chosen.per_cta) longest = chosen.per_cta;
+      work += static_cast<double>(chosen.ctas) * chosen.per_cta;
+      feed += chosen.feed;
+    }
+    if (longest < 0.0) break;
+    if (splits > 1 && ctas > 2 * reach) break;
+    double time = n == 1 ? static_cast<double>((ctas + reach - 1) / reach) * longest : work / reach * 1.1;
+    if (time < longest) time = longest;
+    if (time < feed) time = feed;
+    // What every launch takes, and a cluster's two barriers.
+    time += 4.0 + (splits > 1 ? 0.6 : 0.0);
+    if (plan.cost == 0.0 || time < plan.cost) {
+      plan.cost = time;
+      plan.splits = splits;
+      for (int i = 0; i < n; ++i) plan.tile[i].tm = tm[i];
+      one_wave = ctas <= reach;
     }
   }
-  // More tiles than the grid's second dimension holds: not this way.
-  if ((t.M + plan.tm - 1) / plan.tm > 65535) plan.cost = 1e30;
-  const int x_bytes = t.A.k_major ? plan.tm * kBK * 2 : (plan.tm + 63) / 64 * kBoxBytes;
-  plan.stage_bytes = static_cast<uint32_t>(weights * kWeightBytes + x_bytes);
-  plan.tmem_cols = 32;
-  while (plan.tmem_cols < static_cast<uint32_t>(weights * plan.tm)) plan.tmem_cols *= 2;
-  // Half of an SM's memory where that holds six slots (then the next call's CTAs can be set up beside
-  // these: linear 8x8192x4096 13.1 us against 14.0 with all of it) or more CTAs are to come; otherwise
-  // a ring over all of it (64x4096x4096: 8.7 against 9.0, 128x4096x4096 10.2 against 11.6).
-  const int half = 112 * 1024, whole = 200 * 1024, stage = static_cast<int>(plan.stage_bytes);
-  const int budget = !one_wave || 6 * stage <= half ? half : whole;
-  // The partial sums lie over the ring, so it holds at least those.
-  const int partials = weights * plan.tm * kTileN * 4;
-  const int64_t per_cta = (blocks + plan.splits - 1) / plan.splits;
-  int stages = budget / stage;
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (stages > per_cta) stages = static_cast<int>(per_cta);
-  const int least = (partials + stage - 1) / stage;
-  if (stages < least) stages = least;
-  plan.stages = stages;
-  plan.smem_bytes = stages * stage + 1024 + 512;
-  // CTAs that share an SM must find TMEM for all of them, or clusters could wait for each other's:
-  // shared memory in the proportion of TMEM (and never so little that a CTA fits beside a kernel
-  // that fills the rest) keeps the sum of their columns at most 512.
-  const int share = static_cast<int>(227 * 1024 * static_cast<int64_t>(plan.tmem_cols) / 512);
-  if (plan.smem_bytes < share) plan.smem_bytes = share;
+  for (int i = 0; i < n; ++i) {
+    const Task& t = tasks[i];
+    RowsTile& tile = plan.tile[i];
+    const int weights = t.form == kGated ? 2 : 1;
+    const int x_bytes = t.A.k_major ? tile.tm * kBK * 2 : (tile.tm + 63) / 64 * kBoxBytes;
+    tile.stage_bytes = static_cast<uint32_t>(weights * kWeightBytes + x_bytes);
+    tile.tmem_cols = 32;
+    while (tile.tmem_cols < static_cast<uint32_t>(weights * tile.tm)) tile.tmem_cols *= 2;
+    // Half of an SM's memory where that holds six slots (then the next call's CTAs can be set up beside
+    // these: linear 8x8192x4096 13.1 us against 14.0 with all of it) or more CTAs are to come; otherwise
+    // a ring over all of it (64x4096x4096: 8.7 against 9.0, 128x4096x4096 10.2 against 11.6).
+    const int half = 112 * 1024, whole = 200 * 1024, stage = static_cast<int>(tile.stage_bytes);
+    const int budget = !one_wave || 6 * stage <= half ? half : whole;
+    // The partial sums lie over the ring, so it holds at least those.
+    const int partials = weights * tile.tm * kTileN * 4;
+    const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
+    const int64_t per_cta = (blocks + plan.splits - 1) / plan.splits;
+    int stages = budget / stage;
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages > per_cta) stages = static_cast<int>(per_cta);
+    const int least = (partials + stage - 1) / stage;
+    if (stages < least) stages = least;
+    tile.stages = stages;
+    const int smem = stages * stage + 1024 + 512;
+    if (plan.smem_bytes < smem) plan.smem_bytes = smem;
+    // CTAs that share an SM must find TMEM for all of them, or clusters could wait for each other's:
+    // shared memory in the proportion of TMEM (and never so little that a CTA fits beside a kernel
+    // that fills the rest) keeps the sum of their columns at most 512.
+    const int share = static_cast<int>(227 * 1024 * static_cast<int64_t>(tile.tmem_cols) / 512);
+    if (plan.smem_bytes < share) plan.smem_bytes = share;
+  }
   if (plan.smem_bytes < 48 * 1024) plan.smem_bytes = 48 * 1024;
   return plan;
 }
 
-cudaError_t run_rows(const Context& c, const Task& t, const RowsPlan& plan) {
-  const bool gated = t.form == kGated;
-  if (c.kind == kBf16) return gated ? launch<kBf16, true>(c, t, plan) : launch<kBf16, false>(c, t, plan);
-  return gated ? launch<kF16, true>(c, t, plan) : launch<kF16, false>(c, t, plan);
+cudaError_t run_rows(const Context& c, const Task* tasks, const RowsPlan& plan, int n) {
+  if (n == 0) return cudaSuccess;
+  const bool gated = tasks[0].form == kGated;
+  if (c.kind == kBf16)
+    return gated ? launch<kBf16, true>(c, tasks, plan, n) : launch<kBf16, false>(c, tasks, plan, n);
+  return gated ? launch<kF16, true>(c, tasks, plan, n) : launch<kF16, false>(c, tasks, plan, n);
 }
 
 }  // namespace ff
