@@ -479,6 +479,7 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
   p->N = static_cast<int>(t.N);
   p->mma_n = mma_n;
   p->bn = gated ? mma_n / 2 : mma_n;
+  if (p->bn % kUnit != 0) return cudaErrorInvalidValue;
   p->tiles_m = static_cast<int>((t.M + 2 * kRows - 1) / (2 * kRows));
   p->tiles_n = static_cast<int>((t.N + p->bn - 1) / p->bn);
   const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
@@ -557,6 +558,7 @@ int pair_width(const Task& t, int pairs, double* cost) {
   *cost = 0.0;
   for (const auto& w : kWidths) {
     const int bn = gated ? w.n / 2 : w.n;
+    if (bn % kUnit != 0) continue;  // the epilogue takes whole groups of columns
     const int64_t tiles = tiles_m * ((t.N + bn - 1) / bn);
     const double rounds = static_cast<double>((tiles + pairs - 1) / pairs);
     const double work = static_cast<double>(tiles) * blocks;

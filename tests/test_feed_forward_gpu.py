@@ -169,6 +169,31 @@ def test_gated(m, k, n):
         mk.check_canaries()
 
 
+# Sizes that just fill the GPU with tiles of one width each (256, 224, 192, 128 and 64 sums a row), and
+# widths that do not divide the outputs.
+WIDTHS = [(2000, 1024, 2304), (2000, 1024, 2016), (2000, 1024, 1728), (2000, 1024, 1152), (2000, 512, 576),
+          (3102, 1600, 448), (3102, 1600, 864), (2500, 1600, 288), (1800, 700, 1000), (4000, 320, 1504)]
+
+
+@pytest.mark.parametrize("m,k,n", WIDTHS)
+@pytest.mark.parametrize("wt", [False, True])
+def test_tile_widths(m, k, n, wt):
+    mk = Maker(21, BF16)
+    x, w, wu, bias = mk.normal(m, k), mk.weight(k, n, wt), mk.weight(k, n, wt), mk.vector(n)
+    out, g, u = mk.empty(m, n), mk.empty(m, n), mk.empty(m, n)
+    y, bar, z, zbar = linear_want(x, w, bias, None, "silu", BF16)
+    t2s.linear(x, w, bias, act="silu", out=out, preact=g)
+    within(out, y, bar, "y")
+    within(g, z, zbar, "z")
+    h, bar, gates = gated_want(x, w, wu, "silu", BF16)
+    t2s.gated_linear(x, w, wu, out=out, preact=(g, u))
+    within(out, h, bar, "h")
+    within(g, *gates[0], "g")
+    within(u, *gates[1], "u")
+    assert binding.device_status() == binding.T2S_OK
+    mk.check_canaries()
+
+
 def product_bar(da, a, b, dtype):
     """Bar of a @ b where a (float64) is off by da and enters the product rounded."""
     u, t = U[dtype], TINY[dtype]
@@ -530,3 +555,32 @@ def test_many_rows():
     dx, _, _ = t2s.linear_backward(x[:, :n], x, w, dw=False)
     zero = torch.zeros(m, n, dtype=torch.float64, device="cuda")
     within(dx, *product_bar(zero, x[:, :n].double(), w.double().t(), BF16), "dx")
+
+
+def test_calls_on_several_streams_at_once():
+    """Products of both kernels, gradients and the plain BF16 product side by side on four streams."""
+    mk = Maker(17, BF16)
+    a = [mk.normal(24, 2048), mk.normal(2048, 1536), mk.normal(2048, 1536), mk.normal(24, 1536)]
+    b = [mk.normal(1200, 512), mk.normal(512, 2048), mk.normal(512, 2048), mk.normal(1200, 2048)]
+    c = [mk.normal(640, 768), mk.normal(768, 640)]
+
+    def gradients(x, w, w2, dh):
+        return [*t2s.linear_backward(dh, x, w, dh, act="gelu", db=None),
+                *t2s.gated_linear_backward(dh, x, w, w2, (dh, dh))]
+
+    jobs = [lambda: [t2s.linear(a[0], a[1], act="silu"), t2s.gated_linear(*a[:3])],
+            lambda: [t2s.linear(b[0], b[1], residual=b[3]), t2s.gated_linear(*b[:3])],
+            lambda: gradients(*a) + gradients(*b), lambda: [t2s.gemm_bf16(*c)]]
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(10):
+        for i, (job, stream) in enumerate(zip(jobs, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(job())
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.T2S_OK
+    for results, expected in zip(got, want):
+        for result in results:
+            assert all(torch.equal(r, e) for r, e in zip(result, expected))
