@@ -38,27 +38,32 @@ cudaError_t run_products(const Context& c, const Task* tasks, int n) {
   // All by one kernel, in one launch, or each by the one that is quicker for it alone.
   constexpr double kStart = 4.0, kLaunch = 2.0;  // of a lone launch; of one more
   Task by_rows[kMaxProblems], by_pair[kMaxProblems];
-  int widths[kMaxProblems], own_widths[kMaxProblems], rows = 0, pairs = 0;
-  double all_pair = kStart, mixed = 0.0;
-  for (int i = 0; i < n; ++i) {
-    double cost = 0.0;
-    widths[i] = pair_width(tasks[i], sms / 2, &cost);
-    all_pair += cost - kStart;
-    const double alone = plan_rows(&tasks[i], 1, sms).cost;
-    mixed += (alone < cost ? alone : cost) - kStart;
-    if (alone < cost) {
-      by_rows[rows++] = tasks[i];
-    } else {
-      own_widths[pairs] = widths[i];
-      by_pair[pairs++] = tasks[i];
+  int rows = 0, pairs = 0;
+  if (n > 1) {
+    for (int i = 0; i < n; ++i) {
+      double cost = 0.0;
+      pair_width(&tasks[i], 1, sms / 2, &cost);
+      if (plan_rows(&tasks[i], 1, sms).cost < cost) {
+        by_rows[rows++] = tasks[i];
+      } else {
+        by_pair[pairs++] = tasks[i];
+      }
     }
   }
-  mixed += kStart + (rows > 0 && pairs > 0 ? kLaunch : 0.0);
+  double all_pair = 0.0;
+  const int width = pair_width(tasks, n, sms / 2, &all_pair);
   const RowsPlan plan = plan_rows(tasks, n, sms);
-  if (plan.cost < all_pair && plan.cost < mixed) return run_rows(c, tasks, plan, n);
-  if (all_pair <= mixed) return run_pair(c, tasks, widths, n);
-  if (rows > 0 && (e = run_rows(c, by_rows, plan_rows(by_rows, rows, sms), rows)) != cudaSuccess) return e;
-  return run_pair(c, by_pair, own_widths, pairs);
+  if (rows > 0 && pairs > 0) {
+    double some_pair = 0.0;
+    const int some_width = pair_width(by_pair, pairs, sms / 2, &some_pair);
+    const RowsPlan some_rows = plan_rows(by_rows, rows, sms);
+    const double mixed = some_pair + some_rows.cost - kStart + kLaunch;
+    if (mixed < all_pair && mixed < plan.cost) {
+      if ((e = run_rows(c, by_rows, some_rows, rows)) != cudaSuccess) return e;
+      return run_pair(c, by_pair, some_width, pairs);
+    }
+  }
+  return plan.cost < all_pair ? run_rows(c, tasks, plan, n) : run_pair(c, tasks, width, n);
 }
 
 }  // namespace ff

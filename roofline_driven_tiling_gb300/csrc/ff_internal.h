@@ -55,12 +55,12 @@ inline bool aligned16(const void* p, int64_t ld) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2)) & 15u) == 0;
 }
 
-// Sums per row of a tile that ff_pair.cu takes for a product on `pairs` pairs of SMs, and its
-// expected time in microseconds.
-int pair_width(const Task& t, int pairs, double* cost);
+// Sums per row of the tiles that ff_pair.cu takes for up to three products in one launch on `pairs`
+// pairs of SMs, and the expected time in microseconds.
+int pair_width(const Task* tasks, int n, int pairs, double* cost);
 // Up to three products in one launch, all of the gated form or none. Operands must be readable
 // in place (aligned16), and rows of a single-row operand given a stride that is.
-cudaError_t run_pair(const Context& c, const Task* tasks, const int* widths, int n);
+cudaError_t run_pair(const Context& c, const Task* tasks, int width, int n);
 
 // How ff_rows.cu takes up to three products in one launch: CTAs along K, and for each product the
 // rows of X per tile and the ring slots. `cost` is the expected time in microseconds.

@@ -520,7 +520,7 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
 }
 
 template <int KIND, bool GATED>
-cudaError_t launch(const Context& c, const Task* tasks, const int* widths, int n) {
+cudaError_t launch(const Context& c, const Task* tasks, int width, int n) {
   int resident = 0;
   cudaError_t e = resident_clusters<KIND, GATED>(&resident);
   if (e != cudaSuccess) return e;
@@ -531,7 +531,7 @@ cudaError_t launch(const Context& c, const Task* tasks, const int* widths, int n
   for (int i = 0; i < kMaxProblems; ++i) {
     params.first[i] = static_cast<int>(tiles);
     if (i < n) {
-      if ((e = fill<KIND>(&params.p[i], tasks[i], widths[i])) != cudaSuccess) return e;
+      if ((e = fill<KIND>(&params.p[i], tasks[i], width)) != cudaSuccess) return e;
       tiles += static_cast<int64_t>(params.p[i].tiles_m) * params.p[i].tiles_n;
       if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
     }
@@ -544,26 +544,43 @@ cudaError_t launch(const Context& c, const Task* tasks, const int* widths, int n
 }  // namespace
 
 // Fitted to 17 products of 256 to 4096 rows (most within 10 %): a K block takes a pair of SMs 0.155 us
-// or the time of its MMAs and copies, whichever is longer; all SMs together compute 1.8 PFLOP/s
-// (the power limit) and take in 16 TB/s; starting up, and a last tile's epilogue, take the rest.
-int pair_width(const Task& t, int pairs, double* cost) {
+// or the time of its MMAs and copies, whichever is longer, and a tile that others follow 0.3 us more;
+// all SMs together compute 1.8 PFLOP/s (the power limit) and take in 16 TB/s; starting up, and a last
+// tile's epilogue, take the rest.
+int pair_width(const Task* tasks, int n, int pairs, double* cost) {
   static const struct {
     int n;
     double block;
   } kWidths[] = {{64, 0.155}, {128, 0.158}, {192, 0.185}, {224, 0.22}, {256, 0.255}};
-  const bool gated = t.form == kGated;
-  const double blocks = static_cast<double>((t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1));
-  const int64_t tiles_m = (t.M + 2 * kRows - 1) / (2 * kRows);
   int best = kMaxN;
   *cost = 0.0;
   for (const auto& w : kWidths) {
-    const int bn = gated ? w.n / 2 : w.n;
-    if (bn % kUnit != 0) continue;  // the epilogue takes whole groups of columns
-    const int64_t tiles = tiles_m * ((t.N + bn - 1) / bn);
-    const double rounds = static_cast<double>((tiles + pairs - 1) / pairs);
-    const double work = static_cast<double>(tiles) * blocks;
-    double time = rounds * blocks * w.block;
-    const double flops = work * 2.0 * 2 * kRows * w.n * kBK, bytes = work * (2 * kABytes + w.n * kBK * 2);
+    int64_t first[kMaxProblems + 1] = {};
+    double tile_time[kMaxProblems] = {}, flops = 0.0, bytes = 0.0;
+    bool whole = true;
+    for (int i = 0; i < n; ++i) {
+      const Task& t = tasks[i];
+      const int bn = t.form == kGated ? w.n / 2 : w.n;
+      if (bn % kUnit != 0) whole = false;  // the epilogue takes whole groups of columns
+      const double blocks = static_cast<double>((t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1));
+      const int64_t tiles = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + bn - 1) / bn);
+      first[i + 1] = first[i] + tiles;
+      tile_time[i] = blocks * w.block + 0.3;
+      flops += static_cast<double>(tiles) * blocks * 2.0 * 2 * kRows * w.n * kBK;
+      bytes += static_cast<double>(tiles) * blocks * (2 * kABytes + w.n * kBK * 2);
+    }
+    if (!whole) continue;
+    // The longest share: pair j has the tiles j, j + pairs, ... of all products in turn.
+    double time = 0.0;
+    for (int j = 0; j < pairs && j < first[n]; ++j) {
+      double share = -0.3;
+      for (int i = 0; i < n; ++i) {
+        auto before = [&](int64_t end) { return end > j ? (end - j + pairs - 1) / pairs : 0; };
+        share += static_cast<double>(before(first[i + 1]) - before(first[i])) * tile_time[i];
+      }
+      if (time < share) time = share;
+      if (n == 1) break;  // the first pair's share is the longest
+    }
     if (time < flops / 1.8e9) time = flops / 1.8e9;
     if (time < bytes / 16e6) time = bytes / 16e6;
     time += 4.1 + 0.006 * w.n;
@@ -575,12 +592,12 @@ int pair_width(const Task& t, int pairs, double* cost) {
   return best;
 }
 
-cudaError_t run_pair(const Context& c, const Task* tasks, const int* widths, int n) {
+cudaError_t run_pair(const Context& c, const Task* tasks, int width, int n) {
   if (n == 0) return cudaSuccess;
   const bool gated = tasks[0].form == kGated;
   if (c.kind == kBf16)
-    return gated ? launch<kBf16, true>(c, tasks, widths, n) : launch<kBf16, false>(c, tasks, widths, n);
-  return gated ? launch<kF16, true>(c, tasks, widths, n) : launch<kF16, false>(c, tasks, widths, n);
+    return gated ? launch<kBf16, true>(c, tasks, width, n) : launch<kBf16, false>(c, tasks, width, n);
+  return gated ? launch<kF16, true>(c, tasks, width, n) : launch<kF16, false>(c, tasks, width, n);
 }
 
 }  // namespace ff

@@ -403,6 +403,7 @@ int reach_of(int splits, int sms) { return splits <= 2 ? sms : splits == 4 ? sms
 }  // namespace
 
 RowsPlan plan_rows(const Task* tasks, int n, int sms) {
+  constexpr double kNextCta = 1.5;
   RowsPlan plan;
   plan.cost = 0.0;
   bool one_wave = false;
@@ -430,9 +431,8 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
         if (candidate == tm[i]) continue;
         const Cost c = cost_of(t, candidate, splits);
         // Alone a product's waves count; among others, the SMs' time it takes.
-        const double waves = n == 1 ? static_cast<double>((c.ctas + reach - 1) / reach)
-                                    : 0.5 + static_cast<double>(c.ctas) / reach;
-        double time = waves * c.per_cta;
+        double time = n == 1 ? c.per_cta + static_cast<double>((c.ctas - 1) / reach) * (c.per_cta + kNextCta)
+                             : (0.5 + static_cast<double>(c.ctas) / reach) * c.per_cta;
         if (time < c.feed) time = c.feed;
         if (best == 0.0 || time < best) {
           best = time;
@@ -447,8 +447,9 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
     }
     if (longest < 0.0) break;
     if (splits > 1 && ctas > 2 * reach) break;
-    double time = n == 1 ? static_cast<double>((ctas + reach - 1) / reach) * longest : work / reach * 1.1;
-    if (time < longest) time = longest;
+    // CTAs beyond the first on each SM: as long as the average, and their own start.
+    const double average = work / static_cast<double>(ctas);
+    double time = longest + static_cast<double>((ctas - 1) / reach) * (average + kNextCta);
     if (time < feed) time = feed;
     // What every launch takes, and a cluster's two barriers.
     time += 4.0 + (splits > 1 ? 0.6 : 0.0);
