@@ -175,10 +175,8 @@ __device__ __forceinline__ void put_row(uint32_t box, int lane, const uint64_t (
   }
 }
 
-// The accumulator's 32 columns from `taddr` on, one row per lane.
-__device__ __forceinline__ void load_sums(uint32_t taddr, bool any, uint64_t (&s)[kUnit / 2]) {
-  uint32_t r[kUnit];
-  tc::tmem_ld32(taddr, r);
+// Loaded accumulator columns as sums; of no K block, zeros.
+__device__ __forceinline__ void sums_of(const uint32_t (&r)[kUnit], bool any, uint64_t (&s)[kUnit / 2]) {
 #pragma unroll
   for (int i = 0; i < kUnit / 2; ++i)
     s[i] = any ? pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0ull;
@@ -342,15 +340,25 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       tc::tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b) * kMaxN;
       const bool any = p.nkb > 0;
-      // The two warps of a row quarter take every other group of 32 columns.
-      for (int c = half * kUnit; c < p.bn; c += 2 * kUnit) {
+      // The two warps of a row quarter take every other group of 32 columns inside the matrix; a
+      // group's sums are on their way from TMEM while the one before it is stored.
+      const int columns = m < p.M ? min(p.bn, p.N - n0) : 0;
+      uint32_t sums[kUnit], gated_sums[GATED ? kUnit : 1];
+      auto load = [&](int c) {
+        load_columns(acc + static_cast<uint32_t>(c), sums);
+        if constexpr (GATED) load_columns(acc + static_cast<uint32_t>(p.bn + c), gated_sums);
+      };
+      if (half * kUnit < columns) load(half * kUnit);
+      for (int c = half * kUnit; c < columns; c += 2 * kUnit) {
         const int n = n0 + c;
-        if (n >= p.N || m >= p.M) continue;  // the same for the whole warp
+        const bool more = c + 2 * kUnit < columns;
         uint64_t v[kUnit / 2];
-        load_sums(acc + static_cast<uint32_t>(c), any, v);
+        wait_columns(sums);
+        sums_of(sums, any, v);
         if constexpr (GATED) {
           uint64_t u[kUnit / 2];
-          load_sums(acc + static_cast<uint32_t>(p.bn + c), any, u);
+          wait_columns(gated_sums);
+          sums_of(gated_sums, any, u);
           if (p.Z != nullptr) {
             const uint32_t box = boxes.next();
             put_row<KIND>(box, lane, v);
@@ -367,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           });
           const uint32_t box = boxes.next();
           put_row<KIND>(box, lane, v);
+          if (more) load(c + 2 * kUnit);
           store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
         } else {
           if (p.bias != nullptr) {
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           const uint32_t box = boxes.next();
           if (p.R != nullptr) {
             residual.place(p, box, m, n, lane);
-            if (c + 2 * kUnit < p.bn) residual.fetch(p, m, n + 2 * kUnit, lane);
+            if (more) residual.fetch(p, m, n + 2 * kUnit, lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t r[4];
@@ -408,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
             }
           }
           put_row<KIND>(box, lane, v);
+          if (more) load(c + 2 * kUnit);
           store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
         }
       }
