@@ -355,7 +355,8 @@ int t2s_vector_add_f32(int64_t n, const float *x, const float *y, float *z,
  *   T2S_ACT_GELU z (1 + erf(z / sqrt 2)) / 2,
  *   T2S_ACT_GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  * Sums, activations and db are FP32 (the sums' order is the library's, the same in every call
- * of the same sizes and alignment); every output is rounded to 16 bits once. dZ, dG and dU are
+ * of the same sizes and alignment; the tensor cores truncate their additions, at most 2^-23 of
+ * the sum of magnitudes for every 16 terms); every output is rounded to 16 bits once. dZ, dG and dU are
  * rounded to 16 bits where they enter the products of a gradient.
  *
  * Layout: each matrix has its own row stride (ld, in elements, at least its row length and at
@@ -375,9 +376,11 @@ int t2s_vector_add_f32(int64_t n, const float *x, const float *y, float *z,
  *
  * workspace: a DEVICE buffer, 256-byte aligned, owned by the caller and untouched until the
  * stream has run the call, of t2s_<operator>_workspace_size(M, N, K, aligned) bytes; `aligned`
- * nonzero says that X and the weights (in linear_backward also dY) are read in place. It may be NULL where that is
- * 0. Too small a workspace for the call: T2S_ERR_WORKSPACE. Otherwise the common contract and
- * return codes at the top apply (asynchronous on `stream`, no allocation).
+ * nonzero says that X and the weights (in linear_backward also dY) are read in place. It may be
+ * NULL where that is 0. Too small a workspace for the call: T2S_ERR_WORKSPACE. Otherwise the
+ * common contract and return codes at the top apply (asynchronous on `stream`, no allocation).
+ * The kernels may start up while the one before them on the stream still runs (programmatic
+ * stream serialisation); they touch memory only once it has completed.
  */
 #define T2S_ACT_NONE 0
 #define T2S_ACT_RELU 1

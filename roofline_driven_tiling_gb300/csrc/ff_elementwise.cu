@@ -7,7 +7,8 @@
 // dZ, dG and dU are rounded to the 16-bit type: they are the tensor-core operands of the weight
 // and input gradients. db sums the FP32 values before that rounding, in an order that depends on
 // the sizes alone. Bound by memory: every value is read or written once, 16 bytes per access
-// where rows allow it.
+// where rows allow it (4096^2: db alone with relu 7.6 us, with gelu 16.6, floor 9.9 from HBM; dG and dU about
+// 26 us, floor 24.7).
 //
 // Inputs are read with plain loads (no __restrict__): these kernels may start before the one that
 // writes them has ended (wait_for_earlier_kernels), which read-only loads do not allow for.

@@ -22,7 +22,7 @@
 // Six ring slots of 32 KB leave 35 KB for the epilogue's boxes; five cost 1.5 % at 4096^3.
 //
 // The tensor core adds in FP32 but truncates (relative to the sum of magnitudes at most 2^-23 per 16
-// values of K): below half a unit of 16 bits up to K of 65536, so one accumulator takes all of K.
+// values of K): at most half a unit of binary16 at K = 65536, so one accumulator takes all of K.
 //
 // The gated product needs no wider machinery: rank 0 stages 128 columns of Wg and rank 1 the same
 // 128 columns of Wu, so the lower half of the accumulator's columns holds G, the upper half U.

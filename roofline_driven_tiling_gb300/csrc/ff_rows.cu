@@ -6,7 +6,13 @@
 // split over the CTAs of a cluster (up to 8): each accumulates its K blocks in TMEM, leaves the
 // partial sums in its shared memory, and after a cluster barrier every CTA adds the partial sums of
 // its share of the rows, in rank order through distributed shared memory, applies the epilogue and
-// stores. One launch, no workspace, the same bits every time.
+// stores. One launch (for up to three products of a gradient), no workspace, the same bits every
+// time.
+//
+// What bounds it: one pass over the weight through HBM and what a launch takes around it, about 4 us
+// (start-up, the ring's first block, two cluster barriers, the join). 1 x 4096 x 4096 6.2 us (5.4 TB/s),
+// 8 x 8192 x 4096 13.1 (5.1), gated 1 x 4096 x 8192 22.3 (6.0 of the 6.8 TB/s a copy reaches), 64 x 4096
+// x 4096 8.1, 256 x 4096 x 4096 13.1. Without the split over K, on 32 SMs, 1 x 4096 x 4096 takes 14.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
