@@ -19,6 +19,8 @@ itself. Outputs and workspaces that are not passed are allocated by torch. The w
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding
@@ -39,7 +41,13 @@ def _function(name: str, dtype):
     """The C entry point of an operator for a type."""
     f = _FUNCTIONS.get((name, dtype))
     if f is None:
-        f = _FUNCTIONS[name, dtype] = getattr(binding.lib(), name + _SUFFIX[dtype])
+        full = name + _SUFFIX[dtype]
+        f = binding.lib()[full]
+        # Every argument is an integer in a register or stack slot of 64 bits, and ctypes converts
+        # a c_void_p in two thirds of a c_int64's time.
+        f.argtypes = [ctypes.c_void_p] * len(binding.SIGNATURES[full][0])
+        f.restype = ctypes.c_int
+        _FUNCTIONS[name, dtype] = f
     return f
 
 
