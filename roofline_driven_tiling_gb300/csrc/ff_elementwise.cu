@@ -36,10 +36,20 @@ struct Source {
   int wide;  // rows on 16-byte boundaries
 };
 
-// Eight values of a row from column c on as four words, zeros beyond `cols`.
+// Eight values of a row from column c on as four words, zeros beyond `cols`. Rows that start on odd
+// places are read as words with the two ends by themselves, so that nothing outside the row is read.
 __device__ __forceinline__ uint4 load8(const Source& s, int64_t r, int64_t c, int64_t cols) {
   const uint16_t* p = s.p + r * s.ld + c;
-  if (s.wide && c + kVec <= cols) return *reinterpret_cast<const uint4*>(p);
+  if (c + kVec <= cols) {
+    if (s.wide) return *reinterpret_cast<const uint4*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 2u) == 0) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p + 1);
+    const uint32_t a = p[0], b = w[0], d = w[1], e = w[2], f = p[7];
+    return make_uint4(a | b << 16, b >> 16 | d << 16, d >> 16 | e << 16, e >> 16 | f << 16);
+  }
   uint32_t v[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) v[i] = c + i < cols ? p[i] : 0u;
@@ -157,6 +167,12 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
+// i / d of a count of words; a 32-bit division is a fraction of a 64-bit one (copies of 1000x1999 and
+// 1999x2001 19.8 -> 17.3 us with the product).
+__device__ __forceinline__ int64_t quotient(int64_t i, int64_t d) {
+  return (i | d) >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(d)) : i / d;
+}
+
 // One thread per eight values.
 template <int KIND, int ACT>
 __global__ void __launch_bounds__(kThreads)
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t per_row = ldd / kVec, total = M * per_row;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t m = i / per_row, c = (i - m * per_row) * kVec;
+    const int64_t m = quotient(i, per_row), c = (i - m * per_row) * kVec;
     const uint4 wd = load8(dh, m, c, N), wg = load8(g, m, c, N), wu = load8(u, m, c, N);
     uint64_t d[kPairs], x[kPairs], y[kPairs];
     widen<KIND>(wd, d);
@@ -199,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
   const int64_t step = static_cast<int64_t>(jobs.first[j + 1] - jobs.first[j]) * kThreads;
   const Source s{c.src, c.ld, 0};
   for (int64_t i = static_cast<int64_t>(blockIdx.x - jobs.first[j]) * kThreads + threadIdx.x; i < total; i += step) {
-    const int64_t r = i / per_row, col = (i - r * per_row) * kVec;
+    const int64_t r = quotient(i, per_row), col = (i - r * per_row) * kVec;
     *reinterpret_cast<uint4*>(c.dst + r * ldd + col) = load8(s, r, col, c.cols);
   }
 }

@@ -128,11 +128,23 @@ __device__ __forceinline__ void store_unit(const CUtensorMap* map, bool tma, uin
     return;
   }
   __syncwarp();
-  const int rows = min(32, M - m);
-  for (int r = 0; r < rows; ++r) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + unit_chunk(r, lane >> 3) + (lane & 7) * 2));
-    if (n + lane < N) p[static_cast<int64_t>(m + r) * ld + n + lane] = v;
+  // Eight rows at a time; the swizzle of row 8 g + j is that of row j.
+  uint32_t from[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) from[i] = box + (static_cast<uint32_t>((lane >> 3) ^ i) << 4) + (lane & 7) * 2;
+  uint16_t* out = p + static_cast<int64_t>(m) * ld + n + lane;
+  const int rows = n + lane < N ? M - m : 0;
+#pragma unroll 1
+  for (int r = 0; r < 32; r += 8) {
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[j]) : "r"(from[j >> 1] + static_cast<uint32_t>(r + j) * 64u));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (r + j < rows) *out = v[j];
+      out += ld;
+    }
   }
   __syncwarp();
   // The TMA-store count that next() waits by: an empty group stands for this box.
