@@ -196,7 +196,8 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   const bool products = dX != nullptr || dW != nullptr;
   const bool plane = products && (act != T2S_ACT_NONE || !in_place(dY, M, lddy));
   const int64_t ldd = up8(N);
-  const size_t need = (plane ? plane_bytes(M, N) : 0) + (dW != nullptr ? copy_bytes(X, M, K, ldx) : 0) +
+  const size_t sums = db != nullptr ? up256(db_partial_bytes(M, N)) : 0;
+  const size_t need = (plane ? plane_bytes(M, N) : 0) + sums + (dW != nullptr ? copy_bytes(X, M, K, ldx) : 0) +
                       (dX != nullptr ? weight_copy_bytes(W, K, N, ldw, w_order) : 0);
   const int rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != T2S_OK) return rc;
@@ -208,7 +209,8 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   Operand d{dY, M <= 1 ? ldd : lddy, true};
   if (M > 0 && N > 0 && (plane || db != nullptr)) {
     uint16_t* dz = plane ? static_cast<uint16_t*>(ws.take(plane_bytes(M, N))) : nullptr;
-    e = run_act_backward(c, M, N, act, dY, lddy, Z, ldz, dz, ldd, db);
+    float* partials = sums > 0 ? static_cast<float*>(ws.take(sums)) : nullptr;
+    e = run_act_backward(c, M, N, act, dY, lddy, Z, ldz, dz, ldd, db, partials);
     if (e != cudaSuccess) return done(e);
     if (plane) d = {dz, ldd, true};
   } else if (M == 0 && N > 0 && db != nullptr) {
@@ -348,7 +350,7 @@ size_t t2s_linear_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
 
 size_t t2s_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
   if (bad_sizes(M, N, K)) return 0;
-  return plane_bytes(M, N) + (aligned ? 0 : copies_bytes(M, N, K, 1));
+  return plane_bytes(M, N) + up256(db_partial_bytes(M, N)) + (aligned ? 0 : copies_bytes(M, N, K, 1));
 }
 
 size_t t2s_gated_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {

@@ -7,7 +7,7 @@
 // dZ, dG and dU are rounded to the 16-bit type: they are the tensor-core operands of the weight
 // and input gradients. db sums the FP32 values before that rounding, in an order that depends on
 // the sizes alone. Bound by memory: every value is read or written once, 16 bytes per access
-// where rows allow it (4096^2: db alone with relu 7.6 us, with gelu 16.6, floor 9.9 from HBM; dG and dU about
+// where rows allow it (4096^2: db alone with relu 10.1 us, with gelu 15.8, floor 9.9 from HBM; dG and dU about
 // 26 us, floor 24.7).
 //
 // Inputs are read with plain loads (no __restrict__): these kernels may start before the one that
@@ -80,13 +80,13 @@ __device__ __forceinline__ uint4 narrow(const uint64_t (&v)[kPairs]) {
 }
 
 // kGroups threads along a row. Block (x, y): 8 kGroups columns y, y + gridDim.y, ..., the rows of
-// chunk x, 256 / kGroups at a time; dZ's rows are
-// 16-byte aligned and padded to whole words. With db the chunks are a cluster's CTAs: each leaves its
-// column sums in its shared memory, and the first adds them in rank order.
+// chunk x, 256 / kGroups at a time; dZ's rows are 16-byte aligned and padded to whole words. With db the
+// chunks are a cluster's CTAs: each leaves its column sums in its shared memory, and the first adds them in
+// rank order. With partials each block leaves its column sums there, a row per chunk, for db_sum_kernel.
 template <int KIND, int ACT, int kGroups>
 __global__ void __launch_bounds__(kThreads, 4)
     act_backward_kernel(int64_t M, int64_t N, int64_t chunk, Source dy, Source z, uint16_t* dZ, int64_t lddz,
-                        uint16_t* db) {
+                        uint16_t* db, float* partials) {
   constexpr int kColumns = kGroups * kVec, kLanes = kThreads / kGroups;
   __shared__ float sums[kLanes][kColumns + 1];
   __shared__ float column[kColumns];
@@ -107,11 +107,15 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int i = 0; i < kPairs; ++i) {
           uint64_t value, slope;
           act_pair_slope<ACT>(x[i], value, slope);
+          // The sum takes the unrounded product, whether dZ is stored too or not: left to the compiler,
+          // the two could differ in db's last bit.
+          sum[i] = fma2(d[i], slope, sum[i]);
           d[i] = mul2(d[i], slope);
         }
-      }
+      } else {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) sum[i] = add2(sum[i], d[i]);
+        for (int i = 0; i < kPairs; ++i) sum[i] = add2(sum[i], d[i]);
+      }
       if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + m * lddz + c) = narrow<KIND>(d);
     };
     int64_t m = blockIdx.x * chunk + row;
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (c < N)
       for (; m < m1; m += kLanes)
         take(m, load8(dy, m, c, N), ACT != T2S_ACT_NONE ? load8(z, m, c, N) : make_uint4(0, 0, 0, 0));
-    if (db == nullptr) continue;
+    if (db == nullptr && partials == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
       const float2 f = halves(sum[i]);
@@ -146,6 +150,11 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
       for (int r = 0; r < kLanes; ++r) total += sums[r][threadIdx.x];
       column[threadIdx.x] = total;
+      if (partials != nullptr && c0 + threadIdx.x < N) partials[blockIdx.x * N + c0 + threadIdx.x] = total;
+    }
+    if (partials != nullptr) {
+      __syncthreads();
+      continue;
     }
     cluster_sync_all();
     if (cluster_ctarank() == 0 && threadIdx.x < kColumns && c0 + threadIdx.x < N) {
@@ -165,6 +174,27 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     cluster_sync_all();
   }
+}
+
+// 32 columns per block, the partial sums' rows over its eight warps.
+template <int KIND>
+__global__ void __launch_bounds__(kThreads) db_sum_kernel(int64_t rows, int64_t N, const float* partials, uint16_t* db) {
+  wait_for_earlier_kernels();
+  __shared__ float sums[kThreads / 32][32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float sum = 0.0f;
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t r = warp; r < rows; r += kThreads / 32) sum += partials[r * N + n];
+  }
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || n >= N) return;
+  float total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += sums[w][lane];
+  db[n] = from_f32<KIND>(total);
 }
 
 // i / d of a count of words; a 32-bit division is a fraction of a 64-bit one (copies of 1000x1999 and
@@ -252,27 +282,57 @@ cudaError_t run_copies(const Context& c, const Copy* copies, int n) {
   return launch_early(c.stream, {dim3(blocks), kThreads, 1, 0}, copy_kernel, jobs);
 }
 
+namespace {
+
+// Rows in pieces of 128 bytes where there are blocks enough for the SMs, of 64 bytes otherwise (db of
+// 4096^2 with relu 9.1 us against 11.1; of 1000^2 with gelu 6.4 against 4.3).
+int groups_of(int64_t N) { return N >= 2048 ? 8 : 4; }
+
+int64_t column_blocks(int64_t N) { return (N + groups_of(N) * kVec - 1) / (groups_of(N) * kVec); }
+
+// Chunks of rows that fill the SMs several times over.
+int64_t many_chunks(int64_t M, int64_t N) {
+  const int64_t lanes = kThreads / groups_of(N), most = (M + lanes - 1) / lanes;
+  int64_t chunks = 2048 / column_blocks(N);
+  chunks = chunks < 1 ? 1 : chunks;
+  return chunks < most ? chunks : most;
+}
+
+// db from partial sums and a second launch where a cluster's eight CTAs per column block are too few to
+// keep HBM busy (dZ, db and a 64-wide dX of 16384x1024 54 -> 34 us, of 8192x4096 60 -> 53, of 4096^2 29.3 ->
+// 28.8, of 4096x1024 14.4 -> 14.7).
+bool two_stages(int64_t M, int64_t N) { return M * N >= 1 << 24; }
+
+}  // namespace
+
+size_t db_partial_bytes(int64_t M, int64_t N) {
+  return N > 0 && two_stages(M, N) ? static_cast<size_t>(many_chunks(M, N)) * static_cast<size_t>(N) * 4 : 0;
+}
+
 cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dY,
                              int64_t lddy, const uint16_t* Z, int64_t ldz, uint16_t* dZ,
-                             int64_t lddz, uint16_t* db) {
-  // Rows in pieces of 128 bytes where there are blocks enough for the SMs, of 64 bytes otherwise
-  // (db of 4096^2 with relu 9.1 us against 11.1; of 1000^2 with gelu 6.4 against 4.3).
-  const int groups = N >= 2048 ? 8 : 4;
-  const int64_t columns = groups * kVec, lanes = kThreads / groups;
-  const int64_t blocks = (N + columns - 1) / columns, most = (M + lanes - 1) / lanes;
-  int64_t chunks = db != nullptr ? kMaxChunks : 2048 / blocks;
-  while (db != nullptr && chunks > most) chunks /= 2;
-  chunks = chunks < 1 ? 1 : chunks < most ? chunks : most;
+                             int64_t lddz, uint16_t* db, float* partials) {
+  const bool clustered = db != nullptr && !two_stages(M, N);
+  const int groups = groups_of(N);
+  const int64_t most = (M + kThreads / groups - 1) / (kThreads / groups);
+  int64_t chunks = many_chunks(M, N);
+  if (clustered)
+    for (chunks = kMaxChunks; chunks > most;) chunks /= 2;
   const int64_t chunk = (M + chunks - 1) / chunks;
-  const LaunchShape shape{dim3(static_cast<unsigned>(chunks), capped(blocks, 65535)), kThreads,
-                          db != nullptr ? static_cast<int>(chunks) : 1, 0};
-  return for_act(act, [&](auto a) {
+  const LaunchShape shape{dim3(static_cast<unsigned>(chunks), capped(column_blocks(N), 65535)), kThreads,
+                          clustered ? static_cast<int>(chunks) : 1, 0};
+  float* parts = db != nullptr && !clustered ? partials : nullptr;
+  const cudaError_t e = for_act(act, [&](auto a) {
     constexpr int kAct = decltype(a)::value;
     auto kern = groups == 8
                     ? (c.kind == kBf16 ? act_backward_kernel<kBf16, kAct, 8> : act_backward_kernel<kF16, kAct, 8>)
                     : (c.kind == kBf16 ? act_backward_kernel<kBf16, kAct, 4> : act_backward_kernel<kF16, kAct, 4>);
-    return launch_early(c.stream, shape, kern, M, N, chunk, source(dY, lddy), source(Z, ldz), dZ, lddz, db);
+    return launch_early(c.stream, shape, kern, M, N, chunk, source(dY, lddy), source(Z, ldz), dZ, lddz,
+                        clustered ? db : nullptr, parts);
   });
+  if (e != cudaSuccess || parts == nullptr) return e;
+  return launch_early(c.stream, {dim3(static_cast<unsigned>((N + 31) / 32)), kThreads, 1, 0},
+                      c.kind == kBf16 ? db_sum_kernel<kBf16> : db_sum_kernel<kF16>, chunks, N, parts, db);
 }
 
 cudaError_t run_gated_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dH,

@@ -93,7 +93,9 @@ cudaError_t run_copies(const Context& c, const Copy* copies, int n);
 // nullptr, its column sums.
 cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dY,
                              int64_t lddy, const uint16_t* Z, int64_t ldz, uint16_t* dZ,
-                             int64_t lddz, uint16_t* db);
+                             int64_t lddz, uint16_t* db, float* partials);
+// Bytes of `partials` that db needs for these sizes (0: it may be nullptr).
+size_t db_partial_bytes(int64_t M, int64_t N);
 // dG = dH * U * act'(G), dU = dH * act(G).
 cudaError_t run_gated_backward(const Context& c, int64_t M, int64_t N, int act, const uint16_t* dH,
                                int64_t lddh, const uint16_t* G, int64_t ldg, const uint16_t* U,

@@ -184,9 +184,9 @@ __device__ __forceinline__ void act_pair_slope(uint64_t z, uint64_t& value, uint
       const uint64_t w = kSilu ? mul2(x, both(-kLog2E))
                                : mul2(x, fma2(x2, both(-2.0f * kLog2E * kGeluC * kGeluA), both(-2.0f * kLog2E * kGeluC)));
       const uint64_t s = reciprocal_of(add2(exp2_of(w), one));
-      const uint64_t bell = mul2(x, fma2(mul2(s, both(-1.0f)), s, s));
-      slope = kSilu ? add2(bell, s)
-                    : fma2(bell, fma2(x2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC)), s);
+      const uint64_t bell = fma2(mul2(s, both(-1.0f)), s, s);
+      slope = kSilu ? fma2(x, bell, s)
+                    : fma2(mul2(x, bell), fma2(x2, both(6.0f * kGeluC * kGeluA), both(2.0f * kGeluC)), s);
       value = mul2(z, s);
     }
   }

@@ -545,6 +545,19 @@ def test_refusals():
         t2s.linear_backward(r, x, w, r, act="silu", workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
 
 
+@pytest.mark.parametrize("m,n", [(1 << 14, 1024), ((1 << 14) + 3, 1025), (1 << 21, 8), (6000, 4000)])
+def test_many_column_sums(m, n):
+    """db of more values than a cluster's CTAs share."""
+    mk = Maker(18, F16)
+    dy, z, x, w = mk.normal(m, n), mk.normal(m, n), mk.normal(m, 16), mk.normal(16, n)
+    dx, _, db = t2s.linear_backward(dy, x, w, z, act="silu", dw=False, db=None)
+    d = dy.double() * act64(z.double(), "silu")[1]
+    off = 2.0 ** -17 * (z.double().abs() + 1) * dy.double().abs()
+    within(db, *sum_bar(off, d, F16), "db")
+    within(dx, *product_bar(off, d, w.double().t(), F16), "dx")
+    assert torch.equal(db, t2s.linear_backward(dy, x, w, z, act="silu", dx=False, dw=False, db=None)[2])
+
+
 def test_many_rows():
     """More rows than a grid's second dimension has tiles, one output per row."""
     m, k, n = (1 << 24) + 1000, 8, 1
