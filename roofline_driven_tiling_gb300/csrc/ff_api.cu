@@ -141,6 +141,7 @@ Task weight_gradient(int64_t M, int64_t N, int64_t K, Operand x, Operand d, int 
   t.A = w_order == T2S_W_KN ? x : d;
   t.B = w_order == T2S_W_KN ? d : x;
   t.Y = out;
+  t.split = true;
   return t;
 }
 
@@ -197,7 +198,8 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   const bool plane = products && (act != T2S_ACT_NONE || !in_place(dY, M, lddy));
   const int64_t ldd = up8(N);
   const size_t sums = db != nullptr ? up256(db_partial_bytes(M, N)) : 0;
-  const size_t need = (plane ? plane_bytes(M, N) : 0) + sums + (dW != nullptr ? copy_bytes(X, M, K, ldx) : 0) +
+  const size_t pieces = dW != nullptr ? weight_partial_bytes(M, N, K, 1) : 0;
+  const size_t need = (plane ? plane_bytes(M, N) : 0) + sums + pieces + (dW != nullptr ? copy_bytes(X, M, K, ldx) : 0) +
                       (dX != nullptr ? weight_copy_bytes(W, K, N, ldw, w_order) : 0);
   const int rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != T2S_OK) return rc;
@@ -206,6 +208,7 @@ int linear_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* 
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
   Copies copies{&ws};
+  if (pieces > 0) c.partials = static_cast<float*>(ws.take(c.partial_bytes = pieces));
   Operand d{dY, M <= 1 ? ldd : lddy, true};
   if (M > 0 && N > 0 && (plane || db != nullptr)) {
     uint16_t* dz = plane ? static_cast<uint16_t*>(ws.take(plane_bytes(M, N))) : nullptr;
@@ -288,6 +291,8 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
     return T2S_ERR_INVALID;
   const int64_t ldd = up8(N);
   size_t need = 2 * plane_bytes(M, N);
+  const size_t pieces = dw ? weight_partial_bytes(M, N, K, (dWg != nullptr) + (dWu != nullptr)) : 0;
+  need += pieces;
   if (dw) need += copy_bytes(X, M, K, ldx);
   if (dX != nullptr) need += weight_copy_bytes(Wg, K, N, ldwg, w_order) + weight_copy_bytes(Wu, K, N, ldwu, w_order);
   const int rc = check_workspace(workspace, workspace_bytes, need);
@@ -297,6 +302,7 @@ int gated_backward(Kind kind, int64_t M, int64_t N, int64_t K, const uint16_t* d
   if (e != cudaSuccess) return done(e);
   Workspace ws{static_cast<uint8_t*>(workspace)};
   Copies copies{&ws};
+  if (pieces > 0) c.partials = static_cast<float*>(ws.take(c.partial_bytes = pieces));
   uint16_t *dG = nullptr, *dU = nullptr;
   if (M > 0 && N > 0 && (dw || dX != nullptr)) {
     dG = static_cast<uint16_t*>(ws.take(plane_bytes(M, N)));
@@ -350,7 +356,8 @@ size_t t2s_linear_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
 
 size_t t2s_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
   if (bad_sizes(M, N, K)) return 0;
-  return plane_bytes(M, N) + up256(db_partial_bytes(M, N)) + (aligned ? 0 : copies_bytes(M, N, K, 1));
+  return plane_bytes(M, N) + up256(db_partial_bytes(M, N)) + weight_partial_bytes(M, N, K, 1) +
+         (aligned ? 0 : copies_bytes(M, N, K, 1));
 }
 
 size_t t2s_gated_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
@@ -359,7 +366,9 @@ size_t t2s_gated_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
 
 size_t t2s_gated_backward_workspace_size(int64_t M, int64_t N, int64_t K, int aligned) {
   if (bad_sizes(M, N, K)) return 0;
-  return 2 * plane_bytes(M, N) + (aligned ? 0 : copies_bytes(M, N, K, 2));
+  // The gradient of one weight can be split where those of two cannot.
+  const size_t one = weight_partial_bytes(M, N, K, 1), two = weight_partial_bytes(M, N, K, 2);
+  return 2 * plane_bytes(M, N) + (one > two ? one : two) + (aligned ? 0 : copies_bytes(M, N, K, 2));
 }
 
 int t2s_linear_bf16(int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,

@@ -1,5 +1,5 @@
 // ff_dispatch.cu -- which kernel takes a product of the feed-forward operators: the one whose own
-// estimate of the time (plan_rows, pair_width) is shorter.
+// estimate of the time (plan_rows, plan_pair) is shorter.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -41,29 +41,25 @@ cudaError_t run_products(const Context& c, const Task* tasks, int n) {
   int rows = 0, pairs = 0;
   if (n > 1) {
     for (int i = 0; i < n; ++i) {
-      double cost = 0.0;
-      pair_width(&tasks[i], 1, sms / 2, &cost);
-      if (plan_rows(&tasks[i], 1, sms).cost < cost) {
+      if (plan_rows(&tasks[i], 1, sms).cost < plan_pair(&tasks[i], 1, sms / 2, c.partial_bytes).cost) {
         by_rows[rows++] = tasks[i];
       } else {
         by_pair[pairs++] = tasks[i];
       }
     }
   }
-  double all_pair = 0.0;
-  const int width = pair_width(tasks, n, sms / 2, &all_pair);
-  const RowsPlan plan = plan_rows(tasks, n, sms);
+  const PairPlan all_pair = plan_pair(tasks, n, sms / 2, c.partial_bytes);
+  const RowsPlan all_rows = plan_rows(tasks, n, sms);
   if (rows > 0 && pairs > 0) {
-    double some_pair = 0.0;
-    const int some_width = pair_width(by_pair, pairs, sms / 2, &some_pair);
+    const PairPlan some_pair = plan_pair(by_pair, pairs, sms / 2, c.partial_bytes);
     const RowsPlan some_rows = plan_rows(by_rows, rows, sms);
-    const double mixed = some_pair + some_rows.cost - kStart + kLaunch;
-    if (mixed < all_pair && mixed < plan.cost) {
+    const double mixed = some_pair.cost + some_rows.cost - kStart + kLaunch;
+    if (mixed < all_pair.cost && mixed < all_rows.cost) {
       if ((e = run_rows(c, by_rows, some_rows, rows)) != cudaSuccess) return e;
-      return run_pair(c, by_pair, some_width, pairs);
+      return run_pair(c, by_pair, some_pair, pairs);
     }
   }
-  return plan.cost < all_pair ? run_rows(c, tasks, plan, n) : run_pair(c, tasks, width, n);
+  return all_rows.cost < all_pair.cost ? run_rows(c, tasks, all_rows, n) : run_pair(c, tasks, all_pair, n);
 }
 
 }  // namespace ff

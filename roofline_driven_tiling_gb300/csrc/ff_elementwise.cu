@@ -176,24 +176,26 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
 }
 
-// 32 columns per block, the partial sums' rows over its eight warps.
+// 32 columns per block, the partial sums' rows over its warps (65536x64: 1024 rows, db 17.8 us with
+// eight warps, 10.1 with 32).
+constexpr int kSumWarps = 32;
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) db_sum_kernel(int64_t rows, int64_t N, const float* partials, uint16_t* db) {
+__global__ void __launch_bounds__(32 * kSumWarps) db_sum_kernel(int64_t rows, int64_t N, const float* partials, uint16_t* db) {
   wait_for_earlier_kernels();
-  __shared__ float sums[kThreads / 32][32];
+  __shared__ float sums[kSumWarps][32];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float sum = 0.0f;
   if (n < N) {
-#pragma unroll 4
-    for (int64_t r = warp; r < rows; r += kThreads / 32) sum += partials[r * N + n];
+#pragma unroll 8
+    for (int64_t r = warp; r < rows; r += kSumWarps) sum += partials[r * N + n];
   }
   sums[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || n >= N) return;
   float total = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) total += sums[w][lane];
+  for (int w = 0; w < kSumWarps; ++w) total += sums[w][lane];
   db[n] = from_f32<KIND>(total);
 }
 
@@ -299,9 +301,9 @@ int64_t many_chunks(int64_t M, int64_t N) {
 }
 
 // db from partial sums and a second launch where a cluster's eight CTAs per column block are too few to
-// keep HBM busy (dZ, db and a 64-wide dX of 16384x1024 54 -> 34 us, of 8192x4096 60 -> 53, of 4096^2 29.3 ->
-// 28.8, of 4096x1024 14.4 -> 14.7).
-bool two_stages(int64_t M, int64_t N) { return M * N >= 1 << 24; }
+// keep HBM busy (dZ, db and a 64-wide dX of 16384x1024 54 -> 34 us, 16384x512 31 -> 17, 16384x64 15 -> 10,
+// 8192x1024 19 -> 17; but 8192x512 13.4 -> 14.0, 4096x1024 14.3 -> 14.7, 512x1024 8.1 -> 8.5).
+bool two_stages(int64_t M, int64_t N) { return M >= 16384 || M * N >= 1 << 23; }
 
 }  // namespace
 
@@ -331,7 +333,7 @@ cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, co
                         clustered ? db : nullptr, parts);
   });
   if (e != cudaSuccess || parts == nullptr) return e;
-  return launch_early(c.stream, {dim3(static_cast<unsigned>((N + 31) / 32)), kThreads, 1, 0},
+  return launch_early(c.stream, {dim3(static_cast<unsigned>((N + 31) / 32)), 32 * kSumWarps, 1, 0},
                       c.kind == kBf16 ? db_sum_kernel<kBf16> : db_sum_kernel<kF16>, chunks, N, parts, db);
 }
 

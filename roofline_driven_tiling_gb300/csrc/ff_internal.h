@@ -41,6 +41,7 @@ struct Task {
   const uint16_t* bias = nullptr;
   Matrix R, Y, Z, Z2;
   int act = 0;
+  bool split = false;  // its sum may be cut into pieces that Context::partials takes (no epilogue)
 };
 
 constexpr int kMaxProblems = 3;  // products of one launch
@@ -49,18 +50,26 @@ struct Context {
   Kind kind;
   cudaStream_t stream;
   unsigned* status;
+  float* partials = nullptr;  // for weight gradients over many rows, see weight_partial_bytes
+  size_t partial_bytes = 0;
 };
 
 inline bool aligned16(const void* p, int64_t ld) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2)) & 15u) == 0;
 }
 
-// Sums per row of the tiles that ff_pair.cu takes for up to three products in one launch on `pairs`
-// pairs of SMs, and the expected time in microseconds.
-int pair_width(const Task* tasks, int n, int pairs, double* cost);
-// Up to three products in one launch, all of the gated form or none. Operands must be readable
-// in place (aligned16), and rows of a single-row operand given a stride that is.
-cudaError_t run_pair(const Context& c, const Task* tasks, int width, int n);
+// How ff_pair.cu takes up to three products in one launch: sums per row of a tile, and pieces of the
+// sum over K of those that may be split. `cost` is the expected time in microseconds.
+struct PairPlan {
+  int width = 256, splits = 1;
+  double cost = 0.0;
+};
+PairPlan plan_pair(const Task* tasks, int n, int pairs, size_t partial_bytes);
+// Up to three products in one launch (and one that adds the pieces), all of the gated form or none.
+// Operands must be readable in place (aligned16), and rows of a single-row operand given a stride that is.
+cudaError_t run_pair(const Context& c, const Task* tasks, const PairPlan& plan, int n);
+// Bytes of Context::partials for the gradients of `weights` weights of K x N from M rows.
+size_t weight_partial_bytes(int64_t M, int64_t N, int64_t K, int weights);
 
 // How ff_rows.cu takes up to three products in one launch: CTAs along K, and for each product the
 // rows of X per tile and the ring slots. `cost` is the expected time in microseconds.

@@ -18,6 +18,12 @@
 // bias and residual 30.6). A K block needs 64 bytes a clock into each SM, what its port takes; narrower
 // tiles need more, so widths below 256 are for sizes that do not fill the pairs.
 //
+// A small weight's gradient over many rows has too few tiles for the pairs (1024 x 1024: 16), so its sum is
+// cut into pieces along K: the pieces are tiles like any other, their FP32 sums go to the workspace (through
+// L2) and a second launch adds them in their order. Gradients 32768x256x1024 with silu and db 133 -> 59 us,
+// gated 65536x512x512 218 -> 153, 16384x1024x1024 130 -> 119 (floor of
+// both 72).
+//
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the next tile's MMAs.
 // Six ring slots of 32 KB leave 35 KB for the epilogue's boxes; five cost 1.5 % at 4096^3.
 //
@@ -70,6 +76,8 @@ struct PairProblem {
   int M, N;
   int nkb, nkb_first;  // K blocks, and how many of them come from a[0], b[0]
   int tiles_m, tiles_n;
+  int splits, split_blocks;  // pieces of the sum over K, and their K blocks (the last: the rest)
+  float* partials;           // of the pieces' sums; nullptr: one piece, stored through the epilogue
   int bn;       // columns of Y in a tile
   int mma_n;    // sums per row in a tile (gated: 2 bn)
   uint32_t idesc;
@@ -89,6 +97,17 @@ struct PairParams {
 // and B in the L2 cache.
 __device__ __forceinline__ void tile_at(const PairProblem& p, int t, int& m0, int& n0) {
   tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, p.bn, m0, n0);
+}
+
+// The K blocks of a piece of the sum; pieces of the same blocks follow each other in the tile order.
+struct Piece {
+  int tile, first, blocks;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Piece piece_at(const PairProblem& p, int t) {
+  if (!SPLIT || p.splits == 1) return {t, 0, p.nkb};
+  const int tiles = p.tiles_m * p.tiles_n, piece = t / tiles, first = piece * p.split_blocks;
+  return {t - piece * tiles, first, min(p.split_blocks, p.nkb - first)};
 }
 
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
@@ -211,7 +230,7 @@ __device__ __forceinline__ void sums_of(const uint32_t (&r)[kUnit], bool any, ui
 // Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 are the
 // epilogue (warp 3 only holds TMEM). full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
 // that gives up a bounded wait records it and stops, and the others' own waits end the same way.
-template <int KIND, bool GATED>
+template <int KIND, bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_constant__ PairParams params) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -264,32 +283,35 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         const int pi = problem_of(t);
         const PairProblem& p = params.p[pi];
+        const Piece piece = piece_at<SPLIT>(p, t - params.first[pi]);
         int m0, n0;
-        tile_at(p, t - params.first[pi], m0, n0);
+        tile_at(p, piece.tile, m0, n0);
         // Gated: the same columns of this rank's weight; otherwise this rank's half of them.
         const int at = is_a ? m0 + rank * kRows : GATED ? n0 : n0 + rank * (p.mma_n / 2);
         const bool k_major = is_a ? p.a_k_major : p.b_k_major;
         const int boxes = is_a ? kRows / 64 : p.b_boxes;
         const uint32_t bytes = p.stage_tx;
-        int blocks = p.nkb_first, left = p.nkb - blocks;
+        int from = piece.first, to = SPLIT ? min(p.nkb_first, from + piece.blocks) : p.nkb_first;
+        int left = from + piece.blocks - to;
         const CUtensorMap* map = is_a ? &p.a[0] : &p.b[GATED ? rank : 0];
         while (ok) {
           if (k_major) {
-            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, k0, at, bar);
             });
           } else if (boxes > 1) {
-            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
               tc::tma_load_2d_pair(st + kBoxBytes, map, at + 64, k0, bar);
             });
           } else {
-            ok = ring.copy(0, blocks, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
+            ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
             });
           }
           if (left == 0) break;
-          blocks = left;
+          from = 0;
+          to = left;
           left = 0;
           map = is_a ? &p.a[1] : &p.b[1];
         }
@@ -303,10 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       uint32_t phase = 0, st = base;
       bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step, ++use) {
-        const PairProblem& p = params.p[problem_of(t)];
+        const int pi = problem_of(t);
+        const PairProblem& p = params.p[pi];
         const OperandForm fa = operand_form(p.a_k_major), fb = operand_form(p.b_k_major);
         const uint32_t idesc = p.idesc;
-        const int nkb = p.nkb, b = use & 1;
+        const int nkb = piece_at<SPLIT>(p, t - params.first[pi]).blocks, b = use & 1;
         const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
         if (!__all_sync(0xffffffffu, wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status))) break;
         tc::tc_fence_after();
@@ -345,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       const int pi = problem_of(t);
       const PairProblem& p = params.p[pi];
       int m0, n0;
-      tile_at(p, t - params.first[pi], m0, n0);
+      tile_at(p, piece_at<SPLIT>(p, t - params.first[pi]).tile, m0, n0);
       const int b = use & 1, m = m0 + rank * kRows + 32 * q;
       // What the epilogue reads from memory is on its way before the sums are there: the bias of
       // this warp's columns (lane i has column i of each group of 32) and the first residual box.
@@ -403,6 +426,16 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           put_row<KIND>(box, lane, v);
           if (more) load(c + 2 * kUnit);
           store_unit(&p.y, p.y_tma, box, p.Y, p.ldy, m, n, p.M, p.N, lane);
+        } else if (SPLIT && p.partials != nullptr) {
+          // Four columns of 256 rows together, so that a warp's store is 512 bytes in a row.
+          float4* out = reinterpret_cast<float4*>(p.partials) +
+                        (static_cast<int64_t>(t - params.first[pi]) * p.bn + c) / 4 * (2 * kRows) + rank * kRows + 32 * q + lane;
+#pragma unroll
+          for (int i = 0; i < kUnit / 4; ++i) {
+            const float2 lo = halves(v[2 * i]), hi = halves(v[2 * i + 1]);
+            out[i * 2 * kRows] = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+          if (more) load(c + 2 * kUnit);
         } else {
           if (p.bias != nullptr) {
             const int i = c / (2 * kUnit);
@@ -463,8 +496,61 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   }
 }
 
+// Adds the pieces' sums in their order. A block takes eight columns of a tile's 256 rows.
+struct PieceSums {
+  const float4* partials[kMaxProblems];
+  uint16_t* Y[kMaxProblems];
+  int64_t ldy[kMaxProblems];
+  int M[kMaxProblems], N[kMaxProblems], tiles_m[kMaxProblems], tiles_n[kMaxProblems], splits[kMaxProblems];
+  int wide[kMaxProblems];
+  unsigned first[kMaxProblems + 1];  // first block of each
+  int bn;
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(2 * kRows) piece_sum_kernel(const __grid_constant__ PieceSums s) {
+  wait_for_earlier_kernels();
+  const int i = blockIdx.x < s.first[1] ? 0 : blockIdx.x < s.first[2] ? 1 : 2;
+  const int chunks = s.bn / 8, unit = static_cast<int>(blockIdx.x - s.first[i]), tile = unit / chunks;
+  int m0, n0;
+  tc::tile_origin(tile, s.tiles_m[i], s.tiles_n[i], 2 * kRows, s.bn, m0, n0);
+  const int m = m0 + static_cast<int>(threadIdx.x), n = n0 + (unit - tile * chunks) * 8;
+  if (m >= s.M[i] || n >= s.N[i]) return;
+  const int64_t step = static_cast<int64_t>(s.tiles_m[i]) * s.tiles_n[i] * (s.bn / 4) * (2 * kRows);
+  const float4* from = s.partials[i] + static_cast<int64_t>(unit) * 2 * (2 * kRows) + threadIdx.x;
+  float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+  constexpr int kAhead = 8;  // pieces on their way before the first is added (four: 0.5 to 3 us slower)
+  for (int j = 0; j < s.splits[i]; j += kAhead) {
+    float4 a[kAhead], b[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      a[k] = b[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j + k < s.splits[i]) {
+        a[k] = from[0];
+        b[k] = from[2 * kRows];
+        from += step;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      lo.x += a[k].x, lo.y += a[k].y, lo.z += a[k].z, lo.w += a[k].w;
+      hi.x += b[k].x, hi.y += b[k].y, hi.z += b[k].z, hi.w += b[k].w;
+    }
+  }
+  const uint32_t w[4] = {pack_f32<KIND>(lo.x, lo.y), pack_f32<KIND>(lo.z, lo.w), pack_f32<KIND>(hi.x, hi.y),
+                         pack_f32<KIND>(hi.z, hi.w)};
+  uint16_t* y = s.Y[i] + m * s.ldy[i] + n;
+  if (s.wide[i] && n + 8 <= s.N[i]) {
+    *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < s.N[i]) y[j] = static_cast<uint16_t>(w[j / 2] >> 16 * (j & 1));
+  }
+}
+
 // Resident clusters of a kernel on the current device, looked up once.
-template <int KIND, bool GATED>
+template <int KIND, bool GATED, bool SPLIT>
 cudaError_t resident_clusters(int* out) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
@@ -474,7 +560,7 @@ cudaError_t resident_clusters(int* out) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   int n = known[dev].load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = ff_pair_kernel<KIND, GATED>;
+    auto kern = ff_pair_kernel<KIND, GATED, SPLIT>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
       return e;
     int sms = 0;
@@ -508,7 +594,7 @@ cudaError_t output_map(CUtensorMap* m, int* usable, const Matrix& o, int64_t M, 
 }
 
 template <int KIND>
-cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
+cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   const bool gated = t.form == kGated;
   cudaError_t e = cudaSuccess;
   p->M = static_cast<int>(t.M);
@@ -521,6 +607,12 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
   const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
   p->nkb_first = blocks;
   p->nkb = t.form == kJoined ? 2 * blocks : blocks;
+  p->splits = 1;
+  p->split_blocks = p->nkb;
+  if (t.split && splits > 1) {
+    p->split_blocks = (blocks + splits - 1) / splits;
+    p->splits = (blocks + p->split_blocks - 1) / p->split_blocks;
+  }
   p->a_k_major = t.A.k_major;
   p->b_k_major = t.B.k_major;
   p->b_boxes = (mma_n / 2 + 63) / 64;
@@ -555,26 +647,45 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n) {
   return output_map(&p->z2, &p->z2_tma, t.Z2, t.M, t.N);
 }
 
-template <int KIND, bool GATED>
-cudaError_t launch(const Context& c, const Task* tasks, int width, int n) {
+template <int KIND, bool GATED, bool SPLIT>
+cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, int n) {
   int resident = 0;
-  cudaError_t e = resident_clusters<KIND, GATED>(&resident);
+  cudaError_t e = resident_clusters<KIND, GATED, SPLIT>(&resident);
   if (e != cudaSuccess) return e;
   PairParams params;
   memset(&params, 0, sizeof(params));
   params.status = c.status;
-  int64_t tiles = 0;
+  PieceSums sums;
+  memset(&sums, 0, sizeof(sums));
+  sums.bn = plan.width;
+  int64_t tiles = 0, blocks = 0;
+  size_t used = 0;
   for (int i = 0; i < kMaxProblems; ++i) {
     params.first[i] = static_cast<int>(tiles);
-    if (i < n) {
-      if ((e = fill<KIND>(&params.p[i], tasks[i], width)) != cudaSuccess) return e;
-      tiles += static_cast<int64_t>(params.p[i].tiles_m) * params.p[i].tiles_n;
-      if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    }
+    sums.first[i] = static_cast<unsigned>(blocks);
+    if (i >= n) continue;
+    PairProblem& p = params.p[i];
+    if ((e = fill<KIND>(&p, tasks[i], plan.width, plan.splits)) != cudaSuccess) return e;
+    const int64_t outputs = static_cast<int64_t>(p.tiles_m) * p.tiles_n, pieces = outputs * p.splits;
+    tiles += pieces;
+    if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (p.splits == 1) continue;
+    p.partials = c.partials + used / 4;
+    used += static_cast<size_t>(pieces) * 2 * kRows * p.bn * 4;
+    if (used > c.partial_bytes) return cudaErrorInvalidConfiguration;
+    sums.partials[i] = reinterpret_cast<const float4*>(p.partials);
+    sums.Y[i] = p.Y, sums.ldy[i] = p.ldy;
+    sums.M[i] = p.M, sums.N[i] = p.N;
+    sums.tiles_m[i] = p.tiles_m, sums.tiles_n[i] = p.tiles_n, sums.splits[i] = p.splits;
+    sums.wide[i] = aligned16(p.Y, p.ldy);
+    blocks += outputs * (p.bn / 8);
   }
+  sums.first[kMaxProblems] = static_cast<unsigned>(blocks);
   params.first[kMaxProblems] = static_cast<int>(tiles);
   const LaunchShape shape{dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident))), kThreads, 2, kSmemBytes};
-  return launch_early(c.stream, shape, ff_pair_kernel<KIND, GATED>, params);
+  e = launch_early(c.stream, shape, ff_pair_kernel<KIND, GATED, SPLIT>, params);
+  if (!SPLIT || e != cudaSuccess || blocks == 0) return e;
+  return launch_early(c.stream, {dim3(static_cast<unsigned>(blocks)), 2 * kRows, 1, 0}, piece_sum_kernel<KIND>, sums);
 }
 
 }  // namespace
@@ -583,57 +694,94 @@ cudaError_t launch(const Context& c, const Task* tasks, int width, int n) {
 // or the time of its MMAs and copies, whichever is longer, and a tile that others follow 0.3 us more;
 // all SMs together compute 1.8 PFLOP/s (the power limit) and take in 16 TB/s; starting up, and a last
 // tile's epilogue, take the rest.
-int pair_width(const Task* tasks, int n, int pairs, double* cost) {
+PairPlan plan_pair(const Task* tasks, int n, int pairs, size_t partial_bytes) {
   static const struct {
     int n;
     double block;
   } kWidths[] = {{64, 0.155}, {128, 0.158}, {192, 0.185}, {224, 0.22}, {256, 0.255}};
-  int best = kMaxN;
-  *cost = 0.0;
+  // Pieces of a sum have eight K blocks at least (their stores take as long as four), and there is room
+  // for them. Adding the pieces is a launch more, and their way through the L2 cache: fitted to dW of 256^2
+  // to 1024^2 weights from 4096 to 65536 rows in 2 to 19 pieces (most within 10 %).
+  constexpr int kLeastBlocks = 8;
+  constexpr double kSumLaunch = 1.2, kSumPiece = 0.03;
+  PairPlan plan;
+  int64_t longest = 0;
+  for (int i = 0; i < n; ++i)
+    if (tasks[i].split && longest < tasks[i].K) longest = tasks[i].K;
+  const int64_t most_splits = partial_bytes > 0 ? longest / (kLeastBlocks * kBK) : 1;
   for (const auto& w : kWidths) {
-    int64_t first[kMaxProblems + 1] = {};
-    double tile_time[kMaxProblems] = {}, flops = 0.0, bytes = 0.0;
+    int64_t tiles[kMaxProblems] = {};
+    double blocks[kMaxProblems] = {}, flops = 0.0, bytes = 0.0;
     bool whole = true;
     for (int i = 0; i < n; ++i) {
       const Task& t = tasks[i];
       const int bn = t.form == kGated ? w.n / 2 : w.n;
       if (bn % kUnit != 0) whole = false;  // the epilogue takes whole groups of columns
-      const double blocks = static_cast<double>((t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1));
-      const int64_t tiles = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + bn - 1) / bn);
-      first[i + 1] = first[i] + tiles;
-      tile_time[i] = blocks * w.block + 0.3;
-      flops += static_cast<double>(tiles) * blocks * 2.0 * 2 * kRows * w.n * kBK;
-      bytes += static_cast<double>(tiles) * blocks * (2 * kABytes + w.n * kBK * 2);
+      blocks[i] = static_cast<double>((t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1));
+      tiles[i] = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + bn - 1) / bn);
+      flops += static_cast<double>(tiles[i]) * blocks[i] * 2.0 * 2 * kRows * w.n * kBK;
+      bytes += static_cast<double>(tiles[i]) * blocks[i] * (2 * kABytes + w.n * kBK * 2);
     }
     if (!whole) continue;
-    // The longest share: pair j has the tiles j, j + pairs, ... of all products in turn.
-    double time = 0.0;
-    for (int j = 0; j < pairs && j < first[n]; ++j) {
-      double share = -0.3;
+    double least = flops / 1.8e9;
+    if (least < bytes / 16e6) least = bytes / 16e6;
+    for (int splits = 1; splits == 1 || splits <= most_splits; ++splits) {
+      int64_t first[kMaxProblems + 1] = {}, pieces = 0;
+      double tile_time[kMaxProblems] = {};
       for (int i = 0; i < n; ++i) {
-        auto before = [&](int64_t end) { return end > j ? (end - j + pairs - 1) / pairs : 0; };
-        share += static_cast<double>(before(first[i + 1]) - before(first[i])) * tile_time[i];
+        const bool cut = splits > 1 && tasks[i].split;
+        first[i + 1] = first[i] + tiles[i] * (cut ? splits : 1);
+        tile_time[i] = cut ? static_cast<double>((static_cast<int64_t>(blocks[i]) + splits - 1) / splits) * w.block + 0.8
+                           : blocks[i] * w.block + 0.3;
+        if (cut) pieces += tiles[i] * splits;
       }
-      if (time < share) time = share;
-      if (n == 1) break;  // the first pair's share is the longest
-    }
-    if (time < flops / 1.8e9) time = flops / 1.8e9;
-    if (time < bytes / 16e6) time = bytes / 16e6;
-    time += 4.1 + 0.006 * w.n;
-    if (*cost == 0.0 || time <= *cost) {
-      *cost = time;
-      best = w.n;
+      const size_t room = static_cast<size_t>(pieces) * 2 * kRows * w.n * 4;
+      if (room > partial_bytes) break;
+      // The longest share: pair j has the tiles j, j + pairs, ... of all products in turn, and a product
+      // gives the pairs from its first tile's on one more than the others. So the longest begins where a
+      // product begins.
+      double time = 0.0;
+      for (int i = 0; i < n; ++i) {
+        const int64_t j = first[i] % pairs;
+        double share = -0.3;
+        for (int k = 0; k < n; ++k) {
+          auto before = [&](int64_t end) { return end > j ? (end - j + pairs - 1) / pairs : 0; };
+          share += static_cast<double>(before(first[k + 1]) - before(first[k])) * tile_time[k];
+        }
+        if (time < share) time = share;
+      }
+      if (time < least) time = least;
+      time += 4.1 + 0.006 * w.n;
+      if (pieces > 0) time += kSumLaunch + kSumPiece * splits + static_cast<double>(room) / 5e6;
+      if (plan.cost == 0.0 || (splits == 1 ? time <= plan.cost : time < plan.cost)) {
+        plan.cost = time;
+        plan.width = w.n;
+        plan.splits = splits;
+      }
     }
   }
-  return best;
+  return plan;
 }
 
-cudaError_t run_pair(const Context& c, const Task* tasks, int width, int n) {
+// Room for one piece of 256 x 256 sums on every pair of SMs, where the weights have so few tiles that they
+// leave half of the pairs idle and the rows allow two pieces.
+size_t weight_partial_bytes(int64_t M, int64_t N, int64_t K, int weights) {
+  constexpr int64_t kPairs = 80;
+  const int64_t splits = M / (8 * kBK);
+  if (N == 0 || K == 0 || splits < 2 || weights == 0) return 0;
+  const int64_t tiles_n = (N + kMaxN - 1) / kMaxN, tiles_k = (K + kMaxN - 1) / kMaxN;
+  if (tiles_n > kPairs || tiles_k > kPairs || weights * tiles_n * tiles_k > kPairs / 2) return 0;
+  const int64_t tiles = weights * tiles_n * tiles_k, most = tiles * splits;
+  return static_cast<size_t>(most < kPairs ? most : kPairs) * kMaxN * kMaxN * 4;
+}
+
+cudaError_t run_pair(const Context& c, const Task* tasks, const PairPlan& plan, int n) {
   if (n == 0) return cudaSuccess;
-  const bool gated = tasks[0].form == kGated;
-  if (c.kind == kBf16)
-    return gated ? launch<kBf16, true>(c, tasks, width, n) : launch<kBf16, false>(c, tasks, width, n);
-  return gated ? launch<kF16, true>(c, tasks, width, n) : launch<kF16, false>(c, tasks, width, n);
+  if (tasks[0].form == kGated)
+    return c.kind == kBf16 ? launch<kBf16, true, false>(c, tasks, plan, n) : launch<kF16, true, false>(c, tasks, plan, n);
+  if (plan.splits > 1)
+    return c.kind == kBf16 ? launch<kBf16, false, true>(c, tasks, plan, n) : launch<kF16, false, true>(c, tasks, plan, n);
+  return c.kind == kBf16 ? launch<kBf16, false, false>(c, tasks, plan, n) : launch<kF16, false, false>(c, tasks, plan, n);
 }
 
 }  // namespace ff

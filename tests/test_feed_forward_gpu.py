@@ -545,7 +545,8 @@ def test_refusals():
         t2s.linear_backward(r, x, w, r, act="silu", workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))
 
 
-@pytest.mark.parametrize("m,n", [(1 << 14, 1024), ((1 << 14) + 3, 1025), (1 << 21, 8), (6000, 4000)])
+@pytest.mark.parametrize("m,n", [(1 << 14, 1024), ((1 << 14) + 3, 1025), (1 << 21, 8), (6000, 4000),
+                                 (40000, 44), (1 << 16, 64), (9000, 1000)])
 def test_many_column_sums(m, n):
     """db of more values than a cluster's CTAs share."""
     mk = Maker(18, F16)
@@ -597,3 +598,32 @@ def test_calls_on_several_streams_at_once():
     for results, expected in zip(got, want):
         for result in results:
             assert all(torch.equal(r, e) for r, e in zip(result, expected))
+
+
+@pytest.mark.parametrize("m,k,n,pad", [(1024, 64, 64, 0), (4096, 256, 256, 0), (4100, 264, 250, 6), (4100, 257, 131, 3),
+                                       (16400, 768, 520, 0), (40001, 40, 1000, 8)])
+def test_weight_gradients_over_many_rows(m, k, n, pad):
+    """Rows enough that the weights' gradients are sums of several pieces."""
+    for i, (dtype, wt) in enumerate([(BF16, False), (F16, True), (F16, False), (BF16, True)]):
+        mk = Maker(500 + i, dtype, pad)
+        dy, x, w, z, up = mk.normal(m, n), mk.normal(m, k), mk.weight(k, n, wt), mk.normal(m, n), mk.normal(m, n)
+        dws = [mk.empty(n, k).t() if wt else mk.empty(k, n) for _ in range(5)]
+        dx, db = mk.empty(m, k), mk.empty(1, n).reshape(n)
+        value, slope = act64(z.double(), "silu")
+        d, dl, du = dy.double() * slope, dy.double() * up.double() * slope, dy.double() * value
+        off = 2.0 ** -17 * (z.double().abs() + 1) * dy.double().abs()
+        ol = off * up.double().abs()
+        t2s.linear_backward(dy, x, w, z, act="silu", dx=False, dw=dws[0], db=False)
+        t2s.linear_backward(dy, x, w, z, act="silu", dx=dx, dw=dws[1], db=db)
+        t2s.gated_linear_backward(dy, x, w, w, (z, up), act="silu", dx=False, dw_gate=dws[2], dw_up=False)
+        t2s.gated_linear_backward(dy, x, w, w, (z, up), act="silu", dw_gate=dws[3], dw_up=dws[4])
+        assert binding.device_status() == binding.T2S_OK
+        within(dx, *product_bar(off, d, w.double().t(), dtype), "dx")
+        within(db, *sum_bar(off, d, dtype), "db")
+        for got, o, a, name in zip(dws, (off, off, ol, ol, off), (d, d, dl, dl, du),
+                                   ("dw alone", "dw", "dw_gate alone", "dw_gate", "dw_up")):
+            want, bar = product_bar(o.t(), a.t(), x.double(), dtype)
+            within(got, want.t(), bar.t(), name)
+        again = t2s.linear_backward(dy, x, w, z, act="silu", dx=False, dw=None, db=False)[1]
+        assert torch.equal(again, dws[0])
+        mk.check_canaries()

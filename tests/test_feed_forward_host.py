@@ -81,6 +81,10 @@ def test_feed_forward_workspace_sizes(lib):
     assert f.t2s_gated_workspace_size(4, 5, 7, 0) >= 2 * (4 * 8 + 2 * 7 * 8)
     assert f.t2s_linear_backward_workspace_size(64, 72, 80, 1) >= 2 * 64 * 72
     assert f.t2s_gated_backward_workspace_size(64, 72, 80, 1) >= 2 * 2 * 64 * 72
+    # Small weights over many rows: pieces of their gradients' sums; partial sums of db.
+    assert f.t2s_linear_backward_workspace_size(8192, 256, 512, 1) >= 2 * 8192 * 256 + 2 * 4 * 256 * 512
+    assert f.t2s_gated_backward_workspace_size(8192, 256, 512, 1) >= 2 * 2 * 8192 * 256 + 2 * 2 * 4 * 256 * 512
+    assert f.t2s_linear_backward_workspace_size(1 << 16, 64, 1, 1) > 2 * 64 * (1 << 16)
     for g in (f.t2s_linear_workspace_size, f.t2s_linear_backward_workspace_size, f.t2s_gated_workspace_size,
               f.t2s_gated_backward_workspace_size):
         assert g(-1, 2, 3, 0) == 0 and g(2, f.T2S_MAX_DIM + 1, 3, 0) == 0
