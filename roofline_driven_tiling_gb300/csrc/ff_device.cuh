@@ -175,16 +175,18 @@ __device__ __forceinline__ bool elect_one() {
 struct Ring {
   uint32_t first, stride, full, empty, slots;  // its part of slot 0, slot size, barriers of slot 0
   uint32_t st, s = 0, phase = 1;
+  int depth;  // K values of a slot
 
-  __device__ __forceinline__ Ring(uint32_t first_, uint32_t stride_, uint32_t full_, uint32_t empty_, uint32_t slots_)
-      : first(first_), stride(stride_), full(full_), empty(empty_), slots(slots_), st(first_) {}
+  __device__ __forceinline__ Ring(uint32_t first_, uint32_t stride_, uint32_t full_, uint32_t empty_, uint32_t slots_,
+                                  int depth_)
+      : first(first_), stride(stride_), full(full_), empty(empty_), slots(slots_), st(first_), depth(depth_) {}
 
-  // K blocks [kb0, kb1), each into the next slot once that is free: issue(slot, k, barrier offset
+  // Slots of K [kb0, kb1), each into the next slot once that is free: issue(slot, k, barrier offset
   // from `bar0` by slot). `expect` bytes are announced on the slot's full barrier if not 0.
   template <class F>
   __device__ __forceinline__ bool copy(int kb0, int kb1, uint32_t expect, uint32_t bar0, unsigned* status, F&& issue) {
 #pragma unroll 1
-    for (int k0 = kb0 * kBK; k0 < kb1 * kBK; k0 += kBK) {
+    for (int k0 = kb0 * depth; k0 < kb1 * depth; k0 += depth) {
       if (!__all_sync(0xffffffffu, wait_bounded(empty + 8u * s, phase, status))) return false;
       if (elect_one()) {
         if (expect != 0) mbar_arrive_expect_tx(full + 8u * s, expect);

@@ -51,11 +51,18 @@ namespace ff {
 namespace {
 
 constexpr int kRows = 128;    // A rows of one CTA
-constexpr int kStages = 6;    // ring slots of 32 KB
+constexpr int kStages = 6;    // ring slots of 32 KB (narrow tiles: four of 48 KB)
 constexpr int kMaxN = 256;    // widest MMA
 constexpr int kABytes = kRows * kBK * 2;
 constexpr int kBBytes = kMaxN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
+// Tiles of up to 128 columns take two K blocks per slot: a slot's waits, commit and copies take longer to issue
+// than a narrow block's MMAs take to run (a K block of 128 columns 0.20 -> 0.17 us, of 64 0.19 -> 0.16;
+// 512x4096x4096 19.3 -> 16.5 us, 256x8192x8192 37.4 -> 32.6 with the widths chosen accordingly).
+constexpr int kNarrowN = 128;
+constexpr int kNarrowStages = 4;
+constexpr int kNarrowStageBytes = 2 * (kABytes + kBoxBytes);
+static_assert(kNarrowStages * kNarrowStageBytes <= kStages * kStageBytes, "the ring");
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kUnit = 32;                        // columns an epilogue warp takes at a time
@@ -74,14 +81,14 @@ struct PairProblem {
   uint16_t *Y, *Z, *Z2;
   int64_t ldr, ldy, ldz, ldz2;
   int M, N;
-  int nkb, nkb_first;  // K blocks, and how many of them come from a[0], b[0]
+  int nkb, nkb_first;  // ring slots of K, and how many of them come from a[0], b[0]
   int tiles_m, tiles_n;
-  int splits, split_blocks;  // pieces of the sum over K, and their K blocks (the last: the rest)
+  int splits, split_blocks;  // pieces of the sum over K, and their slots (the last: the rest)
   float* partials;           // of the pieces' sums; nullptr: one piece, stored through the epilogue
   int bn;       // columns of Y in a tile
   int mma_n;    // sums per row in a tile (gated: 2 bn)
   uint32_t idesc;
-  uint32_t stage_tx;  // bytes that both CTAs copy per K block
+  uint32_t stage_tx;  // bytes that both CTAs copy per slot
   int a_k_major, b_k_major, b_boxes;
   int y_tma, z_tma, z2_tma, r_wide;
   int act;
@@ -90,6 +97,7 @@ struct PairProblem {
 struct PairParams {
   PairProblem p[kMaxProblems];
   int first[kMaxProblems + 1];  // first tile of each problem; the last entry is the tile count
+  int narrow;                   // two K blocks per slot
   unsigned* status;
 };
 
@@ -99,7 +107,7 @@ __device__ __forceinline__ void tile_at(const PairProblem& p, int t, int& m0, in
   tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, p.bn, m0, n0);
 }
 
-// The K blocks of a piece of the sum; pieces of the same blocks follow each other in the tile order.
+// The slots of K of a piece of the sum; pieces of the same slots follow each other in the tile order.
 struct Piece {
   int tile, first, blocks;
 };
@@ -246,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
   const int rank = static_cast<int>(cluster_ctarank());
   const int tile0 = static_cast<int>(cluster_id_x()), tile_step = static_cast<int>(cluster_count_x());
   const int tiles = params.first[kMaxProblems];
+  const bool narrow = params.narrow != 0;
+  const int stages = narrow ? kNarrowStages : kStages;
+  const uint32_t stage_bytes = narrow ? kNarrowStageBytes : kStageBytes, b_offset = narrow ? 2 * kABytes : kABytes;
   auto problem_of = [&](int t) { return t < params.first[1] ? 0 : t < params.first[2] ? 1 : 2; };
 
   if (threadIdx.x == 0) {
@@ -276,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
     // between two copies hold up the other's.
     {
       const bool is_a = warp == 0;
-      Ring ring(base + (is_a ? 0 : kABytes), kStageBytes, full(0), empty(0), kStages);
+      Ring ring(base + (is_a ? 0 : b_offset), stage_bytes, full(0), empty(0), stages, narrow ? 2 * kBK : kBK);
+      const uint32_t second = narrow ? (is_a ? kABytes : kBoxBytes) : 0u;  // where a slot's second K block lies
       const uint32_t bar0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
       const bool expects = is_a && rank == 0;
       bool ok = true;
@@ -298,15 +310,21 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           if (k_major) {
             ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, k0, at, bar);
+              if (second != 0) tc::tma_load_2d_pair(st + second, map, k0 + kBK, at, bar);
             });
           } else if (boxes > 1) {
             ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
               tc::tma_load_2d_pair(st + kBoxBytes, map, at + 64, k0, bar);
+              if (second != 0) {
+                tc::tma_load_2d_pair(st + second, map, at, k0 + kBK, bar);
+                tc::tma_load_2d_pair(st + second + kBoxBytes, map, at + 64, k0 + kBK, bar);
+              }
             });
           } else {
             ok = ring.copy(from, to, expects ? bytes : 0u, bar0, status, [&](uint32_t st, int k0, uint32_t bar) {
               tc::tma_load_2d_pair(st, map, at, k0, bar);
+              if (second != 0) tc::tma_load_2d_pair(st + second, map, at, k0 + kBK, bar);
             });
           }
           if (left == 0) break;
@@ -317,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         }
       }
       // Every slot's copies have landed and been read before the CTA may go.
-      if (ok) ring.copy(0, kStages, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
+      if (ok) ring.copy(0, stages, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -335,17 +353,18 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
         tc::tc_fence_after();
 #pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
-          const uint64_t da = with_address(fa, st), db = with_address(fb, st + kABytes);
+          const uint64_t da = with_address(fa, st), db = with_address(fb, st + b_offset);
           if (!__all_sync(0xffffffffu, wait_bounded(full(s), phase, status))) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
           mma_block<2>(acc, da, fa.step, db, fb.step, idesc, kb);
+          if (narrow) mma_block<2>(acc, da + (kABytes >> 4), fa.step, db + (kBoxBytes >> 4), fb.step, idesc, 1u);
           if (elect_one()) tc::mma_commit_pair(empty(s));
           __syncwarp();
-          st += kStageBytes;
-          if (++s == kStages) {
+          st += stage_bytes;
+          if (++s == stages) {
             s = 0;
             st = base;
             phase ^= 1u;
@@ -604,7 +623,9 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   if (p->bn % kUnit != 0) return cudaErrorInvalidValue;
   p->tiles_m = static_cast<int>((t.M + 2 * kRows - 1) / (2 * kRows));
   p->tiles_n = static_cast<int>((t.N + p->bn - 1) / p->bn);
-  const int blocks = static_cast<int>((t.K + kBK - 1) / kBK);
+  // A narrow tile's last slot may reach past K: its copies read zeros there.
+  const int depth = mma_n <= kNarrowN ? 2 * kBK : kBK;
+  const int blocks = static_cast<int>((t.K + depth - 1) / depth);
   p->nkb_first = blocks;
   p->nkb = t.form == kJoined ? 2 * blocks : blocks;
   p->splits = 1;
@@ -618,7 +639,7 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   p->b_boxes = (mma_n / 2 + 63) / 64;
   const uint32_t b_bytes = p->b_k_major ? static_cast<uint32_t>(mma_n / 2) * kBK * 2
                                         : static_cast<uint32_t>(p->b_boxes) * kBoxBytes;
-  p->stage_tx = 2 * (kABytes + b_bytes);
+  p->stage_tx = static_cast<uint32_t>(2 * (depth / kBK)) * (kABytes + b_bytes);
   // D FP32, A and B of the 16-bit type, their orders, N and M = 256.
   const uint32_t fmt = KIND == kBf16 ? 1u : 0u;
   p->idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((p->a_k_major ? 0u : 1u) << 15) |
@@ -655,6 +676,7 @@ cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, in
   PairParams params;
   memset(&params, 0, sizeof(params));
   params.status = c.status;
+  params.narrow = plan.width <= kNarrowN;
   PieceSums sums;
   memset(&sums, 0, sizeof(sums));
   sums.bn = plan.width;
@@ -690,7 +712,7 @@ cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, in
 
 }  // namespace
 
-// Fitted to 17 products of 256 to 4096 rows (most within 10 %): a K block takes a pair of SMs 0.155 us
+// Fitted to products of 256 to 4096 rows (most within 10 %): a K block takes a pair of SMs 0.158 us
 // or the time of its MMAs and copies, whichever is longer, and a tile that others follow 0.3 us more;
 // all SMs together compute 1.8 PFLOP/s (the power limit) and take in 16 TB/s; starting up, and a last
 // tile's epilogue, take the rest.
@@ -698,7 +720,7 @@ PairPlan plan_pair(const Task* tasks, int n, int pairs, size_t partial_bytes) {
   static const struct {
     int n;
     double block;
-  } kWidths[] = {{64, 0.155}, {128, 0.158}, {192, 0.185}, {224, 0.22}, {256, 0.255}};
+  } kWidths[] = {{64, 0.158}, {128, 0.17}, {192, 0.215}, {224, 0.235}, {256, 0.26}};
   // Pieces of a sum have eight K blocks at least (their stores take as long as four), and there is room
   // for them. Adding the pieces is a launch more, and their way through the L2 cache: fitted to dW of 256^2
   // to 1024^2 weights from 4096 to 65536 rows in 2 to 19 pieces (most within 10 %).

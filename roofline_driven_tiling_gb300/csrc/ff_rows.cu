@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) ff_rows_kernel(const __grid_constant
       const bool is_w = warp == 0, k_major = p.w_k_major, x_k_major = p.x_k_major;
       const int first = p.nkb_first, x_boxes = p.x_boxes;
       const uint32_t expect = is_w ? p.stage_bytes : 0u;
-      Ring ring(base + (is_w ? 0 : GATED ? kWeightBytes : kXOffset), p.stage_bytes, full(0), empty(0), S);
+      Ring ring(base + (is_w ? 0 : GATED ? kWeightBytes : kXOffset), p.stage_bytes, full(0), empty(0), S, kBK);
       // Joined products: K blocks before `first` from the first pair of operands, then the second.
       for (int part = 0; part < 2; ++part) {
         const int from = part ? max(kb0 - first, 0) : min(kb0, first), to = part ? kb1 - first : min(kb1, first);
@@ -381,25 +381,25 @@ cudaError_t launch(const Context& c, const Task* tasks, const RowsPlan& plan, in
 }
 
 // What a product takes this way in tiles of `tm` rows of X with `splits` CTAs along K, in microseconds.
-// Fitted to 30 products of 1 to 1024 rows (within 15 %): a K block of 16 KB of weights takes a CTA 0.15
-// us, more once X's tile outweighs the weight's (0.165 at 128 rows, 0.24 at 256), the gated form's two
+// Fitted to products of 1 to 1024 rows (within 15 %): a K block of 16 KB of weights takes a CTA 0.16
+// us, more once X's tile outweighs the weight's (0.175 at 128 rows, 0.26 at 256), the gated form's two
 // weights 0.22 to 0.25; the partial sums' way through shared memory 17 ns a row (gated: 25).
 struct Cost {
   int64_t ctas;
   double per_cta;  // one CTA's time
-  double feed;     // all SMs together take in at most 16 TB/s
+  double feed;     // all SMs together take in at most 14 TB/s
 };
 Cost cost_of(const Task& t, int tm, int splits) {
   const bool gated = t.form == kGated;
   const int64_t blocks = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
   const int64_t tiles = (t.N + kTileN - 1) / kTileN * ((t.M + tm - 1) / tm);
-  double block = tm <= 64 ? 0.15 : tm <= 128 ? 0.15 + (tm - 64) * 0.00023 : 0.165 + (tm - 128) * 0.00059;
+  double block = tm <= 64 ? 0.16 : tm <= 128 ? 0.16 + (tm - 64) * 0.00023 : 0.175 + (tm - 128) * 0.00066;
   if (gated) block = 0.22 + tm * 0.00025;
   Cost c;
   c.ctas = tiles * splits;
   c.per_cta = static_cast<double>((blocks + splits - 1) / splits) * block + tm * (gated ? 0.025 : 0.017);
   c.feed = static_cast<double>(tiles) * static_cast<double>(blocks) *
-           ((gated ? 2 : 1) * kWeightBytes + tm * kBK * 2) / 16e6;
+           ((gated ? 2 : 1) * kWeightBytes + tm * kBK * 2) / 14e6;
   return c;
 }
 
