@@ -355,9 +355,10 @@ int t2s_vector_add_f32(int64_t n, const float *x, const float *y, float *z,
  *   T2S_ACT_GELU z (1 + erf(z / sqrt 2)) / 2,
  *   T2S_ACT_GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  * Sums, activations and db are FP32 (the sums' order is the library's, the same in every call
- * of the same sizes, alignment and wanted outputs; the tensor cores truncate their additions, at most 2^-23 of
- * the sum of magnitudes for every 16 terms); every output is rounded to 16 bits once. dZ, dG and dU are
- * rounded to 16 bits where they enter the products of a gradient.
+ * of the same sizes, alignment and wanted outputs; the tensor cores truncate their additions, at
+ * most 2^-23 of the sum of magnitudes for every 16 terms, over pieces of at most 16384 terms that
+ * are then added in FP32); every output is rounded to 16 bits once. dZ, dG and dU are rounded to
+ * 16 bits where they enter the products of a gradient.
  *
  * Layout: each matrix has its own row stride (ld, in elements, at least its row length and at
  * most T2S_MAX_DIM), so views of larger matrices are taken as they are. Weights and their

@@ -46,6 +46,11 @@ struct Task {
 
 constexpr int kMaxProblems = 3;  // products of one launch
 
+// Values of K that one accumulator sums. The tensor cores add in FP32 but truncate, always towards zero:
+// a piece of this length loses at most 2^-13 of the sum of its magnitudes (measured with operands of one sign: 0.8 of
+// that), a quarter of binary16's rounding. Longer sums are taken in pieces that are added in FP32.
+constexpr int64_t kMaxPiece = 16384;
+
 struct Context {
   Kind kind;
   cudaStream_t stream;

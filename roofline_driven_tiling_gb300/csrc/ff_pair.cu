@@ -27,8 +27,10 @@
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the next tile's MMAs.
 // Six ring slots of 32 KB leave 35 KB for the epilogue's boxes; five cost 1.5 % at 4096^3.
 //
-// The tensor core adds in FP32 but truncates (relative to the sum of magnitudes at most 2^-23 per 16
-// values of K): at most half a unit of binary16 at K = 65536, so one accumulator takes all of K.
+// An accumulator takes at most kMaxPiece values of K (its truncation grows with them). A tile of more
+// sums them in turn into the two accumulators, and the epilogue's warps add each piece in FP32 to what the
+// ones before it left in the other accumulator, which then takes the piece after it. The sums of a weight's
+// gradient are cut over the SMs besides, as above.
 //
 // The gated product needs no wider machinery: rank 0 stages 128 columns of Wg and rank 1 the same
 // 128 columns of Wu, so the lower half of the accumulator's columns holds G, the upper half U.
@@ -84,6 +86,7 @@ struct PairProblem {
   int nkb, nkb_first;  // ring slots of K, and how many of them come from a[0], b[0]
   int tiles_m, tiles_n;
   int splits, split_blocks;  // pieces of the sum over K, and their slots (the last: the rest)
+  int acc_blocks;            // slots that one accumulator takes
   float* partials;           // of the pieces' sums; nullptr: one piece, stored through the epilogue
   int bn;       // columns of Y in a tile
   int mma_n;    // sums per row in a tile (gated: 2 bn)
@@ -235,10 +238,26 @@ __device__ __forceinline__ void sums_of(const uint32_t (&r)[kUnit], bool any, ui
     s[i] = any ? pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0ull;
 }
 
+// Adds one accumulator's 32 columns of the warp's 32 rows to another's.
+__device__ __forceinline__ void add_columns(uint32_t to, uint32_t from) {
+#pragma unroll
+  for (uint32_t c = 0; c < kUnit; c += 16) {
+    uint32_t x[16], y[16];
+    tc::tmem_ld16(to + c, x);
+    tc::tmem_ld16(from + c, y);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]), "+r"(y[i]));  // no use before the loads' waits
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(x[i]));
+    store_columns16(to + c, x);
+  }
+}
+
 // Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 are the
 // epilogue (warp 3 only holds TMEM). full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role
 // that gives up a bounded wait records it and stops, and the others' own waits end the same way.
-template <int KIND, bool GATED, bool SPLIT>
+// LONG: some tile's sum takes more than one accumulator.
+template <int KIND, bool GATED, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_constant__ PairParams params) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -342,36 +361,45 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
       int s = 0, use = 0;
       uint32_t phase = 0, st = base;
       bool ok = true;
-      for (int t = tile0; ok && t < tiles; t += tile_step, ++use) {
+      for (int t = tile0; ok && t < tiles; t += tile_step) {
         const int pi = problem_of(t);
         const PairProblem& p = params.p[pi];
         const OperandForm fa = operand_form(p.a_k_major), fb = operand_form(p.b_k_major);
         const uint32_t idesc = p.idesc;
-        const int nkb = piece_at<SPLIT>(p, t - params.first[pi]).blocks, b = use & 1;
-        const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
-        if (!__all_sync(0xffffffffu, wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status))) break;
-        tc::tc_fence_after();
-#pragma unroll 1
-        for (int kb = 0; kb < nkb; ++kb) {
-          const uint64_t da = with_address(fa, st), db = with_address(fb, st + b_offset);
-          if (!__all_sync(0xffffffffu, wait_bounded(full(s), phase, status))) {
+        const int nkb = piece_at<SPLIT>(p, t - params.first[pi]).blocks;
+        int left = nkb;
+        do {
+          const int blocks = LONG ? min(left, p.acc_blocks) : nkb, b = use & 1;
+          const uint32_t acc = tmem + static_cast<uint32_t>(b) * kMaxN;
+          if (!__all_sync(0xffffffffu, wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status))) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          mma_block<2>(acc, da, fa.step, db, fb.step, idesc, kb);
-          if (narrow) mma_block<2>(acc, da + (kABytes >> 4), fa.step, db + (kBoxBytes >> 4), fb.step, idesc, 1u);
-          if (elect_one()) tc::mma_commit_pair(empty(s));
-          __syncwarp();
-          st += stage_bytes;
-          if (++s == stages) {
-            s = 0;
-            st = base;
-            phase ^= 1u;
+#pragma unroll 1
+          for (int kb = 0; kb < blocks; ++kb) {
+            const uint64_t da = with_address(fa, st), db = with_address(fb, st + b_offset);
+            if (!__all_sync(0xffffffffu, wait_bounded(full(s), phase, status))) {
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+            mma_block<2>(acc, da, fa.step, db, fb.step, idesc, kb);
+            if (narrow) mma_block<2>(acc, da + (kABytes >> 4), fa.step, db + (kBoxBytes >> 4), fb.step, idesc, 1u);
+            if (elect_one()) tc::mma_commit_pair(empty(s));
+            __syncwarp();
+            st += stage_bytes;
+            if (++s == stages) {
+              s = 0;
+              st = base;
+              phase ^= 1u;
+            }
           }
-        }
-        if (ok && elect_one()) tc::mma_commit_pair(acc_full + 8u * b);
-        __syncwarp();
+          if (ok && elect_one()) tc::mma_commit_pair(acc_full + 8u * b);
+          __syncwarp();
+          ++use;
+          left -= blocks;
+        } while (LONG && ok && left > 0);
       }
       // Every MMA issued above ends before TMEM is released.
       if (elect_one()) tc::mma_commit<2>(mma_done);
@@ -386,9 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
     for (int t = tile0; t < tiles; t += tile_step, ++use) {
       const int pi = problem_of(t);
       const PairProblem& p = params.p[pi];
+      const Piece piece = piece_at<SPLIT>(p, t - params.first[pi]);
       int m0, n0;
-      tile_at(p, piece_at<SPLIT>(p, t - params.first[pi]).tile, m0, n0);
-      const int b = use & 1, m = m0 + rank * kRows + 32 * q;
+      tile_at(p, piece.tile, m0, n0);
+      const int m = m0 + rank * kRows + 32 * q;
       // What the epilogue reads from memory is on its way before the sums are there: the bias of
       // this warp's columns (lane i has column i of each group of 32) and the first residual box.
       Residual residual;
@@ -403,14 +432,33 @@ __global__ void __launch_bounds__(kThreads, 1) ff_pair_kernel(const __grid_const
           }
         }
       }
-      const bool done = wait_bounded(acc_full + 8u * b, (use >> 1) & 1u, status);
-      if (!__all_sync(0xffffffffu, done)) break;
-      tc::tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b) * kMaxN;
-      const bool any = p.nkb > 0;
       // The two warps of a row quarter take every other group of 32 columns inside the matrix; a
       // group's sums are on their way from TMEM while the one before it is stored.
       const int columns = m < p.M ? min(p.bn, p.N - n0) : 0;
+      const uint32_t rows_at = tmem + (static_cast<uint32_t>(32 * q) << 16);
+      bool done = __all_sync(0xffffffffu, wait_bounded(acc_full + 8u * (use & 1), (use >> 1) & 1u, status));
+      if constexpr (LONG) {
+        for (int left = piece.blocks - p.acc_blocks; done && left > 0; left -= p.acc_blocks) {
+          const uint32_t before = static_cast<uint32_t>(use & 1);
+          ++use;
+          done = __all_sync(0xffffffffu, wait_bounded(acc_full + 8u * (use & 1), (use >> 1) & 1u, status));
+          if (!done) break;
+          tc::tc_fence_after();
+          for (int c = half * kUnit; c < columns; c += 2 * kUnit) {
+            add_columns(rows_at + (before ^ 1u) * kMaxN + c, rows_at + before * kMaxN + c);
+            if (GATED) add_columns(rows_at + (before ^ 1u) * kMaxN + p.bn + c, rows_at + before * kMaxN + p.bn + c);
+          }
+          wait_stored_columns();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(tc::map_to_rank(acc_empty + 8u * before, 0));
+        }
+      }
+      if (!done) break;
+      tc::tc_fence_after();
+      const int b = use & 1;
+      const uint32_t acc = rows_at + static_cast<uint32_t>(b) * kMaxN;
+      const bool any = p.nkb > 0;
       uint32_t sums[kUnit], gated_sums[GATED ? kUnit : 1];
       auto load = [&](int c) {
         load_columns(acc + static_cast<uint32_t>(c), sums);
@@ -569,7 +617,7 @@ __global__ void __launch_bounds__(2 * kRows) piece_sum_kernel(const __grid_const
 }
 
 // Resident clusters of a kernel on the current device, looked up once.
-template <int KIND, bool GATED, bool SPLIT>
+template <int KIND, bool GATED, bool SPLIT, bool LONG>
 cudaError_t resident_clusters(int* out) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
@@ -579,7 +627,7 @@ cudaError_t resident_clusters(int* out) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   int n = known[dev].load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = ff_pair_kernel<KIND, GATED, SPLIT>;
+    auto kern = ff_pair_kernel<KIND, GATED, SPLIT, LONG>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
       return e;
     int sms = 0;
@@ -612,6 +660,9 @@ cudaError_t output_map(CUtensorMap* m, int* usable, const Matrix& o, int64_t M, 
   return encode_tmap_16bit_2d(m, o.p, N, M, o.ld, kUnit, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// K values of a ring slot.
+int slot_depth(int width) { return width <= kNarrowN ? 2 * kBK : kBK; }
+
 template <int KIND>
 cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   const bool gated = t.form == kGated;
@@ -624,7 +675,7 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   p->tiles_m = static_cast<int>((t.M + 2 * kRows - 1) / (2 * kRows));
   p->tiles_n = static_cast<int>((t.N + p->bn - 1) / p->bn);
   // A narrow tile's last slot may reach past K: its copies read zeros there.
-  const int depth = mma_n <= kNarrowN ? 2 * kBK : kBK;
+  const int depth = slot_depth(mma_n);
   const int blocks = static_cast<int>((t.K + depth - 1) / depth);
   p->nkb_first = blocks;
   p->nkb = t.form == kJoined ? 2 * blocks : blocks;
@@ -634,6 +685,7 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
     p->split_blocks = (blocks + splits - 1) / splits;
     p->splits = (blocks + p->split_blocks - 1) / p->split_blocks;
   }
+  p->acc_blocks = static_cast<int>(kMaxPiece) / depth;
   p->a_k_major = t.A.k_major;
   p->b_k_major = t.B.k_major;
   p->b_boxes = (mma_n / 2 + 63) / 64;
@@ -668,10 +720,10 @@ cudaError_t fill(PairProblem* p, const Task& t, int mma_n, int splits) {
   return output_map(&p->z2, &p->z2_tma, t.Z2, t.M, t.N);
 }
 
-template <int KIND, bool GATED, bool SPLIT>
+template <int KIND, bool GATED, bool SPLIT, bool LONG>
 cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, int n) {
   int resident = 0;
-  cudaError_t e = resident_clusters<KIND, GATED, SPLIT>(&resident);
+  cudaError_t e = resident_clusters<KIND, GATED, SPLIT, LONG>(&resident);
   if (e != cudaSuccess) return e;
   PairParams params;
   memset(&params, 0, sizeof(params));
@@ -705,7 +757,7 @@ cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, in
   sums.first[kMaxProblems] = static_cast<unsigned>(blocks);
   params.first[kMaxProblems] = static_cast<int>(tiles);
   const LaunchShape shape{dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident))), kThreads, 2, kSmemBytes};
-  e = launch_early(c.stream, shape, ff_pair_kernel<KIND, GATED, SPLIT>, params);
+  e = launch_early(c.stream, shape, ff_pair_kernel<KIND, GATED, SPLIT, LONG>, params);
   if (!SPLIT || e != cudaSuccess || blocks == 0) return e;
   return launch_early(c.stream, {dim3(static_cast<unsigned>(blocks)), 2 * kRows, 1, 0}, piece_sum_kernel<KIND>, sums);
 }
@@ -797,13 +849,32 @@ size_t weight_partial_bytes(int64_t M, int64_t N, int64_t K, int weights) {
   return static_cast<size_t>(most < kPairs ? most : kPairs) * kMaxN * kMaxN * 4;
 }
 
+namespace {
+
+// Whether a tile's sum is longer than an accumulator takes.
+bool long_sum(const Task& t, const PairPlan& plan) {
+  const int64_t depth = slot_depth(plan.width), blocks = (t.K + depth - 1) / depth;
+  const int64_t piece = t.form == kJoined ? 2 * blocks : t.split ? (blocks + plan.splits - 1) / plan.splits : blocks;
+  return piece > kMaxPiece / depth;
+}
+
+template <int KIND>
+cudaError_t run(const Context& c, const Task* tasks, const PairPlan& plan, int n) {
+  bool any_long = false;
+  for (int i = 0; i < n; ++i) any_long = any_long || long_sum(tasks[i], plan);
+  if (tasks[0].form == kGated)
+    return any_long ? launch<KIND, true, false, true>(c, tasks, plan, n)
+                    : launch<KIND, true, false, false>(c, tasks, plan, n);
+  if (any_long) return launch<KIND, false, true, true>(c, tasks, plan, n);
+  return plan.splits > 1 ? launch<KIND, false, true, false>(c, tasks, plan, n)
+                         : launch<KIND, false, false, false>(c, tasks, plan, n);
+}
+
+}  // namespace
+
 cudaError_t run_pair(const Context& c, const Task* tasks, const PairPlan& plan, int n) {
   if (n == 0) return cudaSuccess;
-  if (tasks[0].form == kGated)
-    return c.kind == kBf16 ? launch<kBf16, true, false>(c, tasks, plan, n) : launch<kF16, true, false>(c, tasks, plan, n);
-  if (plan.splits > 1)
-    return c.kind == kBf16 ? launch<kBf16, false, true>(c, tasks, plan, n) : launch<kF16, false, true>(c, tasks, plan, n);
-  return c.kind == kBf16 ? launch<kBf16, false, false>(c, tasks, plan, n) : launch<kF16, false, false>(c, tasks, plan, n);
+  return c.kind == kBf16 ? run<kBf16>(c, tasks, plan, n) : run<kF16>(c, tasks, plan, n);
 }
 
 }  // namespace ff

@@ -409,7 +409,7 @@ int reach_of(int splits, int sms) { return splits <= 2 ? sms : splits == 4 ? sms
 }  // namespace
 
 RowsPlan plan_rows(const Task* tasks, int n, int sms) {
-  constexpr double kNextCta = 1.5;
+  constexpr double kNextCta = 1.5, kNever = 1e30;
   RowsPlan plan;
   plan.cost = 0.0;
   bool one_wave = false;
@@ -418,6 +418,7 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
     int tm[kMaxProblems] = {};
     int64_t ctas = 0;
     double longest = 0.0, work = 0.0, feed = 0.0;
+    bool too_long = false;
     for (int i = 0; i < n; ++i) {
       const Task& t = tasks[i];
       const int weights = t.form == kGated ? 2 : 1;
@@ -426,6 +427,7 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
         longest = -1.0;  // fewer than two blocks to a CTA
         break;
       }
+      too_long = too_long || (blocks + splits - 1) / splits > kMaxPiece / kBK;
       // Equal shares of M: the fewest tiles that hold 256 sums per TMEM lane, or tiles of fewer rows.
       const int64_t fewest = (t.M * weights + 255) / 256;
       double best = 0.0;
@@ -452,7 +454,8 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
       feed += chosen.feed;
     }
     if (longest < 0.0) break;
-    if (splits > 1 && ctas > 2 * reach) break;
+    if (plan.cost > 0.0 && ctas > 2 * reach) break;
+    if (too_long) continue;
     // CTAs beyond the first on each SM: as long as the average, and their own start.
     const double average = work / static_cast<double>(ctas);
     double time = longest + static_cast<double>((ctas - 1) / reach) * (average + kNextCta);
@@ -465,6 +468,10 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
       for (int i = 0; i < n; ++i) plan.tile[i].tm = tm[i];
       one_wave = ctas <= reach;
     }
+  }
+  if (plan.cost == 0.0) {  // a CTA's sum would be longer than its accumulator takes
+    plan.cost = kNever;
+    return plan;
   }
   for (int i = 0; i < n; ++i) {
     const Task& t = tasks[i];
