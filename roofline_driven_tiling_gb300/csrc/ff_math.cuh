@@ -149,15 +149,21 @@ __device__ __forceinline__ uint64_t act_pair(uint64_t z) {
   return z;
 }
 
-// z within [-100, 100]; a NaN stays.
-__device__ __forceinline__ float within_100(float z) {
+// max(z, -100) and min(z, 100); a NaN stays.
+__device__ __forceinline__ float least_100(float z) {
   float x;
-  asm("max.NaN.f32 %0, %1, 0fC2C80000;\n\tmin.NaN.f32 %0, %0, 0f42C80000;" : "=f"(x) : "f"(z));
+  asm("max.NaN.f32 %0, %1, 0fC2C80000;" : "=f"(x) : "f"(z));
+  return x;
+}
+__device__ __forceinline__ float most_100(float z) {
+  float x;
+  asm("min.NaN.f32 %0, %1, 0f42C80000;" : "=f"(x) : "f"(z));
   return x;
 }
 
 // Both act(z) and act'(z) of two values, from one exponential each. From |z| = 100 on every slope
-// here is exactly 0 or 1 in FP32 (e^100 overflows), so slopes take z clamped there: no product is 0 times infinity.
+// here is exactly 0 or 1 in FP32 (e^100 overflows), so slopes take z clamped there, and values take it
+// clamped below (binary16 keeps a gate of -70000 as -inf): no product is 0 times infinity.
 template <int ACT>
 __device__ __forceinline__ void act_pair_slope(uint64_t z, uint64_t& value, uint64_t& slope) {
   const float2 f = halves(z);
@@ -168,7 +174,9 @@ __device__ __forceinline__ void act_pair_slope(uint64_t z, uint64_t& value, uint
     value = positive_of(z);
     slope = pack2(f.x <= 0.0f ? 0.0f : 1.0f, f.y <= 0.0f ? 0.0f : 1.0f);
   } else {
-    const uint64_t x = pack2(within_100(f.x), within_100(f.y)), x2 = mul2(x, x), one = both(1.0f);
+    const float2 low = make_float2(least_100(f.x), least_100(f.y));
+    z = pack2(low.x, low.y);
+    const uint64_t x = pack2(most_100(low.x), most_100(low.y)), x2 = mul2(x, x), one = both(1.0f);
     if constexpr (ACT == T2S_ACT_GELU) {
       // P(x) + x p(x) with the normal distribution P and its density p.
       const float2 c = halves(x);
