@@ -83,21 +83,21 @@ __device__ __forceinline__ uint4 narrow(const uint64_t (&v)[kPairs]) {
 // chunk x, 256 / kGroups at a time; dZ's rows are 16-byte aligned and padded to whole words. With db the
 // chunks are a cluster's CTAs: each leaves its column sums in its shared memory, and the first adds them in
 // rank order. With partials each block leaves its column sums there, a row per chunk, for db_sum_kernel.
+// Rows and columns are 32-bit (T2S_MAX_DIM is 2^30): with 64-bit ones gelu's slope spills at four blocks to an SM.
 template <int KIND, int ACT, int kGroups>
 __global__ void __launch_bounds__(kThreads, 4)
-    act_backward_kernel(int64_t M, int64_t N, int64_t chunk, Source dy, Source z, uint16_t* dZ, int64_t lddz,
+    act_backward_kernel(int M, int N, int chunk, Source dy, Source z, uint16_t* dZ, int64_t lddz,
                         uint16_t* db, float* partials) {
   constexpr int kColumns = kGroups * kVec, kLanes = kThreads / kGroups;
   __shared__ float sums[kLanes][kColumns + 1];
   __shared__ float column[kColumns];
   wait_for_earlier_kernels();
   const int group = threadIdx.x % kGroups, row = threadIdx.x / kGroups;
-  const int64_t m1 = min((blockIdx.x + 1) * chunk, M);
-  for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * kColumns; c0 < N;
-       c0 += static_cast<int64_t>(gridDim.y) * kColumns) {
-    const int64_t c = c0 + group * kVec;
+  const int x = static_cast<int>(blockIdx.x), m1 = min((x + 1) * chunk, M);
+  for (int c0 = static_cast<int>(blockIdx.y) * kColumns; c0 < N; c0 += static_cast<int>(gridDim.y) * kColumns) {
+    const int c = c0 + group * kVec;
     uint64_t sum[kPairs] = {};
-    auto take = [&](int64_t m, const uint4& wy, const uint4& wz) {
+    auto take = [&](int m, const uint4& wy, const uint4& wz) {
       uint64_t d[kPairs];
       widen<KIND>(wy, d);
       if constexpr (ACT != T2S_ACT_NONE) {
@@ -116,9 +116,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) sum[i] = add2(sum[i], d[i]);
       }
-      if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + m * lddz + c) = narrow<KIND>(d);
+      if (dZ != nullptr) *reinterpret_cast<uint4*>(dZ + static_cast<int64_t>(m) * lddz + c) = narrow<KIND>(d);
     };
-    int64_t m = blockIdx.x * chunk + row;
+    int m = x * chunk + row;
     if (dy.wide && (ACT == T2S_ACT_NONE || z.wide) && c + kVec <= N) {
       // Two rows' loads before the first row's arithmetic, four blocks to an SM (4096^2 with gelu
       // 16.6 us, floor 9.9; four rows and three blocks 19.2).
@@ -127,8 +127,9 @@ __global__ void __launch_bounds__(kThreads, 4)
         uint4 wy[kAhead], wz[kAhead] = {};
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          wy[j] = *reinterpret_cast<const uint4*>(dy.p + (m + j * kLanes) * dy.ld + c);
-          if (ACT != T2S_ACT_NONE) wz[j] = *reinterpret_cast<const uint4*>(z.p + (m + j * kLanes) * z.ld + c);
+          wy[j] = *reinterpret_cast<const uint4*>(dy.p + static_cast<int64_t>(m + j * kLanes) * dy.ld + c);
+          if (ACT != T2S_ACT_NONE)
+            wz[j] = *reinterpret_cast<const uint4*>(z.p + static_cast<int64_t>(m + j * kLanes) * z.ld + c);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) take(m + j * kLanes, wy[j], wz[j]);
@@ -150,14 +151,15 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
       for (int r = 0; r < kLanes; ++r) total += sums[r][threadIdx.x];
       column[threadIdx.x] = total;
-      if (partials != nullptr && c0 + threadIdx.x < N) partials[blockIdx.x * N + c0 + threadIdx.x] = total;
+      if (partials != nullptr && c0 + static_cast<int>(threadIdx.x) < N)
+        partials[static_cast<int64_t>(x) * N + c0 + threadIdx.x] = total;
     }
     if (partials != nullptr) {
       __syncthreads();
       continue;
     }
     cluster_sync_all();
-    if (cluster_ctarank() == 0 && threadIdx.x < kColumns && c0 + threadIdx.x < N) {
+    if (cluster_ctarank() == 0 && threadIdx.x < kColumns && c0 + static_cast<int>(threadIdx.x) < N) {
       // All CTAs' sums on their way before the first is added.
       float part[kMaxChunks], total = 0.0f;
 #pragma unroll
@@ -329,8 +331,8 @@ cudaError_t run_act_backward(const Context& c, int64_t M, int64_t N, int act, co
     auto kern = groups == 8
                     ? (c.kind == kBf16 ? act_backward_kernel<kBf16, kAct, 8> : act_backward_kernel<kF16, kAct, 8>)
                     : (c.kind == kBf16 ? act_backward_kernel<kBf16, kAct, 4> : act_backward_kernel<kF16, kAct, 4>);
-    return launch_early(c.stream, shape, kern, M, N, chunk, source(dY, lddy), source(Z, ldz), dZ, lddz,
-                        clustered ? db : nullptr, parts);
+    return launch_early(c.stream, shape, kern, static_cast<int>(M), static_cast<int>(N), static_cast<int>(chunk),
+                        source(dY, lddy), source(Z, ldz), dZ, lddz, clustered ? db : nullptr, parts);
   });
   if (e != cudaSuccess || parts == nullptr) return e;
   return launch_early(c.stream, {dim3(static_cast<unsigned>((N + 31) / 32)), 32 * kSumWarps, 1, 0},
