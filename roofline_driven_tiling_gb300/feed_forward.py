@@ -163,6 +163,8 @@ def _workspace(given, need, device, stream):
         return given, given.data_ptr(), need
     if not isinstance(given, _Tensor) or not given.is_cuda or not given.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
+    if given.get_device() != device.index:
+        raise ValueError("workspace must be on the device of the other tensors")
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
