@@ -16,6 +16,9 @@ of a tensor whose width is a multiple of 8.
 ``act`` is "none", "relu", "silu", "gelu" (erf) or "gelu_tanh". ``out`` may be the residual
 itself. Outputs and workspaces that are not passed are allocated by torch. The work runs on
 ``stream`` (the integer value of a cudaStream_t; default: torch's current stream).
+
+No autograd history is recorded: ``linear`` and ``gated_linear`` refuse tensors that require grad
+unless gradients are off (``torch.no_grad()``); the gradients are the backward functions' results.
 """
 from __future__ import annotations
 
@@ -33,6 +36,7 @@ _FUNCTIONS = {}
 # A single token's call lasts a few microseconds on the device: what surrounds the launch is kept short.
 _Tensor, _strided = torch.Tensor, torch.empty_strided
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_grad_enabled = torch.is_grad_enabled
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -66,6 +70,11 @@ def _first(t, name):
         raise ValueError("%s must be 2-D" % name)
     rows, cols = size
     return dtype, t.device, index, t.data_ptr(), _row_stride(t, name, rows, cols), rows, cols
+
+
+def _refuse_history(name):
+    raise ValueError("%s records no autograd history, and an input requires grad: call it under torch.no_grad() and "
+                     "%s_backward for the gradients" % (name, name))
 
 
 def _refuse(t, name, dtype):
@@ -177,6 +186,9 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, wo
     rp, ldr = (None, N) if residual is None else _matrix(residual, "residual", dtype, index, (M, N))
     zp, ldz = (None, N) if preact is None else _matrix(preact, "preact", dtype, index, (M, N))
     code = _act(act)
+    if _grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
+                            or (residual is not None and residual.requires_grad)):
+        _refuse_history("linear")
     if out is None:
         out = _new((M, N), (N, 1), dtype, device, stream)
         yp, ldy = out.data_ptr(), N
@@ -255,6 +267,8 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, preact=None, workspace=N
         zg, ldzg = _matrix(preact[0], "preact[0]", dtype, index, (M, N))
         zu, ldzu = _matrix(preact[1], "preact[1]", dtype, index, (M, N))
     code = _act(act)
+    if _grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+        _refuse_history("gated_linear")
     if out is None:
         out = _new((M, N), (N, 1), dtype, device, stream)
         hp, ldh = out.data_ptr(), N
