@@ -769,69 +769,130 @@ cudaError_t launch(const Context& c, const Task* tasks, const PairPlan& plan, in
 // all SMs together compute 1.8 PFLOP/s (the power limit) and take in 16 TB/s; starting up, and a last
 // tile's epilogue, take the rest.
 PairPlan plan_pair(const Task* tasks, int n, int pairs, size_t partial_bytes) {
-  static const struct {
+  struct Width {
     int n;
     double block;
-  } kWidths[] = {{64, 0.158}, {128, 0.17}, {192, 0.215}, {224, 0.235}, {256, 0.26}};
+  };
+  static constexpr Width kWidths[] = {{64, 0.158}, {128, 0.17}, {192, 0.215}, {224, 0.235}, {256, 0.26}};
   // Pieces of a sum have eight K blocks at least (their stores take as long as four), and there is room
   // for them. Adding the pieces is a launch more, and their way through the L2 cache: fitted to dW of 256^2
   // to 1024^2 weights from 4096 to 65536 rows in 2 to 19 pieces (most within 10 %).
   constexpr int kLeastBlocks = 8;
   constexpr double kSumLaunch = 1.2, kSumPiece = 0.03;
+  constexpr double kNextTile = 0.3, kCutTile = 0.8;  // a tile that others follow, and a piece with its stores
   PairPlan plan;
   int64_t longest = 0;
   for (int i = 0; i < n; ++i)
     if (tasks[i].split && longest < tasks[i].K) longest = tasks[i].K;
   const int64_t most_splits = partial_bytes > 0 ? longest / (kLeastBlocks * kBK) : 1;
-  for (const auto& w : kWidths) {
-    int64_t tiles[kMaxProblems] = {};
-    double blocks[kMaxProblems] = {}, flops = 0.0, bytes = 0.0;
+
+  // The tiles of one width, and what no number of pieces makes shorter.
+  struct Way {
+    int width;
+    double block, least;
+    int64_t tiles[kMaxProblems], blocks[kMaxProblems], cut_tiles, cut_blocks;
+    double whole_work, cut_work;  // SM pairs' time for the products that stay whole, and that are cut
+  };
+  Way ways[sizeof(kWidths) / sizeof(kWidths[0])];
+  int n_ways = 0;
+  for (const Width& w : kWidths) {
+    Way& way = ways[n_ways];
+    way.width = w.n, way.block = w.block;
+    way.cut_tiles = way.cut_blocks = 0;
+    way.whole_work = way.cut_work = 0.0;
+    double flops = 0.0, bytes = 0.0;
     bool whole = true;
     for (int i = 0; i < n; ++i) {
       const Task& t = tasks[i];
       const int bn = t.form == kGated ? w.n / 2 : w.n;
       if (bn % kUnit != 0) whole = false;  // the epilogue takes whole groups of columns
-      blocks[i] = static_cast<double>((t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1));
-      tiles[i] = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + bn - 1) / bn);
-      flops += static_cast<double>(tiles[i]) * blocks[i] * 2.0 * 2 * kRows * w.n * kBK;
-      bytes += static_cast<double>(tiles[i]) * blocks[i] * (2 * kABytes + w.n * kBK * 2);
+      way.blocks[i] = (t.K + kBK - 1) / kBK * (t.form == kJoined ? 2 : 1);
+      way.tiles[i] = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + bn - 1) / bn);
+      const double units = static_cast<double>(way.tiles[i]) * static_cast<double>(way.blocks[i]);
+      flops += units * 2.0 * 2 * kRows * w.n * kBK;
+      bytes += units * (2 * kABytes + w.n * kBK * 2);
+      if (t.split) {
+        way.cut_tiles += way.tiles[i];
+        way.cut_work += units * w.block;
+        if (way.cut_blocks < way.blocks[i]) way.cut_blocks = way.blocks[i];
+      } else {
+        way.whole_work += units * w.block + static_cast<double>(way.tiles[i]) * kNextTile;
+      }
     }
     if (!whole) continue;
-    double least = flops / 1.8e9;
-    if (least < bytes / 16e6) least = bytes / 16e6;
-    for (int splits = 1; splits == 1 || splits <= most_splits; ++splits) {
-      int64_t first[kMaxProblems + 1] = {}, pieces = 0;
-      double tile_time[kMaxProblems] = {};
-      for (int i = 0; i < n; ++i) {
-        const bool cut = splits > 1 && tasks[i].split;
-        first[i + 1] = first[i] + tiles[i] * (cut ? splits : 1);
-        tile_time[i] = cut ? static_cast<double>((static_cast<int64_t>(blocks[i]) + splits - 1) / splits) * w.block + 0.8
-                           : blocks[i] * w.block + 0.3;
-        if (cut) pieces += tiles[i] * splits;
+    way.least = flops / 1.8e9;
+    if (way.least < bytes / 16e6) way.least = bytes / 16e6;
+    ++n_ways;
+  }
+
+  // What is added to the longest share: the launch, and with pieces the second launch and their way.
+  auto around = [&](const Way& w, int64_t splits) {
+    double time = 4.1 + 0.006 * w.width;
+    if (splits > 1)
+      time += kSumLaunch + kSumPiece * static_cast<double>(splits) +
+              static_cast<double>(w.cut_tiles * splits) * (2 * kRows * 4.0 / 5e6) * w.width;
+    return time;
+  };
+  auto room = [&](const Way& w, int64_t splits) {
+    return splits == 1 ||
+           static_cast<size_t>(w.cut_tiles * splits) * 2 * kRows * static_cast<size_t>(w.width) * 4 <= partial_bytes;
+  };
+  auto consider = [&](const Way& w, int64_t splits) {
+    int64_t first[kMaxProblems + 1] = {};
+    double tile_time[kMaxProblems] = {};
+    for (int i = 0; i < n; ++i) {
+      const bool cut = splits > 1 && tasks[i].split;
+      first[i + 1] = first[i] + w.tiles[i] * (cut ? splits : 1);
+      tile_time[i] = cut ? static_cast<double>((w.blocks[i] + splits - 1) / splits) * w.block + kCutTile
+                         : static_cast<double>(w.blocks[i]) * w.block + kNextTile;
+    }
+    // The longest share: pair j has the tiles j, j + pairs, ... of all products in turn, and a product
+    // gives the pairs from its first tile's on one more than the others. So the longest begins where a
+    // product begins.
+    double time = w.least;
+    for (int i = 0; i < n; ++i) {
+      const int64_t j = first[i] % pairs;
+      auto before = [&](int64_t end) { return end > j ? (end - j + pairs - 1) / pairs : 0; };
+      double share = -kNextTile;
+      int64_t done = before(first[0]);
+      for (int k = 0; k < n; ++k) {
+        const int64_t next = before(first[k + 1]);
+        share += static_cast<double>(next - done) * tile_time[k];
+        done = next;
       }
-      const size_t room = static_cast<size_t>(pieces) * 2 * kRows * w.n * 4;
-      if (room > partial_bytes) break;
-      // The longest share: pair j has the tiles j, j + pairs, ... of all products in turn, and a product
-      // gives the pairs from its first tile's on one more than the others. So the longest begins where a
-      // product begins.
-      double time = 0.0;
-      for (int i = 0; i < n; ++i) {
-        const int64_t j = first[i] % pairs;
-        double share = -0.3;
-        for (int k = 0; k < n; ++k) {
-          auto before = [&](int64_t end) { return end > j ? (end - j + pairs - 1) / pairs : 0; };
-          share += static_cast<double>(before(first[k + 1]) - before(first[k])) * tile_time[k];
-        }
-        if (time < share) time = share;
-      }
-      if (time < least) time = least;
-      time += 4.1 + 0.006 * w.n;
-      if (pieces > 0) time += kSumLaunch + kSumPiece * splits + static_cast<double>(room) / 5e6;
-      if (plan.cost == 0.0 || (splits == 1 ? time <= plan.cost : time < plan.cost)) {
-        plan.cost = time;
-        plan.width = w.n;
-        plan.splits = splits;
-      }
+      if (time < share) time = share;
+    }
+    time += around(w, splits);
+    if (plan.cost == 0.0 || (splits == 1 ? time <= plan.cost : time < plan.cost)) {
+      plan.cost = time;
+      plan.width = w.width;
+      plan.splits = static_cast<int>(splits);
+    }
+  };
+
+  for (int i = 0; i < n_ways; ++i) consider(ways[i], 1);
+  if (most_splits < 2) return plan;
+  // One round of the pairs first: near the best, it rules out most of the other counts by two bounds. A piece's
+  // own time falls with their number, so that the counts begin where it fits; the rest only grows with it, and
+  // they end where that alone is longer. The choice is the same as without the bounds (enqueueing the gradients of a
+  // 64 x 64 weight over 65536 rows took 31 us, gated 40 to 50, and takes 18 to 21 as with few rows).
+  for (int i = 0; i < n_ways; ++i) {
+    int64_t once = pairs / ways[i].cut_tiles;
+    if (once > most_splits) once = most_splits;
+    if (once > 1 && room(ways[i], once)) consider(ways[i], once);
+  }
+  for (int i = 0; i < n_ways; ++i) {
+    const Way& w = ways[i];
+    const double fits = plan.cost - around(w, 2) + kNextTile - kCutTile;  // for the blocks of one piece
+    if (fits <= 0.0) continue;
+    int64_t splits = static_cast<int64_t>(static_cast<double>(w.cut_blocks) * w.block / fits);
+    if (splits < 2) splits = 2;
+    for (; splits <= most_splits && room(w, splits); ++splits) {
+      double bound =
+          (w.whole_work + w.cut_work + static_cast<double>(w.cut_tiles * splits) * kCutTile) / pairs - kNextTile;
+      if (bound < w.least) bound = w.least;
+      if (bound + around(w, splits) >= plan.cost) break;
+      consider(w, splits);
     }
   }
   return plan;
