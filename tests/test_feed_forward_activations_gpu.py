@@ -81,6 +81,28 @@ def test_gelu(dtype, m):
     assert binding.device_status() == binding.T2S_OK
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("act,lo", [("silu", -60), ("gelu_tanh", -8)])
+def test_logistic_activations(dtype, act, lo):
+    """Down to where their logistic factor is 2^-87 and 2^-72; slopes but around their zeros."""
+    for first, last in ((lo, -2), (-2, -2.0 ** -6), (2.0 ** -6, 12)):
+        z = numbers(dtype, first, last)
+        n, z64 = z.numel(), z.double()
+        c, a = math.sqrt(2 / math.pi), 0.044715
+        v, dv = (z64, 1.0) if act == "silu" else (2 * c * (z64 + a * z64 ** 3), 2 * c * (1 + 3 * a * z64 ** 2))
+        s = torch.sigmoid(v)
+        value, slope = z64 * s, s + z64 * s * torch.sigmoid(-v) * dv
+        x, w = torch.zeros(1, 8, dtype=dtype, device="cuda"), torch.zeros(8, n, dtype=dtype, device="cuda")
+        x[:, 0], w[0] = 1, z
+        check(t2s.linear(x, w, act=act)[0], value, dtype)
+        one, zz = torch.ones(1, n, dtype=dtype, device="cuda"), z.view(1, n).clone()
+        _, dg, du = t2s.gated_linear_backward(one, x, w, w, (zz, one), act=act, dx=False)
+        check(du[0], value, dtype)
+        if first != -2:
+            check(dg[0], slope, dtype, 2.0 ** -13)
+    assert binding.device_status() == binding.T2S_OK
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
 def test_pre_activations_beyond_the_type(act):
     """A gate of -70000 is kept as -inf in binary16: its activation and slope are 0, forward and backward."""
