@@ -46,8 +46,8 @@
  *  - T2S_ERR_CUDA:      a CUDA runtime or driver call failed (for example no
  *                       sm_103a device, or a launch error); the CUDA error code
  *                       is available from t2s_last_cuda_error().
- *  - T2S_ERR_WORKSPACE: the workspace passed to t2s_gemm_f32_tf32x3 is NULL
- *                       or smaller than t2s_gemm_f32_tf32x3_workspace_size().
+ *  - T2S_ERR_WORKSPACE: the workspace passed to an entry point that takes one is
+ *                       NULL, smaller than it needs or not aligned as it states.
  *  - T2S_ERR_TOO_LARGE: only from t2s_gemm_f32_tf32x3_noalloc: the problem needs
  *                       more scratch than its built-in array holds.
  *  - T2S_ERR_TIMEOUT:   only from t2s_device_status(): a kernel gave up a

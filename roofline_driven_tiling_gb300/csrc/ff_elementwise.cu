@@ -7,8 +7,8 @@
 // dZ, dG and dU are rounded to the 16-bit type: they are the tensor-core operands of the weight
 // and input gradients. db sums the FP32 values before that rounding, in an order that depends on
 // the sizes alone. Bound by memory: every value is read or written once, 16 bytes per access
-// where rows allow it (4096^2: db alone with relu 10.1 us, with gelu 15.8, floor 9.9 from HBM; dG and dU about
-// 26 us, floor 24.7).
+// where rows allow it (4096^2, from HBM: db alone with relu 16.1 us, with gelu 19.1, floor 10.0; both inputs fit
+// the L2 cache, and from there it is 9.5 and 14.9, gelu's arithmetic; dG and dU with silu 28 us, floor 25.1).
 //
 // Inputs are read with plain loads (no __restrict__): these kernels may start before the one that
 // writes them has ended (wait_for_earlier_kernels), which read-only loads do not allow for.
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     };
     int m = x * chunk + row;
     if (dy.wide && (ACT == T2S_ACT_NONE || z.wide) && c + kVec <= N) {
-      // Two rows' loads before the first row's arithmetic, four blocks to an SM (4096^2 with gelu
-      // 16.6 us, floor 9.9; four rows and three blocks 19.2).
+      // Two rows' loads before the first row's arithmetic, four blocks to an SM (four rows and three blocks
+      // were 16 % slower at 4096^2 with gelu).
       constexpr int kAhead = 2;
       for (; m + (kAhead - 1) * kLanes < m1; m += kAhead * kLanes) {
         uint4 wy[kAhead], wz[kAhead] = {};
@@ -289,7 +289,7 @@ cudaError_t run_copies(const Context& c, const Copy* copies, int n) {
 namespace {
 
 // Rows in pieces of 128 bytes where there are blocks enough for the SMs, of 64 bytes otherwise (db of
-// 4096^2 with relu 9.1 us against 11.1; of 1000^2 with gelu 6.4 against 4.3).
+// 4096^2 with relu is 18 % shorter in pieces of 128, of 1000^2 with gelu a third shorter in pieces of 64).
 int groups_of(int64_t N) { return N >= 2048 ? 8 : 4; }
 
 int64_t column_blocks(int64_t N) { return (N + groups_of(N) * kVec - 1) / (groups_of(N) * kVec); }
@@ -303,8 +303,8 @@ int64_t many_chunks(int64_t M, int64_t N) {
 }
 
 // db from partial sums and a second launch where a cluster's eight CTAs per column block are too few to
-// keep HBM busy (dZ, db and a 64-wide dX of 16384x1024 54 -> 34 us, 16384x512 31 -> 17, 16384x64 15 -> 10,
-// 8192x1024 19 -> 17; but 8192x512 13.4 -> 14.0, 4096x1024 14.3 -> 14.7, 512x1024 8.1 -> 8.5).
+// keep HBM busy (dZ, db and a 64-wide dX of 16384x1024 54 -> 34 us, 16384x512 31 -> 17, 16384x64 15 -> 8,
+// 8192x1024 19 -> 16; but 8192x512 13.4 -> 14.0, 4096x1024 14.3 -> 14.7, 512x1024 8.1 -> 8.5).
 bool two_stages(int64_t M, int64_t N) { return M >= 16384 || M * N >= 1 << 23; }
 
 }  // namespace

@@ -10,19 +10,19 @@
 // values x rows) or K rows of outputs (MN-major boxes of 64 outputs x 64 K rows), both in
 // 128-byte swizzle. That covers X W, dZ W^T and X^T dZ for weights of either order.
 //
-// What bounds it: at large sizes the tensor cores under the power limit (8192^3 627-635 us, 1733-1753
-// TFLOP/s; the library's product of the same size 614-630), with the last round of tiles on top (4096^3:
-// 256 tiles on 76 pairs, 84-85 us, 1610-1630 TFLOP/s; with gelu_tanh, bias and saved pre-activations
-// 91-92). Below about K = 1024 the epilogue: a 256 x 256 tile leaves the SM in about 2.2 us, 2.2 us more
-// with gelu and 2 us more with a residual, against 0.26 us per K block (8192x256x2048 13.5 us, with gelu,
-// bias and residual 30.6). A K block needs 64 bytes a clock into each SM, what its port takes; narrower
-// tiles need more, so widths below 256 are for sizes that do not fill the pairs.
+// What bounds it (sizes are rows x inputs x outputs, times those of the device in a captured graph with
+// everything in the L2 cache that fits there): at large sizes the tensor cores under the power limit (8192^3
+// 616-639 us, 1720-1785 TFLOP/s; torch.mm of the same size 590-634), with the last round of tiles on top
+// (4096^3: 256 tiles on 76 pairs, 77 us on a GPU that was idle, 84-85 among other large products; with gelu_tanh,
+// bias and saved pre-activations 82-92). Below about K = 1024 the epilogue: a 256 x 256 tile leaves the SM in about
+// 2.2 us, 2.2 us more with gelu and 2 us more with a residual, against 0.26 us per K block (8192x256x2048
+// 13.3 us, with gelu, bias and residual 30.5). A K block needs 64 bytes a clock into each SM, what its port
+// takes; narrower tiles need more, so widths below 256 are for sizes that do not fill the pairs.
 //
 // A small weight's gradient over many rows has too few tiles for the pairs (1024 x 1024: 16), so its sum is
 // cut into pieces along K: the pieces are tiles like any other, their FP32 sums go to the workspace (through
-// L2) and a second launch adds them in their order. Gradients 32768x256x1024 with silu and db 133 -> 59 us,
-// gated 65536x512x512 218 -> 153, 16384x1024x1024 130 -> 119 (floor of
-// both 72).
+// L2) and a second launch adds them in their order. Gradients 32768x1024x256 with silu and db 133 -> 58 us,
+// gated 65536x512x512 218 -> 150, 16384x1024x1024 130 -> 115-118 (floor of both 72).
 //
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the next tile's MMAs.
 // Six ring slots of 32 KB leave 35 KB for the epilogue's boxes; five cost 1.5 % at 4096^3.
@@ -60,7 +60,7 @@ constexpr int kBBytes = kMaxN / 2 * kBK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 // Tiles of up to 128 columns take two K blocks per slot: a slot's waits, commit and copies take longer to issue
 // than a narrow block's MMAs take to run (a K block of 128 columns 0.20 -> 0.17 us, of 64 0.19 -> 0.16;
-// 512x4096x4096 19.3 -> 16.5 us, 256x8192x8192 37.4 -> 32.6 with the widths chosen accordingly).
+// 512x4096x4096 15 % shorter, 256x8192x8192 13 % with the widths chosen accordingly).
 constexpr int kNarrowN = 128;
 constexpr int kNarrowStages = 4;
 constexpr int kNarrowStageBytes = 2 * (kABytes + kBoxBytes);

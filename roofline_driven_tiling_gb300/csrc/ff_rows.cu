@@ -10,9 +10,11 @@
 // time.
 //
 // What bounds it: one pass over the weight through HBM and what a launch takes around it, about 4 us
-// (start-up, the ring's first block, two cluster barriers, the join). 1 x 4096 x 4096 6.2 us (5.4 TB/s),
-// 8 x 8192 x 4096 13.1 (5.1), gated 1 x 4096 x 8192 22.3 (6.0 of the 6.8 TB/s a copy reaches), 64 x 4096
-// x 4096 8.1, 256 x 4096 x 4096 13.1. Without the split over K, on 32 SMs, 1 x 4096 x 4096 takes 14.
+// (start-up, the ring's first block, two cluster barriers, the join). Rows x inputs x outputs on the device,
+// weights from HBM (and, second, from the L2 cache, as a benchmark finds them that repeats one call):
+// 1x4096x4096 8.4 us, 4.0 TB/s (6.2), 8x8192x4096 13.2, 5.1 TB/s (9.0), gated 1x4096x8192 22.3, 6.0 of the
+// 6.7 TB/s that a copy reaches (larger than the L2), 64x4096x4096 10.3 (7.9), 256x4096x4096 15.2 (13.0). Without
+// the split over K, on 32 SMs, 1x4096x4096 takes 14 from the L2 cache.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -381,7 +383,8 @@ cudaError_t launch(const Context& c, const Task* tasks, const RowsPlan& plan, in
 }
 
 // What a product takes this way in tiles of `tm` rows of X with `splits` CTAs along K, in microseconds.
-// Fitted to products of 1 to 1024 rows (within 15 %): a K block of 16 KB of weights takes a CTA 0.16
+// Fitted to products of 1 to 1024 rows with the weights in the L2 cache (within 15 %; with weights
+// from HBM calls of a few rows take 2 to 6 us more): a K block of 16 KB of weights takes a CTA 0.16
 // us, more once X's tile outweighs the weight's (0.175 at 128 rows, 0.26 at 256), the gated form's two
 // weights 0.22 to 0.25; the partial sums' way through shared memory 17 ns a row (gated: 25).
 struct Cost {
@@ -482,8 +485,8 @@ RowsPlan plan_rows(const Task* tasks, int n, int sms) {
     tile.tmem_cols = 32;
     while (tile.tmem_cols < static_cast<uint32_t>(weights * tile.tm)) tile.tmem_cols *= 2;
     // Half of an SM's memory where that holds six slots (then the next call's CTAs can be set up beside
-    // these: linear 8x8192x4096 13.1 us against 14.0 with all of it) or more CTAs are to come; otherwise
-    // a ring over all of it (64x4096x4096: 8.7 against 9.0, 128x4096x4096 10.2 against 11.6).
+    // these: linear 8x8192x4096 6 % shorter than with all of it) or more CTAs are to come; otherwise
+    // a ring over all of it (64x4096x4096 3 % shorter than with half, 128x4096x4096 12 %).
     const int half = 112 * 1024, whole = 200 * 1024, stage = static_cast<int>(tile.stage_bytes);
     const int budget = !one_wave || 6 * stage <= half ? half : whole;
     // The partial sums lie over the ring, so it holds at least those.
