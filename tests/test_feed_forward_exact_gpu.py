@@ -59,3 +59,44 @@ def test_weight_gradients(m, k, n, dtype):
         alone = t2s.gated_linear_backward(dy, x, w, w, (z, up), act="relu", dx=False, dw_gate=False)[2]
         assert torch.equal(alone, dwu)
     assert binding.device_status() == binding.T2S_OK
+
+
+@pytest.mark.parametrize("k", [16383, 16384, 16385, 32768, 32776, 49160])
+@pytest.mark.parametrize("m,n", [(1, 72), (24, 264), (300, 136), (520, 1100)])
+def test_sums_around_an_accumulators_length(m, n, k):
+    """16384 values go to one accumulator; a value more, and several accumulators' worth."""
+    gen = torch.Generator(device="cuda").manual_seed(k)
+
+    def ints(rows, cols):
+        return torch.randint(-2, 3, (rows, cols), generator=gen, device="cuda").half()
+
+    x, bias, r = ints(m, k), ints(1, n).reshape(n), ints(m, n)
+    for wt in (False, True):
+        w, w2 = [ints(n, k).t() if wt else ints(k, n) for _ in range(2)]
+        z, z2 = x.double() @ w.double(), x.double() @ w2.double()
+        kept, g, u = [torch.empty(m, n, dtype=torch.float16, device="cuda") for _ in range(3)]
+        y = t2s.linear(x, w, bias, r, act="relu", preact=kept)
+        assert torch.equal(kept, (z + bias.double()).half())
+        assert torch.equal(y, ((z + bias.double()).clamp(min=0) + r.double()).half())
+        h = t2s.gated_linear(x, w, w2, act="relu", preact=(g, u))
+        assert torch.equal(g, z.half()) and torch.equal(u, z2.half())
+        assert torch.equal(h, (z.clamp(min=0) * z2).half())
+        # The joined gradient's two halves are one sum: dX = dH W^T + dH W2^T where G = U = 1.
+        one = torch.ones(m, k // 2, dtype=torch.float16, device="cuda")
+        a, b = [v[:k // 2].t() for v in (w, w2)]
+        dx = t2s.gated_linear_backward(x[:, :k // 2], r, a, b, (one, one), act="relu", dw_gate=False, dw_up=False)[0]
+        assert torch.equal(dx, (x[:, :k // 2].double() @ (w + w2)[:k // 2].double()).half())
+    assert binding.device_status() == binding.T2S_OK
+
+
+@pytest.mark.parametrize("m", [33000, 70001])
+def test_pieces_longer_than_an_accumulator(m):
+    """36 tiles of a weight leave room for two pieces, each longer than an accumulator takes from 32769 rows on."""
+    k = n = 1536
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x, dy = [torch.randint(-2, 3, (m, k), generator=gen, device="cuda").half() for _ in range(2)]
+    w = torch.zeros(k, n, dtype=torch.float16, device="cuda")
+    want = (x.double().t() @ dy.double()).half()
+    assert torch.equal(t2s.linear_backward(dy, x, w, dx=False)[1], want)
+    assert torch.equal(t2s.linear_backward(dy, x, w.t())[1], want)
+    assert binding.device_status() == binding.T2S_OK
