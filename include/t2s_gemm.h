@@ -439,6 +439,156 @@ int t2s_gated_backward_f16(int64_t M, int64_t N, int64_t K, const uint16_t *dH, 
                            int64_t lddwu, void *workspace, size_t workspace_bytes,
                            t2s_stream_t stream);
 
+/*
+ * Products of 8-bit floating-point operands (not on the pages): e4m3 (T2S_E4M3: 4 exponent and 3
+ * fraction bits, largest value 448, no infinities) or e5m2 (T2S_E5M2: largest value 57344), each
+ * block of 128 values of the sum with an FP32 scale.
+ *
+ * t2s_quantize_fp8_*: X (M x N, bfloat16, binary16 or FP32) in 8 bits, along its rows (Q, M rows of N
+ * bytes, a scale for every 128 values of a row), along its columns (Qt, N rows of M bytes, a scale
+ * for every 128 values of a column), or both from one read; Q or Qt is NULL where it is not wanted.
+ * With `square` 1 a scale is for a block of 128 x 128 values. A block's scale is the least power of
+ * two s, at least 2^-126, with amax / s not above the type's largest value; q = x / s to nearest
+ * even (the quotient is exact, so each value is rounded once). An infinity or NaN in a block makes
+ * its scale and all of its values NaN. The scale of row (square: group of rows) r of Q and block b
+ * is S[r * s_row + b * s_block], that of Qt's St[r * st_row + b * st_block]; no two may share a place.
+ *
+ * t2s_gemm_fp8_bf16, _f16, _f32: C (M x N, bfloat16, binary16 or FP32) = A B^T with A M rows and B N
+ * rows of K 8-bit values: the sum over blocks b of 128 values of K of
+ *     SA[m * sa_row + b * sa_block] * SB[(n / b_group) * sb_row + b * sb_block] * (A_b B_b^T)[m, n];
+ * b_group is 1 (every row of B has scales) or 128 (a scale for 128 x 128). A and B may have either
+ * format each, and any scales, in any order of places (strides >= 0; a stride of 0 repeats one). The
+ * tensor cores add a block's 128 products in FP32 (truncating, at most 2^-22 of the block's sum of
+ * magnitudes); blocks are scaled and added in FP32, in an order that the sizes alone decide, and C
+ * is rounded once. A scale that is not finite, or products of scales beyond FP32, give NaN or infinity
+ * as FP32 arithmetic does. Rows of A and B must start on 16-byte boundaries (pointer, and lda, ldb
+ * multiples of 16 where there is more than one row); bytes between rows are not read.
+ * C's rows have ldc values. K = 0 sets C to 0. Otherwise the common contract and return codes at the
+ * top apply (asynchronous on `stream`, no allocation, no workspace), with programmatic launches as above.
+ */
+#define T2S_E4M3 0
+#define T2S_E5M2 1
+
+int t2s_quantize_fp8_bf16(int64_t M, int64_t N, const uint16_t *X, int64_t ldx, int format, int square,
+                          uint8_t *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_block,
+                          uint8_t *Qt, int64_t ldqt, float *St, int64_t st_row, int64_t st_block,
+                          t2s_stream_t stream);
+int t2s_quantize_fp8_f16(int64_t M, int64_t N, const uint16_t *X, int64_t ldx, int format, int square,
+                          uint8_t *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_block,
+                          uint8_t *Qt, int64_t ldqt, float *St, int64_t st_row, int64_t st_block,
+                          t2s_stream_t stream);
+int t2s_quantize_fp8_f32(int64_t M, int64_t N, const float *X, int64_t ldx, int format, int square,
+                          uint8_t *Q, int64_t ldq, float *S, int64_t s_row, int64_t s_block,
+                          uint8_t *Qt, int64_t ldqt, float *St, int64_t st_row, int64_t st_block,
+                          t2s_stream_t stream);
+int t2s_gemm_fp8_bf16(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int format_a,
+                      const float *SA, int64_t sa_row, int64_t sa_block, const uint8_t *B,
+                      int64_t ldb, int format_b, const float *SB, int64_t sb_row, int64_t sb_block,
+                      int b_group, uint16_t *C, int64_t ldc, t2s_stream_t stream);
+int t2s_gemm_fp8_f16(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int format_a,
+                      const float *SA, int64_t sa_row, int64_t sa_block, const uint8_t *B,
+                      int64_t ldb, int format_b, const float *SB, int64_t sb_row, int64_t sb_block,
+                      int b_group, uint16_t *C, int64_t ldc, t2s_stream_t stream);
+int t2s_gemm_fp8_f32(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int format_a,
+                      const float *SA, int64_t sa_row, int64_t sa_block, const uint8_t *B,
+                      int64_t ldb, int format_b, const float *SB, int64_t sb_row, int64_t sb_block,
+                      int b_group, float *C, int64_t ldc, t2s_stream_t stream);
+
+/*
+ * What stands between two blocks of a transformer, on 16-bit types (not on the pages): a norm after
+ * the block, dropout, a gate, the residual sum, and the norm before the next block,
+ *
+ *   n = post(H) * post_weight + post_bias
+ *   r = scale * X + gate * drop(n)             (rounded to 16 bits, R)
+ *   y = norm(r) * weight + bias                (of the rounded r, Y)
+ *
+ * over rows of N values. norm and post are each T2S_NORM_NONE, T2S_NORM_RMS (v / sqrt(mean(v^2) +
+ * eps)) or T2S_NORM_LAYER ((v - mean) / sqrt(variance + eps)). Weights and biases are vectors of N
+ * values, NULL for 1 and 0; without a norm they must be NULL, for `norm` T2S_NORM_NONE Y too. gate
+ * has `gates` rows of N values (gates >= 1, a divisor of M), each for M / gates consecutive rows;
+ * NULL for 1. H NULL: only y = norm(X) is computed; gate, post norm, dropout and R must then be
+ * absent and scale 1. R may be X (with ldr = ldx).
+ *
+ * drop: dropped_of_65536 of 65536 values are dropped on average (0: none, 65536: all), the others
+ * multiplied by 65536 / (65536 - dropped_of_65536). Value (m, n) is dropped where bits
+ * 16 (n % 4) .. 16 (n % 4) + 15 of SplitMix64 output m * ceil(N / 4) + n / 4 of the key are below
+ * dropped_of_65536; the key is output `sequence` of `seed` (output i of seed s: mix(s + (i + 1) *
+ * 0x9E3779B97F4A7C15)). seed_device, if not NULL, is one value in DEVICE memory (8-byte aligned) that
+ * the kernels read in place of `seed`: a captured graph drops other values in every replay that finds
+ * another seed there. What is dropped is 0, also where it was infinite or NaN.
+ *
+ * t2s_residual_norm_backward_*: from dY (NULL where norm is T2S_NORM_NONE), dR (the gradient of r's
+ * other uses, NULL for none), R (what the forward pass wrote, or X where there was no H) and H:
+ *
+ *   d = dR + the gradient of norm at r for dY * weight,   dX = scale * d
+ *   dgate = sum over a gate's rows of d * drop(n),        dn = drop's gradient of d * gate
+ *   dH = the gradient of post at H for dn * post_weight
+ *   dweight, dbias, dpost_weight, dpost_bias: sums over all rows of dY * norm(r), dY, dn * post(H), dn
+ *
+ * Each output that is not wanted is NULL. Without H: dX and the sums for weight and bias only. A
+ * weight's, bias's or gate's gradient may be asked for where the parameter itself is NULL (all ones,
+ * zeros), dgate then with `gates` rows. seed, sequence and dropped_of_65536 are the forward pass's.
+ * R is only needed for a norm; X never.
+ *
+ * t2s_dropout_*: Y = drop(X) + R (R may be NULL; Y may be X or R, with its row stride). Its own
+ * gradient is t2s_dropout of dY with the same seed and sequence, and no R.
+ *
+ * Statistics, sums and arithmetic are FP32 (squares overflow from about 1e19 on), in an order that
+ * sizes, alignment and wanted outputs alone decide; every output is rounded to 16 bits once. eps and
+ * scale are finite, eps >= 0 (0 with a row of zeros gives NaN). Matrices have row strides of at least N
+ * values; any 2-byte alignment is taken (16-byte aligned rows are read with wide loads). Outputs equal to
+ * other arguments are rejected except as said. M = 0: the sums over rows are 0. N = 0: nothing to do.
+ * workspace of the backward pass: a DEVICE buffer, 256-byte aligned, of
+ * t2s_residual_norm_backward_workspace_size(M, N, gates, vectors) bytes, `vectors` the number of
+ * wanted gradients among those of weight, bias, gate, post_weight and post_bias; untouched until the
+ * stream has run the call; calls that may overlap need one each. Otherwise the common contract and return
+ * codes at the top apply (asynchronous on `stream`, no allocation), with programmatic launches as above.
+ */
+#define T2S_NORM_NONE 0
+#define T2S_NORM_RMS 1
+#define T2S_NORM_LAYER 2
+
+size_t t2s_residual_norm_backward_workspace_size(int64_t M, int64_t N, int64_t gates, int vectors);
+
+int t2s_residual_norm_bf16(int64_t M, int64_t N, int norm, int post, const uint16_t *X, int64_t ldx,
+                           const uint16_t *H, int64_t ldh, const uint16_t *weight,
+                           const uint16_t *bias, const uint16_t *post_weight,
+                           const uint16_t *post_bias, const uint16_t *gate, int64_t ldgate,
+                           int64_t gates, float scale, float eps, int dropped_of_65536,
+                           const int64_t *seed_device, int64_t seed, int64_t sequence,
+                           uint16_t *R, int64_t ldr, uint16_t *Y, int64_t ldy, t2s_stream_t stream);
+int t2s_residual_norm_f16(int64_t M, int64_t N, int norm, int post, const uint16_t *X, int64_t ldx,
+                           const uint16_t *H, int64_t ldh, const uint16_t *weight,
+                           const uint16_t *bias, const uint16_t *post_weight,
+                           const uint16_t *post_bias, const uint16_t *gate, int64_t ldgate,
+                           int64_t gates, float scale, float eps, int dropped_of_65536,
+                           const int64_t *seed_device, int64_t seed, int64_t sequence,
+                           uint16_t *R, int64_t ldr, uint16_t *Y, int64_t ldy, t2s_stream_t stream);
+int t2s_residual_norm_backward_bf16(
+    int64_t M, int64_t N, int norm, int post, const uint16_t *dY, int64_t lddy, const uint16_t *dR,
+    int64_t lddr, const uint16_t *R, int64_t ldr, const uint16_t *H, int64_t ldh,
+    const uint16_t *weight, const uint16_t *post_weight, const uint16_t *post_bias,
+    const uint16_t *gate, int64_t ldgate, int64_t gates, float scale, float eps,
+    int dropped_of_65536, const int64_t *seed_device, int64_t seed, int64_t sequence, uint16_t *dX,
+    int64_t lddx, uint16_t *dH, int64_t lddh, uint16_t *dweight, uint16_t *dbias,
+    uint16_t *dpost_weight, uint16_t *dpost_bias, uint16_t *dgate, int64_t lddgate, void *workspace,
+    size_t workspace_bytes, t2s_stream_t stream);
+int t2s_residual_norm_backward_f16(
+    int64_t M, int64_t N, int norm, int post, const uint16_t *dY, int64_t lddy, const uint16_t *dR,
+    int64_t lddr, const uint16_t *R, int64_t ldr, const uint16_t *H, int64_t ldh,
+    const uint16_t *weight, const uint16_t *post_weight, const uint16_t *post_bias,
+    const uint16_t *gate, int64_t ldgate, int64_t gates, float scale, float eps,
+    int dropped_of_65536, const int64_t *seed_device, int64_t seed, int64_t sequence, uint16_t *dX,
+    int64_t lddx, uint16_t *dH, int64_t lddh, uint16_t *dweight, uint16_t *dbias,
+    uint16_t *dpost_weight, uint16_t *dpost_bias, uint16_t *dgate, int64_t lddgate, void *workspace,
+    size_t workspace_bytes, t2s_stream_t stream);
+int t2s_dropout_bf16(int64_t M, int64_t N, const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                     int dropped_of_65536, const int64_t *seed_device, int64_t seed, int64_t sequence,
+                     uint16_t *Y, int64_t ldy, t2s_stream_t stream);
+int t2s_dropout_f16(int64_t M, int64_t N, const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                     int dropped_of_65536, const int64_t *seed_device, int64_t seed, int64_t sequence,
+                     uint16_t *Y, int64_t ldy, t2s_stream_t stream);
+
 /* Static description of a return code. Never NULL. */
 const char *t2s_status_string(int status);
 

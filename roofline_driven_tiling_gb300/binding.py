@@ -27,6 +27,8 @@ T2S_TF32X3_NOALLOC_MAX_SCRATCH = 32 << 20
 T2S_MAX_DIM = 1 << 30
 T2S_ACT_NONE, T2S_ACT_RELU, T2S_ACT_SILU, T2S_ACT_GELU, T2S_ACT_GELU_TANH = range(5)
 T2S_W_KN, T2S_W_NK = 0, 1
+T2S_E4M3, T2S_E5M2 = 0, 1
+T2S_NORM_NONE, T2S_NORM_RMS, T2S_NORM_LAYER = range(3)
 
 #: Every function the header declares, with (argtypes, restype).
 _i64, _p, _i, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -35,6 +37,14 @@ _LINEAR = [_i64] * 3 + 2 * _MAT + [_i, _p] + _MAT + [_i] + 2 * _MAT + _TAIL
 _LINEAR_BACKWARD = [_i64] * 3 + 3 * _MAT + [_i] + _MAT + [_i] + 2 * _MAT + [_p] + _TAIL
 _GATED = [_i64] * 3 + 3 * _MAT + [_i, _i] + 3 * _MAT + _TAIL
 _GATED_BACKWARD = [_i64] * 3 + 4 * _MAT + [_i] + 2 * _MAT + [_i] + 3 * _MAT + _TAIL
+_f = ctypes.c_float
+_SCALES = [_p, _i64, _i64]  # pointer, strides of rows and blocks
+_QUANTIZE = [_i64] * 2 + _MAT + [_i, _i] + 2 * (_MAT + _SCALES) + [_p]
+_GEMM_FP8 = [_i64] * 3 + 2 * (_MAT + [_i] + _SCALES) + [_i] + _MAT + [_p]
+_DROP = [_i, _p, _i64, _i64]  # dropped of 65536, the seed's address, seed, sequence
+_NORM = [_i64, _i64, _i, _i] + 2 * _MAT + 4 * [_p] + _MAT + [_i64, _f, _f] + _DROP + 2 * _MAT + [_p]
+_NORM_BACKWARD = [_i64, _i64, _i, _i] + 4 * _MAT + 3 * [_p] + _MAT + [_i64, _f, _f] + _DROP + 2 * _MAT + 4 * [_p] + _MAT + _TAIL
+_DROPOUT = [_i64, _i64] + 2 * _MAT + _DROP + _MAT + [_p]
 SIGNATURES = {
     "t2s_gemm_f32": ([_i64, _i64, _i64, _p, _p, _p, _p], _i),
     "t2s_gemm_f32_host": ([_i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p], _i),
@@ -69,6 +79,19 @@ SIGNATURES = {
     "t2s_gated_f16": (_GATED, _i),
     "t2s_gated_backward_bf16": (_GATED_BACKWARD, _i),
     "t2s_gated_backward_f16": (_GATED_BACKWARD, _i),
+    "t2s_quantize_fp8_bf16": (_QUANTIZE, _i),
+    "t2s_quantize_fp8_f16": (_QUANTIZE, _i),
+    "t2s_quantize_fp8_f32": (_QUANTIZE, _i),
+    "t2s_gemm_fp8_bf16": (_GEMM_FP8, _i),
+    "t2s_gemm_fp8_f16": (_GEMM_FP8, _i),
+    "t2s_gemm_fp8_f32": (_GEMM_FP8, _i),
+    "t2s_residual_norm_backward_workspace_size": ([_i64, _i64, _i64, _i], _sz),
+    "t2s_residual_norm_bf16": (_NORM, _i),
+    "t2s_residual_norm_f16": (_NORM, _i),
+    "t2s_residual_norm_backward_bf16": (_NORM_BACKWARD, _i),
+    "t2s_residual_norm_backward_f16": (_NORM_BACKWARD, _i),
+    "t2s_dropout_bf16": (_DROPOUT, _i),
+    "t2s_dropout_f16": (_DROPOUT, _i),
     "t2s_status_string": ([_i], ctypes.c_char_p),
     "t2s_device_status": ([_p], _i),
     "t2s_last_cuda_error": ([], _i),
@@ -188,6 +211,10 @@ def t2s_gemm_f16_f32_workspace_size(M, N, K) -> int:
 
 def t2s_gemm_f16_f32(M, N, K, A, B, C, workspace, workspace_bytes, stream=0) -> int:
     return lib().t2s_gemm_f16_f32(M, N, K, A, B, C, workspace, workspace_bytes, stream)
+
+
+def t2s_residual_norm_backward_workspace_size(M, N, gates, vectors) -> int:
+    return lib().t2s_residual_norm_backward_workspace_size(M, N, gates, vectors)
 
 
 def t2s_vector_add_f32(n, x, y, z, stream=0) -> int:

@@ -3,58 +3,18 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <initializer_list>
 
 #include "ff_internal.h"
+#include "matrix_args.h"
 #include "t2s_internal.h"
 
 namespace t2s {
 namespace ff {
 namespace {
 
-size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
 size_t plane_bytes(int64_t rows, int64_t cols) {
   return up256(static_cast<size_t>(rows) * static_cast<size_t>(up8(cols)) * 2);
-}
-
-bool bad_size(int64_t x) { return x < 0 || x > T2S_MAX_DIM; }
-
-// A 16-bit matrix argument of rows x cols (a vector: rows = 1).
-struct Arg {
-  const void* p;
-  int64_t ld, rows, cols;
-};
-
-bool bad_matrix(const Arg& a, bool required) {
-  if (a.rows == 0 || a.cols == 0) return false;
-  if (a.p == nullptr) return required;
-  if ((reinterpret_cast<uintptr_t>(a.p) & 1u) != 0) return true;
-  return a.ld < a.cols || a.ld > T2S_MAX_DIM;
-}
-
-bool same(const Arg& a, const Arg& b) {
-  return a.p != nullptr && a.p == b.p && a.rows > 0 && a.cols > 0 && b.rows > 0 && b.cols > 0;
-}
-
-// Inputs that are required, inputs and outputs that may be absent, and no output that is
-// another argument.
-bool bad_arguments(std::initializer_list<Arg> required, std::initializer_list<Arg> optional,
-                   std::initializer_list<Arg> outputs) {
-  for (const Arg& a : required)
-    if (bad_matrix(a, true)) return true;
-  for (const Arg& a : optional)
-    if (bad_matrix(a, false)) return true;
-  for (const Arg* o = outputs.begin(); o != outputs.end(); ++o) {
-    if (bad_matrix(*o, false)) return true;
-    for (const Arg& a : required)
-      if (same(*o, a)) return true;
-    for (const Arg& a : optional)
-      if (same(*o, a)) return true;
-    for (const Arg* q = outputs.begin(); q != o; ++q)
-      if (same(*o, *q)) return true;
-  }
-  return false;
 }
 
 bool bad_flags(int w_order, int act) {
@@ -117,18 +77,6 @@ struct Copies {
 
 size_t weight_copy_bytes(const void* p, int64_t K, int64_t N, int64_t ld, int w_order) {
   return w_order == T2S_W_KN ? copy_bytes(p, K, N, ld) : copy_bytes(p, N, K, ld);
-}
-
-int check_workspace(const void* p, size_t have, size_t need) {
-  if (need == 0) return T2S_OK;
-  if (p == nullptr || have < need || (reinterpret_cast<uintptr_t>(p) & 255u) != 0) return T2S_ERR_WORKSPACE;
-  return T2S_OK;
-}
-
-int done(cudaError_t e) {
-  if (e == cudaSuccess) return T2S_OK;
-  set_last_cuda_error(e);
-  return T2S_ERR_CUDA;
 }
 
 // The gradient of a weight: X^T D for a K x N weight, D^T X for an N x K one.
@@ -347,6 +295,7 @@ size_t copies_bytes(int64_t M, int64_t N, int64_t K, int weights) {
 }  // namespace t2s
 
 using namespace t2s::ff;
+using t2s::up256;
 
 extern "C" {
 

@@ -1,0 +1,265 @@
+// fp8_quantize.cu -- 8-bit floating-point values with a scale for each block of 128: along rows, along
+// columns (written transposed), or both from one read.
+//
+// A block's scale is the least power of two s with amax / s <= the type's largest value (448 = 1.75 2^8 for
+// e4m3, 57344 = 1.75 2^15 for e5m2), at least 2^-126: an exponent off the bits of amax. x / s is then exact, and
+// every value is rounded once. amax is taken over bit patterns, so that an infinity or NaN anywhere in a block
+// makes the scale NaN and with it the whole block.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ff_device.cuh"
+#include "ff_math.cuh"
+#include "fp8_internal.h"
+
+namespace t2s {
+namespace fp8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// A thread's eight consecutive values of a row; zeros beyond its end.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* x, int64_t at, int64_t left, bool wide, float (&v)[8]) {
+  if constexpr (TYPE == kF32) {
+    const float* p = static_cast<const float*>(x) + at;
+    if (wide && left >= 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+    }
+  } else {
+    constexpr int kKind = TYPE == kBf16 ? ff::kBf16 : ff::kF16;
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+    if (wide && left >= 8) {
+      const uint4 w = *reinterpret_cast<const uint4*>(p);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = ff::to_f32x2<kKind>(u[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? ff::to_f32<kKind>(p[i]) : 0.0f;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A block's scale and 1 / scale from the bits of its largest magnitude.
+struct Scale {
+  float value, inverse;
+};
+template <int FORMAT>
+__device__ __forceinline__ Scale scale_of(uint32_t amax) {
+  if (amax >= 0x7f800000u) return {__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu)};
+  // amax = f 2^e with 1 <= f < 2: the power is e - 8 (e5m2: e - 15), one more where f > 1.75.
+  int e = static_cast<int>(amax >> 23) - (FORMAT == T2S_E4M3 ? 8 : 15) + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (e < 1) e = 1;
+  return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
+}
+
+// Two values in 8 bits each, `lo` in the low byte.
+template <int FORMAT>
+__device__ __forceinline__ uint32_t pack_fp8x2(float lo, float hi) {
+  uint16_t r;
+  if constexpr (FORMAT == T2S_E4M3) {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  } else {
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  }
+  return r;
+}
+
+template <int FORMAT>
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float inverse) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_fp8x2<FORMAT>(v[2 * i] * inverse, v[2 * i + 1] * inverse);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// Eight bytes of a row, fewer at its end or off 8-byte boundaries.
+__device__ __forceinline__ void store8(uint8_t* p, int64_t left, bool wide, uint2 w) {
+  if (wide && left >= 8) {
+    *reinterpret_cast<uint2*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> 8 * (i & 3));
+  }
+}
+
+// The largest over a half-warp's 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+struct QuantizeParams {
+  int64_t M, N, ldx;
+  const void* X;
+  Quantized rows, columns;
+  int64_t row_tiles;
+  int x_wide, rows_wide, columns_wide;
+};
+
+// Along rows: a half-warp takes a block, a CTA 16 rows of kAhead blocks (so that the scales of a block leave
+// as 64 consecutive bytes where rows' scales are neighbours).
+constexpr int kAhead = 4;
+
+template <int TYPE, int FORMAT>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
+  ff::wait_for_earlier_kernels();
+  const int64_t tile = blockIdx.x, m = tile % p.row_tiles * 16 + threadIdx.x / 16;
+  const int64_t b0 = tile / p.row_tiles * kAhead, n0 = b0 * kBlock + threadIdx.x % 16 * 8;
+  const int64_t left = m < p.M ? p.N - n0 : 0;
+  float v[kAhead][8];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    load8<TYPE>(p.X, m * p.ldx + n0 + i * kBlock, left - i * kBlock, p.x_wide, v[i]);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[i][j]));
+    const Scale s = scale_of<FORMAT>(half_warp_max(amax));
+    if (left - i * kBlock > 0) {
+      store8(p.rows.q + m * p.rows.ld + n0 + i * kBlock, left - i * kBlock, p.rows_wide, pack8<FORMAT>(v[i], s.inverse));
+      if (threadIdx.x % 16 == 0) p.rows.s.p[m * p.rows.s.row + (b0 + i) * p.rows.s.block] = s.value;
+    }
+  }
+}
+
+// Along columns, or both, or with a scale for 128 x 128: a CTA takes a tile of 128 x 128 in its threads'
+// registers (eight columns of every 16th row each), reduces over rows and columns, and writes the transposed
+// values through shared memory so that they leave in rows of 128 bytes.
+constexpr int kPitch = kBlock + 4;  // bytes between the transposed tile's rows in shared memory
+
+template <int TYPE, int FORMAT, bool SQUARE>
+__global__ void __launch_bounds__(kThreads) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
+  __shared__ uint32_t column_max[kBlock];
+  __shared__ float column_inverse[kBlock];
+  __shared__ uint32_t transposed[kBlock * kPitch / 4];
+  ff::wait_for_earlier_kernels();
+  const int64_t tile = blockIdx.x, mb = tile % p.row_tiles, nb = tile / p.row_tiles;
+  const int64_t m0 = mb * kBlock + threadIdx.x / 16;
+  const int c0 = threadIdx.x % 16 * 8;
+  const int64_t n0 = nb * kBlock + c0, left = p.N - n0;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    load8<TYPE>(p.X, (m0 + 16 * i) * p.ldx + n0, m0 + 16 * i < p.M ? left : 0, p.x_wide, v[i]);
+  if (threadIdx.x < kBlock) column_max[threadIdx.x] = 0;
+  __syncthreads();
+  Scale all = {};
+  if (SQUARE || p.columns.q != nullptr) {
+    uint32_t amax[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax[j] = max(amax[j], magnitude(v[i][j]));
+    if (SQUARE) {
+#pragma unroll
+      for (int j = 1; j < 8; ++j) amax[0] = max(amax[0], amax[j]);
+      amax[0] = half_warp_max(amax[0]);
+      if (threadIdx.x % 16 == 0) atomicMax(&column_max[0], amax[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        amax[j] = max(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], 16));
+        if ((threadIdx.x & 16) == 0) atomicMax(&column_max[c0 + j], amax[j]);
+      }
+    }
+    __syncthreads();
+    if (SQUARE) {
+      all = scale_of<FORMAT>(column_max[0]);
+    } else if (threadIdx.x < kBlock) {
+      const Scale s = scale_of<FORMAT>(column_max[threadIdx.x]);
+      const int64_t n = nb * kBlock + threadIdx.x;
+      column_inverse[threadIdx.x] = s.inverse;
+      if (n < p.N) p.columns.s.p[n * p.columns.s.row + mb * p.columns.s.block] = s.value;
+    }
+    if (SQUARE && threadIdx.x == 0) {
+      if (p.rows.q != nullptr) p.rows.s.p[mb * p.rows.s.row + nb * p.rows.s.block] = all.value;
+      if (p.columns.q != nullptr) p.columns.s.p[nb * p.columns.s.row + mb * p.columns.s.block] = all.value;
+    }
+  }
+  if (p.rows.q != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t m = m0 + 16 * i;
+      Scale s = all;
+      if (!SQUARE) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[i][j]));
+        s = scale_of<FORMAT>(half_warp_max(amax));
+        if (threadIdx.x % 16 == 0 && m < p.M) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = s.value;
+      }
+      if (m < p.M) store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v[i], s.inverse));
+    }
+  }
+  if (p.columns.q == nullptr) return;
+  __syncthreads();
+  uint8_t* bytes = reinterpret_cast<uint8_t*>(transposed);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float inverse = SQUARE ? all.inverse : column_inverse[c0 + j];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint32_t w = pack_fp8x2<FORMAT>(v[i][j] * inverse, v[i + 1][j] * inverse);
+      uint8_t* at = bytes + (c0 + j) * kPitch + threadIdx.x / 16 + 16 * i;
+      at[0] = static_cast<uint8_t>(w);
+      at[16] = static_cast<uint8_t>(w >> 8);
+    }
+  }
+  __syncthreads();
+  // Sixteen threads to a transposed row of 128 bytes.
+  const int64_t rows_left = p.M - mb * kBlock - c0;
+#pragma unroll 4
+  for (int c = threadIdx.x / 16; c < kBlock; c += kThreads / 16) {
+    const int64_t n = nb * kBlock + c;
+    if (n >= p.N) break;
+    const uint32_t* from = transposed + (c * kPitch + c0) / 4;
+    store8(p.columns.q + n * p.columns.ld + mb * kBlock + c0, rows_left, p.columns_wide, make_uint2(from[0], from[1]));
+  }
+}
+
+template <int TYPE, int FORMAT>
+cudaError_t launch(const QuantizeTask& t, cudaStream_t stream) {
+  QuantizeParams p{t.M, t.N, t.ldx, t.X, t.rows, t.columns, 0, 0, 0, 0};
+  const int64_t ld_bytes = t.ldx * (TYPE == kF32 ? 4 : 2);
+  p.x_wide = ((reinterpret_cast<uintptr_t>(t.X) | static_cast<uintptr_t>(t.M > 1 ? ld_bytes : 0)) & 15u) == 0;
+  p.rows_wide = ((reinterpret_cast<uintptr_t>(t.rows.q) | static_cast<uintptr_t>(t.rows.ld)) & 7u) == 0;
+  p.columns_wide = ((reinterpret_cast<uintptr_t>(t.columns.q) | static_cast<uintptr_t>(t.columns.ld)) & 7u) == 0;
+  const bool tiles = t.square || t.columns.q != nullptr;
+  p.row_tiles = tiles ? blocks_of(t.M) : (t.M + 15) / 16;
+  const int64_t across = tiles ? blocks_of(t.N) : (blocks_of(t.N) + kAhead - 1) / kAhead;
+  if (p.row_tiles > 0x7fffffff / across) return cudaErrorInvalidConfiguration;
+  const ff::LaunchShape shape{dim3(static_cast<unsigned>(p.row_tiles * across)), kThreads, 1, 0};
+  if (!tiles) return ff::launch_early(stream, shape, quantize_rows_kernel<TYPE, FORMAT>, p);
+  return t.square ? ff::launch_early(stream, shape, quantize_tile_kernel<TYPE, FORMAT, true>, p)
+                  : ff::launch_early(stream, shape, quantize_tile_kernel<TYPE, FORMAT, false>, p);
+}
+
+template <int TYPE>
+cudaError_t launch_format(const QuantizeTask& t, cudaStream_t stream) {
+  return t.format == T2S_E4M3 ? launch<TYPE, T2S_E4M3>(t, stream) : launch<TYPE, T2S_E5M2>(t, stream);
+}
+
+}  // namespace
+
+cudaError_t run_quantize(const QuantizeTask& t, cudaStream_t stream) {
+  return t.type == kF32 ? launch_format<kF32>(t, stream)
+                        : t.type == kBf16 ? launch_format<kBf16>(t, stream) : launch_format<kF16>(t, stream);
+}
+
+}  // namespace fp8
+}  // namespace t2s
