@@ -1,0 +1,74 @@
+// fp8_device.cuh -- device helpers of the 8-bit product kernels beside ff_device.cuh.
+#pragma once
+
+#include "ff_device.cuh"
+#include "ff_math.cuh"
+#include "fp8_internal.h"
+
+namespace t2s {
+namespace fp8 {
+
+constexpr int kUnit = 32;  // accumulator columns that a warp takes at a time
+
+// The MMAs of one block of 128 values of K (four of K = 32) by one elected thread of a converged warp, from
+// 128-byte swizzled K-major rows; D starts from the first product.
+template <int G>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  if constexpr (G == 2) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, 0;\n\t"
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+        "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+        "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, 0;\n\t"
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+        "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t"
+        "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+  }
+}
+
+// Starts reading 16 accumulator columns of the warp's 32 rows (one row per lane); the registers hold them after
+// wait_columns16, which stands between the load and every use.
+__device__ __forceinline__ void load_columns16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void wait_columns16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Instruction descriptor: D FP32, the operands' formats, both K-major, N and M.
+inline uint32_t instruction(int format_a, int format_b, int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(format_a) << 7) | (static_cast<uint32_t>(format_b) << 10) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// The scale of row (or group) r and block b.
+__device__ __forceinline__ float scale_at(const Scales& s, int64_t r, int64_t b) { return s.p[r * s.row + b * s.block]; }
+
+}  // namespace fp8
+}  // namespace t2s

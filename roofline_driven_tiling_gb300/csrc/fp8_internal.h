@@ -55,6 +55,8 @@ struct ProductTask {
   int64_t ldc;
 };
 cudaError_t run_product(const ProductTask& t, cudaStream_t stream);
+// By SM pairs in tiles of 256 rows x `width` (64, 128 or 256) columns (fp8_pair.cu).
+cudaError_t run_pair(const ProductTask& t, int width, cudaStream_t stream, unsigned* status);
 
 }  // namespace fp8
 }  // namespace t2s

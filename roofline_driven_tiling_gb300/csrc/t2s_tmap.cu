@@ -59,4 +59,14 @@ cudaError_t encode_tmap_16bit_2d(CUtensorMap* map, const void* base, int64_t col
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, ld, box_cols, box_rows, swizzle);
 }
 
+cudaError_t encode_tmap_8bit_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, ld, box_cols, box_rows, swizzle);
+}
+
+cudaError_t encode_tmap_f32_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                               uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, cols, rows, ld, box_cols, box_rows, swizzle);
+}
+
 }  // namespace t2s

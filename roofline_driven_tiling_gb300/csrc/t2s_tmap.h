@@ -26,4 +26,10 @@ cudaError_t encode_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t cols
 cudaError_t encode_tmap_16bit_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
                                  uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// The same for bytes, and for FP32 values in rows `ld` elements apart.
+cudaError_t encode_tmap_8bit_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+cudaError_t encode_tmap_f32_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                               uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
 }  // namespace t2s
