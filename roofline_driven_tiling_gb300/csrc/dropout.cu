@@ -10,29 +10,68 @@ namespace norm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;  // words of a thread that are on their way at once
 
-// A thread takes the four values of one output of the generator.
-template <int KIND>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutTask t, int64_t groups) {
+struct DropoutParams {
+  DropoutTask t;
+  int64_t words, per_row;  // of eight values
+  int x_wide, r_wide, y_wide;
+};
+
+// INDEX: 32 bits where the words' numbers fit, for the division by a row's words.
+template <int KIND, class INDEX>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
   ff::wait_for_earlier_kernels();
-  const uint64_t key = drop_key(t.drop);
-  const int64_t all = t.M * groups, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; g < all; g += step) {
-    const int64_t m = g / groups, n = (g - m * groups) * 4;
-    const uint64_t bits = drop_bits(key, static_cast<uint64_t>(g));
-    for (int j = 0; j < 4 && n + j < t.N; ++j) {
-      const float v = drop(ff::to_f32<KIND>(t.X.p[m * t.X.ld + n + j]), bits, j, t.drop.dropped, t.drop.factor);
-      t.Y.p[m * t.Y.ld + n + j] =
-          ff::from_f32<KIND>(t.R.p == nullptr ? v : v + ff::to_f32<KIND>(t.R.p[m * t.R.ld + n + j]));
+  const DropoutTask& t = p.t;
+  const uint64_t key = drop_key(t.drop), groups = static_cast<uint64_t>((t.N + 3) / 4);
+  const INDEX words = static_cast<INDEX>(p.words), per_row = static_cast<INDEX>(p.per_row);
+  const INDEX step = static_cast<INDEX>(gridDim.x) * (kAhead * kThreads);
+  for (INDEX first = static_cast<INDEX>(blockIdx.x) * (kAhead * kThreads) + threadIdx.x; first < words; first += step) {
+    uint4 x[kAhead], r[kAhead];
+    int64_t m[kAhead];
+    int n[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const INDEX w = first + i * kThreads;
+      m[i] = -1;
+      if (w >= words) break;
+      const INDEX row = w / per_row;
+      m[i] = row;
+      n[i] = static_cast<int>(w - row * per_row) * kWord;
+      const int left = static_cast<int>(t.N) - n[i];
+      x[i] = load_word(t.X.p + m[i] * t.X.ld + n[i], left, p.x_wide);
+      if (t.R.p != nullptr) r[i] = load_word(t.R.p + m[i] * t.R.ld + n[i], left, p.r_wide);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (m[i] < 0) break;
+      float v[kWord];
+      unpack<KIND>(x[i], v);
+      drop_word(t.drop, key, static_cast<uint64_t>(m[i]) * groups + static_cast<uint64_t>(n[i] / 4), v);
+      if (t.R.p != nullptr) {
+        float u[kWord];
+        unpack<KIND>(r[i], u);
+#pragma unroll
+        for (int j = 0; j < kWord; ++j) v[j] += u[j];
+      }
+      store_word(t.Y.p + m[i] * t.Y.ld + n[i], static_cast<int>(t.N) - n[i], p.y_wide, pack<KIND>(v));
     }
   }
 }
 
 template <int KIND>
 cudaError_t run(const DropoutTask& t, cudaStream_t stream) {
-  const int64_t groups = (t.N + 3) / 4, blocks = (t.M * groups + kThreads - 1) / kThreads;
-  const unsigned grid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
-  return ff::launch_early(stream, {dim3(grid), kThreads, 1, 0}, dropout_kernel<KIND>, t, groups);
+  DropoutParams p{t};
+  p.per_row = (t.N + kWord - 1) / kWord;
+  p.words = t.M * p.per_row;
+  p.x_wide = wide_rows(t.X.p, t.X.ld, t.M), p.r_wide = wide_rows(t.R.p, t.R.ld, t.M);
+  p.y_wide = wide_rows(t.Y.p, t.Y.ld, t.M);
+  const int64_t blocks = (p.words + kAhead * kThreads - 1) / (kAhead * kThreads);
+  constexpr int64_t kMost = 152 * 4;
+  const ff::LaunchShape shape{dim3(static_cast<unsigned>(blocks < kMost ? blocks : kMost)), kThreads, 1, 0};
+  return p.words < (int64_t{1} << 31) - kMost * kAhead * kThreads
+             ? ff::launch_early(stream, shape, dropout_kernel<KIND, uint32_t>, p)
+             : ff::launch_early(stream, shape, dropout_kernel<KIND, uint64_t>, p);
 }
 
 }  // namespace

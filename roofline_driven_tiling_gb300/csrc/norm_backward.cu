@@ -8,6 +8,7 @@
 // CTAs' shares in their order.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -170,6 +171,186 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
   }
 }
 
+// Rows of up to 8192 values: a group of threads keeps a row in registers, a word of eight values a thread; a block
+// holds several groups. The sums over rows are added in shared memory, each group's in its own place, every value by
+// one thread; at the end of a block's rows (of a gate's for dgate) the groups' sums are added in their order.
+struct RowParams {
+  BackwardParams b;
+  int threads;  // of a row
+  int dy_wide, dr_wide, r_wide, h_wide, dx_wide, dh_wide, gate_wide, vectors_wide;
+};
+
+template <int KIND, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
+  extern __shared__ float sums[];  // slots x N for each group
+  __shared__ float rooms[Group::kRoomFloats];
+  const BackwardTask& t = p.b.t;
+  Group group(p.threads, rooms);
+  const int n = static_cast<int>(t.N), slots = p.b.slots, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
+  const int pitch = (n + kWord - 1) / kWord * kWord;
+  float* const mine = sums + static_cast<int64_t>(group.index) * slots * pitch;
+  for (int i = threadIdx.x; i < rows_at_once * slots * pitch; i += blockDim.x) sums[i] = 0.0f;
+  __syncthreads();
+  ff::wait_for_earlier_kernels();
+  const int64_t groups = (t.N + 3) / 4;
+  const float inv_n = 1.0f / static_cast<float>(n);
+  const uint64_t key = t.drop.dropped != 0 ? drop_key(t.drop) : 0;
+  const bool has_h = t.H.p != nullptr, has_norm = t.norm != T2S_NORM_NONE, has_post = has_h && t.post != T2S_NORM_NONE;
+  const bool layer = t.norm == T2S_NORM_LAYER, post_layer = has_post && t.post == T2S_NORM_LAYER;
+  const Rows rows = rows_of(p.b, blockIdx.x);
+  const int at = group.rank * kWord, left = n - at;
+  auto add = [&](int vector, const float (&v)[kWord]) {
+    if (p.b.slot[vector] < 0) return;
+    float4* to = reinterpret_cast<float4*>(mine + p.b.slot[vector] * pitch + at);
+    float4 a = to[0], b = to[1];
+    a.x += v[0], a.y += v[1], a.z += v[2], a.w += v[3];
+    b.x += v[4], b.y += v[5], b.z += v[6], b.w += v[7];
+    to[0] = a, to[1] = b;
+  };
+  // One gate's rows after another (one stretch of rows where a gate has several blocks).
+  const int64_t stretch = p.b.split.pieces > 0 ? rows.last - rows.first : rows.per_gate;
+  for (int64_t m0 = rows.first; m0 < rows.last; m0 += stretch) {
+    const int64_t gate_row = m0 / rows.per_gate;
+    const uint16_t* gate = t.gate.p == nullptr ? nullptr : t.gate.p + gate_row * t.gate.ld;
+    for (int64_t m = m0 + group.index; m < m0 + stretch; m += rows_at_once) {
+      uint4 r4 = make_uint4(0, 0, 0, 0), dy4 = r4, dr4 = r4, h4 = r4;
+      if (left > 0) {
+        if (has_norm) {
+          r4 = load_word(t.R.p + m * t.R.ld + at, left, p.r_wide);
+          dy4 = load_word(t.dY.p + m * t.dY.ld + at, left, p.dy_wide);
+        }
+        if (t.dR.p != nullptr) dr4 = load_word(t.dR.p + m * t.dR.ld + at, left, p.dr_wide);
+        if (has_h) h4 = load_word(t.H.p + m * t.H.ld + at, left, p.h_wide);
+      }
+      float xh[kWord], g[kWord], hh[kWord];
+      unpack<KIND>(r4, xh);
+      unpack<KIND>(h4, hh);
+      float means[2] = {0.0f, 0.0f};
+      if (layer || post_layer) {
+#pragma unroll
+        for (int i = 0; i < kWord; ++i) means[0] += xh[i], means[1] += hh[i];
+        group.sums(means);
+        means[0] = layer ? means[0] * inv_n : 0.0f;
+        means[1] = post_layer ? means[1] * inv_n : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWord; ++i)
+          if (i < left) xh[i] -= means[0], hh[i] -= means[1];
+      }
+      unpack<KIND>(dy4, g);
+      float w[kWord];
+      if (left > 0 && t.weight != nullptr) {
+        parameter<KIND>(t.weight, at, left, p.vectors_wide, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < kWord; ++i) g[i] *= w[i];
+      }
+      float s[4] = {};
+#pragma unroll
+      for (int i = 0; i < kWord; ++i) {
+        s[0] = fmaf(xh[i], xh[i], s[0]);
+        s[1] += g[i];
+        s[2] = fmaf(g[i], xh[i], s[2]);
+        s[3] = fmaf(hh[i], hh[i], s[3]);
+      }
+      if (has_norm || has_post) group.sums(s);
+      const float rho = rsqrtf(s[0] * inv_n + t.eps), sigma = has_post ? rsqrtf(s[3] * inv_n + t.eps) : 1.0f;
+      const float mean_g = layer ? s[1] * inv_n : 0.0f, mean_gx = s[2] * inv_n * rho;
+      float d[kWord];
+      unpack<KIND>(dr4, d);
+      if (has_norm) {
+#pragma unroll
+        for (int i = 0; i < kWord; ++i) {
+          xh[i] *= rho;
+          d[i] += rho * (g[i] - mean_g - xh[i] * mean_gx);
+          if (i >= left) d[i] = 0.0f;  // the means are not for the values beyond the row's end
+        }
+      }
+      float q[2] = {0.0f, 0.0f};
+      if (left > 0) {
+        if (has_norm) {
+          unpack<KIND>(dy4, g);
+          add(kBias, g);
+#pragma unroll
+          for (int i = 0; i < kWord; ++i) g[i] *= xh[i];
+          add(kWeight, g);
+        }
+        if (t.dX.p != nullptr) {
+#pragma unroll
+          for (int i = 0; i < kWord; ++i) g[i] = t.scale * d[i];
+          store_word(t.dX.p + m * t.dX.ld + at, left, p.dx_wide, pack<KIND>(g));
+        }
+        if (has_h) {
+          float pw[kWord];
+          parameter<KIND>(t.post_weight, at, left, p.vectors_wide, 1.0f, pw);
+#pragma unroll
+          for (int i = 0; i < kWord; ++i) hh[i] *= sigma;
+          const uint64_t word = static_cast<uint64_t>(m * groups + at / 4);
+          if (p.b.slot[kGate] >= 0) {
+            if (has_post) {
+              parameter<KIND>(t.post_bias, at, left, p.vectors_wide, 0.0f, w);
+#pragma unroll
+              for (int i = 0; i < kWord; ++i) g[i] = fmaf(hh[i], pw[i], w[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kWord; ++i) g[i] = hh[i];
+            }
+            if (t.drop.dropped != 0) drop_word(t.drop, key, word, g);
+#pragma unroll
+            for (int i = 0; i < kWord; ++i) g[i] *= d[i];
+            add(kGate, g);
+          }
+          if (gate != nullptr) {
+            parameter<KIND>(gate, at, left, p.gate_wide, 1.0f, w);
+#pragma unroll
+            for (int i = 0; i < kWord; ++i) d[i] *= w[i];
+          }
+          if (t.drop.dropped != 0) drop_word(t.drop, key, word, d);
+          if (has_post) {
+            add(kPostBias, d);
+#pragma unroll
+            for (int i = 0; i < kWord; ++i) g[i] = d[i] * hh[i];
+            add(kPostWeight, g);
+#pragma unroll
+            for (int i = 0; i < kWord; ++i) {
+              d[i] *= pw[i];
+              q[0] += d[i];
+              q[1] = fmaf(d[i], hh[i], q[1]);
+            }
+          }
+        }
+      }
+      if (!has_h || t.dH.p == nullptr) continue;
+      if (has_post) {
+        group.sums(q);
+        const float mean_q = post_layer ? q[0] * inv_n : 0.0f, mean_qh = q[1] * inv_n;
+#pragma unroll
+        for (int i = 0; i < kWord; ++i) d[i] = sigma * (d[i] - mean_q - hh[i] * mean_qh);
+      }
+      if (left > 0) store_word(t.dH.p + m * t.dH.ld + at, left, p.dh_wide, pack<KIND>(d));
+    }
+    if (p.b.split.pieces == 0 && p.b.slot[kGate] >= 0) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        float sum = 0.0f;
+        for (int j = 0; j < rows_at_once; ++j) {
+          float* from = sums + (static_cast<int64_t>(j) * slots + p.b.slot[kGate]) * pitch + i;
+          sum += *from;
+          *from = 0.0f;
+        }
+        t.dgate.p[gate_row * t.dgate.ld + i] = ff::from_f32<KIND>(sum);
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  float* const out = t.partials + static_cast<int64_t>(blockIdx.x) * slots * n;
+  for (int slot = 0; slot < slots; ++slot)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      float sum = 0.0f;
+      for (int j = 0; j < rows_at_once; ++j) sum += sums[(static_cast<int64_t>(j) * slots + slot) * pitch + i];
+      out[static_cast<int64_t>(slot) * n + i] = sum;
+    }
+}
+
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
 // kSumWarps-th share each.
 constexpr int kSumWarps = 16;
@@ -216,6 +397,32 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
   p.out[which][row * p.ldgate + n] = ff::from_f32<KIND>(sum);
 }
 
+template <int KIND, int THREADS>
+cudaError_t launch_rows(const BackwardParams& b, cudaStream_t stream) {
+  constexpr int kMaxDevices = 64, kMaxSmem = 5 * 8192 * 4;
+  static std::atomic<bool> prepared[kMaxDevices];
+  auto kern = row_backward_kernel<KIND, THREADS>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!prepared[dev].load(std::memory_order_acquire)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) != cudaSuccess) return e;
+    prepared[dev].store(true, std::memory_order_release);
+  }
+  const BackwardTask& t = b.t;
+  const int words = static_cast<int>((t.N + kWord - 1) / kWord);
+  RowParams p{b, (words + 31) / 32 * 32};
+  p.dy_wide = wide_rows(t.dY.p, t.dY.ld, t.M), p.dr_wide = wide_rows(t.dR.p, t.dR.ld, t.M);
+  p.r_wide = wide_rows(t.R.p, t.R.ld, t.M), p.h_wide = wide_rows(t.H.p, t.H.ld, t.M);
+  p.dx_wide = wide_rows(t.dX.p, t.dX.ld, t.M), p.dh_wide = wide_rows(t.dH.p, t.dH.ld, t.M);
+  p.gate_wide = wide_rows(t.gate.p, t.gate.ld, t.gates);
+  p.vectors_wide = wide_rows(t.weight, 0, 1) && wide_rows(t.post_weight, 0, 1) && wide_rows(t.post_bias, 0, 1);
+  const int rows = THREADS / p.threads;
+  const int smem = rows * b.slots * words * kWord * 4;
+  return ff::launch_early(stream, {dim3(static_cast<unsigned>(b.split.ctas)), rows * p.threads, 1, smem}, kern, p);
+}
+
 template <int KIND>
 cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
   BackwardParams p;
@@ -231,8 +438,11 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
     if (i != kGate && outs[i] != nullptr) ++s.vectors;
   }
   if (p.slots == 0 && t.dX.p == nullptr && t.dH.p == nullptr) return cudaSuccess;
-  cudaError_t e = ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), kWideThreads, 1, 0},
-                                   wide_backward_kernel<KIND>, p);
+  cudaError_t e = t.N <= 4096 ? launch_rows<KIND, 512>(p, stream)
+                  : t.N <= 8192
+                      ? launch_rows<KIND, 1024>(p, stream)
+                      : ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), kWideThreads, 1, 0},
+                                         wide_backward_kernel<KIND>, p);
   if (e != cudaSuccess) return e;
   s.gate_rows = t.dgate.p != nullptr && p.split.pieces > 0 ? static_cast<int>(t.gates) : 0;
   if (s.vectors + s.gate_rows == 0) return cudaSuccess;
