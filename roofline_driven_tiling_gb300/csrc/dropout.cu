@@ -3,75 +3,88 @@
 
 #include <cstdint>
 
-#include "norm_device.cuh"
+#include "ff_device.cuh"
+#include "norm_internal.h"
+#include "row_words.cuh"
 
 namespace t2s {
 namespace norm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // words of a thread that are on their way at once
+constexpr int kAhead = 4;  // rows of a thread that are on their way at once
 
 struct DropoutParams {
-  DropoutTask t;
-  int64_t words, per_row;  // of eight values
-  int x_wide, r_wide, y_wide;
+  row::View x, r, y;
+  int64_t M, step;  // rows that all blocks take at once
+  int N, across;    // threads along a row
+  Dropout drop;
 };
 
-// INDEX: 32 bits where the words' numbers fit, for the division by a row's words.
-template <int KIND, class INDEX>
+// A block takes 256 / across rows of up to `across` words each, a thread the same words of kAhead rows at a time: so
+// the place in a row is found once, and the generator's counter only moves on.
+template <int KIND, bool WIDE>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
   ff::wait_for_earlier_kernels();
-  const DropoutTask& t = p.t;
-  const uint64_t key = drop_key(t.drop), groups = static_cast<uint64_t>((t.N + 3) / 4);
-  const INDEX words = static_cast<INDEX>(p.words), per_row = static_cast<INDEX>(p.per_row);
-  const INDEX step = static_cast<INDEX>(gridDim.x) * (kAhead * kThreads);
-  for (INDEX first = static_cast<INDEX>(blockIdx.x) * (kAhead * kThreads) + threadIdx.x; first < words; first += step) {
+  const int down = static_cast<int>(threadIdx.x) / p.across;
+  const int n = (static_cast<int>(blockIdx.x) * p.across + static_cast<int>(threadIdx.x) - down * p.across) * row::kWord;
+  const int left = p.N - n;
+  const int64_t at_once = p.step / kAhead;
+  int64_t m = static_cast<int64_t>(blockIdx.y) * (kThreads / p.across) + down;
+  const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(p.N) + 3) / 4);
+  const uint64_t key = drop_key(p.drop);
+  const bool residual = p.r.p != nullptr;
+  // Every lane of a warp stays for the stores' shuffles as long as one of its rows is left.
+  const int64_t first_of_warp = __shfl_sync(0xffffffffu, m, 0);
+  for (int64_t ahead = first_of_warp; ahead < p.M; ahead += p.step, m += p.step) {
     uint4 x[kAhead], r[kAhead];
-    int64_t m[kAhead];
-    int n[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const INDEX w = first + i * kThreads;
-      m[i] = -1;
-      if (w >= words) break;
-      const INDEX row = w / per_row;
-      m[i] = row;
-      n[i] = static_cast<int>(w - row * per_row) * kWord;
-      const int left = static_cast<int>(t.N) - n[i];
-      x[i] = load_word(t.X.p + m[i] * t.X.ld + n[i], left, p.x_wide);
-      if (t.R.p != nullptr) r[i] = load_word(t.R.p + m[i] * t.R.ld + n[i], left, p.r_wide);
+      const int64_t row = m + i * at_once;
+      const int inside = row < p.M ? left : 0;
+      x[i] = row::load_word<WIDE>(p.x, p.x.p + row * p.x.ld + n, inside);
+      if (residual) r[i] = row::load_word<WIDE>(p.r, p.r.p + row * p.r.ld + n, inside);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (m[i] < 0) break;
-      float v[kWord];
-      unpack<KIND>(x[i], v);
-      drop_word(t.drop, key, static_cast<uint64_t>(m[i]) * groups + static_cast<uint64_t>(n[i] / 4), v);
-      if (t.R.p != nullptr) {
-        float u[kWord];
-        unpack<KIND>(r[i], u);
+      const int64_t row = m + i * at_once;
+      uint64_t v[4];
+      row::unpack<KIND>(x[i], v);
+      row::Keep keep;
+      keep.draw(key, static_cast<uint64_t>(row) * groups + static_cast<uint64_t>(n / 4), p.drop.dropped);
+      keep.apply(v, p.drop.factor);
+      if (residual) {
+        uint64_t u[4];
+        row::unpack<KIND>(r[i], u);
 #pragma unroll
-        for (int j = 0; j < kWord; ++j) v[j] += u[j];
+        for (int j = 0; j < 4; ++j) v[j] = row::add2(v[j], u[j]);
       }
-      store_word(t.Y.p + m[i] * t.Y.ld + n[i], static_cast<int>(t.N) - n[i], p.y_wide, pack<KIND>(v));
+      row::store_word<WIDE>(p.y, p.y.p + row * p.y.ld + n, row < p.M ? left : 0, row::pack<KIND>(v));
     }
   }
 }
 
 template <int KIND>
 cudaError_t run(const DropoutTask& t, cudaStream_t stream) {
-  DropoutParams p{t};
-  p.per_row = (t.N + kWord - 1) / kWord;
-  p.words = t.M * p.per_row;
-  p.x_wide = wide_rows(t.X.p, t.X.ld, t.M), p.r_wide = wide_rows(t.R.p, t.R.ld, t.M);
-  p.y_wide = wide_rows(t.Y.p, t.Y.ld, t.M);
-  const int64_t blocks = (p.words + kAhead * kThreads - 1) / (kAhead * kThreads);
-  constexpr int64_t kMost = 152 * 4;
-  const ff::LaunchShape shape{dim3(static_cast<unsigned>(blocks < kMost ? blocks : kMost)), kThreads, 1, 0};
-  return p.words < (int64_t{1} << 31) - kMost * kAhead * kThreads
-             ? ff::launch_early(stream, shape, dropout_kernel<KIND, uint32_t>, p)
-             : ff::launch_early(stream, shape, dropout_kernel<KIND, uint64_t>, p);
+  DropoutParams p;
+  p.x = row::view_of(t.X.p, t.X.ld, t.M, t.N), p.r = row::view_of(t.R.p, t.R.ld, t.M, t.N);
+  p.y = row::view_of(t.Y.p, t.Y.ld, t.M, t.N);
+  p.M = t.M, p.N = static_cast<int>(t.N), p.drop = t.drop;
+  // Threads along a row: a block, or a power of two where rows are short (whole warps unless rows are of whole aligned words: lanes
+  // that follow each other then hold words that do).
+  const int64_t words = (t.N + row::kWord - 1) / row::kWord;
+  const bool wide = row::whole_words(p.x, t.N) && row::whole_words(p.r, t.N) && row::whole_words(p.y, t.N);
+  p.across = wide ? 1 : 32;
+  while (p.across < words && p.across < kThreads) p.across *= 2;
+  const int64_t columns = (words + p.across - 1) / p.across, rows = kThreads / p.across;
+  const int64_t blocks = (t.M + rows * kAhead - 1) / (rows * kAhead);
+  int64_t most = 152 * 8 / columns;
+  if (most < 1) most = 1;
+  const int64_t grid = blocks < most ? blocks : most;
+  p.step = grid * rows * kAhead;
+  const ff::LaunchShape shape{dim3(static_cast<unsigned>(columns), static_cast<unsigned>(grid)), kThreads, 1, 0};
+  return wide ? ff::launch_early(stream, shape, dropout_kernel<KIND, true>, p)
+              : ff::launch_early(stream, shape, dropout_kernel<KIND, false>, p);
 }
 
 }  // namespace

@@ -28,11 +28,11 @@ enum Vector : int { kWeight = 0, kBias = 1, kGate = 2, kPostWeight = 3, kPostBia
 struct Split {
   int ctas, pieces;  // pieces 0: whole gates
 };
-constexpr int kMostCtas = 304;
-Split split_of(int64_t M, int64_t gates) {
+constexpr int kSms = 152, kMostCtas = 2 * kSms;
+Split split_of(int64_t M, int64_t gates, int ctas) {
   const int64_t rows = M / gates;
-  if (2 * gates > kMostCtas) return {static_cast<int>(gates < kMostCtas ? gates : kMostCtas), 0};
-  int64_t pieces = kMostCtas / gates;
+  if (2 * gates > ctas) return {static_cast<int>(gates < ctas ? gates : ctas), 0};
+  int64_t pieces = ctas / gates;
   if (pieces > rows) pieces = rows;
   return {static_cast<int>(gates * pieces), static_cast<int>(pieces)};
 }
@@ -171,184 +171,291 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
   }
 }
 
-// Rows of up to 8192 values: a group of threads keeps a row in registers, a word of eight values a thread; a block
-// holds several groups. The sums over rows are added in shared memory, each group's in its own place, every value by
-// one thread; at the end of a block's rows (of a gate's for dgate) the groups' sums are added in their order.
+// Rows of up to 8192 values: a group of threads takes a row, C words of eight values a thread; a block holds several
+// groups. The row's r, dy, dr and h come into shared memory, r and h of the next row as soon as this row's are in
+// registers. The sums over rows are added in shared memory too, each group's in its own place; all of these places
+// belong to one thread each. At the end of a block's rows (of a gate's for dgate) the groups' sums are added in their order.
+enum Buffer : int { kR = 0, kDy = 1, kDr = 2, kH = 3 };
 struct RowParams {
-  BackwardParams b;
-  int threads;  // of a row
-  int dy_wide, dr_wide, r_wide, h_wide, dx_wide, dh_wide, gate_wide, vectors_wide;
+  row::View in[4], vector[5], dx, dh;  // in: see Buffer; vector: of Vector's parameters (kBias: none)
+  int in_slot[4], vector_slot[5], sum_slot[5];  // places in shared memory; -1: absent, or no room
+  int in_slots, vector_slots, sum_slots;
+  int64_t M, rows_per_gate, gates;
+  Split split;
+  int N, threads;  // threads of a row
+  int norm, post;
+  float scale, eps;
+  Dropout drop;
+  Matrix dgate;
+  float* partials;
 };
 
-template <int KIND, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
-  extern __shared__ float sums[];  // slots x N for each group
-  __shared__ float rooms[Group::kRoomFloats];
-  const BackwardTask& t = p.b.t;
-  Group group(p.threads, rooms);
-  const int n = static_cast<int>(t.N), slots = p.b.slots, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
-  const int pitch = (n + kWord - 1) / kWord * kWord;
-  float* const mine = sums + static_cast<int64_t>(group.index) * slots * pitch;
-  for (int i = threadIdx.x; i < rows_at_once * slots * pitch; i += blockDim.x) sums[i] = 0.0f;
-  __syncthreads();
+template <int KIND, bool WIDE, int C, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
+  extern __shared__ uint4 words[];
+  __shared__ float rooms[row::Group::kRoomFloats];
+  row::Group group(p.threads, rooms);
+  const int n = p.N, threads = static_cast<int>(blockDim.x), rows_at_once = threads / p.threads;
+  auto column = [&](int c) { return (group.rank + c * p.threads) * row::kWord; };
+  auto place = [&](int slot, int c) { return words + (slot * C + c) * threads + static_cast<int>(threadIdx.x); };
+  const int first_sum = p.in_slots + p.vector_slots;  // a sum's eight values are two places of 16 bytes
+  for (int i = 0; i < 2 * p.sum_slots * C; ++i) words[(first_sum * C + i) * threads + threadIdx.x] = make_uint4(0, 0, 0, 0);
   ff::wait_for_earlier_kernels();
-  const int64_t groups = (t.N + 3) / 4;
-  const float inv_n = 1.0f / static_cast<float>(n);
-  const uint64_t key = t.drop.dropped != 0 ? drop_key(t.drop) : 0;
-  const bool has_h = t.H.p != nullptr, has_norm = t.norm != T2S_NORM_NONE, has_post = has_h && t.post != T2S_NORM_NONE;
-  const bool layer = t.norm == T2S_NORM_LAYER, post_layer = has_post && t.post == T2S_NORM_LAYER;
-  const Rows rows = rows_of(p.b, blockIdx.x);
-  const int at = group.rank * kWord, left = n - at;
-  auto add = [&](int vector, const float (&v)[kWord]) {
-    if (p.b.slot[vector] < 0) return;
-    float4* to = reinterpret_cast<float4*>(mine + p.b.slot[vector] * pitch + at);
-    float4 a = to[0], b = to[1];
-    a.x += v[0], a.y += v[1], a.z += v[2], a.w += v[3];
-    b.x += v[4], b.y += v[5], b.z += v[6], b.w += v[7];
-    to[0] = a, to[1] = b;
+  // A parameter's words: in shared memory, or read again for each row where that is full.
+  int64_t gate_row = 0;
+  auto read_vector = [&](int vector, int c) {
+    const row::View& v = p.vector[vector];
+    return row::load_word<WIDE>(v, v.p + (vector == kGate ? gate_row * v.ld : 0) + column(c), n - column(c));
   };
+  auto load_vector = [&](int vector) {
+    if (p.vector_slot[vector] < 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) *place(p.vector_slot[vector], c) = read_vector(vector, c);
+  };
+  auto parameter = [&](int vector, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(p.vector_slot[vector] >= 0 ? *place(p.vector_slot[vector], c) : read_vector(vector, c), f);
+  };
+  load_vector(kWeight);
+  load_vector(kPostWeight);
+  load_vector(kPostBias);
+  const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(n) + 3) / 4);
+  const float inv_n = 1.0f / static_cast<float>(n);
+  const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
+  const bool has_h = p.in[kH].p != nullptr, has_norm = p.norm != T2S_NORM_NONE, has_post = has_h && p.post != T2S_NORM_NONE;
+  const bool layer = p.norm == T2S_NORM_LAYER, post_layer = has_post && p.post == T2S_NORM_LAYER;
+
+  auto fetch = [&](int buffer, int64_t m, int64_t end) {
+    if (p.in_slot[buffer] < 0 || m >= end) return;
+    const row::View& v = p.in[buffer];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint16_t* from = v.p + m * v.ld + column(c);
+      uint4* to = place(p.in_slot[buffer], c);
+      const int left = n - column(c);
+      if (WIDE ? left > 0 : v.wide && left >= row::kWord) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+      } else {
+        *to = row::load_word<WIDE>(v, from, left);
+      }
+    }
+  };
+  auto add = [&](int vector, int c, const uint64_t(&f)[4]) {
+    if (p.sum_slot[vector] < 0) return;
+    ulonglong2* to = reinterpret_cast<ulonglong2*>(words + (first_sum + 2 * p.sum_slot[vector]) * C * threads) +
+                     2 * c * threads + threadIdx.x;
+    ulonglong2 lo = to[0], hi = to[threads];
+    lo.x = row::add2(lo.x, f[0]), lo.y = row::add2(lo.y, f[1]);
+    hi.x = row::add2(hi.x, f[2]), hi.y = row::add2(hi.y, f[3]);
+    to[0] = lo, to[threads] = hi;
+  };
+  // The sum of column i over the groups, which are cleared if `clear`.
+  auto total = [&](int slot, int i, bool clear) {
+    float s = 0.0f;
+    const int word = i / row::kWord, c = word / p.threads, thread = word - c * p.threads, j = i % row::kWord;
+    float* from = reinterpret_cast<float*>(words + (first_sum + 2 * slot) * C * threads) +
+                  ((2 * c + j / 4) * threads + thread) * 4 + j % 4;
+    for (int g = 0; g < rows_at_once; ++g, from += p.threads * 4) {
+      s += *from;
+      if (clear) *from = 0.0f;
+    }
+    return s;
+  };
+
+  int64_t first, last;
+  if (p.split.pieces > 0) {
+    const int64_t g = blockIdx.x / p.split.pieces, j = blockIdx.x % p.split.pieces;
+    first = g * p.rows_per_gate + p.rows_per_gate * j / p.split.pieces;
+    last = g * p.rows_per_gate + p.rows_per_gate * (j + 1) / p.split.pieces;
+  } else {
+    first = p.gates * blockIdx.x / p.split.ctas * p.rows_per_gate;
+    last = p.gates * (blockIdx.x + 1) / p.split.ctas * p.rows_per_gate;
+  }
   // One gate's rows after another (one stretch of rows where a gate has several blocks).
-  const int64_t stretch = p.b.split.pieces > 0 ? rows.last - rows.first : rows.per_gate;
-  for (int64_t m0 = rows.first; m0 < rows.last; m0 += stretch) {
-    const int64_t gate_row = m0 / rows.per_gate;
-    const uint16_t* gate = t.gate.p == nullptr ? nullptr : t.gate.p + gate_row * t.gate.ld;
-    for (int64_t m = m0 + group.index; m < m0 + stretch; m += rows_at_once) {
-      uint4 r4 = make_uint4(0, 0, 0, 0), dy4 = r4, dr4 = r4, h4 = r4;
-      if (left > 0) {
-        if (has_norm) {
-          r4 = load_word(t.R.p + m * t.R.ld + at, left, p.r_wide);
-          dy4 = load_word(t.dY.p + m * t.dY.ld + at, left, p.dy_wide);
-        }
-        if (t.dR.p != nullptr) dr4 = load_word(t.dR.p + m * t.dR.ld + at, left, p.dr_wide);
-        if (has_h) h4 = load_word(t.H.p + m * t.H.ld + at, left, p.h_wide);
+  const int64_t stretch = p.split.pieces > 0 ? last - first : p.rows_per_gate;
+  for (int64_t m0 = first; m0 < last; m0 += stretch) {
+    const int64_t end = m0 + stretch;
+    gate_row = m0 / p.rows_per_gate;
+    load_vector(kGate);
+    int64_t m = m0 + group.index;
+    for (int b = 0; b < 4; ++b) fetch(b, m, end);
+    for (; m < end; m += rows_at_once) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      uint64_t xh[C][4], hh[C][4], d[C][4];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (has_norm) row::unpack<KIND>(*place(p.in_slot[kR], c), xh[c]);
+        if (has_h) row::unpack<KIND>(*place(p.in_slot[kH], c), hh[c]);
       }
-      float xh[kWord], g[kWord], hh[kWord];
-      unpack<KIND>(r4, xh);
-      unpack<KIND>(h4, hh);
-      float means[2] = {0.0f, 0.0f};
+      fetch(kR, m + rows_at_once, end);
+      fetch(kH, m + rows_at_once, end);
       if (layer || post_layer) {
+        float means[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kWord; ++i) means[0] += xh[i], means[1] += hh[i];
-        group.sums(means);
-        means[0] = layer ? means[0] * inv_n : 0.0f;
-        means[1] = post_layer ? means[1] * inv_n : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kWord; ++i)
-          if (i < left) xh[i] -= means[0], hh[i] -= means[1];
-      }
-      unpack<KIND>(dy4, g);
-      float w[kWord];
-      if (left > 0 && t.weight != nullptr) {
-        parameter<KIND>(t.weight, at, left, p.vectors_wide, 1.0f, w);
-#pragma unroll
-        for (int i = 0; i < kWord; ++i) g[i] *= w[i];
-      }
-      float s[4] = {};
-#pragma unroll
-      for (int i = 0; i < kWord; ++i) {
-        s[0] = fmaf(xh[i], xh[i], s[0]);
-        s[1] += g[i];
-        s[2] = fmaf(g[i], xh[i], s[2]);
-        s[3] = fmaf(hh[i], hh[i], s[3]);
-      }
-      if (has_norm || has_post) group.sums(s);
-      const float rho = rsqrtf(s[0] * inv_n + t.eps), sigma = has_post ? rsqrtf(s[3] * inv_n + t.eps) : 1.0f;
-      const float mean_g = layer ? s[1] * inv_n : 0.0f, mean_gx = s[2] * inv_n * rho;
-      float d[kWord];
-      unpack<KIND>(dr4, d);
-      if (has_norm) {
-#pragma unroll
-        for (int i = 0; i < kWord; ++i) {
-          xh[i] *= rho;
-          d[i] += rho * (g[i] - mean_g - xh[i] * mean_gx);
-          if (i >= left) d[i] = 0.0f;  // the means are not for the values beyond the row's end
+        for (int c = 0; c < C; ++c) {
+          if (layer) means[0] += row::sum(xh[c]);
+          if (post_layer) means[1] += row::sum(hh[c]);
         }
+        group.sums(means);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (layer) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xh[c][i] = row::add2(xh[c][i], row::both(-means[0] * inv_n));
+            row::clear_from<WIDE>(xh[c], n - column(c));
+          }
+          if (post_layer) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hh[c][i] = row::add2(hh[c][i], row::both(-means[1] * inv_n));
+            row::clear_from<WIDE>(hh[c], n - column(c));
+          }
+        }
+      }
+      float rho = 1.0f, sigma = 1.0f, mean_g = 0.0f, mean_gx = 0.0f;
+      if (has_norm || has_post) {
+        float s[4] = {};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (has_norm) {
+            uint64_t g[4], w[4];
+            row::unpack<KIND>(*place(p.in_slot[kDy], c), g);
+            if (p.vector[kWeight].p != nullptr) {
+              parameter(kWeight, c, w);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) g[i] = row::mul2(g[i], w[i]);
+            }
+            s[0] += row::dot(xh[c], xh[c]);
+            s[1] += row::dot(g, xh[c]);
+            if (layer) s[2] += row::sum(g);
+          }
+          if (has_post) s[3] += row::dot(hh[c], hh[c]);
+        }
+        if (layer || has_post) {
+          group.sums(s);
+        } else {
+          float two[2] = {s[0], s[1]};
+          group.sums(two);
+          s[0] = two[0], s[1] = two[1];
+        }
+        if (has_norm) {
+          rho = rsqrtf(s[0] * inv_n + p.eps);
+          mean_gx = s[1] * inv_n * rho;
+          mean_g = s[2] * inv_n;
+        }
+        if (has_post) sigma = rsqrtf(s[3] * inv_n + p.eps);
       }
       float q[2] = {0.0f, 0.0f};
-      if (left > 0) {
-        if (has_norm) {
-          unpack<KIND>(dy4, g);
-          add(kBias, g);
 #pragma unroll
-          for (int i = 0; i < kWord; ++i) g[i] *= xh[i];
-          add(kWeight, g);
+      for (int c = 0; c < C; ++c) {
+        const int at = column(c), left = n - at;
+        uint64_t f[4], w[4];
+        if (p.in_slot[kDr] >= 0) {
+          row::unpack<KIND>(*place(p.in_slot[kDr], c), d[c]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[c][i] = 0;
         }
-        if (t.dX.p != nullptr) {
+        if (has_norm) {
+          row::unpack<KIND>(*place(p.in_slot[kDy], c), f);
+          add(kBias, c, f);
+          uint64_t g[4];
 #pragma unroll
-          for (int i = 0; i < kWord; ++i) g[i] = t.scale * d[i];
-          store_word(t.dX.p + m * t.dX.ld + at, left, p.dx_wide, pack<KIND>(g));
+          for (int i = 0; i < 4; ++i) {
+            xh[c][i] = row::mul2(xh[c][i], row::both(rho));
+            g[i] = row::mul2(f[i], xh[c][i]);
+          }
+          add(kWeight, c, g);
+          if (p.vector[kWeight].p != nullptr) {
+            parameter(kWeight, c, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = row::fma2(xh[c][i], row::both(-mean_gx), f[i]);
+            if (layer) f[i] = row::add2(f[i], row::both(-mean_g));
+            d[c][i] = row::fma2(f[i], row::both(rho), d[c][i]);
+          }
+          if (layer) row::clear_from<WIDE>(d[c], left);  // the mean is not for the values beyond the row's end
+        }
+        if (p.dx.p != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], row::both(p.scale));
+          row::store_word<WIDE>(p.dx, p.dx.p + m * p.dx.ld + at, left, row::pack<KIND>(f));
         }
         if (has_h) {
-          float pw[kWord];
-          parameter<KIND>(t.post_weight, at, left, p.vectors_wide, 1.0f, pw);
+          row::Keep keep;
+          if (p.drop.dropped != 0)
+            keep.draw(key, static_cast<uint64_t>(m) * groups + static_cast<uint64_t>(at / 4), p.drop.dropped);
 #pragma unroll
-          for (int i = 0; i < kWord; ++i) hh[i] *= sigma;
-          const uint64_t word = static_cast<uint64_t>(m * groups + at / 4);
-          if (p.b.slot[kGate] >= 0) {
-            if (has_post) {
-              parameter<KIND>(t.post_bias, at, left, p.vectors_wide, 0.0f, w);
+          for (int i = 0; i < 4; ++i) hh[c][i] = row::mul2(hh[c][i], row::both(sigma));
+          if (p.sum_slot[kGate] >= 0) {
 #pragma unroll
-              for (int i = 0; i < kWord; ++i) g[i] = fmaf(hh[i], pw[i], w[i]);
-            } else {
+            for (int i = 0; i < 4; ++i) f[i] = hh[c][i];
+            if (p.vector[kPostWeight].p != nullptr) {
+              parameter(kPostWeight, c, w);
 #pragma unroll
-              for (int i = 0; i < kWord; ++i) g[i] = hh[i];
+              for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
             }
-            if (t.drop.dropped != 0) drop_word(t.drop, key, word, g);
+            if (p.vector[kPostBias].p != nullptr) {
+              parameter(kPostBias, c, w);
 #pragma unroll
-            for (int i = 0; i < kWord; ++i) g[i] *= d[i];
-            add(kGate, g);
-          }
-          if (gate != nullptr) {
-            parameter<KIND>(gate, at, left, p.gate_wide, 1.0f, w);
+              for (int i = 0; i < 4; ++i) f[i] = row::add2(f[i], w[i]);
+            }
+            if (p.drop.dropped != 0) keep.apply(f, p.drop.factor);
 #pragma unroll
-            for (int i = 0; i < kWord; ++i) d[i] *= w[i];
+            for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], d[c][i]);
+            add(kGate, c, f);
           }
-          if (t.drop.dropped != 0) drop_word(t.drop, key, word, d);
+          if (p.vector[kGate].p != nullptr) {
+            parameter(kGate, c, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
+          }
+          if (p.drop.dropped != 0) keep.apply(d[c], p.drop.factor);
           if (has_post) {
-            add(kPostBias, d);
+            add(kPostBias, c, d[c]);
 #pragma unroll
-            for (int i = 0; i < kWord; ++i) g[i] = d[i] * hh[i];
-            add(kPostWeight, g);
+            for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], hh[c][i]);
+            add(kPostWeight, c, f);
+            if (p.vector[kPostWeight].p != nullptr) {
+              parameter(kPostWeight, c, w);
 #pragma unroll
-            for (int i = 0; i < kWord; ++i) {
-              d[i] *= pw[i];
-              q[0] += d[i];
-              q[1] = fmaf(d[i], hh[i], q[1]);
+              for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
             }
+            if (post_layer) q[0] += row::sum(d[c]);
+            q[1] += row::dot(d[c], hh[c]);
           }
         }
       }
-      if (!has_h || t.dH.p == nullptr) continue;
+      fetch(kDy, m + rows_at_once, end);
+      fetch(kDr, m + rows_at_once, end);
+      if (p.dh.p == nullptr) continue;
       if (has_post) {
         group.sums(q);
-        const float mean_q = post_layer ? q[0] * inv_n : 0.0f, mean_qh = q[1] * inv_n;
 #pragma unroll
-        for (int i = 0; i < kWord; ++i) d[i] = sigma * (d[i] - mean_q - hh[i] * mean_qh);
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            d[c][i] = row::fma2(hh[c][i], row::both(-q[1] * inv_n), d[c][i]);
+            if (post_layer) d[c][i] = row::add2(d[c][i], row::both(-q[0] * inv_n));
+            d[c][i] = row::mul2(d[c][i], row::both(sigma));
+          }
       }
-      if (left > 0) store_word(t.dH.p + m * t.dH.ld + at, left, p.dh_wide, pack<KIND>(d));
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        row::store_word<WIDE>(p.dh, p.dh.p + m * p.dh.ld + column(c), n - column(c), row::pack<KIND>(d[c]));
     }
-    if (p.b.split.pieces == 0 && p.b.slot[kGate] >= 0) {
+    if (p.split.pieces == 0 && p.sum_slot[kGate] >= 0) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        float sum = 0.0f;
-        for (int j = 0; j < rows_at_once; ++j) {
-          float* from = sums + (static_cast<int64_t>(j) * slots + p.b.slot[kGate]) * pitch + i;
-          sum += *from;
-          *from = 0.0f;
-        }
-        t.dgate.p[gate_row * t.dgate.ld + i] = ff::from_f32<KIND>(sum);
-      }
+      for (int i = threadIdx.x; i < n; i += threads)
+        p.dgate.p[gate_row * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_slot[kGate], i, true));
       __syncthreads();
     }
   }
   __syncthreads();
-  float* const out = t.partials + static_cast<int64_t>(blockIdx.x) * slots * n;
-  for (int slot = 0; slot < slots; ++slot)
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      float sum = 0.0f;
-      for (int j = 0; j < rows_at_once; ++j) sum += sums[(static_cast<int64_t>(j) * slots + slot) * pitch + i];
-      out[static_cast<int64_t>(slot) * n + i] = sum;
-    }
+  float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * n;
+  for (int slot = 0; slot < p.sum_slots; ++slot)
+    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(slot, i, false);
 }
 
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
@@ -397,61 +504,99 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
   p.out[which][row * p.ldgate + n] = ff::from_f32<KIND>(sum);
 }
 
-template <int KIND, int THREADS>
-cudaError_t launch_rows(const BackwardParams& b, cudaStream_t stream) {
-  constexpr int kMaxDevices = 64, kMaxSmem = 5 * 8192 * 4;
-  static std::atomic<bool> prepared[kMaxDevices];
-  auto kern = row_backward_kernel<KIND, THREADS>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!prepared[dev].load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) != cudaSuccess) return e;
-    prepared[dev].store(true, std::memory_order_release);
-  }
-  const BackwardTask& t = b.t;
-  const int words = static_cast<int>((t.N + kWord - 1) / kWord);
-  RowParams p{b, (words + 31) / 32 * 32};
-  p.dy_wide = wide_rows(t.dY.p, t.dY.ld, t.M), p.dr_wide = wide_rows(t.dR.p, t.dR.ld, t.M);
-  p.r_wide = wide_rows(t.R.p, t.R.ld, t.M), p.h_wide = wide_rows(t.H.p, t.H.ld, t.M);
-  p.dx_wide = wide_rows(t.dX.p, t.dX.ld, t.M), p.dh_wide = wide_rows(t.dH.p, t.dH.ld, t.M);
-  p.gate_wide = wide_rows(t.gate.p, t.gate.ld, t.gates);
-  p.vectors_wide = wide_rows(t.weight, 0, 1) && wide_rows(t.post_weight, 0, 1) && wide_rows(t.post_bias, 0, 1);
-  const int rows = THREADS / p.threads;
-  const int smem = rows * b.slots * words * kWord * 4;
-  return ff::launch_early(stream, {dim3(static_cast<unsigned>(b.split.ctas)), rows * p.threads, 1, smem}, kern, p);
+// How the row kernel takes a row: words of a thread, threads of a row, threads of a block.
+struct RowPlan {
+  int words, threads, block;  // words 0: too long
+};
+RowPlan row_plan(int64_t N) {
+  const int64_t words = (N + row::kWord - 1) / row::kWord;
+  if (words <= 32) return {1, 32, 256};
+  if (words > 1024) return {0, 0, 0};
+  const int threads = static_cast<int>((words + 63) / 64 * 32);
+  return {2, threads, threads <= 256 ? 256 / threads * threads : threads};
+}
+
+constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
+
+template <int KIND, bool WIDE, int C, int THREADS>
+cudaError_t launch_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
+  constexpr int kAll = (4 + 4 + 2 * kVectors) * C * THREADS * 16, kMaxSmem = kAll < kMostSmem ? kAll : kMostSmem;
+  static_assert((4 + 2 * kVectors) * C * THREADS * 16 <= kMostSmem, "without the parameters there is room");
+  cudaError_t e = prepare_smem<row_backward_kernel<KIND, WIDE, C, THREADS>>(kMaxSmem);
+  return e != cudaSuccess ? e
+                          : ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), plan.block, 1, smem},
+                                             row_backward_kernel<KIND, WIDE, C, THREADS>, p);
+}
+
+template <int KIND, bool WIDE>
+cudaError_t run_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
+  return plan.words == 1     ? launch_rows<KIND, WIDE, 1, 256>(p, plan, smem, stream)
+         : plan.block <= 256 ? launch_rows<KIND, WIDE, 2, 256>(p, plan, smem, stream)
+                             : launch_rows<KIND, WIDE, 2, 512>(p, plan, smem, stream);
 }
 
 template <int KIND>
 cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
-  BackwardParams p;
-  p.t = t;
-  p.split = split_of(t.M, t.gates);
   uint16_t* const outs[kVectors] = {t.dweight, t.dbias, t.dgate.p, t.dpost_weight, t.dpost_bias};
-  p.slots = 0;
+  int slot[kVectors], slots = 0;
   SumParams s;
   memset(&s, 0, sizeof(s));
   for (int i = 0; i < kVectors; ++i) {
-    p.slot[i] = s.slot[i] = outs[i] != nullptr ? p.slots++ : -1;
+    slot[i] = s.slot[i] = outs[i] != nullptr ? slots++ : -1;
     s.out[i] = outs[i];
     if (i != kGate && outs[i] != nullptr) ++s.vectors;
   }
-  if (p.slots == 0 && t.dX.p == nullptr && t.dH.p == nullptr) return cudaSuccess;
-  cudaError_t e = t.N <= 4096 ? launch_rows<KIND, 512>(p, stream)
-                  : t.N <= 8192
-                      ? launch_rows<KIND, 1024>(p, stream)
-                      : ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), kWideThreads, 1, 0},
-                                         wide_backward_kernel<KIND>, p);
+  if (slots == 0 && t.dX.p == nullptr && t.dH.p == nullptr) return cudaSuccess;
+  const RowPlan plan = row_plan(t.N);
+  cudaError_t e;
+  Split split;
+  if (plan.words > 0) {
+    RowParams p;
+    memset(&p, 0, sizeof(p));
+    const Input in[4] = {t.norm != T2S_NORM_NONE ? t.R : Input{}, t.dY, t.dR, t.H};
+    const uint16_t* const vectors[kVectors] = {t.weight, nullptr, t.gate.p, t.post_weight, t.post_bias};
+    for (int i = 0; i < 4; ++i) {
+      p.in[i] = row::view_of(in[i].p, in[i].ld, t.M, t.N);
+      p.in_slot[i] = in[i].p != nullptr ? p.in_slots++ : -1;
+    }
+    for (int i = 0; i < kVectors; ++i) {
+      p.vector[i] = row::view_of(vectors[i], t.gate.ld, i == kGate ? t.gates : 1, t.N);
+      p.vector_slot[i] = vectors[i] != nullptr ? p.in_slots + p.vector_slots++ : -1;
+      p.sum_slot[i] = slot[i];
+    }
+    p.sum_slots = slots;
+    p.dx = row::view_of(t.dX.p, t.dX.ld, t.M, t.N), p.dh = row::view_of(t.dH.p, t.dH.ld, t.M, t.N);
+    p.M = t.M, p.rows_per_gate = t.M / t.gates, p.gates = t.gates, p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
+    p.dgate = t.dgate, p.partials = t.partials;
+    bool wide = row::whole_words(p.dx, t.N) && row::whole_words(p.dh, t.N);
+    for (const row::View& v : p.in) wide = wide && row::whole_words(v, t.N);
+    for (const row::View& v : p.vector) wide = wide && row::whole_words(v, t.N);
+    const int slot_bytes = plan.words * plan.block * 16;
+    if ((p.in_slots + p.vector_slots + 2 * slots) * slot_bytes > kMostSmem) {
+      p.vector_slots = 0;
+      for (int& v : p.vector_slot) v = -1;
+    }
+    const int smem = (p.in_slots + p.vector_slots + 2 * slots) * slot_bytes;
+    p.split = split = split_of(t.M, t.gates, plan.block <= 256 && smem <= 112 * 1024 ? kMostCtas : kSms);
+    e = wide ? run_rows<KIND, true>(p, plan, smem, stream) : run_rows<KIND, false>(p, plan, smem, stream);
+  } else {
+    BackwardParams p;
+    p.t = t;
+    p.split = split = split_of(t.M, t.gates, kMostCtas);
+    for (int i = 0; i < kVectors; ++i) p.slot[i] = slot[i];
+    p.slots = slots;
+    e = ff::launch_early(stream, {dim3(static_cast<unsigned>(split.ctas)), kWideThreads, 1, 0}, wide_backward_kernel<KIND>, p);
+  }
   if (e != cudaSuccess) return e;
-  s.gate_rows = t.dgate.p != nullptr && p.split.pieces > 0 ? static_cast<int>(t.gates) : 0;
+  s.gate_rows = t.dgate.p != nullptr && split.pieces > 0 ? static_cast<int>(t.gates) : 0;
   if (s.vectors + s.gate_rows == 0) return cudaSuccess;
   s.partials = t.partials;
   s.N = t.N;
   s.ldgate = t.dgate.ld;
-  s.slots = p.slots;
-  s.ctas = p.split.ctas;
-  s.pieces = p.split.pieces;
+  s.slots = slots;
+  s.ctas = split.ctas;
+  s.pieces = split.pieces;
   const dim3 grid(static_cast<unsigned>((t.N + 31) / 32), static_cast<unsigned>(s.vectors + s.gate_rows));
   return ff::launch_early(stream, {grid, 32 * kSumWarps, 1, 0}, share_sum_kernel<KIND>, s);
 }
@@ -460,7 +605,7 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
 
 size_t backward_workspace_bytes(int64_t M, int64_t N, int64_t gates, int vectors) {
   if (M == 0 || N == 0 || vectors == 0) return 0;
-  return static_cast<size_t>(split_of(M, gates).ctas) * static_cast<size_t>(vectors) * static_cast<size_t>(N) * 4;
+  return static_cast<size_t>(split_of(M, gates, kMostCtas).ctas) * static_cast<size_t>(vectors) * static_cast<size_t>(N) * 4;
 }
 
 cudaError_t run_backward(const BackwardTask& t, cudaStream_t stream) {
