@@ -172,15 +172,16 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
 }
 
 // Rows of up to 8192 values: a group of threads takes a row, C words of eight values a thread; a block holds several
-// groups. The row's r, dy, dr and h come into shared memory, r and h of the next row as soon as this row's are in
-// registers. The sums over rows are added in shared memory too, each group's in its own place; all of these places
-// belong to one thread each. At the end of a block's rows (of a gate's for dgate) the groups' sums are added in their order.
-enum Buffer : int { kR = 0, kDy = 1, kDr = 2, kH = 3 };
+// groups. The row's r, dy, dr and h come to shared memory, r and h of the next row as soon as this row's are in
+// registers, and the parameters' words stay there. The sums over rows are added in shared memory too, each group's in its
+// own place. All of these places belong to one thread each. At the end of a block's rows (of a gate's for dgate) the
+// groups' sums are added in their order.
+enum Place : int { kR = 0, kDy = 1, kDr = 2, kH = 3, kW = 4, kG = 5, kPw = 6, kPb = 7, kPlaces = 8 };
 struct RowParams {
-  row::View in[4], vector[5], dx, dh;  // in: see Buffer; vector: of Vector's parameters (kBias: none)
-  int in_slot[4], vector_slot[5], sum_slot[5];  // places in shared memory; -1: absent, or no room
-  int in_slots, vector_slots, sum_slots;
-  int64_t M, rows_per_gate, gates;
+  row::View in[kPlaces], dx, dh;
+  int at[kPlaces], sum_at[kVectors];  // of these words in shared memory; -1: absent, or no room
+  int sum_slots, sum_first;
+  int64_t rows_per_gate, gates;
   Split split;
   int N, threads;  // threads of a row
   int norm, post;
@@ -194,66 +195,58 @@ template <int KIND, bool WIDE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
+  constexpr int kNext = C * THREADS;  // from a word's first place to its second (not WIDE)
   row::Group group(p.threads, rooms);
   const int n = p.N, threads = static_cast<int>(blockDim.x), rows_at_once = threads / p.threads;
-  auto column = [&](int c) { return (group.rank + c * p.threads) * row::kWord; };
-  auto place = [&](int slot, int c) { return words + (slot * C + c) * threads + static_cast<int>(threadIdx.x); };
-  const int first_sum = p.in_slots + p.vector_slots;  // a sum's eight values are two places of 16 bytes
-  for (int i = 0; i < 2 * p.sum_slots * C; ++i) words[(first_sum * C + i) * threads + threadIdx.x] = make_uint4(0, 0, 0, 0);
+  const uint32_t first_column = static_cast<uint32_t>(group.rank) * row::kWord;
+  auto column = [&](int c) { return first_column + static_cast<uint32_t>(c * p.threads * row::kWord); };
+  auto left_of = [&](int c) { return n - static_cast<int>(column(c)); };
+  // A sum's eight values are two places of 16 bytes.
+  for (int i = 0; i < 2 * p.sum_slots * C; ++i) words[p.sum_first + i * THREADS + threadIdx.x] = make_uint4(0, 0, 0, 0);
   ff::wait_for_earlier_kernels();
-  // A parameter's words: in shared memory, or read again for each row where that is full.
-  int64_t gate_row = 0;
-  auto read_vector = [&](int vector, int c) {
-    const row::View& v = p.vector[vector];
-    return row::load_word<WIDE>(v, v.p + (vector == kGate ? gate_row * v.ld : 0) + column(c), n - column(c));
-  };
-  auto load_vector = [&](int vector) {
-    if (p.vector_slot[vector] < 0) return;
+  auto fetch = [&](int place, int64_t m) {
+    if (p.at[place] < 0) return;
+    const uint16_t* from = p.in[place].p + m * p.in[place].ld;
 #pragma unroll
-    for (int c = 0; c < C; ++c) *place(p.vector_slot[vector], c) = read_vector(vector, c);
+    for (int c = 0; c < C; ++c)
+      row::fetch_word<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, p.in[place], from + column(c), left_of(c));
   };
-  auto parameter = [&](int vector, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(p.vector_slot[vector] >= 0 ? *place(p.vector_slot[vector], c) : read_vector(vector, c), f);
+  auto get = [&](int place, int64_t m, int c, uint64_t(&f)[4]) {
+    const uint16_t* from = p.in[place].p + m * p.in[place].ld + column(c);
+    row::unpack<KIND>(row::arrived<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, from, left_of(c)), f);
   };
-  load_vector(kWeight);
-  load_vector(kPostWeight);
-  load_vector(kPostBias);
+  // A parameter's words, in shared memory, or read again for each row where that is full.
+  int64_t gate_row = 0;
+  auto parameter = [&](int place, int c, uint64_t(&f)[4]) {
+    const int64_t m = place == kG ? gate_row : 0;
+    if (p.at[place] >= 0) {
+      get(place, m, c, f);
+    } else {
+      row::unpack<KIND>(row::load_word<WIDE>(p.in[place], p.in[place].p + m * p.in[place].ld + column(c), left_of(c)), f);
+    }
+  };
+  fetch(kW, 0);
+  fetch(kPw, 0);
+  fetch(kPb, 0);
   const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(n) + 3) / 4);
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
   const bool has_h = p.in[kH].p != nullptr, has_norm = p.norm != T2S_NORM_NONE, has_post = has_h && p.post != T2S_NORM_NONE;
   const bool layer = p.norm == T2S_NORM_LAYER, post_layer = has_post && p.post == T2S_NORM_LAYER;
 
-  auto fetch = [&](int buffer, int64_t m, int64_t end) {
-    if (p.in_slot[buffer] < 0 || m >= end) return;
-    const row::View& v = p.in[buffer];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint16_t* from = v.p + m * v.ld + column(c);
-      uint4* to = place(p.in_slot[buffer], c);
-      const int left = n - column(c);
-      if (WIDE ? left > 0 : v.wide && left >= row::kWord) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-      } else {
-        *to = row::load_word<WIDE>(v, from, left);
-      }
-    }
-  };
   auto add = [&](int vector, int c, const uint64_t(&f)[4]) {
-    if (p.sum_slot[vector] < 0) return;
-    ulonglong2* to = reinterpret_cast<ulonglong2*>(words + (first_sum + 2 * p.sum_slot[vector]) * C * threads) +
-                     2 * c * threads + threadIdx.x;
-    ulonglong2 lo = to[0], hi = to[threads];
+    if (p.sum_at[vector] < 0) return;
+    ulonglong2* to = reinterpret_cast<ulonglong2*>(words + p.sum_at[vector] + 2 * c * THREADS + threadIdx.x);
+    ulonglong2 lo = to[0], hi = to[THREADS];
     lo.x = row::add2(lo.x, f[0]), lo.y = row::add2(lo.y, f[1]);
     hi.x = row::add2(hi.x, f[2]), hi.y = row::add2(hi.y, f[3]);
-    to[0] = lo, to[threads] = hi;
+    to[0] = lo, to[THREADS] = hi;
   };
-  // The sum of column i over the groups, which are cleared if `clear`.
-  auto total = [&](int slot, int i, bool clear) {
+  // A sum's column i over the groups, which are cleared if `clear`.
+  auto total = [&](int sum_at, int i, bool clear) {
     float s = 0.0f;
-    const int word = i / row::kWord, c = word / p.threads, thread = word - c * p.threads, j = i % row::kWord;
-    float* from = reinterpret_cast<float*>(words + (first_sum + 2 * slot) * C * threads) +
-                  ((2 * c + j / 4) * threads + thread) * 4 + j % 4;
+    const int word = i / row::kWord, c = word < p.threads ? 0 : 1, thread = word - c * p.threads, j = i % row::kWord;
+    float* from = reinterpret_cast<float*>(words + sum_at + (2 * c + j / 4) * THREADS + thread) + j % 4;
     for (int g = 0; g < rows_at_once; ++g, from += p.threads * 4) {
       s += *from;
       if (clear) *from = 0.0f;
@@ -275,19 +268,24 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
   for (int64_t m0 = first; m0 < last; m0 += stretch) {
     const int64_t end = m0 + stretch;
     gate_row = m0 / p.rows_per_gate;
-    load_vector(kGate);
+    fetch(kG, gate_row);
     int64_t m = m0 + group.index;
-    for (int b = 0; b < 4; ++b) fetch(b, m, end);
+    if (m < end)
+#pragma unroll 1
+      for (int i = kR; i <= kH; ++i) fetch(i, m);
     for (; m < end; m += rows_at_once) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      const bool more = m + rows_at_once < end;
+      row::wait_copies();
       uint64_t xh[C][4], hh[C][4], d[C][4];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (has_norm) row::unpack<KIND>(*place(p.in_slot[kR], c), xh[c]);
-        if (has_h) row::unpack<KIND>(*place(p.in_slot[kH], c), hh[c]);
+        if (has_norm) get(kR, m, c, xh[c]);
+        if (has_h) get(kH, m, c, hh[c]);
       }
-      fetch(kR, m + rows_at_once, end);
-      fetch(kH, m + rows_at_once, end);
+      if (more) {
+        fetch(kR, m + rows_at_once);
+        fetch(kH, m + rows_at_once);
+      }
       if (layer || post_layer) {
         float means[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -301,12 +299,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
           if (layer) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) xh[c][i] = row::add2(xh[c][i], row::both(-means[0] * inv_n));
-            row::clear_from<WIDE>(xh[c], n - column(c));
+            row::clear_from<WIDE>(xh[c], left_of(c));
           }
           if (post_layer) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) hh[c][i] = row::add2(hh[c][i], row::both(-means[1] * inv_n));
-            row::clear_from<WIDE>(hh[c], n - column(c));
+            row::clear_from<WIDE>(hh[c], left_of(c));
           }
         }
       }
@@ -317,9 +315,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
         for (int c = 0; c < C; ++c) {
           if (has_norm) {
             uint64_t g[4], w[4];
-            row::unpack<KIND>(*place(p.in_slot[kDy], c), g);
-            if (p.vector[kWeight].p != nullptr) {
-              parameter(kWeight, c, w);
+            get(kDy, m, c, g);
+            if (p.in[kW].p != nullptr) {
+              parameter(kW, c, w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) g[i] = row::mul2(g[i], w[i]);
             }
@@ -346,16 +344,16 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
       float q[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int at = column(c), left = n - at;
+        const int left = left_of(c);
         uint64_t f[4], w[4];
-        if (p.in_slot[kDr] >= 0) {
-          row::unpack<KIND>(*place(p.in_slot[kDr], c), d[c]);
+        if (p.at[kDr] >= 0) {
+          get(kDr, m, c, d[c]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[c][i] = 0;
         }
         if (has_norm) {
-          row::unpack<KIND>(*place(p.in_slot[kDy], c), f);
+          get(kDy, m, c, f);
           add(kBias, c, f);
           uint64_t g[4];
 #pragma unroll
@@ -364,8 +362,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
             g[i] = row::mul2(f[i], xh[c][i]);
           }
           add(kWeight, c, g);
-          if (p.vector[kWeight].p != nullptr) {
-            parameter(kWeight, c, w);
+          if (p.in[kW].p != nullptr) {
+            parameter(kW, c, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
           }
@@ -380,24 +378,24 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
         if (p.dx.p != nullptr) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], row::both(p.scale));
-          row::store_word<WIDE>(p.dx, p.dx.p + m * p.dx.ld + at, left, row::pack<KIND>(f));
+          row::store_word<WIDE>(p.dx, p.dx.p + m * p.dx.ld + column(c), left, row::pack<KIND>(f));
         }
         if (has_h) {
           row::Keep keep;
           if (p.drop.dropped != 0)
-            keep.draw(key, static_cast<uint64_t>(m) * groups + static_cast<uint64_t>(at / 4), p.drop.dropped);
+            keep.draw(key, static_cast<uint64_t>(m) * groups + column(c) / 4, p.drop.dropped);
 #pragma unroll
           for (int i = 0; i < 4; ++i) hh[c][i] = row::mul2(hh[c][i], row::both(sigma));
-          if (p.sum_slot[kGate] >= 0) {
+          if (p.sum_at[kGate] >= 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = hh[c][i];
-            if (p.vector[kPostWeight].p != nullptr) {
-              parameter(kPostWeight, c, w);
+            if (p.in[kPw].p != nullptr) {
+              parameter(kPw, c, w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
             }
-            if (p.vector[kPostBias].p != nullptr) {
-              parameter(kPostBias, c, w);
+            if (p.in[kPb].p != nullptr) {
+              parameter(kPb, c, w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) f[i] = row::add2(f[i], w[i]);
             }
@@ -406,8 +404,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
             for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], d[c][i]);
             add(kGate, c, f);
           }
-          if (p.vector[kGate].p != nullptr) {
-            parameter(kGate, c, w);
+          if (p.in[kG].p != nullptr) {
+            parameter(kG, c, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
           }
@@ -417,8 +415,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], hh[c][i]);
             add(kPostWeight, c, f);
-            if (p.vector[kPostWeight].p != nullptr) {
-              parameter(kPostWeight, c, w);
+            if (p.in[kPw].p != nullptr) {
+              parameter(kPw, c, w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
             }
@@ -427,8 +425,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
           }
         }
       }
-      fetch(kDy, m + rows_at_once, end);
-      fetch(kDr, m + rows_at_once, end);
+      if (more) {
+        fetch(kDy, m + rows_at_once);
+        fetch(kDr, m + rows_at_once);
+      }
       if (p.dh.p == nullptr) continue;
       if (has_post) {
         group.sums(q);
@@ -443,19 +443,19 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
       }
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        row::store_word<WIDE>(p.dh, p.dh.p + m * p.dh.ld + column(c), n - column(c), row::pack<KIND>(d[c]));
+        row::store_word<WIDE>(p.dh, p.dh.p + m * p.dh.ld + column(c), left_of(c), row::pack<KIND>(d[c]));
     }
-    if (p.split.pieces == 0 && p.sum_slot[kGate] >= 0) {
+    if (p.split.pieces == 0 && p.sum_at[kGate] >= 0) {
       __syncthreads();
       for (int i = threadIdx.x; i < n; i += threads)
-        p.dgate.p[gate_row * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_slot[kGate], i, true));
+        p.dgate.p[gate_row * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_at[kGate], i, true));
       __syncthreads();
     }
   }
   __syncthreads();
   float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * n;
   for (int slot = 0; slot < p.sum_slots; ++slot)
-    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(slot, i, false);
+    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * C * THREADS, i, false);
 }
 
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
   }
   float sum = 0.0f;
   if (n < p.N)
-#pragma unroll 4
+#pragma unroll 10
     for (int c = first + warp; c < last; c += kSumWarps)
       sum += p.partials[(static_cast<int64_t>(c) * p.slots + p.slot[which]) * p.N + n];
   room[warp][lane] = sum;
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
 // How the row kernel takes a row: words of a thread, threads of a row, threads of a block.
 struct RowPlan {
   int words, threads, block;  // words 0: too long
+  int pitch() const { return block <= 256 ? 256 : 512; }  // the kernel's THREADS
 };
 RowPlan row_plan(int64_t N) {
   const int64_t words = (N + row::kWord - 1) / row::kWord;
@@ -518,11 +519,35 @@ RowPlan row_plan(int64_t N) {
 
 constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
 
+// Places in shared memory: inputs, parameters (those only while there is room for them all), sums. False: the inputs
+// and sums alone do not fit.
+template <bool WIDE>
+bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
+  const int word = plan.words * plan.pitch(), in_word = WIDE ? word : 2 * word;
+  int ins = 0, all = 0;
+  for (int i = 0; i < kPlaces; ++i) {
+    const bool present = p->in[i].p != nullptr;
+    ins += present && i <= kH;
+    all += present;
+  }
+  const int sums = 2 * p->sum_slots * word;
+  const bool parameters = (all * in_word + sums) * 16 <= kMostSmem;
+  if ((ins * in_word + sums) * 16 > kMostSmem) return false;
+  int used = 0;
+  for (int i = 0; i < kPlaces; ++i) {
+    const bool here = p->in[i].p != nullptr && (i <= kH || parameters);
+    p->at[i] = here ? used : -1;
+    if (here) used += in_word;
+  }
+  p->sum_first = used;
+  for (int i = 0; i < kVectors; ++i) p->sum_at[i] = slot[i] >= 0 ? used + 2 * slot[i] * word : -1;
+  *bytes = (used + sums) * 16;
+  return true;
+}
+
 template <int KIND, bool WIDE, int C, int THREADS>
 cudaError_t launch_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
-  constexpr int kAll = (4 + 4 + 2 * kVectors) * C * THREADS * 16, kMaxSmem = kAll < kMostSmem ? kAll : kMostSmem;
-  static_assert((4 + 2 * kVectors) * C * THREADS * 16 <= kMostSmem, "without the parameters there is room");
-  cudaError_t e = prepare_smem<row_backward_kernel<KIND, WIDE, C, THREADS>>(kMaxSmem);
+  cudaError_t e = prepare_smem<row_backward_kernel<KIND, WIDE, C, THREADS>>(kMostSmem);
   return e != cudaSuccess ? e
                           : ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), plan.block, 1, smem},
                                              row_backward_kernel<KIND, WIDE, C, THREADS>, p);
@@ -547,46 +572,38 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
     if (i != kGate && outs[i] != nullptr) ++s.vectors;
   }
   if (slots == 0 && t.dX.p == nullptr && t.dH.p == nullptr) return cudaSuccess;
-  const RowPlan plan = row_plan(t.N);
+  RowPlan plan = row_plan(t.N);
   cudaError_t e;
   Split split;
+  RowParams p;
+  memset(&p, 0, sizeof(p));
+  bool wide = false;
+  int smem = 0;
   if (plan.words > 0) {
-    RowParams p;
-    memset(&p, 0, sizeof(p));
-    const Input in[4] = {t.norm != T2S_NORM_NONE ? t.R : Input{}, t.dY, t.dR, t.H};
-    const uint16_t* const vectors[kVectors] = {t.weight, nullptr, t.gate.p, t.post_weight, t.post_bias};
-    for (int i = 0; i < 4; ++i) {
-      p.in[i] = row::view_of(in[i].p, in[i].ld, t.M, t.N);
-      p.in_slot[i] = in[i].p != nullptr ? p.in_slots++ : -1;
-    }
-    for (int i = 0; i < kVectors; ++i) {
-      p.vector[i] = row::view_of(vectors[i], t.gate.ld, i == kGate ? t.gates : 1, t.N);
-      p.vector_slot[i] = vectors[i] != nullptr ? p.in_slots + p.vector_slots++ : -1;
-      p.sum_slot[i] = slot[i];
+    const Input in[kPlaces] = {t.norm != T2S_NORM_NONE ? t.R : Input{}, t.dY, t.dR, t.H, {t.weight, 0}, t.gate,
+                               {t.post_weight, 0}, {t.post_bias, 0}};
+    p.dx = row::view_of(t.dX.p, t.dX.ld, t.M, t.N), p.dh = row::view_of(t.dH.p, t.dH.ld, t.M, t.N);
+    wide = row::whole_words(p.dx, t.N) && row::whole_words(p.dh, t.N);
+    for (int i = 0; i < kPlaces; ++i) {
+      p.in[i] = row::view_of(in[i].p, in[i].ld, i <= kH ? t.M : i == kG ? t.gates : 1, t.N);
+      wide = wide && row::whole_words(p.in[i], t.N);
     }
     p.sum_slots = slots;
-    p.dx = row::view_of(t.dX.p, t.dX.ld, t.M, t.N), p.dh = row::view_of(t.dH.p, t.dH.ld, t.M, t.N);
-    p.M = t.M, p.rows_per_gate = t.M / t.gates, p.gates = t.gates, p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.rows_per_gate = t.M / t.gates, p.gates = t.gates, p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
-    bool wide = row::whole_words(p.dx, t.N) && row::whole_words(p.dh, t.N);
-    for (const row::View& v : p.in) wide = wide && row::whole_words(v, t.N);
-    for (const row::View& v : p.vector) wide = wide && row::whole_words(v, t.N);
-    const int slot_bytes = plan.words * plan.block * 16;
-    if ((p.in_slots + p.vector_slots + 2 * slots) * slot_bytes > kMostSmem) {
-      p.vector_slots = 0;
-      for (int& v : p.vector_slot) v = -1;
-    }
-    const int smem = (p.in_slots + p.vector_slots + 2 * slots) * slot_bytes;
+    if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.words = 0;
+  }
+  if (plan.words > 0) {
     p.split = split = split_of(t.M, t.gates, plan.block <= 256 && smem <= 112 * 1024 ? kMostCtas : kSms);
     e = wide ? run_rows<KIND, true>(p, plan, smem, stream) : run_rows<KIND, false>(p, plan, smem, stream);
   } else {
-    BackwardParams p;
-    p.t = t;
-    p.split = split = split_of(t.M, t.gates, kMostCtas);
-    for (int i = 0; i < kVectors; ++i) p.slot[i] = slot[i];
-    p.slots = slots;
-    e = ff::launch_early(stream, {dim3(static_cast<unsigned>(split.ctas)), kWideThreads, 1, 0}, wide_backward_kernel<KIND>, p);
+    BackwardParams b;
+    b.t = t;
+    b.split = split = split_of(t.M, t.gates, kMostCtas);
+    for (int i = 0; i < kVectors; ++i) b.slot[i] = slot[i];
+    b.slots = slots;
+    e = ff::launch_early(stream, {dim3(static_cast<unsigned>(split.ctas)), kWideThreads, 1, 0}, wide_backward_kernel<KIND>, b);
   }
   if (e != cudaSuccess) return e;
   s.gate_rows = t.dgate.p != nullptr && split.pieces > 0 ? static_cast<int>(t.gates) : 0;

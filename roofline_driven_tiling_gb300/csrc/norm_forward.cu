@@ -73,18 +73,18 @@ __global__ void __launch_bounds__(kWideThreads) wide_forward_kernel(const __grid
   }
 }
 
-// Rows of up to 16384 values: a group of threads keeps a row in registers, C words of eight values a thread, the next
-// row's words on their way meanwhile. A thread's words of the parameters lie in shared memory, at places of its own.
+// Rows of up to 8192 values: a group of threads keeps a row in registers, C words of eight values a thread. The next
+// row's words come to shared memory meanwhile, and the parameters' words stay there; a thread reads what it fetched itself.
+enum Place : int { kX = 0, kH = 1, kPostWeight = 2, kPostBias = 3, kGate = 4, kWeight = 5, kBias = 6, kPlaces = 7 };
 struct RowParams {
-  row::View x, h, r, y, vector[5];  // see Vector
-  int slot[5];                      // of a vector's words in shared memory; -1: absent, or a gate that changes
+  row::View in[kPlaces], r, y;
+  int at[kPlaces];  // of this word in shared memory; -1: absent, or a gate that changes
   int64_t M, rows_per_gate;
   int N, threads;  // threads of a row
   int norm, post;
   float scale, eps;
   Dropout drop;
 };
-enum Vector : int { kPostWeight = 0, kPostBias = 1, kGate = 2, kWeight = 3, kBias = 4 };
 
 // Blocks that an SM holds: 64 registers a thread, four words a thread twice as many.
 template <int C, int THREADS>
@@ -96,6 +96,7 @@ template <int KIND, bool WIDE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
+  constexpr int kNext = C * THREADS;  // from a word's first place to its second (not WIDE)
   ff::wait_for_earlier_kernels();
   row::Group group(p.threads, rooms);
   const int n = p.N, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
@@ -103,26 +104,21 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(n) + 3) / 4);
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
-  const bool has_h = p.h.p != nullptr;
-  auto column = [&](int c) { return (group.rank + c * p.threads) * row::kWord; };
-  auto parameter = [&](int vector, int c) -> uint4& {
-    return words[(p.slot[vector] * C + c) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)];
+  const bool has_h = p.in[kH].p != nullptr;
+  const uint32_t first = static_cast<uint32_t>(group.rank) * row::kWord;
+  auto column = [&](int c) { return first + static_cast<uint32_t>(c * p.threads * row::kWord); };
+  auto left = [&](int c) { return n - static_cast<int>(column(c)); };
+  auto fetch = [&](int place, int64_t m) {
+    const uint16_t* from = p.in[place].p + m * p.in[place].ld;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      row::fetch_word<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, p.in[place], from + column(c), left(c));
   };
-#pragma unroll
-  for (int i = 0; i < 5; ++i)
-    if (p.slot[i] >= 0)
-#pragma unroll
-      for (int c = 0; c < C; ++c) parameter(i, c) = row::load_word<WIDE>(p.vector[i], p.vector[i].p + column(c), n - column(c));
+  auto get = [&](int place, int64_t m, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(row::arrived<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext,
+                                         p.in[place].p + m * p.in[place].ld + column(c), left(c)), f);
+  };
 
-  uint4 x[C], h[C];
-  auto fetch = [&](int64_t m) {
-    if (m >= p.M) return;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      x[c] = row::load_word<WIDE>(p.x, p.x.p + m * p.x.ld + column(c), n - column(c));
-      if (has_h) h[c] = row::load_word<WIDE>(p.h, p.h.p + m * p.h.ld + column(c), n - column(c));
-    }
-  };
   uint64_t v[C][4];
   // The mean off the values (layer), and 1 / the root of their mean square.
   auto scale_of = [&](int kind) {
@@ -136,7 +132,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
       for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] = row::add2(v[c][i], mean);
-        row::clear_from<WIDE>(v[c], n - column(c));
+        row::clear_from<WIDE>(v[c], left(c));
       }
       s[0] = 0.0f;
     }
@@ -150,68 +146,74 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
     uint64_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], row::both(rstd));
-    if (p.slot[weight] >= 0) {
-      row::unpack<KIND>(parameter(weight, c), w);
+    if (p.at[weight] >= 0) {
+      get(weight, 0, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], w[i]);
     }
-    if (p.slot[bias] >= 0) {
-      row::unpack<KIND>(parameter(bias, c), w);
+    if (p.at[bias] >= 0) {
+      get(bias, 0, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::add2(v[c][i], w[i]);
     }
   };
 
   int64_t m = static_cast<int64_t>(blockIdx.x) * rows_at_once + group.index;
-  fetch(m);
+#pragma unroll 1
+  for (int i = kPostWeight; i < kPlaces; ++i)
+    if (p.at[i] >= 0) fetch(i, 0);
+  if (m < p.M) {
+    fetch(kX, m);
+    if (has_h) fetch(kH, m);
+  }
   for (; m < p.M; m += step) {
+    row::wait_copies();
     if (has_h) {
-      uint4 r[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        row::unpack<KIND>(h[c], v[c]);
-        r[c] = x[c];
-      }
-      fetch(m + step);
+      for (int c = 0; c < C; ++c) get(kH, m, c, v[c]);
+      if (m + step < p.M) fetch(kH, m + step);
       const float rstd = p.post != T2S_NORM_NONE ? scale_of(p.post) : 1.0f;
+      uint16_t* out = p.r.p + m * p.r.ld;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int at = column(c);
         uint64_t u[4];
         if (p.post != T2S_NORM_NONE) affine(rstd, kPostWeight, kPostBias, c);
         if (p.drop.dropped != 0) {
           row::Keep keep;
-          keep.draw(key, static_cast<uint64_t>(m) * groups + static_cast<uint64_t>(at / 4), p.drop.dropped);
+          keep.draw(key, static_cast<uint64_t>(m) * groups + column(c) / 4, p.drop.dropped);
           keep.apply(v[c], p.drop.factor);
         }
-        if (p.vector[kGate].p != nullptr) {
-          row::unpack<KIND>(p.slot[kGate] >= 0
-                                ? parameter(kGate, c)
-                                : row::load_word<WIDE>(p.vector[kGate], p.vector[kGate].p + m / p.rows_per_gate * p.vector[kGate].ld + at, n - at),
-                            u);
+        if (p.in[kGate].p != nullptr) {
+          if (p.at[kGate] >= 0) {
+            get(kGate, 0, c, u);
+          } else {
+            row::unpack<KIND>(row::load_word<WIDE>(p.in[kGate], p.in[kGate].p + m / p.rows_per_gate * p.in[kGate].ld + column(c),
+                                                   left(c)), u);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], u[i]);
         }
-        row::unpack<KIND>(r[c], u);
+        get(kX, m, c, u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] = row::fma2(u[i], row::both(p.scale), v[c][i]);
         // The norm that follows is of the rounded values.
-        r[c] = row::pack<KIND>(v[c]);
-        row::store_word<WIDE>(p.r, p.r.p + m * p.r.ld + at, n - at, r[c]);
-        row::unpack<KIND>(r[c], v[c]);
-        row::clear_from<WIDE>(v[c], n - at);
+        const uint4 r = row::pack<KIND>(v[c]);
+        row::store_word<WIDE>(p.r, out + column(c), left(c), r);
+        row::unpack<KIND>(r, v[c]);
+        row::clear_from<WIDE>(v[c], left(c));
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) row::unpack<KIND>(x[c], v[c]);
-      fetch(m + step);
+      for (int c = 0; c < C; ++c) get(kX, m, c, v[c]);
     }
+    if (m + step < p.M) fetch(kX, m + step);
     if (p.norm == T2S_NORM_NONE) continue;
     const float rstd = scale_of(p.norm);
+    uint16_t* out = p.y.p + m * p.y.ld;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       affine(rstd, kWeight, kBias, c);
-      row::store_word<WIDE>(p.y, p.y.p + m * p.y.ld + column(c), n - column(c), row::pack<KIND>(v[c]));
+      row::store_word<WIDE>(p.y, out + column(c), left(c), row::pack<KIND>(v[c]));
     }
   }
 }
@@ -219,38 +221,45 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
 constexpr int kSms = 152;
 
 template <int KIND, bool WIDE, int C, int THREADS>
-cudaError_t launch_rows(const RowParams& p, const ff::LaunchShape& shape, cudaStream_t stream) {
-  static_assert(5 * C * THREADS * 16 <= 160 * 1024, "the parameters' words");
-  cudaError_t e = prepare_smem<row_forward_kernel<KIND, WIDE, C, THREADS>>(5 * C * THREADS * 16);
-  return e != cudaSuccess ? e : ff::launch_early(stream, shape, row_forward_kernel<KIND, WIDE, C, THREADS>, p);
+cudaError_t launch_rows(RowParams& p, int blocks, int block, cudaStream_t stream) {
+  constexpr int kSlot = C * THREADS * (WIDE ? 1 : 2), kMost = kPlaces * kSlot * 16;
+  static_assert(kMost <= 224 * 1024 || !WIDE, "shared memory of one CTA");
+  int used = 0;
+  for (int i = 0; i < kPlaces; ++i)
+    if (p.at[i] >= 0) {
+      p.at[i] = used;
+      used += kSlot;
+    }
+  cudaError_t e = prepare_smem<row_forward_kernel<KIND, WIDE, C, THREADS>>(kMost < 224 * 1024 ? kMost : 224 * 1024);
+  if (e != cudaSuccess) return e;
+  return ff::launch_early(stream, {dim3(static_cast<unsigned>(blocks)), block, 1, used * 16},
+                          row_forward_kernel<KIND, WIDE, C, THREADS>, p);
 }
 
 template <int KIND, int C, int THREADS>
 cudaError_t run_rows(const ForwardTask& t, int threads, cudaStream_t stream) {
   RowParams p;
   bool wide = true;
-  p.x = row::view_of(t.X.p, t.X.ld, t.M, t.N), p.h = row::view_of(t.H.p, t.H.ld, t.M, t.N);
-  p.r = row::view_of(t.R.p, t.R.ld, t.M, t.N), p.y = row::view_of(t.Y.p, t.Y.ld, t.M, t.N);
-  const uint16_t* const vectors[5] = {t.post_weight, t.post_bias, t.gate.p, t.weight, t.bias};
-  int slots = 0;
-  for (int i = 0; i < 5; ++i) {
-    const int64_t rows = i == kGate ? t.gates : 1;
-    p.vector[i] = row::view_of(vectors[i], t.gate.ld, rows, t.N);
-    wide = wide && row::whole_words(p.vector[i], t.N);
-    p.slot[i] = vectors[i] != nullptr && rows == 1 ? slots++ : -1;
+  const uint16_t* const inputs[kPlaces] = {t.X.p, t.H.p, t.post_weight, t.post_bias, t.gate.p, t.weight, t.bias};
+  const int64_t ld[kPlaces] = {t.X.ld, t.H.ld, 0, 0, t.gate.ld, 0, 0}, rows[kPlaces] = {t.M, t.M, 1, 1, t.gates, 1, 1};
+  for (int i = 0; i < kPlaces; ++i) {
+    p.in[i] = row::view_of(inputs[i], ld[i], rows[i], t.N);
+    p.at[i] = inputs[i] != nullptr && (i != kGate || t.gates == 1) ? 0 : -1;
+    wide = wide && row::whole_words(p.in[i], t.N);
   }
-  for (const row::View& v : {p.x, p.h, p.r, p.y}) wide = wide && row::whole_words(v, t.N);
+  p.r = row::view_of(t.R.p, t.R.ld, t.M, t.N), p.y = row::view_of(t.Y.p, t.Y.ld, t.M, t.N);
+  wide = wide && row::whole_words(p.r, t.N) && row::whole_words(p.y, t.N);
   p.M = t.M, p.rows_per_gate = t.M / t.gates, p.N = static_cast<int>(t.N), p.threads = threads;
   p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
-  const int rows = THREADS / threads;
-  const int64_t blocks = (t.M + rows - 1) / rows, most = kSms * blocks_of<C, THREADS>();
-  const ff::LaunchShape shape{dim3(static_cast<unsigned>(blocks < most ? blocks : most)), rows * threads, 1,
-                              slots * C * rows * threads * 16};
-  return wide ? launch_rows<KIND, true, C, THREADS>(p, shape, stream) : launch_rows<KIND, false, C, THREADS>(p, shape, stream);
+  const int at_once = THREADS / threads;
+  const int64_t blocks = (t.M + at_once - 1) / at_once, most = kSms * blocks_of<C, THREADS>();
+  const int grid = static_cast<int>(blocks < most ? blocks : most);
+  return wide ? launch_rows<KIND, true, C, THREADS>(p, grid, at_once * threads, stream)
+              : launch_rows<KIND, false, C, THREADS>(p, grid, at_once * threads, stream);
 }
 
-// A row of up to 1024 values by one warp (no barriers), up to 8192 in two words a thread, up to 16384 with as many
-// threads as a block has; longer ones in passes over memory.
+// A row of up to 1024 values by one warp (no barriers), up to 8192 in two words a thread; longer ones in passes over
+// memory.
 template <int KIND>
 cudaError_t run(const ForwardTask& t, cudaStream_t stream) {
   const int64_t words = (t.N + row::kWord - 1) / row::kWord;
@@ -260,7 +269,6 @@ cudaError_t run(const ForwardTask& t, cudaStream_t stream) {
   const int threads = static_cast<int>((words + 63) / 64 * 32);
   if (threads <= 256) return run_rows<KIND, 2, 256>(t, threads, stream);
   if (threads <= 512) return run_rows<KIND, 2, 512>(t, threads, stream);
-  if (threads <= 1024) return run_rows<KIND, 2, 1024>(t, threads, stream);
   const unsigned blocks = static_cast<unsigned>(t.M < 2 * kSms ? t.M : 2 * kSms);
   return ff::launch_early(stream, {dim3(blocks), kWideThreads, 1, 0}, wide_forward_kernel<KIND>, t);
 }

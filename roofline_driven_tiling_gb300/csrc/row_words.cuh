@@ -4,6 +4,7 @@
 
 #include "drop.cuh"
 #include "ff_math.cuh"
+#include "t2s_device.cuh"
 
 namespace t2s {
 namespace row {
@@ -54,9 +55,44 @@ __device__ __forceinline__ uint4 first_of(const uint4& v, int left) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight values of a row from p on, `left` > 0 of them inside the row, the others 0. Off 16-byte boundaries the two
-// aligned words around them are read where both lie within the matrix [begin, end). Not inlined: a norm kernel reads
-// and writes words at two dozen places, and with this code at each of them it was 130 KB long and bound by fetching it.
+// Sixteen bytes from p to shared memory in the background, `bytes` of them read and the others 0.
+__device__ __forceinline__ void copy_async(uint4* to, const void* p, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight values of v's row from p on, `left` (perhaps none) of them inside the row, on their way to this thread's places
+// in shared memory, from where arrived() takes them after wait_copies(). WIDE: every row starts on a 16-byte boundary
+// and holds whole words: one place. Otherwise the two aligned words around them come to to[0] and to[next], as far as
+// the matrix reaches.
+template <bool WIDE>
+__device__ __forceinline__ void fetch_word(uint4* to, int next, const View& v, const uint16_t* p, int left) {
+  if (left <= 0) return;
+  if (WIDE) {
+    copy_async(to, p, 16);
+    return;
+  }
+  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
+  const uint16_t* from = p - o;
+  if (from >= v.p) {
+    copy_async(to, from, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from))));
+  } else {  // the first word of the matrix
+    uint16_t* values = reinterpret_cast<uint16_t*>(to);
+    for (int i = 0; i < n && o + i < kWord; ++i) values[o + i] = p[i];
+  }
+  if (o + n > kWord) copy_async(to + next, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from - kWord))));
+}
+// The values that fetch_word(to, next, v, p, left) brought, zeros beyond the row's end.
+template <bool WIDE>
+__device__ __forceinline__ uint4 arrived(const uint4* to, int next, const uint16_t* p, int left) {
+  if (left <= 0) return make_uint4(0, 0, 0, 0);
+  if (WIDE) return *to;
+  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+  return first_of(o == 0 ? *to : shifted(to[0], to[next], o), left);
+}
+
+// The same at once, where there is no place for it. Not inlined: a kernel reads and writes words at many places, and with
+// the code for odd alignments at each of them the norm kernels were up to 130 KB long and bound by fetching it.
 static __device__ __noinline__ uint4 load_part(const uint16_t* p, int left, const uint16_t* begin, const uint16_t* end) {
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
   const uint16_t* from = p - o;
@@ -74,9 +110,6 @@ static __device__ __noinline__ uint4 load_part(const uint16_t* p, int left, cons
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-// Eight values of v's row from p on, `left` (perhaps none) of them inside the row, the others 0. WIDE: every row starts
-// on a 16-byte boundary and holds whole words.
 template <bool WIDE>
 __device__ __forceinline__ uint4 load_word(const View& v, const uint16_t* p, int left) {
   if (left <= 0) return make_uint4(0, 0, 0, 0);
@@ -207,14 +240,14 @@ struct Keep {
 // next sum's barrier, which every thread reaches after it has read.
 struct Group {
   static constexpr int kMostSums = 4;
-  int index, threads, rank;  // of the group in the block; its threads; this one among them
+  int index, threads, rank;  // of the group in the block (the same in a warp, and shown to be); its threads; this one's
   float* room;               // 2 buffers of kMostSums floats for each of 32 warps
   uint32_t turn = 0;
 
   static constexpr int kRoomFloats = 2 * 32 * kMostSums;
 
   __device__ __forceinline__ Group(int threads_, float* rooms)
-      : index(static_cast<int>(threadIdx.x) / threads_), threads(threads_),
+      : index(__shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / threads_, 0)), threads(threads_),
         rank(static_cast<int>(threadIdx.x) - index * threads_),
         room(rooms + (static_cast<int>(threadIdx.x) - rank) / 32 * kMostSums) {}
 
@@ -245,8 +278,8 @@ struct Group {
       float* buffer = room + (turn++ & 1u) * (32 * kMostSums);
       if (lane < V) buffer[(rank >> 5) * V + lane] = x;
       barrier();
-      x = 0.0f;
-      for (int i = lane; i < warps * V; i += 32) x += buffer[i];
+      x = lane < warps * V ? buffer[lane] : 0.0f;
+      for (int i = lane + 32; i < warps * V; i += 32) x += buffer[i];
 #pragma unroll
       for (int d = 16; d >= V; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     }
