@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
 enum Place : int { kR = 0, kDy = 1, kDr = 2, kH = 3, kW = 4, kG = 5, kPw = 6, kPb = 7, kPlaces = 8 };
 struct RowParams {
   row::View in[kPlaces], dx, dh;
-  int at[kPlaces], sum_at[kVectors];  // of these words in shared memory; -1: absent, or no room
+  int at[kPlaces], sum_at[kVectors];  // of their words in shared memory, in bytes; -1: absent, or no room
   int sum_slots, sum_first;
-  int64_t rows_per_gate, gates;
+  int rows_per_gate, gates;
   Split split;
   int N, threads;  // threads of a row
   int norm, post;
@@ -192,43 +192,43 @@ struct RowParams {
 };
 
 template <int KIND, bool WIDE, int C, int THREADS>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
-  constexpr int kNext = C * THREADS;  // from a word's first place to its second (not WIDE)
+  // In shared memory: from one of a thread's words to the next, and from a word's first place to its second (not WIDE).
+  constexpr uint32_t kPitch = THREADS * 16, kNext = C * kPitch;
   row::Group group(p.threads, rooms);
   const int n = p.N, threads = static_cast<int>(blockDim.x), rows_at_once = threads / p.threads;
-  const uint32_t first_column = static_cast<uint32_t>(group.rank) * row::kWord;
-  auto column = [&](int c) { return first_column + static_cast<uint32_t>(c * p.threads * row::kWord); };
-  auto left_of = [&](int c) { return n - static_cast<int>(column(c)); };
+  const int first_column = group.rank * row::kWord, stride = p.threads * row::kWord;
+  const uint32_t first_byte = 2u * static_cast<uint32_t>(first_column);
+  auto left_of = [&](int c) { return n - first_column - c * stride; };
+  const uint32_t mine = smem_u32(words) + threadIdx.x * 16u;
   // A sum's eight values are two places of 16 bytes.
-  for (int i = 0; i < 2 * p.sum_slots * C; ++i) words[p.sum_first + i * THREADS + threadIdx.x] = make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(mine + p.sum_first + i * kPitch, 0u, 0u, 0u, 0u);
   ff::wait_for_earlier_kernels();
-  auto fetch = [&](int place, int64_t m) {
+  auto fetch = [&](int place, const uint16_t* from) {
     if (p.at[place] < 0) return;
-    const uint16_t* from = p.in[place].p + m * p.in[place].ld;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, p.in[place], from + column(c), left_of(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left_of(c));
   };
-  auto get = [&](int place, int64_t m, int c, uint64_t(&f)[4]) {
-    const uint16_t* from = p.in[place].p + m * p.in[place].ld + column(c);
-    row::unpack<KIND>(row::arrived<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, from, left_of(c)), f);
+  auto get = [&](int place, const uint16_t* from, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left_of(c)), f);
   };
   // A parameter's words, in shared memory, or read again for each row where that is full.
-  int64_t gate_row = 0;
+  int gate_row = 0;
   auto parameter = [&](int place, int c, uint64_t(&f)[4]) {
-    const int64_t m = place == kG ? gate_row : 0;
+    const uint16_t* from = p.in[place].row(place == kG ? gate_row : 0, first_byte);
     if (p.at[place] >= 0) {
-      get(place, m, c, f);
+      get(place, from, c, f);
     } else {
-      row::unpack<KIND>(row::load_word<WIDE>(p.in[place], p.in[place].p + m * p.in[place].ld + column(c), left_of(c)), f);
+      row::unpack<KIND>(row::load_word<WIDE>(p.in[place], from + c * stride, left_of(c)), f);
     }
   };
-  fetch(kW, 0);
-  fetch(kPw, 0);
-  fetch(kPb, 0);
-  const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(n) + 3) / 4);
+  fetch(kW, p.in[kW].row(0, first_byte));
+  fetch(kPw, p.in[kPw].row(0, first_byte));
+  fetch(kPb, p.in[kPb].row(0, first_byte));
+  const uint32_t groups = (static_cast<uint32_t>(n) + 3u) / 4u;
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
   const bool has_h = p.in[kH].p != nullptr, has_norm = p.norm != T2S_NORM_NONE, has_post = has_h && p.post != T2S_NORM_NONE;
@@ -236,17 +236,20 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
 
   auto add = [&](int vector, int c, const uint64_t(&f)[4]) {
     if (p.sum_at[vector] < 0) return;
-    ulonglong2* to = reinterpret_cast<ulonglong2*>(words + p.sum_at[vector] + 2 * c * THREADS + threadIdx.x);
-    ulonglong2 lo = to[0], hi = to[THREADS];
-    lo.x = row::add2(lo.x, f[0]), lo.y = row::add2(lo.y, f[1]);
-    hi.x = row::add2(hi.x, f[2]), hi.y = row::add2(hi.y, f[3]);
-    to[0] = lo, to[THREADS] = hi;
+    const uint32_t to = mine + p.sum_at[vector] + 2 * c * kPitch;
+    uint64_t a, b;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lds128_pairs(to + i * kPitch, a, b);
+      a = row::add2(a, f[2 * i]), b = row::add2(b, f[2 * i + 1]);
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + i * kPitch), "l"(a), "l"(b) : "memory");
+    }
   };
   // A sum's column i over the groups, which are cleared if `clear`.
   auto total = [&](int sum_at, int i, bool clear) {
     float s = 0.0f;
     const int word = i / row::kWord, c = word < p.threads ? 0 : 1, thread = word - c * p.threads, j = i % row::kWord;
-    float* from = reinterpret_cast<float*>(words + sum_at + (2 * c + j / 4) * THREADS + thread) + j % 4;
+    float* from = reinterpret_cast<float*>(words + sum_at / 16 + (2 * c + j / 4) * THREADS + thread) + j % 4;
     for (int g = 0; g < rows_at_once; ++g, from += p.threads * 4) {
       s += *from;
       if (clear) *from = 0.0f;
@@ -254,38 +257,39 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
     return s;
   };
 
-  int64_t first, last;
+  int first, last;
   if (p.split.pieces > 0) {
-    const int64_t g = blockIdx.x / p.split.pieces, j = blockIdx.x % p.split.pieces;
-    first = g * p.rows_per_gate + p.rows_per_gate * j / p.split.pieces;
-    last = g * p.rows_per_gate + p.rows_per_gate * (j + 1) / p.split.pieces;
+    const int g = static_cast<int>(blockIdx.x) / p.split.pieces, j = static_cast<int>(blockIdx.x) - g * p.split.pieces;
+    first = g * p.rows_per_gate + static_cast<int>(static_cast<int64_t>(p.rows_per_gate) * j / p.split.pieces);
+    last = g * p.rows_per_gate + static_cast<int>(static_cast<int64_t>(p.rows_per_gate) * (j + 1) / p.split.pieces);
   } else {
-    first = p.gates * blockIdx.x / p.split.ctas * p.rows_per_gate;
-    last = p.gates * (blockIdx.x + 1) / p.split.ctas * p.rows_per_gate;
+    first = static_cast<int>(static_cast<int64_t>(p.gates) * blockIdx.x / p.split.ctas) * p.rows_per_gate;
+    last = static_cast<int>(static_cast<int64_t>(p.gates) * (blockIdx.x + 1) / p.split.ctas) * p.rows_per_gate;
   }
   // One gate's rows after another (one stretch of rows where a gate has several blocks).
-  const int64_t stretch = p.split.pieces > 0 ? last - first : p.rows_per_gate;
-  for (int64_t m0 = first; m0 < last; m0 += stretch) {
-    const int64_t end = m0 + stretch;
+  const int stretch = p.split.pieces > 0 ? last - first : p.rows_per_gate;
+  for (int m0 = first; m0 < last; m0 += stretch) {
+    const int end = m0 + stretch;
     gate_row = m0 / p.rows_per_gate;
-    fetch(kG, gate_row);
-    int64_t m = m0 + group.index;
+    fetch(kG, p.in[kG].row(gate_row, first_byte));
+    int m = m0 + group.index;
     if (m < end)
 #pragma unroll 1
-      for (int i = kR; i <= kH; ++i) fetch(i, m);
+      for (int i = kR; i <= kH; ++i) fetch(i, p.in[i].row(m, first_byte));
     for (; m < end; m += rows_at_once) {
-      const bool more = m + rows_at_once < end;
+      auto fetch_next = [&](int i) {
+        if (m + rows_at_once < end) fetch(i, p.in[i].row(m + rows_at_once, first_byte));
+      };
+      auto get_row = [&](int i, int c, uint64_t(&f)[4]) { get(i, p.in[i].row(m, first_byte), c, f); };
       row::wait_copies();
       uint64_t xh[C][4], hh[C][4], d[C][4];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (has_norm) get(kR, m, c, xh[c]);
-        if (has_h) get(kH, m, c, hh[c]);
+        if (has_norm) get_row(kR, c, xh[c]);
+        if (has_h) get_row(kH, c, hh[c]);
       }
-      if (more) {
-        fetch(kR, m + rows_at_once);
-        fetch(kH, m + rows_at_once);
-      }
+      fetch_next(kR);
+      fetch_next(kH);
       if (layer || post_layer) {
         float means[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
         for (int c = 0; c < C; ++c) {
           if (has_norm) {
             uint64_t g[4], w[4];
-            get(kDy, m, c, g);
+            get_row(kDy, c, g);
             if (p.in[kW].p != nullptr) {
               parameter(kW, c, w);
 #pragma unroll
@@ -347,13 +351,13 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
         const int left = left_of(c);
         uint64_t f[4], w[4];
         if (p.at[kDr] >= 0) {
-          get(kDr, m, c, d[c]);
+          get_row(kDr, c, d[c]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[c][i] = 0;
         }
         if (has_norm) {
-          get(kDy, m, c, f);
+          get_row(kDy, c, f);
           add(kBias, c, f);
           uint64_t g[4];
 #pragma unroll
@@ -378,12 +382,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
         if (p.dx.p != nullptr) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], row::both(p.scale));
-          row::store_word<WIDE>(p.dx, p.dx.p + m * p.dx.ld + column(c), left, row::pack<KIND>(f));
+          row::store_word<WIDE>(p.dx, p.dx.row(m, first_byte) + c * stride, left, row::pack<KIND>(f));
         }
         if (has_h) {
           row::Keep keep;
           if (p.drop.dropped != 0)
-            keep.draw(key, static_cast<uint64_t>(m) * groups + column(c) / 4, p.drop.dropped);
+            keep.draw(key, static_cast<uint64_t>(static_cast<uint32_t>(m)) * groups + static_cast<uint32_t>(first_column + c * stride) / 4u, p.drop.dropped);
 #pragma unroll
           for (int i = 0; i < 4; ++i) hh[c][i] = row::mul2(hh[c][i], row::both(sigma));
           if (p.sum_at[kGate] >= 0) {
@@ -425,10 +429,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
           }
         }
       }
-      if (more) {
-        fetch(kDy, m + rows_at_once);
-        fetch(kDr, m + rows_at_once);
-      }
+      fetch_next(kDy);
+      fetch_next(kDr);
       if (p.dh.p == nullptr) continue;
       if (has_post) {
         group.sums(q);
@@ -443,19 +445,19 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) row_backward_kernel(co
       }
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        row::store_word<WIDE>(p.dh, p.dh.p + m * p.dh.ld + column(c), left_of(c), row::pack<KIND>(d[c]));
+        row::store_word<WIDE>(p.dh, p.dh.row(m, first_byte) + c * stride, left_of(c), row::pack<KIND>(d[c]));
     }
     if (p.split.pieces == 0 && p.sum_at[kGate] >= 0) {
       __syncthreads();
       for (int i = threadIdx.x; i < n; i += threads)
-        p.dgate.p[gate_row * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_at[kGate], i, true));
+        p.dgate.p[static_cast<int64_t>(gate_row) * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_at[kGate], i, true));
       __syncthreads();
     }
   }
   __syncthreads();
   float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * n;
   for (int slot = 0; slot < p.sum_slots; ++slot)
-    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * C * THREADS, i, false);
+    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * static_cast<int>(kNext), i, false);
 }
 
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
@@ -507,14 +509,13 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
 // How the row kernel takes a row: words of a thread, threads of a row, threads of a block.
 struct RowPlan {
   int words, threads, block;  // words 0: too long
-  int pitch() const { return block <= 256 ? 256 : 512; }  // the kernel's THREADS
+  int pitch() const { return block <= 512 ? 512 : 1024; }  // the kernel's THREADS
 };
 RowPlan row_plan(int64_t N) {
   const int64_t words = (N + row::kWord - 1) / row::kWord;
-  if (words <= 32) return {1, 32, 256};
   if (words > 1024) return {0, 0, 0};
-  const int threads = static_cast<int>((words + 63) / 64 * 32);
-  return {2, threads, threads <= 256 ? 256 / threads * threads : threads};
+  const int threads = static_cast<int>((words + 31) / 32 * 32);
+  return {1, threads, threads <= 512 ? 512 / threads * threads : threads};
 }
 
 constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
@@ -523,7 +524,7 @@ constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
 // and sums alone do not fit.
 template <bool WIDE>
 bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
-  const int word = plan.words * plan.pitch(), in_word = WIDE ? word : 2 * word;
+  const int word = plan.words * plan.pitch() * 16, in_word = WIDE ? word : 2 * word;
   int ins = 0, all = 0;
   for (int i = 0; i < kPlaces; ++i) {
     const bool present = p->in[i].p != nullptr;
@@ -531,8 +532,8 @@ bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
     all += present;
   }
   const int sums = 2 * p->sum_slots * word;
-  const bool parameters = (all * in_word + sums) * 16 <= kMostSmem;
-  if ((ins * in_word + sums) * 16 > kMostSmem) return false;
+  const bool parameters = all * in_word + sums <= kMostSmem;
+  if (ins * in_word + sums > kMostSmem) return false;
   int used = 0;
   for (int i = 0; i < kPlaces; ++i) {
     const bool here = p->in[i].p != nullptr && (i <= kH || parameters);
@@ -541,7 +542,7 @@ bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
   }
   p->sum_first = used;
   for (int i = 0; i < kVectors; ++i) p->sum_at[i] = slot[i] >= 0 ? used + 2 * slot[i] * word : -1;
-  *bytes = (used + sums) * 16;
+  *bytes = used + sums;
   return true;
 }
 
@@ -555,9 +556,8 @@ cudaError_t launch_rows(const RowParams& p, const RowPlan& plan, int smem, cudaS
 
 template <int KIND, bool WIDE>
 cudaError_t run_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
-  return plan.words == 1     ? launch_rows<KIND, WIDE, 1, 256>(p, plan, smem, stream)
-         : plan.block <= 256 ? launch_rows<KIND, WIDE, 2, 256>(p, plan, smem, stream)
-                             : launch_rows<KIND, WIDE, 2, 512>(p, plan, smem, stream);
+  return plan.block <= 512 ? launch_rows<KIND, WIDE, 1, 512>(p, plan, smem, stream)
+                           : launch_rows<KIND, WIDE, 1, 1024>(p, plan, smem, stream);
 }
 
 template <int KIND>
@@ -589,13 +589,13 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
       wide = wide && row::whole_words(p.in[i], t.N);
     }
     p.sum_slots = slots;
-    p.rows_per_gate = t.M / t.gates, p.gates = t.gates, p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.rows_per_gate = static_cast<int>(t.M / t.gates), p.gates = static_cast<int>(t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
     if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.words = 0;
   }
   if (plan.words > 0) {
-    p.split = split = split_of(t.M, t.gates, plan.block <= 256 && smem <= 112 * 1024 ? kMostCtas : kSms);
+    p.split = split = split_of(t.M, t.gates, plan.block <= 512 && smem <= 112 * 1024 ? kMostCtas : kSms);
     e = wide ? run_rows<KIND, true>(p, plan, smem, stream) : run_rows<KIND, false>(p, plan, smem, stream);
   } else {
     BackwardParams b;

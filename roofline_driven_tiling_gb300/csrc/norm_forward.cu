@@ -78,8 +78,9 @@ __global__ void __launch_bounds__(kWideThreads) wide_forward_kernel(const __grid
 enum Place : int { kX = 0, kH = 1, kPostWeight = 2, kPostBias = 3, kGate = 4, kWeight = 5, kBias = 6, kPlaces = 7 };
 struct RowParams {
   row::View in[kPlaces], r, y;
-  int at[kPlaces];  // of this word in shared memory; -1: absent, or a gate that changes
-  int64_t M, rows_per_gate;
+  int at[kPlaces];  // of its words in shared memory, in bytes; -1: absent, or a gate that changes
+  int64_t M, rows_per_gate, step;  // rows that all groups take at once
+  int64_t x_step, h_step, r_step, y_step;
   int N, threads;  // threads of a row
   int norm, post;
   float scale, eps;
@@ -96,27 +97,25 @@ template <int KIND, bool WIDE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
-  constexpr int kNext = C * THREADS;  // from a word's first place to its second (not WIDE)
+  // In shared memory: from one of a thread's words to the next, and from a word's first place to its second (not WIDE).
+  constexpr uint32_t kPitch = THREADS * 16, kNext = C * kPitch;
   ff::wait_for_earlier_kernels();
   row::Group group(p.threads, rooms);
   const int n = p.N, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows_at_once;
   const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(n) + 3) / 4);
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
   const bool has_h = p.in[kH].p != nullptr;
-  const uint32_t first = static_cast<uint32_t>(group.rank) * row::kWord;
-  auto column = [&](int c) { return first + static_cast<uint32_t>(c * p.threads * row::kWord); };
-  auto left = [&](int c) { return n - static_cast<int>(column(c)); };
-  auto fetch = [&](int place, int64_t m) {
-    const uint16_t* from = p.in[place].p + m * p.in[place].ld;
+  const int first = group.rank * row::kWord, stride = p.threads * row::kWord;
+  auto left = [&](int c) { return n - first - c * stride; };
+  const uint32_t mine = smem_u32(words) + threadIdx.x * 16u;
+  auto fetch = [&](int place, const uint16_t* from) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext, p.in[place], from + column(c), left(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left(c));
   };
-  auto get = [&](int place, int64_t m, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived<WIDE>(words + p.at[place] + c * THREADS + threadIdx.x, kNext,
-                                         p.in[place].p + m * p.in[place].ld + column(c), left(c)), f);
+  auto get = [&](int place, const uint16_t* from, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left(c)), f);
   };
 
   uint64_t v[C][4];
@@ -147,73 +146,76 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], row::both(rstd));
     if (p.at[weight] >= 0) {
-      get(weight, 0, c, w);
+      get(weight, p.in[weight].p + first, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], w[i]);
     }
     if (p.at[bias] >= 0) {
-      get(bias, 0, c, w);
+      get(bias, p.in[bias].p + first, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::add2(v[c][i], w[i]);
     }
   };
 
   int64_t m = static_cast<int64_t>(blockIdx.x) * rows_at_once + group.index;
+  const uint16_t* x = p.in[kX].p + m * p.in[kX].ld + first;
+  const uint16_t* h = p.in[kH].p + m * p.in[kH].ld + first;
+  uint16_t* r = p.r.p + m * p.r.ld + first;
+  uint16_t* y = p.y.p + m * p.y.ld + first;
 #pragma unroll 1
   for (int i = kPostWeight; i < kPlaces; ++i)
-    if (p.at[i] >= 0) fetch(i, 0);
+    if (p.at[i] >= 0) fetch(i, p.in[i].p + first);
   if (m < p.M) {
-    fetch(kX, m);
-    if (has_h) fetch(kH, m);
+    fetch(kX, x);
+    if (has_h) fetch(kH, h);
   }
-  for (; m < p.M; m += step) {
+  for (; m < p.M; m += p.step, x += p.x_step, h += p.h_step, r += p.r_step, y += p.y_step) {
+    const bool more = m + p.step < p.M;
     row::wait_copies();
     if (has_h) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) get(kH, m, c, v[c]);
-      if (m + step < p.M) fetch(kH, m + step);
+      for (int c = 0; c < C; ++c) get(kH, h, c, v[c]);
+      if (more) fetch(kH, h + p.h_step);
       const float rstd = p.post != T2S_NORM_NONE ? scale_of(p.post) : 1.0f;
-      uint16_t* out = p.r.p + m * p.r.ld;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         uint64_t u[4];
         if (p.post != T2S_NORM_NONE) affine(rstd, kPostWeight, kPostBias, c);
         if (p.drop.dropped != 0) {
           row::Keep keep;
-          keep.draw(key, static_cast<uint64_t>(m) * groups + column(c) / 4, p.drop.dropped);
+          keep.draw(key, static_cast<uint64_t>(m) * groups + static_cast<uint64_t>((first + c * stride) / 4), p.drop.dropped);
           keep.apply(v[c], p.drop.factor);
         }
         if (p.in[kGate].p != nullptr) {
           if (p.at[kGate] >= 0) {
-            get(kGate, 0, c, u);
+            get(kGate, p.in[kGate].p + first, c, u);
           } else {
-            row::unpack<KIND>(row::load_word<WIDE>(p.in[kGate], p.in[kGate].p + m / p.rows_per_gate * p.in[kGate].ld + column(c),
-                                                   left(c)), u);
+            const uint16_t* gate = p.in[kGate].p + m / p.rows_per_gate * p.in[kGate].ld + first + c * stride;
+            row::unpack<KIND>(row::load_word<WIDE>(p.in[kGate], gate, left(c)), u);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], u[i]);
         }
-        get(kX, m, c, u);
+        get(kX, x, c, u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] = row::fma2(u[i], row::both(p.scale), v[c][i]);
         // The norm that follows is of the rounded values.
-        const uint4 r = row::pack<KIND>(v[c]);
-        row::store_word<WIDE>(p.r, out + column(c), left(c), r);
-        row::unpack<KIND>(r, v[c]);
+        const uint4 rounded = row::pack<KIND>(v[c]);
+        row::store_word<WIDE>(p.r, r + c * stride, left(c), rounded);
+        row::unpack<KIND>(rounded, v[c]);
         row::clear_from<WIDE>(v[c], left(c));
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) get(kX, m, c, v[c]);
+      for (int c = 0; c < C; ++c) get(kX, x, c, v[c]);
     }
-    if (m + step < p.M) fetch(kX, m + step);
+    if (more) fetch(kX, x + p.x_step);
     if (p.norm == T2S_NORM_NONE) continue;
     const float rstd = scale_of(p.norm);
-    uint16_t* out = p.y.p + m * p.y.ld;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       affine(rstd, kWeight, kBias, c);
-      row::store_word<WIDE>(p.y, out + column(c), left(c), row::pack<KIND>(v[c]));
+      row::store_word<WIDE>(p.y, y + c * stride, left(c), row::pack<KIND>(v[c]));
     }
   }
 }
@@ -222,7 +224,7 @@ constexpr int kSms = 152;
 
 template <int KIND, bool WIDE, int C, int THREADS>
 cudaError_t launch_rows(RowParams& p, int blocks, int block, cudaStream_t stream) {
-  constexpr int kSlot = C * THREADS * (WIDE ? 1 : 2), kMost = kPlaces * kSlot * 16;
+  constexpr int kSlot = C * THREADS * (WIDE ? 16 : 32), kMost = kPlaces * kSlot;
   static_assert(kMost <= 224 * 1024 || !WIDE, "shared memory of one CTA");
   int used = 0;
   for (int i = 0; i < kPlaces; ++i)
@@ -232,7 +234,7 @@ cudaError_t launch_rows(RowParams& p, int blocks, int block, cudaStream_t stream
     }
   cudaError_t e = prepare_smem<row_forward_kernel<KIND, WIDE, C, THREADS>>(kMost < 224 * 1024 ? kMost : 224 * 1024);
   if (e != cudaSuccess) return e;
-  return ff::launch_early(stream, {dim3(static_cast<unsigned>(blocks)), block, 1, used * 16},
+  return ff::launch_early(stream, {dim3(static_cast<unsigned>(blocks)), block, 1, used},
                           row_forward_kernel<KIND, WIDE, C, THREADS>, p);
 }
 
@@ -254,6 +256,8 @@ cudaError_t run_rows(const ForwardTask& t, int threads, cudaStream_t stream) {
   const int at_once = THREADS / threads;
   const int64_t blocks = (t.M + at_once - 1) / at_once, most = kSms * blocks_of<C, THREADS>();
   const int grid = static_cast<int>(blocks < most ? blocks : most);
+  p.step = static_cast<int64_t>(grid) * at_once;
+  p.x_step = p.step * p.in[kX].ld, p.h_step = p.step * p.in[kH].ld, p.r_step = p.step * p.r.ld, p.y_step = p.step * p.y.ld;
   return wide ? launch_rows<KIND, true, C, THREADS>(p, grid, at_once * threads, stream)
               : launch_rows<KIND, false, C, THREADS>(p, grid, at_once * threads, stream);
 }

@@ -17,6 +17,12 @@ struct View {
   int64_t ld;
   const uint16_t* end;  // after its last value
   int wide;             // every row starts on a 16-byte boundary
+
+  // Row m from byte `at` on: sizes and strides are at most 2^30, so that 32-bit factors do.
+  __device__ __forceinline__ uint16_t* row(int m, uint32_t at) const {
+    return reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(p) +
+                                       static_cast<uint64_t>(static_cast<uint32_t>(m)) * (2u * static_cast<uint32_t>(ld)) + at);
+  }
 };
 // Whether a matrix consists of whole aligned words, or is absent.
 inline bool whole_words(const View& v, int64_t cols) { return v.p == nullptr || (v.wide && cols % kWord == 0); }
@@ -56,20 +62,25 @@ __device__ __forceinline__ uint4 first_of(const uint4& v, int left) {
 }
 
 // Sixteen bytes from p to shared memory in the background, `bytes` of them read and the others 0.
-__device__ __forceinline__ void copy_async(uint4* to, const void* p, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(p), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t to, const void* p, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
 // Eight values of v's row from p on, `left` (perhaps none) of them inside the row, on their way to this thread's places
 // in shared memory, from where arrived() takes them after wait_copies(). WIDE: every row starts on a 16-byte boundary
-// and holds whole words: one place. Otherwise the two aligned words around them come to to[0] and to[next], as far as
+// and holds whole words: one place. Otherwise the two aligned words around them come to `to` and `to` + `next`, as far as
 // the matrix reaches.
 template <bool WIDE>
-__device__ __forceinline__ void fetch_word(uint4* to, int next, const View& v, const uint16_t* p, int left) {
+__device__ __forceinline__ void fetch_word(uint32_t to, uint32_t next, const View& v, const uint16_t* p, int left) {
   if (left <= 0) return;
   if (WIDE) {
-    copy_async(to, p, 16);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
     return;
   }
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
@@ -77,18 +88,18 @@ __device__ __forceinline__ void fetch_word(uint4* to, int next, const View& v, c
   if (from >= v.p) {
     copy_async(to, from, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from))));
   } else {  // the first word of the matrix
-    uint16_t* values = reinterpret_cast<uint16_t*>(to);
-    for (int i = 0; i < n && o + i < kWord; ++i) values[o + i] = p[i];
+    for (int i = 0; i < n && o + i < kWord; ++i)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * static_cast<uint32_t>(o + i)), "h"(p[i]) : "memory");
   }
   if (o + n > kWord) copy_async(to + next, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from - kWord))));
 }
 // The values that fetch_word(to, next, v, p, left) brought, zeros beyond the row's end.
 template <bool WIDE>
-__device__ __forceinline__ uint4 arrived(const uint4* to, int next, const uint16_t* p, int left) {
+__device__ __forceinline__ uint4 arrived(uint32_t to, uint32_t next, const uint16_t* p, int left) {
   if (left <= 0) return make_uint4(0, 0, 0, 0);
-  if (WIDE) return *to;
+  if (WIDE) return load_shared(to);
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
-  return first_of(o == 0 ? *to : shifted(to[0], to[next], o), left);
+  return first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
 }
 
 // The same at once, where there is no place for it. Not inlined: a kernel reads and writes words at many places, and with
