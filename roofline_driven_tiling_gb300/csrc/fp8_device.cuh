@@ -8,7 +8,6 @@
 namespace t2s {
 namespace fp8 {
 
-constexpr int kUnit = 32;  // accumulator columns that a warp takes at a time
 
 // The MMAs of one block of 128 values of K (four of K = 32) by one elected thread of a converged warp, from
 // 128-byte swizzled K-major rows; D starts from the first product.
@@ -41,6 +40,25 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc)
         : "memory");
   }
+}
+
+// A bounded barrier wait without a call in it (a kernel that moves registers between its warps can make none): the
+// thread sleeps in the barrier hardware, up to 100 us a try, and gives up after 2^17 of them.
+__device__ __forceinline__ bool wait_counted(uint32_t bar, uint32_t parity, unsigned* status) {
+#pragma unroll 1
+  for (int tries = 0; tries < 1 << 17; ++tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok != 0) return true;
+  }
+  record_status(status, T2S_ERR_TIMEOUT);
+  return false;
 }
 
 // Starts reading 16 accumulator columns of the warp's 32 rows (one row per lane); the registers hold them after

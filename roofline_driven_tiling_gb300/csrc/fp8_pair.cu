@@ -3,9 +3,11 @@
 //
 // A persistent launch takes tiles of 256 rows x 64, 128 or 256 columns, each by a cluster of two CTAs: each
 // stages its 128 rows of A and half of the rows of B, a block of 128 bytes of K per ring slot. A block's sums are
-// started afresh in one of two TMEM accumulators, and eight warps per CTA take them out, multiply them by
-// the block's scales and add them to FP32 sums in their registers (128 a thread for a 256-wide tile), while
-// the other accumulator fills. So the scales may be any FP32 numbers, and the tensor cores' truncating additions never
+// started afresh in one of the TMEM accumulators (two of 256 columns, four of 128, eight of 64), and eight warps
+// per CTA take them out, multiply them by the block's scales and add them to FP32 sums in their registers (128 a
+// thread for a 256-wide tile), while the other accumulators fill. A warp of its own brings the scales to shared
+// memory some blocks ahead: fetched by the sums' warps one block ahead, they held every block up for an L2 latency
+// (0.49 us a block whatever its width). So the scales may be any FP32 numbers, and the tensor cores' truncating additions never
 // run longer than 128 products.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -33,10 +35,18 @@ constexpr int kBBytes = kMaxN / 2 * kBlock;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kStagingBytes = 4096;  // of a warp: 32 x 32 outputs of 4 bytes, or two boxes of 2
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kEpiWarps * kStagingBytes;
+constexpr int kChunk = 32;            // accumulator columns that a warp takes at a time
+constexpr int kStagingBytes = 2048;   // of a warp: 32 rows of 64 bytes
+constexpr int kScaleBlocks = 4;       // blocks whose scales come to shared memory together, side by side for each row
+constexpr int kScaleSlots = 2;
+constexpr int kScaleBytes = (kRows + kMaxN) * kScaleBlocks * 4;
+constexpr int kMaxBuffers = 8;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kEpiWarps * kStagingBytes + kScaleSlots * kScaleBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;
+// Registers: the block is launched with 168 a thread; the sums' warps take 224 and the others keep 56.
+constexpr int kSumRegs = 224, kOtherRegs = 56;
+static_assert(128 * kOtherRegs + 32 * kEpiWarps * kSumRegs <= kThreads * 168, "the launch's registers");
 
 struct PairParams {
   CUtensorMap a, b, c;
@@ -49,42 +59,41 @@ struct PairParams {
   unsigned* status;
 };
 
-// Byte offset of 16-byte chunk `c` of row `r` in a box of 32 rows of 64 (64-byte swizzle) or 128 bytes.
-template <bool WIDE>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  return WIDE ? static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4)
-              : static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(c ^ ((r >> 1) & 3)) << 4);
+// The columns of a warp's box of outputs (32 rows): 64 bytes.
+template <int TYPE>
+constexpr int box_columns() {
+  return TYPE == kF32 ? 16 : 32;
+}
+// Byte offset of 16-byte word `c` of row `r` in a box (64-byte swizzle).
+__device__ __forceinline__ uint32_t word_at(int r, int c) {
+  return static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(c ^ ((r >> 1) & 3)) << 4);
 }
 
-// A lane's row of 32 sums, rounded, into the warp's box.
+// A lane's row of a box of sums, rounded, into the box.
 template <int TYPE>
 __device__ __forceinline__ void put_row(uint32_t box, int lane, const uint64_t* v) {
-  if constexpr (TYPE == kF32) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[4];
+    if constexpr (TYPE == kF32) {
       const float2 lo = ff::halves(v[2 * c]), hi = ff::halves(v[2 * c + 1]);
-      st_shared_v4(box + chunk_at<true>(lane, c), __float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x),
-                   __float_as_uint(hi.y));
-    }
-  } else {
-    constexpr int kKind = TYPE == kBf16 ? ff::kBf16 : ff::kF16;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t w[4];
+      w[0] = __float_as_uint(lo.x), w[1] = __float_as_uint(lo.y), w[2] = __float_as_uint(hi.x), w[3] = __float_as_uint(hi.y);
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = ff::halves(v[4 * c + i]);
-        w[i] = ff::pack_f32<kKind>(f.x, f.y);
+        w[i] = ff::pack_f32<TYPE == kBf16 ? ff::kBf16 : ff::kF16>(f.x, f.y);
       }
-      st_shared_v4(box + chunk_at<false>(lane, c), w[0], w[1], w[2], w[3]);
     }
+    st_shared_v4(box + word_at(lane, c), w[0], w[1], w[2], w[3]);
   }
 }
 
-// Stores a warp's 32 x 32 outputs at (m, n) from its box: by TMA, or a row per instruction where rows do not
-// start on 16-byte boundaries.
+// Stores a warp's box of outputs at (m, n): by TMA, or one or two rows per instruction where rows do not start on
+// 16-byte boundaries.
 template <int TYPE>
-__device__ __forceinline__ void store_unit(const PairParams& p, uint32_t box, int m, int n, int lane) {
+__device__ __forceinline__ void store_box(const PairParams& p, uint32_t box, int m, int n, int lane) {
+  constexpr int kColumns = box_columns<TYPE>(), kSize = TYPE == kF32 ? 4 : 2, kRowsAtOnce = 32 / kColumns;
   if (p.c_tma) {
     fence_proxy_async_smem();
     __syncwarp();
@@ -92,17 +101,18 @@ __device__ __forceinline__ void store_unit(const PairParams& p, uint32_t box, in
     return;
   }
   __syncwarp();
-  const int rows = n + lane < p.N ? min(32, p.M - m) : 0;
-  const int64_t first = static_cast<int64_t>(m) * p.ldc + n + lane;
+  const int r0 = lane / kColumns, col = lane % kColumns, rows = n + col < p.N ? min(32, p.M - m) : 0;
+  const int64_t first = static_cast<int64_t>(m) * p.ldc + n + col;
 #pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
+  for (int r = r0; r < 32; r += kRowsAtOnce) {
+    const uint32_t from = box + word_at(r, col * kSize / 16) + col * kSize % 16;
     if constexpr (TYPE == kF32) {
       float v;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(box + chunk_at<true>(r, lane >> 2) + (lane & 3) * 4));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(from));
       if (r < rows) static_cast<float*>(p.C)[first + r * p.ldc] = v;
     } else {
       uint16_t v;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box + chunk_at<false>(r, lane >> 3) + (lane & 7) * 2));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(from));
       if (r < rows) static_cast<uint16_t*>(p.C)[first + r * p.ldc] = v;
     }
   }
@@ -110,20 +120,24 @@ __device__ __forceinline__ void store_unit(const PairParams& p, uint32_t box, in
 }
 
 // Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 take the sums.
-// full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator; a role that gives up a bounded wait
-// records it and stops, and the others' own waits end the same way.
-// UNITS: groups of 32 columns of each of the two warps of a row quarter. VECTOR: a scale for every row of B.
-template <int TYPE, int UNITS, bool VECTOR>
+// Warp 3 holds TMEM and copies scales. full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator,
+// scale_full[s] / scale_empty[s] per slot of scales; a role that gives up a bounded wait records it and stops, and the
+// others' own waits end the same way.
+// CHUNKS: groups of 32 columns of each of the two warps of a row quarter. VECTOR: a scale for every row of B.
+template <int TYPE, int CHUNKS, bool VECTOR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kBn = 2 * UNITS * kUnit;
+  constexpr int kWarpN = CHUNKS * kChunk, kBn = 2 * kWarpN;
   constexpr uint32_t kSlotBytes = kABytes + kBn / 2 * kBlock;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + kStages * kStageBytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-  const uint32_t acc_full = bars + 16u * kStages, acc_empty = acc_full + 16u, mma_done = acc_empty + 16u;
-  const uint32_t slot = mma_done + 8u, staging = bars + 1024u;
+  constexpr uint32_t kBuffers = kTmemCols / kBn;
+  const uint32_t acc_full = bars + 16u * kStages, acc_empty = acc_full + 8u * kMaxBuffers;
+  const uint32_t scale_full = acc_empty + 8u * kMaxBuffers, scale_empty = scale_full + 8u * kScaleSlots;
+  const uint32_t mma_done = scale_empty + 8u * kScaleSlots, slot = mma_done + 8u;
+  const uint32_t staging = bars + 1024u, scales = staging + kEpiWarps * kStagingBytes;
   unsigned* const status = p.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -135,9 +149,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < kBuffers; ++b) {
       mbar_init(acc_full + 8u * b, 1);
       mbar_init(acc_empty + 8u * b, 2 * kEpiWarps);
+    }
+    for (int b = 0; b < kScaleSlots; ++b) {
+      mbar_init(scale_full + 8u * b, 32);
+      mbar_init(scale_empty + 8u * b, kEpiWarps);
     }
     mbar_init(mma_done, 1);
     mbar_fence_init();
@@ -154,22 +172,45 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot) : "memory");
 
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0 || warp == 2) {
+      // The warp stays converged (its addresses and counters live in uniform registers); one elected lane announces and copies.
       const bool is_a = warp == 0;
-      ff::Ring ring(base + (is_a ? 0 : kABytes), kStageBytes, full(0), empty(0), kStages, kBlock);
-      const uint32_t bar0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
-      const uint32_t expect = is_a && rank == 0 ? 2 * kSlotBytes : 0u;
+      const uint32_t full0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
+      const uint32_t first = base + (is_a ? 0 : kABytes);
+      const bool expects = is_a && rank == 0;
       const CUtensorMap* map = is_a ? &p.a : &p.b;
+      uint32_t s = 0, st = first, phase = 1;
+      auto next = [&] {
+        st += kStageBytes;
+        if (++s == kStages) {
+          s = 0;
+          st = first;
+          phase ^= 1u;
+        }
+      };
       bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         int m0, n0;
         tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
         const int at = is_a ? m0 + rank * kRows : n0 + rank * (kBn / 2);
-        ok = ring.copy(0, blocks, expect, bar0, status,
-                       [&](uint32_t st, int k0, uint32_t bar) { tc::tma_load_2d_pair(st, map, k0, at, bar); });
+#pragma unroll 1
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * s, phase, status));
+          if (!ok) break;
+          if (ff::elect_one()) {
+            if (expects) mbar_arrive_expect_tx(full(0) + 8u * s, 2 * kSlotBytes);
+            tc::tma_load_2d_pair(st, map, kb * kBlock, at, full0 + 8u * s);
+          }
+          __syncwarp();
+          next();
+        }
       }
       // Every slot's copies have landed and been read before the CTA may go.
-      if (ok) ring.copy(0, kStages, 0u, bar0, status, [](uint32_t, int, uint32_t) {});
+      for (int i = 0; ok && i < kStages; ++i) {
+        ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * s, phase, status));
+        next();
+      }
     } else if (warp == 1 && rank == 0) {
       const ff::OperandForm form = ff::operand_form(true);
       int s = 0;
@@ -178,13 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       for (int t = tile0; ok && t < tiles; t += tile_step) {
 #pragma unroll 1
         for (int kb = 0; kb < blocks; ++kb, ++use) {
-          const uint32_t b = use & 1u;
+          const uint32_t b = use % kBuffers;
           const uint64_t da = ff::with_address(form, st), db = ff::with_address(form, st + kABytes);
-          ok = __all_sync(0xffffffffu, ff::wait_bounded(acc_empty + 8u * b, ((use >> 1) & 1u) ^ 1u, status) &&
-                                           ff::wait_bounded(full(s), phase, status));
+          ok = __all_sync(0xffffffffu, wait_counted(acc_empty + 8u * b, ((use / kBuffers) & 1u) ^ 1u, status) &&
+                                           wait_counted(full(s), phase, status));
           if (!ok) break;
           tc::tc_fence_after();
-          mma_block<2>(tmem + b * kMaxN, da, db, p.idesc);
+          mma_block<2>(tmem + b * kBn, da, db, p.idesc);
           if (ff::elect_one()) {
             tc::mma_commit_pair(empty(s));
             tc::mma_commit_pair(acc_full + 8u * b);
@@ -201,97 +242,131 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // Every MMA issued above ends before TMEM is released.
       if (ff::elect_one()) tc::mma_commit<2>(mma_done);
       __syncwarp();
-      ff::wait_bounded(mma_done, 0u, status);
+      wait_counted(mma_done, 0u, status);
+    } else if (warp == 3) {
+      // Scales of this CTA's rows, and of the tile's columns: of each (VECTOR) or of each group of 128.
+      constexpr int kPerLane = kRows / 32, kColumns = VECTOR ? kBn : (kBn + kBlock - 1) / kBlock;
+      uint32_t use = 0;
+      bool ok = true;
+      for (int t = tile0; ok && t < tiles; t += tile_step) {
+        int m0, n0;
+        tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
+        const int m = m0 + rank * kRows + lane, n = VECTOR ? n0 + lane : (n0 + lane * kBlock) / kBlock;
+        const int columns = VECTOR ? p.N : (p.N + kBlock - 1) / kBlock;
+        const float* sa = p.sa.p + static_cast<int64_t>(m) * p.sa.row;
+        const float* sb = p.sb.p + static_cast<int64_t>(n) * p.sb.row;
+#pragma unroll 1
+        for (int kb = 0; kb < blocks; kb += kScaleBlocks, ++use) {
+          const uint32_t s = use % kScaleSlots, at = scales + s * kScaleBytes;
+          ok = __all_sync(0xffffffffu, wait_counted(scale_empty + 8u * s, ((use / kScaleSlots) & 1u) ^ 1u, status));
+          if (!ok) break;
+          const int count = min(kScaleBlocks, blocks - kb);
+          // Rows' scales lie four blocks side by side; columns' scales a block after another (VECTOR), or likewise.
+#pragma unroll 1
+          for (int j = 0; j < count; ++j) {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+              const bool in = m + 32 * i < p.M;
+              cp_async_4(at + 16u * (lane + 32 * i) + 4u * j,
+                         in ? sa + 32 * i * p.sa.row + (kb + j) * p.sa.block : p.sa.p, in ? 4u : 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < (kColumns + 31) / 32; ++i) {
+              const int c = lane + 32 * i;
+              const bool in = c < kColumns && n + 32 * i < columns;
+              const uint32_t to = at + 16u * kRows + (VECTOR ? 4u * (j * kBn + c) : 16u * c + 4u * j);
+              if (c < kColumns)
+                cp_async_4(to, in ? sb + 32 * i * p.sb.row + (kb + j) * p.sb.block : p.sb.p, in ? 4u : 0u);
+            }
+          }
+          cp_async_arrive_noinc(scale_full + 8u * s);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA may go
     }
   } else {
-    const int e = warp - 4, q = warp & 3, half = e >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    const int e = warp - 4, q = warp & 3, half = e >> 2;  // quarter of the rows, half of the columns
     const uint32_t box = staging + static_cast<uint32_t>(e) * kStagingBytes;
-    const uint32_t rows_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * UNITS * kUnit);
-    uint32_t use = 0;
+    const uint32_t rows_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * kWarpN);
+    const uint32_t acc_empty_0 = tc::map_to_rank(acc_empty, 0);
+    uint32_t use = 0, scale_use = 0;
     bool ok = true;
     for (int t = tile0; ok && t < tiles; t += tile_step) {
       int m0, n0;
       tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
-      n0 += half * UNITS * kUnit;
+      n0 += half * kWarpN;
       const int m = m0 + rank * kRows + 32 * q;
-      const bool row_in = m + lane < p.M;
-      const float* sa = p.sa.p + static_cast<int64_t>(row_in ? m + lane : 0) * p.sa.row;
-      // Column scales: of this lane's column of each group (VECTOR), else of all the warp's columns, which lie
-      // within one group of 128.
-      constexpr int kScales = VECTOR ? UNITS : 1;
-      const int n_lane = VECTOR ? n0 + lane : n0;
-      const float* sb = p.sb.p + static_cast<int64_t>(VECTOR ? n_lane : n_lane / kBlock) * p.sb.row;
-      uint64_t sum[UNITS][kUnit / 2];
+      uint64_t sum[CHUNKS][kChunk / 2];
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u)
+      for (int u = 0; u < CHUNKS; ++u)
 #pragma unroll
-        for (int i = 0; i < kUnit / 2; ++i) sum[u][i] = 0;
-      // The next block's scales are on their way while this one's sums are taken.
-      float a_next = 0.0f, b_next[kScales] = {};
-      auto fetch = [&](int kb) {
-        if (kb >= blocks) return;
-        if (row_in) a_next = sa[kb * p.sa.block];
-#pragma unroll
-        for (int u = 0; u < kScales; ++u)
-          if (n_lane + u * kUnit < p.N) b_next[u] = sb[kb * p.sb.block + u * kUnit * p.sb.row];
-      };
-      fetch(0);
+        for (int i = 0; i < kChunk / 2; ++i) sum[u][i] = 0;
 #pragma unroll 1
-      for (int kb = 0; kb < blocks; ++kb, ++use) {
-        const float a = a_next, f = a * b_next[0];
-        if constexpr (VECTOR) {
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < UNITS; ++u)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(box + 4u * (u * kUnit + lane)), "f"(b_next[u]) : "memory");
-          __syncwarp();
-        }
-        fetch(kb + 1);
-        ok = __all_sync(0xffffffffu, ff::wait_bounded(acc_full + 8u * (use & 1u), (use >> 1) & 1u, status));
+      for (int kb = 0; ok && kb < blocks; kb += kScaleBlocks, ++scale_use) {
+        const uint32_t ss = scale_use % kScaleSlots, from = scales + ss * kScaleBytes;
+        ok = __all_sync(0xffffffffu, wait_counted(scale_full + 8u * ss, (scale_use / kScaleSlots) & 1u, status));
         if (!ok) break;
-        tc::tc_fence_after();
-        const uint32_t acc = rows_at + (use & 1u) * kMaxN;
-        uint32_t part[2][16];
-        load_columns16(acc, part[0]);
+        // This lane's row's scales for the four blocks, times those of the warp's columns where they share them (the
+        // columns lie within one group of 128).
+        float4 a = lds128(from + 16u * (32 * q + lane));
+        if constexpr (!VECTOR) {
+          const float4 g = lds128(from + 16u * (kRows + half * kWarpN / kBlock));
+          a.x *= g.x, a.y *= g.y, a.z *= g.z, a.w *= g.w;
+        }
+#pragma unroll 1
+        for (int j = 0; j < kScaleBlocks && kb + j < blocks; ++j, ++use) {
+          const uint32_t b = use % kBuffers;
+          ok = __all_sync(0xffffffffu, wait_counted(acc_full + 8u * b, (use / kBuffers) & 1u, status));
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t acc = rows_at + b * kBn, columns = from + 16u * kRows + 4u * (j * kBn + half * kWarpN);
+          const uint64_t row = ff::both(a.x);
+          a.x = a.y, a.y = a.z, a.z = a.w;
+          uint32_t part[2][kChunk];  // a chunk is on its way from TMEM while the one before it is added
+          ff::load_columns(acc, part[0]);
 #pragma unroll
-        for (int u = 0; u < 2 * UNITS; ++u) {
-          uint32_t(&x)[16] = part[u & 1];
-          uint64_t* to = sum[u / 2] + u % 2 * 8;
-          wait_columns16(x);
-          if (u + 1 < 2 * UNITS) {
-            load_columns16(acc + (u + 1) * 16, part[(u + 1) & 1]);
-          } else {
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ff::arrive_remote(tc::map_to_rank(acc_empty + 8u * (use & 1u), 0));
-          }
-          if constexpr (VECTOR) {
-            const uint64_t row = ff::both(a);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              uint64_t lo, hi;
-              lds128_pairs(box + 4u * (u * 16 + 2 * i), lo, hi);
-              to[i] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), lo), row, to[i]);
-              to[i + 1] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3])), hi), row,
-                                   to[i + 1]);
+          for (int u = 0; u < CHUNKS; ++u) {
+            uint32_t(&x)[kChunk] = part[u & 1];
+            ff::wait_columns(x);
+            if (u + 1 < CHUNKS) {
+              ff::load_columns(acc + (u + 1) * kChunk, part[(u + 1) & 1]);
+            } else {
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ff::arrive_remote(acc_empty_0 + 8u * b);
             }
-          } else {
+            uint64_t* to = sum[u];
+            if constexpr (VECTOR) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              to[i] = ff::fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ff::both(f), to[i]);
+              for (int i = 0; i < kChunk / 2; i += 2) {
+                uint64_t lo, hi;
+                lds128_pairs(columns + 4u * (u * kChunk + 2 * i), lo, hi);
+                to[i] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), lo), row, to[i]);
+                to[i + 1] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3])), hi), row,
+                                     to[i + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kChunk / 2; ++i)
+                to[i] = ff::fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), row, to[i]);
+            }
           }
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scale_empty + 8u * ss);
       }
       if (!ok) break;
+      constexpr int kColumns = box_columns<TYPE>();
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        if (m >= p.M || n0 + u * kUnit >= p.N) break;
+      for (int c = 0; c < kWarpN; c += kColumns) {
+        if (m >= p.M || n0 + c >= p.N) break;
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
-        put_row<TYPE>(box, lane, sum[u]);
-        store_unit<TYPE>(p, box, m, n0 + u * kUnit, lane);
+        put_row<TYPE>(box, lane, sum[c / kChunk] + c % kChunk / 2);
+        store_box<TYPE>(p, box, m, n0 + c, lane);
       }
-      if (VECTOR && lane == 0) bulk_wait_read_all();  // the scales of the next tile go to the same place
     }
     if (lane == 0) bulk_wait_all();  // the stores read this CTA's shared memory
   }
@@ -306,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 }
 
 // Resident clusters of a kernel on the current device, looked up once.
-template <int TYPE, int UNITS, bool VECTOR>
+template <int TYPE, int CHUNKS, bool VECTOR>
 cudaError_t resident_clusters(int* out) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices];
@@ -316,7 +391,7 @@ cudaError_t resident_clusters(int* out) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   int n = known[dev].load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = fp8_pair_kernel<TYPE, UNITS, VECTOR>;
+    auto kern = fp8_pair_kernel<TYPE, CHUNKS, VECTOR>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) != cudaSuccess)
       return e;
     int sms = 0;
@@ -340,12 +415,12 @@ cudaError_t resident_clusters(int* out) {
   return cudaSuccess;
 }
 
-template <int TYPE, int UNITS, bool VECTOR>
+template <int TYPE, int CHUNKS, bool VECTOR>
 cudaError_t launch(const ProductTask& t, cudaStream_t stream, unsigned* status) {
-  constexpr int kBn = 2 * UNITS * kUnit;
+  constexpr int kBn = 2 * CHUNKS * kChunk, kColumns = box_columns<TYPE>();
   constexpr int kBytes = TYPE == kF32 ? 4 : 2;
   int resident = 0;
-  cudaError_t e = resident_clusters<TYPE, UNITS, VECTOR>(&resident);
+  cudaError_t e = resident_clusters<TYPE, CHUNKS, VECTOR>(&resident);
   if (e != cudaSuccess) return e;
   PairParams p;
   memset(&p, 0, sizeof(p));
@@ -369,18 +444,18 @@ cudaError_t launch(const ProductTask& t, cudaStream_t stream, unsigned* status) 
   p.c_tma = ((reinterpret_cast<uintptr_t>(t.C) | static_cast<uintptr_t>(t.ldc * kBytes) |
               static_cast<uintptr_t>(t.N * kBytes)) & 15u) == 0;
   if (p.c_tma) {
-    e = TYPE == kF32 ? encode_tmap_f32_2d(&p.c, t.C, t.N, t.M, t.ldc, kUnit, 32, CU_TENSOR_MAP_SWIZZLE_128B)
-                     : encode_tmap_16bit_2d(&p.c, t.C, t.N, t.M, t.ldc, kUnit, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    e = TYPE == kF32 ? encode_tmap_f32_2d(&p.c, t.C, t.N, t.M, t.ldc, kColumns, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+                     : encode_tmap_16bit_2d(&p.c, t.C, t.N, t.M, t.ldc, kColumns, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
   }
   const int64_t tiles = tiles_m * tiles_n;
   const ff::LaunchShape shape{dim3(static_cast<unsigned>(2 * (tiles < resident ? tiles : resident))), kThreads, 2, kSmemBytes};
-  return ff::launch_early(stream, shape, fp8_pair_kernel<TYPE, UNITS, VECTOR>, p);
+  return ff::launch_early(stream, shape, fp8_pair_kernel<TYPE, CHUNKS, VECTOR>, p);
 }
 
-template <int TYPE, int UNITS>
+template <int TYPE, int CHUNKS>
 cudaError_t launch_scales(const ProductTask& t, cudaStream_t stream, unsigned* status) {
-  return t.b_group == 1 ? launch<TYPE, UNITS, true>(t, stream, status) : launch<TYPE, UNITS, false>(t, stream, status);
+  return t.b_group == 1 ? launch<TYPE, CHUNKS, true>(t, stream, status) : launch<TYPE, CHUNKS, false>(t, stream, status);
 }
 
 template <int TYPE>
