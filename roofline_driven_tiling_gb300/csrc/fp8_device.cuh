@@ -61,6 +61,19 @@ __device__ __forceinline__ bool wait_counted(uint32_t bar, uint32_t parity, unsi
   return false;
 }
 
+// One try.
+__device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Starts reading 16 accumulator columns of the warp's 32 rows (one row per lane); the registers hold them after
 // wait_columns16, which stands between the load and every use.
 __device__ __forceinline__ void load_columns16(uint32_t taddr, uint32_t (&r)[16]) {

@@ -40,7 +40,7 @@ constexpr int kStagingBytes = 2048;   // of a warp: 32 rows of 64 bytes
 constexpr int kScaleBlocks = 4;       // blocks whose scales come to shared memory together, side by side for each row
 constexpr int kScaleSlots = 2;
 constexpr int kScaleBytes = (kRows + kMaxN) * kScaleBlocks * 4;
-constexpr int kMaxBuffers = 8;
+constexpr int kMaxBuffers = 4;
 constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kEpiWarps * kStagingBytes + kScaleSlots * kScaleBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;
@@ -119,9 +119,9 @@ __device__ __forceinline__ void store_box(const PairParams& p, uint32_t box, int
   __syncwarp();
 }
 
-// Roles: warps 0 and 2 copy A and B, warp 1 issues the MMAs (rank 0 only), warps 4..11 take the sums.
-// Warp 3 holds TMEM and copies scales. full[s] / empty[s] per ring slot, acc_full[b] / acc_empty[b] per accumulator,
-// scale_full[s] / scale_empty[s] per slot of scales; a role that gives up a bounded wait records it and stops, and the
+// Roles: warp 0 copies A and B, warps 1 and 2 issue the MMAs (rank 0 only), warps 4..11 take the sums.
+// Warp 3 holds TMEM and copies scales. full[s] / empty[s] per ring slot (empty also says that the slot's sums are in
+// TMEM: one commit for both), acc_empty[b] per accumulator, scale_full[s] / scale_empty[s] per slot of scales; a role that gives up a bounded wait records it and stops, and the
 // others' own waits end the same way.
 // CHUNKS: groups of 32 columns of each of the two warps of a row quarter. VECTOR: a scale for every row of B.
 template <int TYPE, int CHUNKS, bool VECTOR>
@@ -133,8 +133,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   const uint32_t bars = base + kStages * kStageBytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-  constexpr uint32_t kBuffers = kTmemCols / kBn;
-  const uint32_t acc_full = bars + 16u * kStages, acc_empty = acc_full + 8u * kMaxBuffers;
+  // At most as many accumulators as ring slots, so that empty[s] says for one block at a time that its sums are there.
+  constexpr uint32_t kBuffers = kTmemCols / kBn < 4 ? kTmemCols / kBn : 4;
+  static_assert(kBuffers <= kStages, "one commit for the slot and the sums");
+  const uint32_t acc_empty = bars + 16u * kStages;
   const uint32_t scale_full = acc_empty + 8u * kMaxBuffers, scale_empty = scale_full + 8u * kScaleSlots;
   const uint32_t mma_done = scale_empty + 8u * kScaleSlots, slot = mma_done + 8u;
   const uint32_t staging = bars + 1024u, scales = staging + kEpiWarps * kStagingBytes;
@@ -149,19 +151,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (uint32_t b = 0; b < kBuffers; ++b) {
-      mbar_init(acc_full + 8u * b, 1);
-      mbar_init(acc_empty + 8u * b, 2 * kEpiWarps);
-    }
+    for (uint32_t b = 0; b < kBuffers; ++b) mbar_init(acc_empty + 8u * b, 2 * kEpiWarps);
     for (int b = 0; b < kScaleSlots; ++b) {
       mbar_init(scale_full + 8u * b, 32);
       mbar_init(scale_empty + 8u * b, kEpiWarps);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     mbar_fence_init();
   }
   if (warp == 0 && ff::elect_one()) tma_prefetch_desc(&p.a);
-  if (warp == 2 && ff::elect_one()) tma_prefetch_desc(&p.b);
+  if (warp == 1 && ff::elect_one()) tma_prefetch_desc(&p.b);
   if (warp == 3) tc::tmem_alloc<2>(slot, kTmemCols);
   tc::tc_fence_before();
   __syncthreads();
@@ -173,71 +172,60 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 0 || warp == 2) {
+    // Ring slots one after another, `step` at a time.
+    int s = warp == 2 ? 1 : 0;
+    uint32_t phase = 0;
+    auto next = [&](int step) {
+      if ((s += step) >= kStages) {
+        s -= kStages;
+        phase ^= 1u;
+      }
+    };
+    bool ok = true;
+    if (warp == 0) {
       // The warp stays converged (its addresses and counters live in uniform registers); one elected lane announces and copies.
-      const bool is_a = warp == 0;
       const uint32_t full0 = tc::map_to_rank(full(0), 0);  // both CTAs' copies complete on rank 0's
-      const uint32_t first = base + (is_a ? 0 : kABytes);
-      const bool expects = is_a && rank == 0;
-      const CUtensorMap* map = is_a ? &p.a : &p.b;
-      uint32_t s = 0, st = first, phase = 1;
-      auto next = [&] {
-        st += kStageBytes;
-        if (++s == kStages) {
-          s = 0;
-          st = first;
-          phase ^= 1u;
-        }
-      };
-      bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         int m0, n0;
         tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
-        const int at = is_a ? m0 + rank * kRows : n0 + rank * (kBn / 2);
+        m0 += rank * kRows, n0 += rank * (kBn / 2);
 #pragma unroll 1
         for (int kb = 0; kb < blocks; ++kb) {
-          ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * s, phase, status));
+          ok = __all_sync(0xffffffffu, wait_counted(empty(s), phase ^ 1u, status));
           if (!ok) break;
           if (ff::elect_one()) {
-            if (expects) mbar_arrive_expect_tx(full(0) + 8u * s, 2 * kSlotBytes);
-            tc::tma_load_2d_pair(st, map, kb * kBlock, at, full0 + 8u * s);
+            const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+            if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kSlotBytes);
+            tc::tma_load_2d_pair(st, &p.a, kb * kBlock, m0, full0 + 8u * s);
+            tc::tma_load_2d_pair(st + kABytes, &p.b, kb * kBlock, n0, full0 + 8u * s);
           }
           __syncwarp();
-          next();
+          next(1);
         }
       }
       // Every slot's copies have landed and been read before the CTA may go.
       for (int i = 0; ok && i < kStages; ++i) {
-        ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * s, phase, status));
-        next();
+        ok = __all_sync(0xffffffffu, wait_counted(empty(s), phase ^ 1u, status));
+        next(1);
       }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp != 3 && rank == 0) {
+      // Two warps take every other block each: a block's waits, MMAs and commit take one of them longer to issue than the MMAs
+      // of a narrow tile take to run.
       const ff::OperandForm form = ff::operand_form(true);
-      int s = 0;
-      uint32_t phase = 0, use = 0, st = base;
-      bool ok = true;
-      for (int t = tile0; ok && t < tiles; t += tile_step) {
+      const int own_tiles = tile0 < tiles ? (tiles - tile0 + tile_step - 1) / tile_step : 0;
+      const int64_t all = static_cast<int64_t>(own_tiles) * blocks;
 #pragma unroll 1
-        for (int kb = 0; kb < blocks; ++kb, ++use) {
-          const uint32_t b = use % kBuffers;
-          const uint64_t da = ff::with_address(form, st), db = ff::with_address(form, st + kABytes);
-          ok = __all_sync(0xffffffffu, wait_counted(acc_empty + 8u * b, ((use / kBuffers) & 1u) ^ 1u, status) &&
-                                           wait_counted(full(s), phase, status));
-          if (!ok) break;
-          tc::tc_fence_after();
-          mma_block<2>(tmem + b * kBn, da, db, p.idesc);
-          if (ff::elect_one()) {
-            tc::mma_commit_pair(empty(s));
-            tc::mma_commit_pair(acc_full + 8u * b);
-          }
-          __syncwarp();
-          st += kStageBytes;
-          if (++s == kStages) {
-            s = 0;
-            st = base;
-            phase ^= 1u;
-          }
-        }
+      for (int64_t use = warp - 1; use < all; use += 2) {
+        const uint32_t b = static_cast<uint32_t>(use) % kBuffers, parity = (static_cast<uint32_t>(use) / kBuffers & 1u) ^ 1u;
+        const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+        const uint64_t da = ff::with_address(form, st), db = ff::with_address(form, st + kABytes);
+        ok = __all_sync(0xffffffffu, wait_counted(full(s), phase, status) && wait_counted(acc_empty + 8u * b, parity, status));
+        if (!ok) break;
+        tc::tc_fence_after();
+        mma_block<2>(tmem + b * kBn, da, db, p.idesc);
+        if (ff::elect_one()) tc::mma_commit_pair(empty(s));
+        __syncwarp();
+        next(2);
       }
       // Every MMA issued above ends before TMEM is released.
       if (ff::elect_one()) tc::mma_commit<2>(mma_done);
@@ -247,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       // Scales of this CTA's rows, and of the tile's columns: of each (VECTOR) or of each group of 128.
       constexpr int kPerLane = kRows / 32, kColumns = VECTOR ? kBn : (kBn + kBlock - 1) / kBlock;
       uint32_t use = 0;
-      bool ok = true;
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         int m0, n0;
         tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
@@ -257,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         const float* sb = p.sb.p + static_cast<int64_t>(n) * p.sb.row;
 #pragma unroll 1
         for (int kb = 0; kb < blocks; kb += kScaleBlocks, ++use) {
-          const uint32_t s = use % kScaleSlots, at = scales + s * kScaleBytes;
-          ok = __all_sync(0xffffffffu, wait_counted(scale_empty + 8u * s, ((use / kScaleSlots) & 1u) ^ 1u, status));
+          const uint32_t slot_of = use % kScaleSlots, at = scales + slot_of * kScaleBytes;
+          ok = __all_sync(0xffffffffu, wait_counted(scale_empty + 8u * slot_of, ((use / kScaleSlots) & 1u) ^ 1u, status));
           if (!ok) break;
           const int count = min(kScaleBlocks, blocks - kb);
           // Rows' scales lie four blocks side by side; columns' scales a block after another (VECTOR), or likewise.
@@ -279,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
                 cp_async_4(to, in ? sb + 32 * i * p.sb.row + (kb + j) * p.sb.block : p.sb.p, in ? 4u : 0u);
             }
           }
-          cp_async_arrive_noinc(scale_full + 8u * s);
+          cp_async_arrive_noinc(scale_full + 8u * slot_of);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA may go
@@ -290,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
     const uint32_t box = staging + static_cast<uint32_t>(e) * kStagingBytes;
     const uint32_t rows_at = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(half * kWarpN);
     const uint32_t acc_empty_0 = tc::map_to_rank(acc_empty, 0);
-    uint32_t use = 0, scale_use = 0;
+    uint32_t use = 0, scale_use = 0, slot_at = 0, slot_phase = 0;
     bool ok = true;
     for (int t = tile0; ok && t < tiles; t += tile_step) {
       int m0, n0;
@@ -317,7 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 #pragma unroll 1
         for (int j = 0; j < kScaleBlocks && kb + j < blocks; ++j, ++use) {
           const uint32_t b = use % kBuffers;
-          ok = __all_sync(0xffffffffu, wait_counted(acc_full + 8u * b, (use / kBuffers) & 1u, status));
+          ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * slot_at, slot_phase, status));
+          if (++slot_at == kStages) {
+            slot_at = 0;
+            slot_phase ^= 1u;
+          }
           if (!ok) break;
           tc::tc_fence_after();
           const uint32_t acc = rows_at + b * kBn, columns = from + 16u * kRows + 4u * (j * kBn + half * kWarpN);
