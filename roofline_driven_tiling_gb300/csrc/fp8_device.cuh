@@ -42,9 +42,23 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, ui
   }
 }
 
+__device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A bounded barrier wait without a call in it (a kernel that moves registers between its warps can make none): the
-// thread sleeps in the barrier hardware, up to 100 us a try, and gives up after 2^17 of them.
+// thread asks once, which answers sooner where the phase is over already (4096^3 67 -> 65 us), then sleeps in the barrier
+// hardware, up to 100 us a try, and gives up after 2^17 of them.
 __device__ __forceinline__ bool wait_counted(uint32_t bar, uint32_t parity, unsigned* status) {
+  if (try_barrier(bar, parity)) return true;
 #pragma unroll 1
   for (int tries = 0; tries < 1 << 17; ++tries) {
     uint32_t ok;
@@ -59,37 +73,6 @@ __device__ __forceinline__ bool wait_counted(uint32_t bar, uint32_t parity, unsi
   }
   record_status(status, T2S_ERR_TIMEOUT);
   return false;
-}
-
-// One try.
-__device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Starts reading 16 accumulator columns of the warp's 32 rows (one row per lane); the registers hold them after
-// wait_columns16, which stands between the load and every use.
-__device__ __forceinline__ void load_columns16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void wait_columns16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
 }
 
 // Instruction descriptor: D FP32, the operands' formats, both K-major, N and M.

@@ -28,11 +28,10 @@ namespace {
 using ff::pack2;
 
 constexpr int kRows = 128;  // A rows of one CTA
-constexpr int kStages = 6;
+constexpr int kRingBytes = 6 * 32768;
 constexpr int kMaxN = 256;
 constexpr int kABytes = kRows * kBlock;
-constexpr int kBBytes = kMaxN / 2 * kBlock;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kMaxStages = 9;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kChunk = 32;            // accumulator columns that a warp takes at a time
@@ -41,7 +40,7 @@ constexpr int kScaleBlocks = 4;       // blocks whose scales come to shared memo
 constexpr int kScaleSlots = 2;
 constexpr int kScaleBytes = (kRows + kMaxN) * kScaleBlocks * 4;
 constexpr int kMaxBuffers = 4;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024 + kEpiWarps * kStagingBytes + kScaleSlots * kScaleBytes;
+constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kEpiWarps * kStagingBytes + kScaleSlots * kScaleBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512;
 // Registers: the block is launched with 168 a thread; the sums' warps take 224 and the others keep 56.
@@ -129,14 +128,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   constexpr int kWarpN = CHUNKS * kChunk, kBn = 2 * kWarpN;
   constexpr uint32_t kSlotBytes = kABytes + kBn / 2 * kBlock;
+  constexpr int kStages = kRingBytes / kSlotBytes;  // ring slots: six of a 256-wide tile's blocks, eight, nine
+  static_assert(kStages <= kMaxStages, "barriers");
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t bars = base + kRingBytes;
   auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
   // At most as many accumulators as ring slots, so that empty[s] says for one block at a time that its sums are there.
   constexpr uint32_t kBuffers = kTmemCols / kBn < 4 ? kTmemCols / kBn : 4;
   static_assert(kBuffers <= kStages, "one commit for the slot and the sums");
-  const uint32_t acc_empty = bars + 16u * kStages;
+  const uint32_t acc_empty = bars + 16u * kMaxStages;
   const uint32_t scale_full = acc_empty + 8u * kMaxBuffers, scale_empty = scale_full + 8u * kScaleSlots;
   const uint32_t mma_done = scale_empty + 8u * kScaleSlots, slot = mma_done + 8u;
   const uint32_t staging = bars + 1024u, scales = staging + kEpiWarps * kStagingBytes;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           ok = __all_sync(0xffffffffu, wait_counted(empty(s), phase ^ 1u, status));
           if (!ok) break;
           if (ff::elect_one()) {
-            const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+            const uint32_t st = base + static_cast<uint32_t>(s) * kSlotBytes;
             if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * kSlotBytes);
             tc::tma_load_2d_pair(st, &p.a, kb * kBlock, m0, full0 + 8u * s);
             tc::tma_load_2d_pair(st + kABytes, &p.b, kb * kBlock, n0, full0 + 8u * s);
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
 #pragma unroll 1
       for (int64_t use = warp - 1; use < all; use += 2) {
         const uint32_t b = static_cast<uint32_t>(use) % kBuffers, parity = (static_cast<uint32_t>(use) / kBuffers & 1u) ^ 1u;
-        const uint32_t st = base + static_cast<uint32_t>(s) * kStageBytes;
+        const uint32_t st = base + static_cast<uint32_t>(s) * kSlotBytes;
         const uint64_t da = ff::with_address(form, st), db = ff::with_address(form, st + kABytes);
         ok = __all_sync(0xffffffffu, wait_counted(full(s), phase, status) && wait_counted(acc_empty + 8u * b, parity, status));
         if (!ok) break;
@@ -314,15 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           const uint32_t acc = rows_at + b * kBn, columns = from + 16u * kRows + 4u * (j * kBn + half * kWarpN);
           const uint64_t row = ff::both(a.x);
           a.x = a.y, a.y = a.z, a.z = a.w;
-          uint32_t part[2][kChunk];  // a chunk is on its way from TMEM while the one before it is added
-          ff::load_columns(acc, part[0]);
 #pragma unroll
           for (int u = 0; u < CHUNKS; ++u) {
-            uint32_t(&x)[kChunk] = part[u & 1];
+            uint32_t x[kChunk];
+            ff::load_columns(acc + u * kChunk, x);
             ff::wait_columns(x);
-            if (u + 1 < CHUNKS) {
-              ff::load_columns(acc + (u + 1) * kChunk, part[(u + 1) & 1]);
-            } else {
+            if (u + 1 == CHUNKS) {
               tc::tc_fence_before();
               __syncwarp();
               if (lane == 0) ff::arrive_remote(acc_empty_0 + 8u * b);
