@@ -56,7 +56,21 @@ struct ProductTask {
 };
 cudaError_t run_product(const ProductTask& t, cudaStream_t stream);
 // By SM pairs in tiles of 256 rows x `width` (64, 128 or 256) columns (fp8_pair.cu).
-cudaError_t run_pair(const ProductTask& t, int width, cudaStream_t stream, unsigned* status);
+struct PairPlan {
+  int width = 0;
+  double cost = 0.0;  // expected time in microseconds
+};
+PairPlan plan_pair(const ProductTask& t, int pairs);
+cudaError_t run_pair(const ProductTask& t, const PairPlan& plan, cudaStream_t stream, unsigned* status);
+
+// With B's rows along the tensor core's and the sum split over clusters (fp8_rows.cu): rows of A in a tile, CTAs along K,
+// and the SMs that their clusters reach.
+struct RowsPlan {
+  int rows = 0, splits = 1, reach = 0;
+  double cost = 0.0;
+};
+RowsPlan plan_rows(const ProductTask& t, int sms);
+cudaError_t run_rows(const ProductTask& t, const RowsPlan& plan, cudaStream_t stream, unsigned* status);
 
 }  // namespace fp8
 }  // namespace t2s
