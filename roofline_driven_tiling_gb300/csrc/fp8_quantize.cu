@@ -137,98 +137,182 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_co
   }
 }
 
-// Along columns, or both, or with a scale for 128 x 128: a CTA takes a tile of 128 x 128 in its threads'
-// registers (eight columns of every 16th row each), reduces over rows and columns, and writes the transposed
-// values through shared memory so that they leave in rows of 128 bytes.
-constexpr int kPitch = kBlock + 4;  // bytes between the transposed tile's rows in shared memory
+// Along columns, or both, or with a scale for 128 x 128: a CTA takes a tile of 128 x 128, a thread eight consecutive rows
+// of eight consecutive columns. Maxima of columns go through shared memory, those of rows over a half-warp; the
+// transposed values leave through shared memory too, eight bytes (a column's eight rows) at a time, so that they are
+// written in rows of 128 bytes. The eight-byte words of a transposed row are stored in an order that differs from eight
+// columns to the next, so that the lanes of a warp hit different banks both ways.
+__device__ __forceinline__ uint32_t transposed_at(int column, int word) {
+  return static_cast<uint32_t>(column * kBlock + ((word ^ (column / 8)) & 15) * 8);
+}
+
+// Eight values of a row as they were read: 16-bit ones take half the registers.
+template <int TYPE>
+struct Eight {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left, bool wide) {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+    if (wide && left >= 8) {
+      w = *reinterpret_cast<const uint4*>(p);
+    } else {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 2 * i < left ? p[2 * i] : 0u;
+        if (2 * i + 1 < left) v[i] |= static_cast<uint32_t>(p[2 * i + 1]) << 16;
+      }
+      w = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = ff::to_f32x2<TYPE == kBf16 ? ff::kBf16 : ff::kF16>(u[i]);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Eight<kF32> {
+  float f[8];
+  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left, bool wide) { load8<kF32>(x, at, left, wide, f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i];
+  }
+};
+
+// Maxima of eight rows over a half-warp's 16 lanes, in all of them: a lane first gives away half of its rows at a
+// step, until it holds one (16 shuffles instead of 32).
+__device__ __forceinline__ void half_warp_maxima(uint32_t (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v[i];
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) {
+    const bool high = lane & d;
+#pragma unroll
+    for (int i = 0; i < d; ++i) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + d], d);
+      x[i] = max(high ? x[i + d] : x[i], other);
+    }
+  }
+  // The lane holds row lane % 8.
+  x[0] = max(x[0], __shfl_xor_sync(0xffffffffu, x[0], 8));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, x[0], (lane & 16) + i);
+}
 
 template <int TYPE, int FORMAT, bool SQUARE>
-__global__ void __launch_bounds__(kThreads) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
-  __shared__ uint32_t column_max[kBlock];
-  __shared__ float column_inverse[kBlock];
-  __shared__ uint32_t transposed[kBlock * kPitch / 4];
+__global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ __align__(16) uint32_t column_max[kWarps][kBlock];
+  __shared__ __align__(16) float column_inverse[kBlock];
+  __shared__ __align__(16) uint8_t transposed[kBlock * kBlock];
   ff::wait_for_earlier_kernels();
   const int64_t tile = blockIdx.x, mb = tile % p.row_tiles, nb = tile / p.row_tiles;
-  const int64_t m0 = mb * kBlock + threadIdx.x / 16;
-  const int c0 = threadIdx.x % 16 * 8;
-  const int64_t n0 = nb * kBlock + c0, left = p.N - n0;
-  float v[8][8];
+  const int warp = threadIdx.x / 32, r0 = threadIdx.x / 16 * 8, c0 = threadIdx.x % 16 * 8;
+  const int64_t m0 = mb * kBlock + r0, n0 = nb * kBlock + c0, left = p.N - n0;
+  const bool columns = p.columns.q != nullptr;
+  Eight<TYPE> x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    load8<TYPE>(p.X, (m0 + 16 * i) * p.ldx + n0, m0 + 16 * i < p.M ? left : 0, p.x_wide, v[i]);
-  if (threadIdx.x < kBlock) column_max[threadIdx.x] = 0;
-  __syncthreads();
+  for (int i = 0; i < 8; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
+  uint32_t row_max[8], amax[8] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    x[i].get(v);
+    row_max[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a = magnitude(v[j]);
+      row_max[i] = max(row_max[i], a);
+      if (!SQUARE) amax[j] = max(amax[j], a);
+    }
+  }
   Scale all = {};
-  if (SQUARE || p.columns.q != nullptr) {
-    uint32_t amax[8] = {};
+  if (SQUARE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 1; i < 8; ++i) row_max[0] = max(row_max[0], row_max[i]);
+    row_max[0] = half_warp_max(row_max[0]);
+    if (threadIdx.x % 16 == 0) column_max[0][threadIdx.x / 16] = row_max[0];
+    __syncthreads();
+    all = scale_of<FORMAT>(half_warp_max(column_max[0][threadIdx.x % 16]));
+    if (threadIdx.x == 0) {
+      if (p.rows.q != nullptr) p.rows.s.p[mb * p.rows.s.row + nb * p.rows.s.block] = all.value;
+      if (columns) p.columns.s.p[nb * p.columns.s.row + mb * p.columns.s.block] = all.value;
+    }
+  } else if (columns) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax[j] = max(amax[j], magnitude(v[i][j]));
-    if (SQUARE) {
-#pragma unroll
-      for (int j = 1; j < 8; ++j) amax[0] = max(amax[0], amax[j]);
-      amax[0] = half_warp_max(amax[0]);
-      if (threadIdx.x % 16 == 0) atomicMax(&column_max[0], amax[0]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        amax[j] = max(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], 16));
-        if ((threadIdx.x & 16) == 0) atomicMax(&column_max[c0 + j], amax[j]);
-      }
+    for (int j = 0; j < 8; ++j) amax[j] = max(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], 16));
+    if ((threadIdx.x & 16) == 0) {
+      uint4* to = reinterpret_cast<uint4*>(&column_max[warp][c0]);
+      to[0] = make_uint4(amax[0], amax[1], amax[2], amax[3]);
+      to[1] = make_uint4(amax[4], amax[5], amax[6], amax[7]);
     }
     __syncthreads();
-    if (SQUARE) {
-      all = scale_of<FORMAT>(column_max[0]);
-    } else if (threadIdx.x < kBlock) {
-      const Scale s = scale_of<FORMAT>(column_max[threadIdx.x]);
+    if (threadIdx.x < kBlock) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) a = max(a, column_max[i][threadIdx.x]);
+      const Scale s = scale_of<FORMAT>(a);
       const int64_t n = nb * kBlock + threadIdx.x;
       column_inverse[threadIdx.x] = s.inverse;
       if (n < p.N) p.columns.s.p[n * p.columns.s.row + mb * p.columns.s.block] = s.value;
     }
-    if (SQUARE && threadIdx.x == 0) {
-      if (p.rows.q != nullptr) p.rows.s.p[mb * p.rows.s.row + nb * p.rows.s.block] = all.value;
-      if (p.columns.q != nullptr) p.columns.s.p[nb * p.columns.s.row + mb * p.columns.s.block] = all.value;
-    }
+    __syncthreads();
   }
   if (p.rows.q != nullptr) {
+    if (!SQUARE) half_warp_maxima(row_max);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t m = m0 + 16 * i;
-      Scale s = all;
-      if (!SQUARE) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[i][j]));
-        s = scale_of<FORMAT>(half_warp_max(amax));
-        if (threadIdx.x % 16 == 0 && m < p.M) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = s.value;
-      }
-      if (m < p.M) store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v[i], s.inverse));
+      const int64_t m = m0 + i;
+      const Scale s = SQUARE ? all : scale_of<FORMAT>(row_max[i]);
+      float v[8];
+      x[i].get(v);
+      if (m >= p.M) continue;
+      if (!SQUARE && threadIdx.x % 16 == 0) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = s.value;
+      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, s.inverse));
     }
   }
-  if (p.columns.q == nullptr) return;
-  __syncthreads();
-  uint8_t* bytes = reinterpret_cast<uint8_t*>(transposed);
+  if (!columns) return;
+  float inverse[8];
+  if (SQUARE) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float inverse = SQUARE ? all.inverse : column_inverse[c0 + j];
+    for (int j = 0; j < 8; ++j) inverse[j] = all.inverse;
+  } else {
+    const float4 lo = reinterpret_cast<const float4*>(column_inverse + c0)[0], hi = reinterpret_cast<const float4*>(column_inverse + c0)[1];
+    inverse[0] = lo.x, inverse[1] = lo.y, inverse[2] = lo.z, inverse[3] = lo.w;
+    inverse[4] = hi.x, inverse[5] = hi.y, inverse[6] = hi.z, inverse[7] = hi.w;
+  }
+  uint32_t bytes[8][2];  // a column's eight rows
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const uint32_t w = pack_fp8x2<FORMAT>(v[i][j] * inverse, v[i + 1][j] * inverse);
-      uint8_t* at = bytes + (c0 + j) * kPitch + threadIdx.x / 16 + 16 * i;
-      at[0] = static_cast<uint8_t>(w);
-      at[16] = static_cast<uint8_t>(w >> 8);
+  for (int i = 0; i < 8; i += 2) {
+    float v[8], w[8];
+    x[i].get(v);
+    x[i + 1].get(w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t two = pack_fp8x2<FORMAT>(v[j] * inverse[j], w[j] * inverse[j]);
+      bytes[j][i / 4] = i % 4 == 0 ? two : bytes[j][i / 4] | two << 16;
     }
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint2*>(transposed + transposed_at(c0 + j, r0 / 8)) = make_uint2(bytes[j][0], bytes[j][1]);
   __syncthreads();
   // Sixteen threads to a transposed row of 128 bytes.
-  const int64_t rows_left = p.M - mb * kBlock - c0;
-#pragma unroll 4
-  for (int c = threadIdx.x / 16; c < kBlock; c += kThreads / 16) {
+  const int word = threadIdx.x % 16;
+  const int64_t rows_left = p.M - mb * kBlock - word * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = threadIdx.x / 16 + 16 * i;
     const int64_t n = nb * kBlock + c;
-    if (n >= p.N) break;
-    const uint32_t* from = transposed + (c * kPitch + c0) / 4;
-    store8(p.columns.q + n * p.columns.ld + mb * kBlock + c0, rows_left, p.columns_wide, make_uint2(from[0], from[1]));
+    if (n < p.N)
+      store8(p.columns.q + n * p.columns.ld + mb * kBlock + word * 8, rows_left, p.columns_wide,
+             *reinterpret_cast<const uint2*>(transposed + transposed_at(c, word)));
   }
 }
 
