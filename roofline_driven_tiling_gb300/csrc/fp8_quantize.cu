@@ -19,36 +19,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A thread's eight consecutive values of a row; zeros beyond its end.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* x, int64_t at, int64_t left, bool wide, float (&v)[8]) {
-  if constexpr (TYPE == kF32) {
-    const float* p = static_cast<const float*>(x) + at;
-    if (wide && left >= 8) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
-    }
-  } else {
-    constexpr int kKind = TYPE == kBf16 ? ff::kBf16 : ff::kF16;
-    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
-    if (wide && left >= 8) {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = ff::to_f32x2<kKind>(u[i]);
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? ff::to_f32<kKind>(p[i]) : 0.0f;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // A block's scale and 1 / scale from the bits of its largest magnitude.
@@ -102,51 +72,8 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
   return v;
 }
 
-struct QuantizeParams {
-  int64_t M, N, ldx;
-  const void* X;
-  Quantized rows, columns;
-  int64_t row_tiles;
-  int x_wide, rows_wide, columns_wide;
-};
-
-// Along rows: a half-warp takes a block, a CTA 16 rows of kAhead blocks (so that the scales of a block leave
-// as 64 consecutive bytes where rows' scales are neighbours).
-constexpr int kAhead = 4;
-
-template <int TYPE, int FORMAT>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
-  ff::wait_for_earlier_kernels();
-  const int64_t tile = blockIdx.x, m = tile % p.row_tiles * 16 + threadIdx.x / 16;
-  const int64_t b0 = tile / p.row_tiles * kAhead, n0 = b0 * kBlock + threadIdx.x % 16 * 8;
-  const int64_t left = m < p.M ? p.N - n0 : 0;
-  float v[kAhead][8];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    load8<TYPE>(p.X, m * p.ldx + n0 + i * kBlock, left - i * kBlock, p.x_wide, v[i]);
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[i][j]));
-    const Scale s = scale_of<FORMAT>(half_warp_max(amax));
-    if (left - i * kBlock > 0) {
-      store8(p.rows.q + m * p.rows.ld + n0 + i * kBlock, left - i * kBlock, p.rows_wide, pack8<FORMAT>(v[i], s.inverse));
-      if (threadIdx.x % 16 == 0) p.rows.s.p[m * p.rows.s.row + (b0 + i) * p.rows.s.block] = s.value;
-    }
-  }
-}
-
-// Along columns, or both, or with a scale for 128 x 128: a CTA takes a tile of 128 x 128, a thread eight consecutive rows
-// of eight consecutive columns. Maxima of columns go through shared memory, those of rows over a half-warp; the
-// transposed values leave through shared memory too, eight bytes (a column's eight rows) at a time, so that they are
-// written in rows of 128 bytes. The eight-byte words of a transposed row are stored in an order that differs from eight
-// columns to the next, so that the lanes of a warp hit different banks both ways.
-__device__ __forceinline__ uint32_t transposed_at(int column, int word) {
-  return static_cast<uint32_t>(column * kBlock + ((word ^ (column / 8)) & 15) * 8);
-}
-
-// Eight values of a row as they were read: 16-bit ones take half the registers.
+// A thread's eight consecutive values of a row as they were read (16-bit ones take half the registers), zeros beyond its
+// end. Nothing is done with them before all of a thread's loads are on their way.
 template <int TYPE>
 struct Eight {
   uint4 w;
@@ -176,12 +103,69 @@ struct Eight {
 template <>
 struct Eight<kF32> {
   float f[8];
-  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left, bool wide) { load8<kF32>(x, at, left, wide, f); }
+  __device__ __forceinline__ void load(const void* x, int64_t at, int64_t left, bool wide) {
+    const float* p = static_cast<const float*>(x) + at;
+    if (wide && left >= 8) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = i < left ? p[i] : 0.0f;
+    }
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = f[i];
   }
 };
+
+struct QuantizeParams {
+  int64_t M, N, ldx;
+  const void* X;
+  Quantized rows, columns;
+  int64_t row_tiles, column_tiles;
+  int across;  // half-warps along a row
+  int x_wide, rows_wide, columns_wide;
+};
+
+// Along rows: a half-warp takes a block of kAhead rows, all of them on their way at once; a CTA's 16 half-warps lie along
+// a row (up to 4 KB of it) as far as it reaches, then down. (Down first, so that scales left in longer runs, the reads
+// were 256 bytes of each row and 8192 x 8192 took 60 us.)
+constexpr int kAhead = 4;
+
+template <int TYPE, int FORMAT>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
+  ff::wait_for_earlier_kernels();
+  const int half = threadIdx.x / 16, down = half / p.across;
+  const int64_t tile = blockIdx.x, m0 = (tile / p.column_tiles * (16 / p.across) + down) * kAhead;
+  const int64_t b = tile % p.column_tiles * p.across + (half - down * p.across), n0 = b * kBlock + threadIdx.x % 16 * 8;
+  const int64_t left = p.N - n0;
+  Eight<TYPE> x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    float v[8];
+    x[i].get(v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[j]));
+    const Scale s = scale_of<FORMAT>(half_warp_max(amax));
+    const int64_t m = m0 + i;
+    if (m >= p.M) continue;
+    if (left > 0) store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, s.inverse));
+    if (threadIdx.x % 16 == 0 && left > 0) p.rows.s.p[m * p.rows.s.row + b * p.rows.s.block] = s.value;
+  }
+}
+
+// Along columns, or both, or with a scale for 128 x 128: a CTA takes a tile of 128 x 128, a thread eight consecutive rows
+// of eight consecutive columns. Maxima of columns go through shared memory, those of rows over a half-warp; the
+// transposed values leave through shared memory too, eight bytes (a column's eight rows) at a time, so that they are
+// written in rows of 128 bytes. The eight-byte words of a transposed row are stored in an order that differs from eight
+// columns to the next, so that the lanes of a warp hit different banks both ways.
+__device__ __forceinline__ uint32_t transposed_at(int column, int word) {
+  return static_cast<uint32_t>(column * kBlock + ((word ^ (column / 8)) & 15) * 8);
+}
 
 // Maxima of eight rows over a half-warp's 16 lanes, in all of them: a lane first gives away half of its rows at a
 // step, until it holds one (16 shuffles instead of 32).
@@ -206,7 +190,7 @@ __device__ __forceinline__ void half_warp_maxima(uint32_t (&v)[8]) {
 }
 
 template <int TYPE, int FORMAT, bool SQUARE>
-__global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
   constexpr int kWarps = kThreads / 32;
   __shared__ __align__(16) uint32_t column_max[kWarps][kBlock];
   __shared__ __align__(16) float column_inverse[kBlock];
@@ -318,16 +302,19 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const __grid
 
 template <int TYPE, int FORMAT>
 cudaError_t launch(const QuantizeTask& t, cudaStream_t stream) {
-  QuantizeParams p{t.M, t.N, t.ldx, t.X, t.rows, t.columns, 0, 0, 0, 0};
+  QuantizeParams p{t.M, t.N, t.ldx, t.X, t.rows, t.columns};
   const int64_t ld_bytes = t.ldx * (TYPE == kF32 ? 4 : 2);
   p.x_wide = ((reinterpret_cast<uintptr_t>(t.X) | static_cast<uintptr_t>(t.M > 1 ? ld_bytes : 0)) & 15u) == 0;
   p.rows_wide = ((reinterpret_cast<uintptr_t>(t.rows.q) | static_cast<uintptr_t>(t.rows.ld)) & 7u) == 0;
   p.columns_wide = ((reinterpret_cast<uintptr_t>(t.columns.q) | static_cast<uintptr_t>(t.columns.ld)) & 7u) == 0;
   const bool tiles = t.square || t.columns.q != nullptr;
-  p.row_tiles = tiles ? blocks_of(t.M) : (t.M + 15) / 16;
-  const int64_t across = tiles ? blocks_of(t.N) : (blocks_of(t.N) + kAhead - 1) / kAhead;
-  if (p.row_tiles > 0x7fffffff / across) return cudaErrorInvalidConfiguration;
-  const ff::LaunchShape shape{dim3(static_cast<unsigned>(p.row_tiles * across)), kThreads, 1, 0};
+  p.across = 1;
+  while (p.across < 16 && p.across < blocks_of(t.N)) p.across *= 2;
+  const int64_t rows = tiles ? kBlock : 16 / p.across * kAhead;
+  p.row_tiles = (t.M + rows - 1) / rows;
+  p.column_tiles = tiles ? blocks_of(t.N) : (blocks_of(t.N) + p.across - 1) / p.across;
+  if (p.row_tiles > 0x7fffffff / p.column_tiles) return cudaErrorInvalidConfiguration;
+  const ff::LaunchShape shape{dim3(static_cast<unsigned>(p.row_tiles * p.column_tiles)), kThreads, 1, 0};
   if (!tiles) return ff::launch_early(stream, shape, quantize_rows_kernel<TYPE, FORMAT>, p);
   return t.square ? ff::launch_early(stream, shape, quantize_tile_kernel<TYPE, FORMAT, true>, p)
                   : ff::launch_early(stream, shape, quantize_tile_kernel<TYPE, FORMAT, false>, p);
