@@ -390,14 +390,14 @@ cudaError_t launch_rows(const ProductTask& t, const RowsPlan& plan, cudaStream_t
 
 }  // namespace
 
-// Expected time in microseconds: what a launch takes, a CTA's blocks (16 KB of B each, and A's rows) and the join, in as
-// many waves as the CTAs need; all SMs together take in at most 14 TB/s.
+// Expected time in microseconds: what a launch takes, a CTA's blocks (0.27, 0.30, 0.36 or 0.7 each in tiles of 16, 32, 64 or
+// 128 rows, measured) and the join, in as many waves as the CTAs need; all SMs together take in at most 14 TB/s.
 RowsPlan plan_rows(const ProductTask& t, int sms) {
   RowsPlan best;
   const int64_t blocks = blocks_of(t.K), tiles_n = (t.N + kTileN - 1) / kTileN;
   for (const int rows : {16, 32, 64, 128}) {
     const int64_t tiles = tiles_n * ((t.M + rows - 1) / rows);
-    const double block = 0.2 + rows * 0.0012;
+    const double block = rows == 16 ? 0.27 : rows == 32 ? 0.30 : rows == 64 ? 0.36 : 0.7;
     for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
       if (splits > 1 && blocks < 2 * splits) break;
       // SMs that clusters reach when a CTA fills an SM.
