@@ -37,29 +37,30 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   // Every lane of a warp stays for the stores' shuffles as long as one of its rows is left.
   const int64_t first_of_warp = __shfl_sync(0xffffffffu, m, 0);
   for (int64_t ahead = first_of_warp; ahead < p.M; ahead += p.step, m += p.step) {
-    uint4 x[kAhead], r[kAhead];
+    row::RawWord<WIDE> x[kAhead], r[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t row = m + i * at_once;
       const int inside = row < p.M ? left : 0;
-      x[i] = row::load_word<WIDE>(p.x, p.x.p + row * p.x.ld + n, inside);
-      if (residual) r[i] = row::load_word<WIDE>(p.r, p.r.p + row * p.r.ld + n, inside);
+      x[i].load(p.x, p.x.p + row * p.x.ld + n, inside);
+      if (residual) r[i].load(p.r, p.r.p + row * p.r.ld + n, inside);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t row = m + i * at_once;
+      const int inside = row < p.M ? left : 0;
       uint64_t v[4];
-      row::unpack<KIND>(x[i], v);
+      row::unpack<KIND>(x[i].get(p.x, p.x.p + row * p.x.ld + n, inside), v);
       row::Keep keep;
       keep.draw(key, static_cast<uint64_t>(row) * groups + static_cast<uint64_t>(n / 4), p.drop.dropped);
       keep.apply(v, p.drop.factor);
       if (residual) {
         uint64_t u[4];
-        row::unpack<KIND>(r[i], u);
+        row::unpack<KIND>(r[i].get(p.r, p.r.p + row * p.r.ld + n, inside), u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = row::add2(v[j], u[j]);
       }
-      row::store_word<WIDE>(p.y, p.y.p + row * p.y.ld + n, row < p.M ? left : 0, row::pack<KIND>(v));
+      row::store_word<WIDE>(p.y, p.y.p + row * p.y.ld + n, inside, row::pack<KIND>(v));
     }
   }
 }

@@ -181,7 +181,7 @@ struct RowParams {
   row::View in[kPlaces], dx, dh;
   int at[kPlaces], sum_at[kVectors];  // of their words in shared memory, in bytes; -1: absent, or no room
   int sum_slots, sum_first;
-  int rows_per_gate, gates;
+  int rows_per_gate, share, longer;  // a block's rows of a gate, or its gates: one more in the first `longer` blocks
   Split split;
   int N, threads;  // threads of a row
   int norm, post;
@@ -260,11 +260,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   int first, last;
   if (p.split.pieces > 0) {
     const int g = static_cast<int>(blockIdx.x) / p.split.pieces, j = static_cast<int>(blockIdx.x) - g * p.split.pieces;
-    first = g * p.rows_per_gate + static_cast<int>(static_cast<int64_t>(p.rows_per_gate) * j / p.split.pieces);
-    last = g * p.rows_per_gate + static_cast<int>(static_cast<int64_t>(p.rows_per_gate) * (j + 1) / p.split.pieces);
+    first = g * p.rows_per_gate + j * p.share + min(j, p.longer);
+    last = first + p.share + (j < p.longer ? 1 : 0);
   } else {
-    first = static_cast<int>(static_cast<int64_t>(p.gates) * blockIdx.x / p.split.ctas) * p.rows_per_gate;
-    last = static_cast<int>(static_cast<int64_t>(p.gates) * (blockIdx.x + 1) / p.split.ctas) * p.rows_per_gate;
+    const int j = static_cast<int>(blockIdx.x);
+    first = (j * p.share + min(j, p.longer)) * p.rows_per_gate;
+    last = first + (p.share + (j < p.longer ? 1 : 0)) * p.rows_per_gate;
   }
   // One gate's rows after another (one stretch of rows where a gate has several blocks).
   const int stretch = p.split.pieces > 0 ? last - first : p.rows_per_gate;
@@ -589,13 +590,16 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
       wide = wide && row::whole_words(p.in[i], t.N);
     }
     p.sum_slots = slots;
-    p.rows_per_gate = static_cast<int>(t.M / t.gates), p.gates = static_cast<int>(t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
     if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.words = 0;
   }
   if (plan.words > 0) {
     p.split = split = split_of(t.M, t.gates, plan.block <= 512 && smem <= 112 * 1024 ? kMostCtas : kSms);
+    const int parts = split.pieces > 0 ? split.pieces : split.ctas;
+    const int whole = split.pieces > 0 ? p.rows_per_gate : static_cast<int>(t.gates);
+    p.share = whole / parts, p.longer = whole % parts;
     e = wide ? run_rows<KIND, true>(p, plan, smem, stream) : run_rows<KIND, false>(p, plan, smem, stream);
   } else {
     BackwardParams b;

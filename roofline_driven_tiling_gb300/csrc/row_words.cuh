@@ -76,34 +76,41 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at) {
 // in shared memory, from where arrived() takes them after wait_copies(). WIDE: every row starts on a 16-byte boundary
 // and holds whole words: one place. Otherwise the two aligned words around them come to `to` and `to` + `next`, as far as
 // the matrix reaches.
+// What is not WIDE is not inlined here and below: the norm kernels fetch, read and write words at many places, and with the
+// code for odd alignments at each of them they were up to 130 KB long and bound by fetching it.
+static __device__ __noinline__ void fetch_part(uint32_t to, uint32_t next, const uint16_t* begin, const uint16_t* end,
+                                               const uint16_t* p, int left) {
+  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
+  const uint16_t* from = p - o;
+  if (from >= begin) {
+    copy_async(to, from, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from))));
+  } else {  // the first word of the matrix
+    for (int i = 0; i < n && o + i < kWord; ++i)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * static_cast<uint32_t>(o + i)), "h"(p[i]) : "memory");
+  }
+  if (o + n > kWord) copy_async(to + next, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from - kWord))));
+}
 template <bool WIDE>
 __device__ __forceinline__ void fetch_word(uint32_t to, uint32_t next, const View& v, const uint16_t* p, int left) {
   if (left <= 0) return;
   if (WIDE) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-    return;
+  } else {
+    fetch_part(to, next, v.p, v.end, p, left);
   }
-  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
-  const uint16_t* from = p - o;
-  if (from >= v.p) {
-    copy_async(to, from, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from))));
-  } else {  // the first word of the matrix
-    for (int i = 0; i < n && o + i < kWord; ++i)
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * static_cast<uint32_t>(o + i)), "h"(p[i]) : "memory");
-  }
-  if (o + n > kWord) copy_async(to + next, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (v.end - from - kWord))));
 }
 // The values that fetch_word(to, next, v, p, left) brought, zeros beyond the row's end.
+static __device__ __noinline__ uint4 arrived_part(uint32_t to, uint32_t next, int o, int left) {
+  return first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
+}
 template <bool WIDE>
 __device__ __forceinline__ uint4 arrived(uint32_t to, uint32_t next, const uint16_t* p, int left) {
   if (left <= 0) return make_uint4(0, 0, 0, 0);
   if (WIDE) return load_shared(to);
-  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
-  return first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
+  return arrived_part(to, next, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
 }
 
-// The same at once, where there is no place for it. Not inlined: a kernel reads and writes words at many places, and with
-// the code for odd alignments at each of them the norm kernels were up to 130 KB long and bound by fetching it.
+// The same at once, where there is no place for it.
 static __device__ __noinline__ uint4 load_part(const uint16_t* p, int left, const uint16_t* begin, const uint16_t* end) {
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
   const uint16_t* from = p - o;
@@ -127,6 +134,33 @@ __device__ __forceinline__ uint4 load_word(const View& v, const uint16_t* p, int
   if (WIDE || (v.wide && left >= kWord)) return *reinterpret_cast<const uint4*>(p);
   return load_part(p, left, v.p, v.end);
 }
+
+// The same in two steps, so that several words' loads are on their way before the first is put together.
+template <bool WIDE>
+struct RawWord {
+  uint4 a, b;
+  __device__ __forceinline__ static bool whole(const View& v, const uint16_t* p, int left, int o) {
+    return p - o >= v.p && p - o + (o + min(left, kWord) > kWord ? 16 : 8) <= v.end;
+  }
+  __device__ __forceinline__ void load(const View& v, const uint16_t* p, int left) {
+    a = b = make_uint4(0, 0, 0, 0);
+    if (left <= 0) return;
+    if (WIDE) {
+      a = *reinterpret_cast<const uint4*>(p);
+      return;
+    }
+    const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+    if (!whole(v, p, left, o)) return;
+    a = reinterpret_cast<const uint4*>(p - o)[0];
+    if (o + min(left, kWord) > kWord) b = reinterpret_cast<const uint4*>(p - o)[1];
+  }
+  __device__ __forceinline__ uint4 get(const View& v, const uint16_t* p, int left) const {
+    if (WIDE || left <= 0) return a;
+    const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+    if (!whole(v, p, left, o)) return load_part(p, left, v.p, v.end);
+    return first_of(o == 0 ? a : shifted(a, b, o), left);
+  }
+};
 
 __device__ __forceinline__ void store_values(uint16_t* p, int first, int last, const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -120,6 +120,12 @@ def quantize_fp8(x, dtype=torch.float8_e4m3fn, along="rows", square=False, out=N
     return tuple(got)
 
 
+def _check_scale(t, name, index):
+    if not isinstance(t, _Tensor) or t.dtype is not torch.float32 or t.get_device() < 0:
+        raise TypeError("%s must be a float32 CUDA tensor" % name)
+    _on_device(t, name, index)
+
+
 def gemm_fp8(a, a_scale, b, b_scale, dtype=torch.bfloat16, out=None, stream=None):
     """The product of 8-bit a (M x K) and b (K x N) with their scales, in ``dtype`` (bfloat16,
     float16 or float32); each operand is float8_e4m3fn or float8_e5m2."""
@@ -147,14 +153,12 @@ def gemm_fp8(a, a_scale, b, b_scale, dtype=torch.bfloat16, out=None, stream=None
     if (ap | bp | lda | ldb) & 15 and M and N and K:
         raise ValueError("rows of a and of b.t() must start on 16-byte boundaries")
     blocks = (K + 127) // 128
-    for t, name, shape in ((a_scale, "a_scale", (M, blocks)), (b_scale, "b_scale", None)):
-        if not isinstance(t, _Tensor) or t.dtype is not torch.float32 or not t.is_cuda:
-            raise TypeError("%s must be a float32 CUDA tensor" % name)
-        _on_device(t, name, index)
-        if shape is not None and tuple(t.shape) != shape:
-            raise ValueError("%s must be %d x %d, got %s" % (name, *shape, tuple(t.shape)))
-    group = 1 if tuple(b_scale.shape) == (blocks, N) else 128
-    if group == 128 and tuple(b_scale.shape) != (blocks, (N + 127) // 128):
+    _check_scale(a_scale, "a_scale", index)
+    if a_scale.shape != (M, blocks):
+        raise ValueError("a_scale must be %d x %d, got %s" % (M, blocks, tuple(a_scale.shape)))
+    _check_scale(b_scale, "b_scale", index)
+    group = 1 if b_scale.shape == (blocks, N) else 128
+    if group == 128 and b_scale.shape != (blocks, (N + 127) // 128):
         raise ValueError("b_scale must be %d x %d or %d x %d, got %s" % (
             blocks, N, blocks, (N + 127) // 128, tuple(b_scale.shape)))
     if _grad_enabled() and (a_scale.requires_grad or b_scale.requires_grad):

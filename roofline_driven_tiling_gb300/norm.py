@@ -24,6 +24,7 @@ gradients are off (``torch.no_grad()``); the gradients are the backward function
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
@@ -51,8 +52,22 @@ class ResidualNormGradients(NamedTuple):
 def _function(name, dtype):
     f = _FUNCTIONS.get((name, dtype))
     if f is None:
-        f = _FUNCTIONS[name, dtype] = getattr(binding.lib(), name + _SUFFIX[dtype])
+        full = name + _SUFFIX[dtype]
+        f = binding.lib()[full]
+        # All arguments but the two floats are integers, which convert quickest as pointers.
+        f.argtypes = [t if t is ctypes.c_float else ctypes.c_void_p for t in binding.SIGNATURES[full][0]]
+        f.restype = ctypes.c_int
+        _FUNCTIONS[name, dtype] = f
     return f
+
+
+_workspace_size = None
+
+
+def _function_of_size():
+    global _workspace_size
+    _workspace_size = binding.lib().t2s_residual_norm_backward_workspace_size
+    return _workspace_size
 
 
 def _norm(kind, name):
@@ -71,6 +86,8 @@ def _dropped(p):
 
 def _seed(seed, index):
     """The address of a seed in device memory and its value: one of the two."""
+    if type(seed) is int and -2 ** 63 <= seed < 2 ** 63:
+        return None, seed
     if isinstance(seed, _Tensor):
         if seed.dtype is not torch.int64 or not seed.is_cuda:
             raise TypeError("seed must be a number or a one-element int64 CUDA tensor")
@@ -84,6 +101,8 @@ def _seed(seed, index):
 
 def _int64(v, name):
     """v modulo 2^64 as a signed number."""
+    if type(v) is int and -2 ** 63 <= v < 2 ** 63:
+        return v
     if not isinstance(v, int):
         raise TypeError("%s must be an integer" % name)
     v &= 2 ** 64 - 1
@@ -100,10 +119,6 @@ def _gate(gate, dtype, index, M, N):
             raise ValueError("gate must have rows for equal numbers of the %d rows, got %s" % (M, tuple(gate.shape)))
         return (*_matrix(gate, "gate", dtype, index, (rows, N)), rows)
     return _vector(gate, "gate", dtype, index, N), N, 1
-
-
-def _optional(t, name, dtype, index, n):
-    return None if t is None else _vector(t, name, dtype, index, n)
 
 
 def _check(h, norm, weight, bias, gate, scale, post, post_weight, post_bias, p):
@@ -126,9 +141,10 @@ def residual_norm(x, h=None, weight=None, bias=None, gate=None, scale=1.0, norm=
     _check(h, code, weight, bias, gate, scale, post, post_weight, post_bias, p)
     hp, ldh = (None, N) if h is None else _matrix(h, "h", dtype, index, (M, N))
     gp, ldg, gates = _gate(gate, dtype, index, M, N)
-    wp, bp = _optional(weight, "weight", dtype, index, N), _optional(bias, "bias", dtype, index, N)
-    pw = _optional(post_weight, "post_weight", dtype, index, N)
-    pb = _optional(post_bias, "post_bias", dtype, index, N)
+    wp = None if weight is None else _vector(weight, "weight", dtype, index, N)
+    bp = None if bias is None else _vector(bias, "bias", dtype, index, N)
+    pw = None if post_weight is None else _vector(post_weight, "post_weight", dtype, index, N)
+    pb = None if post_bias is None else _vector(post_bias, "post_bias", dtype, index, N)
     if _grad_enabled():
         for t in (x, h, weight, bias, gate, post_weight, post_bias):
             if t is not None and t.requires_grad:
@@ -179,29 +195,31 @@ def residual_norm_backward(dy, dr, r, h=None, weight=None, bias=None, gate=None,
     drp, lddr = (None, N) if dr is None else _matrix(dr, "dr", dtype, index, (M, N))
     hp, ldh = (None, N) if h is None else _matrix(h, "h", dtype, index, (M, N))
     gp, ldg, gates = _gate(gate, dtype, index, M, N)
-    wp = _optional(weight, "weight", dtype, index, N)
-    _optional(bias, "bias", dtype, index, N)
-    pw = _optional(post_weight, "post_weight", dtype, index, N)
-    pb = _optional(post_bias, "post_bias", dtype, index, N)
+    wp = None if weight is None else _vector(weight, "weight", dtype, index, N)
+    if bias is not None:
+        _vector(bias, "bias", dtype, index, N)
+    pw = None if post_weight is None else _vector(post_weight, "post_weight", dtype, index, N)
+    pb = None if post_bias is None else _vector(post_bias, "post_bias", dtype, index, N)
     dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, N), stream)
     dh, dhp, lddh = (False, None, N) if h is None else _output(dh, "dh", dtype, device, (M, N), stream)
     # The parameters' gradients side by side in one allocation, each on a 16-byte boundary.
     wide = N + 7 & -8
-    rows = [t is not None for t in (weight, bias, post_weight, post_bias)] + [gates if gate is not None else 0]
-    grads, ptrs, ldgate = [None] * 5, [None] * 5, N
-    if any(rows):
-        room = _new((sum(rows), wide), (wide, 1), dtype, device, stream)
-        first = 0
-        for i, n in enumerate(rows):
-            if n:
-                part = room[first:first + n, :N]
-                grads[i] = part if i == 4 and gate.dim() == 2 else part[0]
-                ptrs[i] = part.data_ptr()
-                first += n
-        ldgate = wide
-    vectors = sum(1 for n in rows if n)
+    present = (weight is not None, bias is not None, post_weight is not None, post_bias is not None)
+    vectors, grads, ptrs, ldgate = sum(present), [None] * 5, [None] * 5, N
+    rows = vectors + (gates if gate is not None else 0)
+    if rows:
+        room = _new((rows, N), (wide, 1), dtype, device, stream)
+        first, parts = room.data_ptr(), room[:vectors].unbind(0) if vectors else ()
+        i = 0
+        for j in range(4):
+            if present[j]:
+                grads[j], ptrs[j] = parts[i], first + 2 * wide * i
+                i += 1
+        if gate is not None:
+            grads[4], ptrs[4], ldgate = room[vectors] if gate.dim() == 1 else room[vectors:], first + 2 * wide * vectors, wide
+            vectors += 1
     need = 0 if workspace is not None or not vectors or not M else (
-        binding.t2s_residual_norm_backward_workspace_size(M, N, gates, vectors))
+        _workspace_size or _function_of_size())(M, N, gates, vectors)
     keep, ws, size = _workspace(workspace, need, device, stream)
     at, seed = _seed(seed, index)
     f = _FUNCTIONS.get(("t2s_residual_norm_backward", dtype)) or _function("t2s_residual_norm_backward", dtype)
