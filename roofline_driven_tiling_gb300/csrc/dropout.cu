@@ -12,7 +12,6 @@ namespace norm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // rows of a thread that are on their way at once
 
 struct DropoutParams {
   row::View x, r, y;
@@ -21,15 +20,15 @@ struct DropoutParams {
   Dropout drop;
 };
 
-// A block takes 256 / across rows of up to `across` words each, a thread the same words of kAhead rows at a time: so
+// A block takes 256 / across rows of up to `across` words each, a thread the same words of AHEAD rows at a time: so
 // the place in a row is found once, and the generator's counter only moves on.
-template <int KIND, bool WIDE>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
+template <int KIND, bool WIDE, int AHEAD>
+__global__ void __launch_bounds__(kThreads, WIDE ? 4 : 2) dropout_kernel(const __grid_constant__ DropoutParams p) {
   ff::wait_for_earlier_kernels();
   const int down = static_cast<int>(threadIdx.x) / p.across;
   const int n = (static_cast<int>(blockIdx.x) * p.across + static_cast<int>(threadIdx.x) - down * p.across) * row::kWord;
   const int left = p.N - n;
-  const int64_t at_once = p.step / kAhead;
+  const int64_t at_once = p.step / AHEAD;
   int64_t m = static_cast<int64_t>(blockIdx.y) * (kThreads / p.across) + down;
   const uint64_t groups = static_cast<uint64_t>((static_cast<int64_t>(p.N) + 3) / 4);
   const uint64_t key = drop_key(p.drop);
@@ -37,16 +36,16 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
   // Every lane of a warp stays for the stores' shuffles as long as one of its rows is left.
   const int64_t first_of_warp = __shfl_sync(0xffffffffu, m, 0);
   for (int64_t ahead = first_of_warp; ahead < p.M; ahead += p.step, m += p.step) {
-    row::RawWord<WIDE> x[kAhead], r[kAhead];
+    row::RawWord<WIDE> x[AHEAD], r[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const int64_t row = m + i * at_once;
       const int inside = row < p.M ? left : 0;
       x[i].load(p.x, p.x.p + row * p.x.ld + n, inside);
       if (residual) r[i].load(p.r, p.r.p + row * p.r.ld + n, inside);
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       const int64_t row = m + i * at_once;
       const int inside = row < p.M ? left : 0;
       uint64_t v[4];
@@ -78,14 +77,19 @@ cudaError_t run(const DropoutTask& t, cudaStream_t stream) {
   p.across = wide ? 1 : 32;
   while (p.across < words && p.across < kThreads) p.across *= 2;
   const int64_t columns = (words + p.across - 1) / p.across, rows = kThreads / p.across;
-  const int64_t blocks = (t.M + rows * kAhead - 1) / (rows * kAhead);
+  // Four rows of a thread at a time, or one where that leaves SMs without a block.
+  const int ahead = columns * ((t.M + rows * 4 - 1) / (rows * 4)) < 2 * 152 ? 1 : 4;
+  const int64_t blocks = (t.M + rows * ahead - 1) / (rows * ahead);
   int64_t most = 152 * 8 / columns;
   if (most < 1) most = 1;
   const int64_t grid = blocks < most ? blocks : most;
-  p.step = grid * rows * kAhead;
+  p.step = grid * rows * ahead;
   const ff::LaunchShape shape{dim3(static_cast<unsigned>(columns), static_cast<unsigned>(grid)), kThreads, 1, 0};
-  return wide ? ff::launch_early(stream, shape, dropout_kernel<KIND, true>, p)
-              : ff::launch_early(stream, shape, dropout_kernel<KIND, false>, p);
+  if (ahead == 1)
+    return wide ? ff::launch_early(stream, shape, dropout_kernel<KIND, true, 1>, p)
+                : ff::launch_early(stream, shape, dropout_kernel<KIND, false, 1>, p);
+  return wide ? ff::launch_early(stream, shape, dropout_kernel<KIND, true, 4>, p)
+              : ff::launch_early(stream, shape, dropout_kernel<KIND, false, 4>, p);
 }
 
 }  // namespace

@@ -212,22 +212,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
     for (int c = 0; c < C; ++c)
       row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left_of(c));
   };
-  auto get = [&](int place, const uint16_t* from, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left_of(c)), f);
+  auto settle = [&](int place, const uint16_t* from) {
+    if (WIDE || p.at[place] < 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left_of(c));
+  };
+  auto get = [&](int place, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left_of(c)), f);
   };
   // A parameter's words, in shared memory, or read again for each row where that is full.
   int gate_row = 0;
   auto parameter = [&](int place, int c, uint64_t(&f)[4]) {
-    const uint16_t* from = p.in[place].row(place == kG ? gate_row : 0, first_byte);
     if (p.at[place] >= 0) {
-      get(place, from, c, f);
+      get(place, c, f);
     } else {
+      const uint16_t* from = p.in[place].row(place == kG ? gate_row : 0, first_byte);
       row::unpack<KIND>(row::load_word<WIDE>(p.in[place], from + c * stride, left_of(c)), f);
     }
   };
   fetch(kW, p.in[kW].row(0, first_byte));
   fetch(kPw, p.in[kPw].row(0, first_byte));
   fetch(kPb, p.in[kPb].row(0, first_byte));
+  bool settled = WIDE;  // the parameters, once their first words are there
   const uint32_t groups = (static_cast<uint32_t>(n) + 3u) / 4u;
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
@@ -273,6 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
     const int end = m0 + stretch;
     gate_row = m0 / p.rows_per_gate;
     fetch(kG, p.in[kG].row(gate_row, first_byte));
+    bool gate_fresh = true;
     int m = m0 + group.index;
     if (m < end)
 #pragma unroll 1
@@ -281,13 +288,26 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
       auto fetch_next = [&](int i) {
         if (m + rows_at_once < end) fetch(i, p.in[i].row(m + rows_at_once, first_byte));
       };
-      auto get_row = [&](int i, int c, uint64_t(&f)[4]) { get(i, p.in[i].row(m, first_byte), c, f); };
       row::wait_copies();
+      if (!WIDE) {
+        if (!settled) {
+          settled = true;
+          settle(kW, p.in[kW].row(0, first_byte));
+          settle(kPw, p.in[kPw].row(0, first_byte));
+          settle(kPb, p.in[kPb].row(0, first_byte));
+        }
+        if (gate_fresh) {
+          gate_fresh = false;
+          settle(kG, p.in[kG].row(gate_row, first_byte));
+        }
+#pragma unroll 1
+        for (int i = kR; i <= kH; ++i) settle(i, p.in[i].row(m, first_byte));
+      }
       uint64_t xh[C][4], hh[C][4], d[C][4];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (has_norm) get_row(kR, c, xh[c]);
-        if (has_h) get_row(kH, c, hh[c]);
+        if (has_norm) get(kR, c, xh[c]);
+        if (has_h) get(kH, c, hh[c]);
       }
       fetch_next(kR);
       fetch_next(kH);
@@ -320,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         for (int c = 0; c < C; ++c) {
           if (has_norm) {
             uint64_t g[4], w[4];
-            get_row(kDy, c, g);
+            get(kDy, c, g);
             if (p.in[kW].p != nullptr) {
               parameter(kW, c, w);
 #pragma unroll
@@ -352,13 +372,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         const int left = left_of(c);
         uint64_t f[4], w[4];
         if (p.at[kDr] >= 0) {
-          get_row(kDr, c, d[c]);
+          get(kDr, c, d[c]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[c][i] = 0;
         }
         if (has_norm) {
-          get_row(kDy, c, f);
+          get(kDy, c, f);
           add(kBias, c, f);
           uint64_t g[4];
 #pragma unroll

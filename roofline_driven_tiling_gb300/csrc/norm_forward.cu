@@ -114,8 +114,12 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
     for (int c = 0; c < C; ++c)
       row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left(c));
   };
-  auto get = [&](int place, const uint16_t* from, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left(c)), f);
+  auto settle = [&](int place, const uint16_t* from) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left(c));
+  };
+  auto get = [&](int place, int c, uint64_t(&f)[4]) {
+    row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left(c)), f);
   };
 
   uint64_t v[C][4];
@@ -146,12 +150,12 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], row::both(rstd));
     if (p.at[weight] >= 0) {
-      get(weight, p.in[weight].p + first, c, w);
+      get(weight, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], w[i]);
     }
     if (p.at[bias] >= 0) {
-      get(bias, p.in[bias].p + first, c, w);
+      get(bias, c, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[c][i] = row::add2(v[c][i], w[i]);
     }
@@ -169,12 +173,20 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
     fetch(kX, x);
     if (has_h) fetch(kH, h);
   }
+  if (!WIDE) {
+    row::wait_copies();
+#pragma unroll 1
+    for (int i = kPostWeight; i < kPlaces; ++i)
+      if (p.at[i] >= 0) settle(i, p.in[i].p + first);
+  }
   for (; m < p.M; m += p.step, x += p.x_step, h += p.h_step, r += p.r_step, y += p.y_step) {
     const bool more = m + p.step < p.M;
     row::wait_copies();
+    settle(kX, x);
     if (has_h) {
+      settle(kH, h);
 #pragma unroll
-      for (int c = 0; c < C; ++c) get(kH, h, c, v[c]);
+      for (int c = 0; c < C; ++c) get(kH, c, v[c]);
       if (more) fetch(kH, h + p.h_step);
       const float rstd = p.post != T2S_NORM_NONE ? scale_of(p.post) : 1.0f;
 #pragma unroll
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
         }
         if (p.in[kGate].p != nullptr) {
           if (p.at[kGate] >= 0) {
-            get(kGate, p.in[kGate].p + first, c, u);
+            get(kGate, c, u);
           } else {
             const uint16_t* gate = p.in[kGate].p + m / p.rows_per_gate * p.in[kGate].ld + first + c * stride;
             row::unpack<KIND>(row::load_word<WIDE>(p.in[kGate], gate, left(c)), u);
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[c][i] = row::mul2(v[c][i], u[i]);
         }
-        get(kX, x, c, u);
+        get(kX, c, u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] = row::fma2(u[i], row::both(p.scale), v[c][i]);
         // The norm that follows is of the rounded values.
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) get(kX, x, c, v[c]);
+      for (int c = 0; c < C; ++c) get(kX, c, v[c]);
     }
     if (more) fetch(kX, x + p.x_step);
     if (p.norm == T2S_NORM_NONE) continue;

@@ -73,7 +73,7 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at) {
 }
 
 // Eight values of v's row from p on, `left` (perhaps none) of them inside the row, on their way to this thread's places
-// in shared memory, from where arrived() takes them after wait_copies(). WIDE: every row starts on a 16-byte boundary
+// in shared memory, where settle() puts them together after wait_copies(). WIDE: every row starts on a 16-byte boundary
 // and holds whole words: one place. Otherwise the two aligned words around them come to `to` and `to` + `next`, as far as
 // the matrix reaches.
 // What is not WIDE is not inlined here and below: the norm kernels fetch, read and write words at many places, and with the
@@ -99,15 +99,18 @@ __device__ __forceinline__ void fetch_word(uint32_t to, uint32_t next, const Vie
     fetch_part(to, next, v.p, v.end, p, left);
   }
 }
-// The values that fetch_word(to, next, v, p, left) brought, zeros beyond the row's end.
-static __device__ __noinline__ uint4 arrived_part(uint32_t to, uint32_t next, int o, int left) {
-  return first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
+// After wait_copies(): puts the word that fetch_word(to, next, v, p, left) brought together at `to`, zeros beyond the row's
+// end, from where arrived() reads it as often as it is wanted.
+static __device__ __noinline__ void settle_part(uint32_t to, uint32_t next, int o, int left) {
+  const uint4 v = first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
+  st_shared_v4(to, v.x, v.y, v.z, v.w);
 }
 template <bool WIDE>
-__device__ __forceinline__ uint4 arrived(uint32_t to, uint32_t next, const uint16_t* p, int left) {
-  if (left <= 0) return make_uint4(0, 0, 0, 0);
-  if (WIDE) return load_shared(to);
-  return arrived_part(to, next, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
+__device__ __forceinline__ void settle(uint32_t to, uint32_t next, const uint16_t* p, int left) {
+  if (!WIDE && left > 0) settle_part(to, next, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
+}
+__device__ __forceinline__ uint4 arrived(uint32_t to, int left) {
+  return left > 0 ? load_shared(to) : make_uint4(0, 0, 0, 0);
 }
 
 // The same at once, where there is no place for it.
