@@ -195,27 +195,27 @@ template <int KIND, bool WIDE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
-  // In shared memory: from one of a thread's words to the next, and from a word's first place to its second (not WIDE).
-  constexpr uint32_t kPitch = THREADS * 16, kNext = C * kPitch;
+  // In shared memory, from one of a thread's words to the next: of the inputs, and of the sums (two places each).
+  constexpr uint32_t kPitch = THREADS / 32 * row::kWarpBytes<WIDE>, kSumPitch = THREADS * 16;
   row::Group group(p.threads, rooms);
   const int n = p.N, threads = static_cast<int>(blockDim.x), rows_at_once = threads / p.threads;
   const int first_column = group.rank * row::kWord, stride = p.threads * row::kWord;
   const uint32_t first_byte = 2u * static_cast<uint32_t>(first_column);
   auto left_of = [&](int c) { return n - first_column - c * stride; };
-  const uint32_t mine = smem_u32(words) + threadIdx.x * 16u;
+  const uint32_t mine = smem_u32(words) + row::place_of_thread<WIDE>(), my_sums = smem_u32(words) + threadIdx.x * 16u;
   // A sum's eight values are two places of 16 bytes.
-  for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(mine + p.sum_first + i * kPitch, 0u, 0u, 0u, 0u);
+  for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(my_sums + p.sum_first + i * kSumPitch, 0u, 0u, 0u, 0u);
   ff::wait_for_earlier_kernels();
   auto fetch = [&](int place, const uint16_t* from) {
     if (p.at[place] < 0) return;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left_of(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left_of(c));
   };
   auto settle = [&](int place, const uint16_t* from) {
     if (WIDE || p.at[place] < 0) return;
 #pragma unroll
-    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left_of(c));
+    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, from + c * stride, left_of(c));
   };
   auto get = [&](int place, int c, uint64_t(&f)[4]) {
     row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left_of(c)), f);
@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
 
   auto add = [&](int vector, int c, const uint64_t(&f)[4]) {
     if (p.sum_at[vector] < 0) return;
-    const uint32_t to = mine + p.sum_at[vector] + 2 * c * kPitch;
+    const uint32_t to = my_sums + p.sum_at[vector] + 2 * c * kSumPitch;
     uint64_t a, b;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      lds128_pairs(to + i * kPitch, a, b);
+      lds128_pairs(to + i * kSumPitch, a, b);
       a = row::add2(a, f[2 * i]), b = row::add2(b, f[2 * i + 1]);
-      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + i * kPitch), "l"(a), "l"(b) : "memory");
+      asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + i * kSumPitch), "l"(a), "l"(b) : "memory");
     }
   };
   // A sum's column i over the groups, which are cleared if `clear`.
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   __syncthreads();
   float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * n;
   for (int slot = 0; slot < p.sum_slots; ++slot)
-    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * static_cast<int>(kNext), i, false);
+    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * C * static_cast<int>(kSumPitch), i, false);
 }
 
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
@@ -545,7 +545,7 @@ constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
 // and sums alone do not fit.
 template <bool WIDE>
 bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
-  const int word = plan.words * plan.pitch() * 16, in_word = WIDE ? word : 2 * word;
+  const int word = plan.words * plan.pitch() * 16, in_word = plan.words * plan.pitch() / 32 * static_cast<int>(row::kWarpBytes<WIDE>);
   int ins = 0, all = 0;
   for (int i = 0; i < kPlaces; ++i) {
     const bool present = p->in[i].p != nullptr;

@@ -97,8 +97,7 @@ template <int KIND, bool WIDE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
-  // In shared memory: from one of a thread's words to the next, and from a word's first place to its second (not WIDE).
-  constexpr uint32_t kPitch = THREADS * 16, kNext = C * kPitch;
+  constexpr uint32_t kPitch = THREADS / 32 * row::kWarpBytes<WIDE>;  // in shared memory, from one of a thread's words to the next
   ff::wait_for_earlier_kernels();
   row::Group group(p.threads, rooms);
   const int n = p.N, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
@@ -108,15 +107,15 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   const bool has_h = p.in[kH].p != nullptr;
   const int first = group.rank * row::kWord, stride = p.threads * row::kWord;
   auto left = [&](int c) { return n - first - c * stride; };
-  const uint32_t mine = smem_u32(words) + threadIdx.x * 16u;
+  const uint32_t mine = smem_u32(words) + row::place_of_thread<WIDE>();
   auto fetch = [&](int place, const uint16_t* from) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, kNext, p.in[place], from + c * stride, left(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left(c));
   };
   auto settle = [&](int place, const uint16_t* from) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, kNext, from + c * stride, left(c));
+    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, from + c * stride, left(c));
   };
   auto get = [&](int place, int c, uint64_t(&f)[4]) {
     row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left(c)), f);
@@ -232,21 +231,28 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   }
 }
 
-constexpr int kSms = 152;
+constexpr int kSms = 152, kMostSmem = 226 * 1024;
 
 template <int KIND, bool WIDE, int C, int THREADS>
-cudaError_t launch_rows(RowParams& p, int blocks, int block, cudaStream_t stream) {
-  constexpr int kSlot = C * THREADS * (WIDE ? 16 : 32), kMost = kPlaces * kSlot;
-  static_assert(kMost <= 224 * 1024 || !WIDE, "shared memory of one CTA");
+cudaError_t launch_rows(RowParams& p, int block, cudaStream_t stream) {
+  constexpr int kSlot = C * (THREADS / 32) * static_cast<int>(row::kWarpBytes<WIDE>);
+  static_assert(kPlaces * kSlot <= kMostSmem, "shared memory of one CTA");
   int used = 0;
   for (int i = 0; i < kPlaces; ++i)
     if (p.at[i] >= 0) {
       p.at[i] = used;
       used += kSlot;
     }
-  cudaError_t e = prepare_smem<row_forward_kernel<KIND, WIDE, C, THREADS>>(kMost < 224 * 1024 ? kMost : 224 * 1024);
+  cudaError_t e = prepare_smem<row_forward_kernel<KIND, WIDE, C, THREADS>>(kPlaces * kSlot);
   if (e != cudaSuccess) return e;
-  return ff::launch_early(stream, {dim3(static_cast<unsigned>(blocks)), block, 1, used},
+  // As many blocks as the SMs hold, by registers and by shared memory.
+  const int by_smem = kMostSmem / (used + 2048), held = by_smem < blocks_of<C, THREADS>() ? by_smem : blocks_of<C, THREADS>();
+  const int64_t most = static_cast<int64_t>(kSms) * held;
+  const int64_t at_once = block / p.threads, blocks = (p.M + at_once - 1) / at_once;
+  const int grid = static_cast<int>(blocks < most ? blocks : most);
+  p.step = grid * at_once;
+  p.x_step = p.step * p.in[kX].ld, p.h_step = p.step * p.in[kH].ld, p.r_step = p.step * p.r.ld, p.y_step = p.step * p.y.ld;
+  return ff::launch_early(stream, {dim3(static_cast<unsigned>(grid)), block, 1, used},
                           row_forward_kernel<KIND, WIDE, C, THREADS>, p);
 }
 
@@ -265,13 +271,8 @@ cudaError_t run_rows(const ForwardTask& t, int threads, cudaStream_t stream) {
   wide = wide && row::whole_words(p.r, t.N) && row::whole_words(p.y, t.N);
   p.M = t.M, p.rows_per_gate = t.M / t.gates, p.N = static_cast<int>(t.N), p.threads = threads;
   p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
-  const int at_once = THREADS / threads;
-  const int64_t blocks = (t.M + at_once - 1) / at_once, most = kSms * blocks_of<C, THREADS>();
-  const int grid = static_cast<int>(blocks < most ? blocks : most);
-  p.step = static_cast<int64_t>(grid) * at_once;
-  p.x_step = p.step * p.in[kX].ld, p.h_step = p.step * p.in[kH].ld, p.r_step = p.step * p.r.ld, p.y_step = p.step * p.y.ld;
-  return wide ? launch_rows<KIND, true, C, THREADS>(p, grid, at_once * threads, stream)
-              : launch_rows<KIND, false, C, THREADS>(p, grid, at_once * threads, stream);
+  const int block = THREADS / threads * threads;
+  return wide ? launch_rows<KIND, true, C, THREADS>(p, block, stream) : launch_rows<KIND, false, C, THREADS>(p, block, stream);
 }
 
 // A row of up to 1024 values by one warp (no barriers), up to 8192 in two words a thread; longer ones in passes over

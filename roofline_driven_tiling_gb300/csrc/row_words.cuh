@@ -72,14 +72,23 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at) {
   return v;
 }
 
-// Eight values of v's row from p on, `left` (perhaps none) of them inside the row, on their way to this thread's places
-// in shared memory, where settle() puts them together after wait_copies(). WIDE: every row starts on a 16-byte boundary
-// and holds whole words: one place. Otherwise the two aligned words around them come to `to` and `to` + `next`, as far as
-// the matrix reaches.
+// A place in shared memory for a word of each thread: 16 bytes apart, and where words are not WIDE with room for one more
+// after each warp's.
+template <bool WIDE>
+constexpr uint32_t kWarpBytes = WIDE ? 512u : 528u;
+template <bool WIDE>
+__device__ __forceinline__ uint32_t place_of_thread() {
+  return threadIdx.x / 32 * kWarpBytes<WIDE> + threadIdx.x % 32 * 16u;
+}
+
+// Eight values of v's row from p on, `left` (perhaps none) of them inside the row, on their way to this thread's place in
+// shared memory, where settle() puts them together after wait_copies(). WIDE: every row starts on a 16-byte boundary and
+// holds whole words. Otherwise the lanes of a warp, which hold consecutive words of a row, bring the aligned words that
+// their first values lie in, and the last of them one more, as far as the matrix reaches.
 // What is not WIDE is not inlined here and below: the norm kernels fetch, read and write words at many places, and with the
 // code for odd alignments at each of them they were up to 130 KB long and bound by fetching it.
-static __device__ __noinline__ void fetch_part(uint32_t to, uint32_t next, const uint16_t* begin, const uint16_t* end,
-                                               const uint16_t* p, int left) {
+static __device__ __noinline__ void fetch_part(uint32_t to, const uint16_t* begin, const uint16_t* end, const uint16_t* p,
+                                               int left) {
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
   const uint16_t* from = p - o;
   if (from >= begin) {
@@ -88,26 +97,30 @@ static __device__ __noinline__ void fetch_part(uint32_t to, uint32_t next, const
     for (int i = 0; i < n && o + i < kWord; ++i)
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * static_cast<uint32_t>(o + i)), "h"(p[i]) : "memory");
   }
-  if (o + n > kWord) copy_async(to + next, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from - kWord))));
+  if (o + n > kWord && (threadIdx.x % 32 == 31 || left <= kWord))
+    copy_async(to + 16u, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from - kWord))));
 }
 template <bool WIDE>
-__device__ __forceinline__ void fetch_word(uint32_t to, uint32_t next, const View& v, const uint16_t* p, int left) {
+__device__ __forceinline__ void fetch_word(uint32_t to, const View& v, const uint16_t* p, int left) {
   if (left <= 0) return;
   if (WIDE) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
   } else {
-    fetch_part(to, next, v.p, v.end, p, left);
+    fetch_part(to, v.p, v.end, p, left);
   }
 }
-// After wait_copies(): puts the word that fetch_word(to, next, v, p, left) brought together at `to`, zeros beyond the row's
-// end, from where arrived() reads it as often as it is wanted.
-static __device__ __noinline__ void settle_part(uint32_t to, uint32_t next, int o, int left) {
-  const uint4 v = first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + next), o), left);
-  st_shared_v4(to, v.x, v.y, v.z, v.w);
+// After wait_copies(), by all lanes of a warp: puts the words that fetch_word(to, v, p, left) brought together at `to`,
+// zeros beyond the row's end, from where arrived() reads them as often as they are wanted.
+static __device__ __noinline__ void settle_part(uint32_t to, int o, int left) {
+  __syncwarp();  // the lanes' copies, for one another
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (left > 0) v = first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + 16u), o), left);
+  __syncwarp();
+  if (left > 0) st_shared_v4(to, v.x, v.y, v.z, v.w);
 }
 template <bool WIDE>
-__device__ __forceinline__ void settle(uint32_t to, uint32_t next, const uint16_t* p, int left) {
-  if (!WIDE && left > 0) settle_part(to, next, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
+__device__ __forceinline__ void settle(uint32_t to, const uint16_t* p, int left) {
+  if (!WIDE) settle_part(to, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
 }
 __device__ __forceinline__ uint4 arrived(uint32_t to, int left) {
   return left > 0 ? load_shared(to) : make_uint4(0, 0, 0, 0);
