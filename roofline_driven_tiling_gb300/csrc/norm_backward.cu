@@ -181,7 +181,7 @@ struct RowParams {
   row::View in[kPlaces], dx, dh;
   int at[kPlaces], sum_at[kVectors];  // of their words in shared memory, in bytes; -1: absent, or no room
   int sum_slots, sum_first;
-  int rows_per_gate, share, longer;  // a block's rows of a gate, or its gates: one more in the first `longer` blocks
+  int M, rows_per_gate, share, longer;  // a block's rows of a gate, or its gates: one more in the first `longer` blocks
   Split split;
   int N, threads;  // threads of a row
   int norm, post;
@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   // A sum's eight values are two places of 16 bytes.
   for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(my_sums + p.sum_first + i * kSumPitch, 0u, 0u, 0u, 0u);
   ff::wait_for_earlier_kernels();
-  auto fetch = [&](int place, const uint16_t* from) {
+  auto fetch = [&](int place, const uint16_t* from, bool inside) {
     if (p.at[place] < 0) return;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left_of(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left_of(c), inside);
   };
   auto settle = [&](int place, const uint16_t* from) {
     if (WIDE || p.at[place] < 0) return;
@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
       row::unpack<KIND>(row::load_word<WIDE>(p.in[place], from + c * stride, left_of(c)), f);
     }
   };
-  fetch(kW, p.in[kW].row(0, first_byte));
-  fetch(kPw, p.in[kPw].row(0, first_byte));
-  fetch(kPb, p.in[kPb].row(0, first_byte));
-  bool settled = WIDE;  // the parameters, once their first words are there
+  fetch(kW, p.in[kW].row(0, first_byte), false);
+  fetch(kPw, p.in[kPw].row(0, first_byte), false);
+  fetch(kPb, p.in[kPb].row(0, first_byte), false);
+  int fresh = kW;  // which parameters' words are new: all, the gate's (kG), none (kPlaces)
   const uint32_t groups = (static_cast<uint32_t>(n) + 3u) / 4u;
   const float inv_n = 1.0f / static_cast<float>(n);
   const uint64_t key = p.drop.dropped != 0 ? drop_key(p.drop) : 0;
@@ -278,30 +278,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   for (int m0 = first; m0 < last; m0 += stretch) {
     const int end = m0 + stretch;
     gate_row = m0 / p.rows_per_gate;
-    fetch(kG, p.in[kG].row(gate_row, first_byte));
-    bool gate_fresh = true;
+    fetch(kG, p.in[kG].row(gate_row, first_byte), false);
+    if (fresh == kPlaces) fresh = kG;
     int m = m0 + group.index;
     if (m < end)
 #pragma unroll 1
-      for (int i = kR; i <= kH; ++i) fetch(i, p.in[i].row(m, first_byte));
+      for (int i = kR; i <= kH; ++i) fetch(i, p.in[i].row(m, first_byte), false);
     for (; m < end; m += rows_at_once) {
       auto fetch_next = [&](int i) {
-        if (m + rows_at_once < end) fetch(i, p.in[i].row(m + rows_at_once, first_byte));
+        const int r = m + rows_at_once;
+        if (r < end) fetch(i, p.in[i].row(r, first_byte), r < p.M - 1);
       };
       row::wait_copies();
       if (!WIDE) {
-        if (!settled) {
-          settled = true;
-          settle(kW, p.in[kW].row(0, first_byte));
-          settle(kPw, p.in[kPw].row(0, first_byte));
-          settle(kPb, p.in[kPb].row(0, first_byte));
-        }
-        if (gate_fresh) {
-          gate_fresh = false;
-          settle(kG, p.in[kG].row(gate_row, first_byte));
-        }
+        // The row's words, and the parameters' when they are new.
 #pragma unroll 1
-        for (int i = kR; i <= kH; ++i) settle(i, p.in[i].row(m, first_byte));
+        for (int i = kR; i < (fresh < kPlaces ? kPlaces : kW); ++i)
+          if (i <= kH || i == kG || fresh == kW) settle(i, p.in[i].row(i <= kH ? m : i == kG ? gate_row : 0, first_byte));
+        fresh = kPlaces;
       }
       uint64_t xh[C][4], hh[C][4], d[C][4];
 #pragma unroll
@@ -610,7 +604,7 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
       wide = wide && row::whole_words(p.in[i], t.N);
     }
     p.sum_slots = slots;
-    p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.M = static_cast<int>(t.M), p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
     if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.words = 0;

@@ -108,10 +108,10 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   const int first = group.rank * row::kWord, stride = p.threads * row::kWord;
   auto left = [&](int c) { return n - first - c * stride; };
   const uint32_t mine = smem_u32(words) + row::place_of_thread<WIDE>();
-  auto fetch = [&](int place, const uint16_t* from) {
+  auto fetch = [&](int place, const uint16_t* from, bool inside) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left(c));
+      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left(c), inside);
   };
   auto settle = [&](int place, const uint16_t* from) {
 #pragma unroll
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   uint16_t* y = p.y.p + m * p.y.ld + first;
 #pragma unroll 1
   for (int i = kPostWeight; i < kPlaces; ++i)
-    if (p.at[i] >= 0) fetch(i, p.in[i].p + first);
+    if (p.at[i] >= 0) fetch(i, p.in[i].p + first, false);
   if (m < p.M) {
-    fetch(kX, x);
-    if (has_h) fetch(kH, h);
+    fetch(kX, x, false);
+    if (has_h) fetch(kH, h, false);
   }
   if (!WIDE) {
     row::wait_copies();
@@ -179,14 +179,14 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
       if (p.at[i] >= 0) settle(i, p.in[i].p + first);
   }
   for (; m < p.M; m += p.step, x += p.x_step, h += p.h_step, r += p.r_step, y += p.y_step) {
-    const bool more = m + p.step < p.M;
+    const bool more = m + p.step < p.M, inside = m + p.step < p.M - 1;  // the next row, not the last one
     row::wait_copies();
     settle(kX, x);
     if (has_h) {
       settle(kH, h);
 #pragma unroll
       for (int c = 0; c < C; ++c) get(kH, c, v[c]);
-      if (more) fetch(kH, h + p.h_step);
+      if (more) fetch(kH, h + p.h_step, inside);
       const float rstd = p.post != T2S_NORM_NONE ? scale_of(p.post) : 1.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
 #pragma unroll
       for (int c = 0; c < C; ++c) get(kX, c, v[c]);
     }
-    if (more) fetch(kX, x + p.x_step);
+    if (more) fetch(kX, x + p.x_step, inside);
     if (p.norm == T2S_NORM_NONE) continue;
     const float rstd = scale_of(p.norm);
 #pragma unroll

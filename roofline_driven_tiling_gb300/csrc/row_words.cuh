@@ -85,8 +85,9 @@ __device__ __forceinline__ uint32_t place_of_thread() {
 // shared memory, where settle() puts them together after wait_copies(). WIDE: every row starts on a 16-byte boundary and
 // holds whole words. Otherwise the lanes of a warp, which hold consecutive words of a row, bring the aligned words that
 // their first values lie in, and the last of them one more, as far as the matrix reaches.
-// What is not WIDE is not inlined here and below: the norm kernels fetch, read and write words at many places, and with the
-// code for odd alignments at each of them they were up to 130 KB long and bound by fetching it.
+// Rows next to the matrix's ends are brought with care for what lies outside; that code is not inlined (the norm kernels
+// fetch, read and write words at many places, and with the code for every case at each of them they were up to 130 KB long
+// and bound by fetching it).
 static __device__ __noinline__ void fetch_part(uint32_t to, const uint16_t* begin, const uint16_t* end, const uint16_t* p,
                                                int left) {
   const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, n = min(left, kWord);
@@ -100,27 +101,43 @@ static __device__ __noinline__ void fetch_part(uint32_t to, const uint16_t* begi
   if (o + n > kWord && (threadIdx.x % 32 == 31 || left <= kWord))
     copy_async(to + 16u, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from - kWord))));
 }
+// `inside`: a row with others before and after it.
 template <bool WIDE>
-__device__ __forceinline__ void fetch_word(uint32_t to, const View& v, const uint16_t* p, int left) {
+__device__ __forceinline__ void fetch_word(uint32_t to, const View& v, const uint16_t* p, int left, bool inside) {
   if (left <= 0) return;
-  if (WIDE) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-  } else {
-    fetch_part(to, v.p, v.end, p, left);
+  const char* from = reinterpret_cast<const char*>(p);
+  if (!WIDE) {
+    if (!inside) {
+      fetch_part(to, v.p, v.end, p, left);
+      return;
+    }
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    from -= off;
+    if ((threadIdx.x % 32 == 31 || left <= kWord) && static_cast<int>(off) + 2 * min(left, kWord) > 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16u), "l"(from + 16) : "memory");
   }
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 // After wait_copies(), by all lanes of a warp: puts the words that fetch_word(to, v, p, left) brought together at `to`,
 // zeros beyond the row's end, from where arrived() reads them as often as they are wanted.
-static __device__ __noinline__ void settle_part(uint32_t to, int o, int left) {
-  __syncwarp();  // the lanes' copies, for one another
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (left > 0) v = first_of(o == 0 ? load_shared(to) : shifted(load_shared(to), load_shared(to + 16u), o), left);
-  __syncwarp();
-  if (left > 0) st_shared_v4(to, v.x, v.y, v.z, v.w);
-}
 template <bool WIDE>
 __device__ __forceinline__ void settle(uint32_t to, const uint16_t* p, int left) {
-  if (!WIDE) settle_part(to, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1, left);
+  if (WIDE) return;
+  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;  // the same in a warp
+  if (o == 0) {
+    // Each lane's word lies in its place, which no other lane touches.
+    if (left < kWord && left > 0) {
+      const uint4 v = first_of(load_shared(to), left);
+      st_shared_v4(to, v.x, v.y, v.z, v.w);
+    }
+    return;
+  }
+  __syncwarp();  // the lanes' copies, for one another
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (left > 0) v = shifted(load_shared(to), load_shared(to + 16u), o);
+  if (left < kWord) v = first_of(v, left);
+  __syncwarp();
+  if (left > 0) st_shared_v4(to, v.x, v.y, v.z, v.w);
 }
 __device__ __forceinline__ uint4 arrived(uint32_t to, int left) {
   return left > 0 ? load_shared(to) : make_uint4(0, 0, 0, 0);
@@ -188,35 +205,32 @@ __device__ __forceinline__ void store_values(uint16_t* p, int first, int last, c
 // Stores a word of each lane of a converged warp (`left` <= 0: none), consecutive lanes holding consecutive words of
 // a row. Off 16-byte boundaries a lane writes the aligned word that its first values share with the lane before,
 // and the lanes at the ends write the rest value by value.
-static __device__ __noinline__ void store_part(uint16_t* p, int left, uint4 x) {
-  const int lane = threadIdx.x & 31, o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;
+static __device__ __noinline__ void store_some(uint16_t* p, int first, int last, uint4 x) { store_values(p, first, last, x); }
+template <bool WIDE>
+__device__ __forceinline__ void store_word(const View& v, uint16_t* p, int left, const uint4& x) {
+  if (WIDE) {
+    if (left > 0) *reinterpret_cast<uint4*>(p) = x;
+    return;
+  }
+  const int o = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) >> 1;  // the same in a warp
+  if (v.wide || o == 0) {
+    if (left >= kWord) {
+      *reinterpret_cast<uint4*>(p) = x;
+    } else if (left > 0) {
+      store_some(p, 0, left, x);
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31, head = kWord - o;  // this lane's values in the aligned word that holds p
   uint4 before;
   before.x = __shfl_up_sync(0xffffffffu, x.x, 1);
   before.y = __shfl_up_sync(0xffffffffu, x.y, 1);
   before.z = __shfl_up_sync(0xffffffffu, x.z, 1);
   before.w = __shfl_up_sync(0xffffffffu, x.w, 1);
-  if (left <= 0) return;
-  if (o == 0 && left >= kWord) {
-    *reinterpret_cast<uint4*>(p) = x;
-    return;
-  }
-  const int head = kWord - o;  // this lane's values in the aligned word that holds p
-  const bool whole = o > 0 && lane > 0 && left >= head;
+  const bool whole = lane > 0 && left >= head, next_whole = lane < 31 && left - kWord >= head;
   if (whole) *reinterpret_cast<uint4*>(p - o) = shifted(before, x, head);
-  const bool next_whole = o > 0 && lane < 31 && left - kWord >= head;
-  store_values(p, whole ? head : 0, next_whole ? head : min(left, kWord), x);
-}
-template <bool WIDE>
-__device__ __forceinline__ void store_word(const View& v, uint16_t* p, int left, const uint4& x) {
-  if (WIDE || v.wide) {
-    if (WIDE ? left > 0 : left >= kWord) {
-      *reinterpret_cast<uint4*>(p) = x;
-    } else if (!WIDE) {
-      store_values(p, 0, left, x);
-    }
-  } else {
-    store_part(p, left, x);
-  }
+  const int first = whole ? head : 0, last = next_whole ? head : min(left, kWord);
+  if (first < last) store_some(p, first, last, x);
 }
 
 // ------------------------------------------------------------------ words as packed FP32 pairs
