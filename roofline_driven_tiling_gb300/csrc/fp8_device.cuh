@@ -81,8 +81,33 @@ inline uint32_t instruction(int format_a, int format_b, int m, int n) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// The scale of row (or group) r and block b.
-__device__ __forceinline__ float scale_at(const Scales& s, int64_t r, int64_t b) { return s.p[r * s.row + b * s.block]; }
+// A warp's copies of COUNT scales (rows or groups first .. first + COUNT - 1 of a block, zeros from `limit` on) to `to` in the
+// background; `from` is that of row `first`. `wide`: rows are neighbours on 16-byte boundaries in every block.
+template <int COUNT>
+__device__ __forceinline__ void copy_scales(uint32_t to, const float* from, const Scales& s, bool wide, int first, int limit,
+                                            int lane) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < COUNT; i += 128) {
+      const int r = i + 4 * lane, left = limit - first - r;
+      if (r < COUNT)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to + 4u * r), "l"(left > 0 ? from + r : s.p),
+                     "r"(left >= 4 ? 16 : left > 0 ? 4 * left : 0)
+                     : "memory");
+    }
+  } else {
+    const float* at = from + lane * s.row;
+#pragma unroll
+    for (int i = 0; i < COUNT; i += 32, at += 32 * s.row) {
+      const int r = i + lane;
+      const bool in = first + r < limit;
+      if (r < COUNT) cp_async_4(to + 4u * r, in ? at : s.p, in ? 4u : 0u);
+    }
+  }
+}
+inline bool wide_scales(const Scales& s) {
+  return s.row == 1 && (reinterpret_cast<uintptr_t>(s.p) & 15u) == 0 && s.block % 4 == 0;
+}
 
 }  // namespace fp8
 }  // namespace t2s

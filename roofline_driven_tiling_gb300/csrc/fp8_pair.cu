@@ -36,9 +36,10 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kChunk = 32;            // accumulator columns that a warp takes at a time
 constexpr int kStagingBytes = 2048;   // of a warp: 32 rows of 64 bytes
-constexpr int kScaleBlocks = 4;       // blocks whose scales come to shared memory together, side by side for each row
+constexpr int kScaleBlocks = 4;       // blocks whose scales come to shared memory together
 constexpr int kScaleSlots = 2;
-constexpr int kScaleBytes = (kRows + kMaxN) * kScaleBlocks * 4;
+constexpr int kBlockScales = (kRows + kMaxN) * 4;  // of one block: its rows', its columns'
+constexpr int kScaleBytes = kScaleBlocks * kBlockScales;
 constexpr int kMaxBuffers = 4;
 constexpr int kSmemBytes = kRingBytes + 1024 + 1024 + kEpiWarps * kStagingBytes + kScaleSlots * kScaleBytes;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
@@ -53,7 +54,7 @@ struct PairParams {
   void* C;
   int64_t ldc;
   int M, N, blocks, tiles_m, tiles_n;
-  int c_tma;
+  int c_tma, sa_wide, sb_wide;
   uint32_t idesc;
   unsigned* status;
 };
@@ -234,38 +235,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
       wait_counted(mma_done, 0u, status);
     } else if (warp == 3) {
       // Scales of this CTA's rows, and of the tile's columns: of each (VECTOR) or of each group of 128.
-      constexpr int kPerLane = kRows / 32, kColumns = VECTOR ? kBn : (kBn + kBlock - 1) / kBlock;
+      constexpr int kColumns = VECTOR ? kBn : (kBn + kBlock - 1) / kBlock;
+      const int columns = VECTOR ? p.N : (p.N + kBlock - 1) / kBlock;
       uint32_t use = 0;
       for (int t = tile0; ok && t < tiles; t += tile_step) {
         int m0, n0;
         tc::tile_origin(t, p.tiles_m, p.tiles_n, 2 * kRows, kBn, m0, n0);
-        const int m = m0 + rank * kRows + lane, n = VECTOR ? n0 + lane : (n0 + lane * kBlock) / kBlock;
-        const int columns = VECTOR ? p.N : (p.N + kBlock - 1) / kBlock;
-        const float* sa = p.sa.p + static_cast<int64_t>(m) * p.sa.row;
-        const float* sb = p.sb.p + static_cast<int64_t>(n) * p.sb.row;
+        m0 += rank * kRows;
+        if (!VECTOR) n0 /= kBlock;
+        const float* sa = p.sa.p + static_cast<int64_t>(m0) * p.sa.row;
+        const float* sb = p.sb.p + static_cast<int64_t>(n0) * p.sb.row;
 #pragma unroll 1
         for (int kb = 0; kb < blocks; kb += kScaleBlocks, ++use) {
-          const uint32_t slot_of = use % kScaleSlots, at = scales + slot_of * kScaleBytes;
+          const uint32_t slot_of = use % kScaleSlots;
           ok = __all_sync(0xffffffffu, wait_counted(scale_empty + 8u * slot_of, ((use / kScaleSlots) & 1u) ^ 1u, status));
           if (!ok) break;
-          const int count = min(kScaleBlocks, blocks - kb);
-          // Rows' scales lie four blocks side by side; columns' scales a block after another (VECTOR), or likewise.
+          uint32_t at = scales + slot_of * kScaleBytes;
 #pragma unroll 1
-          for (int j = 0; j < count; ++j) {
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-              const bool in = m + 32 * i < p.M;
-              cp_async_4(at + 16u * (lane + 32 * i) + 4u * j,
-                         in ? sa + 32 * i * p.sa.row + (kb + j) * p.sa.block : p.sa.p, in ? 4u : 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < (kColumns + 31) / 32; ++i) {
-              const int c = lane + 32 * i;
-              const bool in = c < kColumns && n + 32 * i < columns;
-              const uint32_t to = at + 16u * kRows + (VECTOR ? 4u * (j * kBn + c) : 16u * c + 4u * j);
-              if (c < kColumns)
-                cp_async_4(to, in ? sb + 32 * i * p.sb.row + (kb + j) * p.sb.block : p.sb.p, in ? 4u : 0u);
-            }
+          for (int j = kb; j < min(kb + kScaleBlocks, blocks); ++j, at += kBlockScales, sa += p.sa.block, sb += p.sb.block) {
+            copy_scales<kRows>(at, sa, p.sa, p.sa_wide, m0, p.M, lane);
+            copy_scales<kColumns>(at + 4u * kRows, sb, p.sb, VECTOR && p.sb_wide, n0, columns, lane);
           }
           cp_async_arrive_noinc(scale_full + 8u * slot_of);
         }
@@ -295,16 +284,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
         const uint32_t ss = scale_use % kScaleSlots, from = scales + ss * kScaleBytes;
         ok = __all_sync(0xffffffffu, wait_counted(scale_full + 8u * ss, (scale_use / kScaleSlots) & 1u, status));
         if (!ok) break;
-        // This lane's row's scales for the four blocks, times those of the warp's columns where they share them (the
-        // columns lie within one group of 128).
-        float4 a = lds128(from + 16u * (32 * q + lane));
-        if constexpr (!VECTOR) {
-          const float4 g = lds128(from + 16u * (kRows + half * kWarpN / kBlock));
-          a.x *= g.x, a.y *= g.y, a.z *= g.z, a.w *= g.w;
-        }
 #pragma unroll 1
         for (int j = 0; j < kScaleBlocks && kb + j < blocks; ++j, ++use) {
-          const uint32_t b = use % kBuffers;
+          // This lane's row's scale, times that of the warp's columns where they share one (they lie within one group of 128).
+          const uint32_t b = use % kBuffers, at = from + j * kBlockScales;
+          const uint32_t columns = at + 4u * (kRows + (VECTOR ? half * kWarpN : half * kWarpN / kBlock));
+          float a, g = 1.0f;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(a) : "r"(at + 4u * (32 * q + lane)) : "memory");
+          if (!VECTOR) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g) : "r"(columns) : "memory");
           ok = __all_sync(0xffffffffu, wait_counted(empty(0) + 8u * slot_at, slot_phase, status));
           if (++slot_at == kStages) {
             slot_at = 0;
@@ -312,13 +299,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
           }
           if (!ok) break;
           tc::tc_fence_after();
-          const uint32_t acc = rows_at + b * kBn, columns = from + 16u * kRows + 4u * (j * kBn + half * kWarpN);
-          const uint64_t row = ff::both(a.x);
-          a.x = a.y, a.y = a.z, a.z = a.w;
+          const uint32_t acc = rows_at + b * kBn;
+          const uint64_t row = ff::both(VECTOR ? a : a * g);
 #pragma unroll
           for (int u = 0; u < CHUNKS; ++u) {
             uint32_t x[kChunk];
             ff::load_columns(acc + u * kChunk, x);
+            // The columns' scales come while the sums do.
+            uint64_t w[VECTOR ? kChunk / 2 : 1];
+            if constexpr (VECTOR) {
+#pragma unroll
+              for (int i = 0; i < kChunk / 2; i += 2) lds128_pairs(columns + 4u * (u * kChunk + 2 * i), w[i], w[i + 1]);
+            }
             ff::wait_columns(x);
             if (u + 1 == CHUNKS) {
               tc::tc_fence_before();
@@ -328,13 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
             uint64_t* to = sum[u];
             if constexpr (VECTOR) {
 #pragma unroll
-              for (int i = 0; i < kChunk / 2; i += 2) {
-                uint64_t lo, hi;
-                lds128_pairs(columns + 4u * (u * kChunk + 2 * i), lo, hi);
-                to[i] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), lo), row, to[i]);
-                to[i + 1] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i + 2]), __uint_as_float(x[2 * i + 3])), hi), row,
-                                     to[i + 1]);
-              }
+              for (int i = 0; i < kChunk / 2; ++i)
+                to[i] = ff::fma2(ff::mul2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), w[i]), row, to[i]);
             } else {
 #pragma unroll
               for (int i = 0; i < kChunk / 2; ++i)
@@ -413,7 +400,7 @@ cudaError_t launch(const ProductTask& t, cudaStream_t stream, unsigned* status) 
   if (e != cudaSuccess) return e;
   PairParams p;
   memset(&p, 0, sizeof(p));
-  p.sa = t.sa, p.sb = t.sb;
+  p.sa = t.sa, p.sb = t.sb, p.sa_wide = wide_scales(t.sa), p.sb_wide = wide_scales(t.sb);
   p.C = t.C, p.ldc = t.ldc;
   p.M = static_cast<int>(t.M), p.N = static_cast<int>(t.N);
   p.blocks = static_cast<int>(blocks_of(t.K));

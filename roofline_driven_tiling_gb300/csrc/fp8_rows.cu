@@ -41,7 +41,7 @@ struct RowsParams {
   void* C;
   int64_t ldc;
   int M, N, blocks, tiles_n, stages, splits;
-  int b_group;
+  int b_group, sa_wide, sb_wide;
   uint32_t idesc, stage_bytes;
   unsigned* status;
 };
@@ -52,7 +52,8 @@ struct Shape {
   static constexpr int kBuffers = TM <= 64 ? 4 : 2;
   static constexpr uint32_t kColumns = kBuffers * TM;  // of TMEM
   static constexpr int kStageBytes = kWeightBytes + TM * kBlock;
-  static constexpr int kScaleBytes = (kTileN + TM) * kScaleBlocks * 4;
+  static constexpr int kBlockScales = (kTileN + TM) * 4;  // of one block
+  static constexpr int kScaleBytes = kScaleBlocks * kBlockScales;
   static constexpr int kShareBytes = TM * kTileN * 4;  // the sums that are joined lie over the ring
 };
 
@@ -219,28 +220,25 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
     if (ff::elect_one()) tc::mma_commit<1>(done);
     __syncwarp();
   } else if (warp == 2) {
-    // Scales of the tile's rows of B (of each, or one for all 128), four blocks side by side, and of its rows of A, a block
-    // after another.
-    const int n_rows = p.b_group == 1 ? kTileN : 1;
+    // Scales of the tile's rows of B (of each, or one for all 128) and of its rows of A.
+    const bool each = p.b_group == 1;
+    const int first = each ? n0 : n0 / kBlock;
+    const float* sb = p.sb.p + first * p.sb.row + kb0 * p.sb.block;
+    const float* sa = p.sa.p + m0 * p.sa.row + kb0 * p.sa.block;
     uint32_t use = 0;
 #pragma unroll 1
     for (int kb = kb0; kb < kb1; kb += kScaleBlocks, ++use) {
-      const uint32_t at = scales + use % kScaleSlots * T::kScaleBytes;
+      uint32_t at = scales + use % kScaleSlots * T::kScaleBytes;
       ok = __all_sync(0xffffffffu, wait_counted(scale_empty + 8u * (use % kScaleSlots), (use / kScaleSlots & 1u) ^ 1u, status));
       if (!ok) break;
-      const int count = min(kScaleBlocks, kb1 - kb);
 #pragma unroll 1
-      for (int j = 0; j < count; ++j) {
-        for (int i = lane; i < n_rows; i += 32) {
-          const bool in = n0 + i < p.N;
-          const int64_t r = p.b_group == 1 ? n0 + i : n0 / kBlock;
-          cp_async_4(at + 16u * i + 4u * j, in ? p.sb.p + r * p.sb.row + (kb + j) * p.sb.block : p.sb.p, in ? 4u : 0u);
+      for (int j = kb; j < min(kb + kScaleBlocks, kb1); ++j, at += T::kBlockScales, sa += p.sa.block, sb += p.sb.block) {
+        if (each) {
+          copy_scales<kTileN>(at, sb, p.sb, p.sb_wide, first, p.N, lane);
+        } else {
+          copy_scales<1>(at, sb, p.sb, false, first, first + 1, lane);
         }
-        for (int i = lane; i < TM; i += 32) {
-          const bool in = m0 + i < p.M;
-          cp_async_4(at + 16u * kTileN + 4u * (j * TM + i),
-                     in ? p.sa.p + (m0 + static_cast<int64_t>(i)) * p.sa.row + (kb + j) * p.sa.block : p.sa.p, in ? 4u : 0u);
-        }
+        copy_scales<TM>(at + 4u * kTileN, sa, p.sa, p.sa_wide, m0, p.M, lane);
       }
       cp_async_arrive_noinc(scale_full + 8u * (use % kScaleSlots));
     }
@@ -254,16 +252,16 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
       const uint32_t ss = scale_use % kScaleSlots, at = scales + ss * T::kScaleBytes;
       ok = __all_sync(0xffffffffu, wait_counted(scale_full + 8u * ss, scale_use / kScaleSlots & 1u, status));
       if (!ok) break;
-      float4 w = lds128(at + (p.b_group == 1 ? 16u * (32 * q + lane) : 0u));
 #pragma unroll 1
       for (int j = 0; j < kScaleBlocks && kb + j < kb1; ++j, ++use) {
-        const uint32_t b = use % T::kBuffers, columns = at + 16u * kTileN + 4u * (j * TM);
+        const uint32_t b = use % T::kBuffers, of_rows = at + j * T::kBlockScales, columns = of_rows + 4u * kTileN;
+        float w;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(of_rows + (p.b_group == 1 ? 4u * (32 * q + lane) : 0u)) : "memory");
         ok = __all_sync(0xffffffffu, wait_counted(empty(s), phase, status));
         if (!ok) break;
         next();
         tc::tc_fence_after();
-        const uint64_t row = ff::both(w.x);
-        w.x = w.y, w.y = w.z, w.z = w.w;
+        const uint64_t row = ff::both(w);
 #pragma unroll
         for (int c = 0; c < TM; c += 16) {
           uint32_t x[16];
@@ -343,7 +341,7 @@ cudaError_t launch(const ProductTask& t, const RowsPlan& plan, cudaStream_t stre
   }
   RowsParams p;
   memset(&p, 0, sizeof(p));
-  p.sa = t.sa, p.sb = t.sb, p.b_group = t.b_group;
+  p.sa = t.sa, p.sb = t.sb, p.b_group = t.b_group, p.sa_wide = wide_scales(t.sa), p.sb_wide = wide_scales(t.sb);
   p.C = t.C, p.ldc = t.ldc;
   p.M = static_cast<int>(t.M), p.N = static_cast<int>(t.N);
   p.blocks = static_cast<int>(blocks_of(t.K));

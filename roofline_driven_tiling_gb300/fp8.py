@@ -55,10 +55,10 @@ def _on_device(t, name, index):
 
 
 def _new_quantized(rows, cols, group, dtype, device, stream):
-    """8-bit rows on 16-byte boundaries, and scales whose rows are neighbours."""
+    """8-bit rows on 16-byte boundaries, and scales whose rows are neighbours, each block's on one too."""
     ld, blocks, groups = cols + 15 & -16, (cols + 127) // 128, (rows + group - 1) // group
     q = _new((rows, cols), (ld, 1), dtype, device, stream)
-    return q, _new((groups, blocks), (1, max(groups, 1)), torch.float32, device, stream)
+    return q, _new((groups, blocks), (1, groups + 3 & -4), torch.float32, device, stream)
 
 
 def _given(out, name, shape, dtype, group, index):
