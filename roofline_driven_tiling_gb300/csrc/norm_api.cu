@@ -41,7 +41,8 @@ int forward(Kind kind, int64_t M, int64_t N, int norm, int post, const uint16_t*
   if (bad_shape(M, N, norm, post, gates, scale, eps) || bad_drop(dropped, seed_device)) return T2S_ERR_INVALID;
   if (norm == T2S_NORM_NONE && (weight != nullptr || bias != nullptr || Y != nullptr)) return T2S_ERR_INVALID;
   if (post == T2S_NORM_NONE && (post_weight != nullptr || post_bias != nullptr)) return T2S_ERR_INVALID;
-  if (H == nullptr && (post != T2S_NORM_NONE || gate != nullptr || dropped != 0 || scale != 1.0f || R != nullptr))
+  if (H == nullptr && M > 0 && N > 0 &&
+      (post != T2S_NORM_NONE || gate != nullptr || dropped != 0 || scale != 1.0f || R != nullptr))
     return T2S_ERR_INVALID;
   // R may be X itself: every value of X is read by the thread that then writes it.
   const bool in_place = R != nullptr && R == X;

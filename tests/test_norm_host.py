@@ -98,6 +98,15 @@ def test_forward_arguments(lib):
     assert _call(lib, "t2s_residual_norm", a, dict(M=0)) == OK == _call(lib, "t2s_residual_norm", a, dict(N=0))
 
 
+def test_matrices_without_values_have_no_address(lib):
+    a = dict(M=0, N=8, norm=1, post=1, X=None, ldx=8, H=None, ldh=8, weight=F + 8192, bias=None, pw=F + 12288, pb=None,
+             gate=F + 16384, ldgate=8, gates=1, scale=0.5, eps=1e-6, dropped=7, at=None, seed=1, sequence=0, R=None,
+             ldr=8, Y=None, ldy=8, stream=None)
+    nothing = dict(M=4, N=0, weight=None, pw=None, gate=None)
+    for kw in (dict(), dict(gates=5), dict(R=F), nothing, dict(M=0, N=0, norm=2)):
+        assert _call(lib, "t2s_residual_norm", a, kw) == OK, kw
+
+
 def test_backward_arguments(lib):
     a = dict(M=4, N=8, norm=1, post=1, dY=F, lddy=8, dR=F + 4096, lddr=8, R=F + 8192, ldr=8, H=F + 12288, ldh=8,
              weight=F + 16384, pw=F + 20480, pb=None, gate=F + 24576, ldgate=8, gates=2, scale=0.5, eps=1e-6, dropped=0,
