@@ -3,7 +3,7 @@
 //
 // A persistent launch takes tiles of 256 rows x 64, 128 or 256 columns, each by a cluster of two CTAs: each
 // stages its 128 rows of A and half of the rows of B, a block of 128 bytes of K per ring slot. A block's sums are
-// started afresh in one of the TMEM accumulators (two of 256 columns, four of 128, eight of 64), and eight warps
+// started afresh in one of the TMEM accumulators (two of 256 columns, four of 128 or 64), and eight warps
 // per CTA take them out, multiply them by the block's scales and add them to FP32 sums in their registers (128 a
 // thread for a 256-wide tile), while the other accumulators fill. A warp of its own brings the scales to shared
 // memory some blocks ahead: fetched by the sums' warps one block ahead, they held every block up for an L2 latency
@@ -442,16 +442,19 @@ cudaError_t launch_width(const ProductTask& t, int width, cudaStream_t stream, u
 
 }  // namespace
 
-// The tile width with the shortest rounds of all pairs of SMs: a block of 128 of K takes a pair 0.28, 0.32 or 0.5 us in
-// tiles of 64, 128 or 256 columns (with a scale for every column 0.30, 0.58, 0.9), a tile's end 1.5 us, a launch 4.
+// The tile width with the shortest rounds of all pairs of SMs: a block of 128 of K takes a pair 0.21, 0.27 or 0.40 us in
+// tiles of 64, 128 or 256 columns (with a scale for every column 0.28, 0.37, 0.62), a tile's end 0.3, 0.6 or 1.2 us, a
+// launch 3.2. Measured in the three widths: 256 x 4096 x 4096 (N last) 10.5, 12.2 and 16.8 us, 512 x 4096 x 4096 17.1, 12.7
+// and 16.9, 4096 x 4096 x 4096 99, 66 and 59.6.
 PairPlan plan_pair(const ProductTask& t, int pairs) {
   static constexpr int kWidths[] = {256, 128, 64};
-  static constexpr double kBlockTime[2][3] = {{0.5, 0.32, 0.28}, {0.9, 0.58, 0.30}};
+  static constexpr double kBlockTime[2][3] = {{0.40, 0.27, 0.21}, {0.62, 0.37, 0.28}};
+  static constexpr double kTileTime[3] = {1.2, 0.6, 0.3};
   PairPlan best;
   for (int i = 0; i < 3; ++i) {
     const int64_t tiles = (t.M + 2 * kRows - 1) / (2 * kRows) * ((t.N + kWidths[i] - 1) / kWidths[i]);
-    const double time = 4.0 + static_cast<double>((tiles + pairs - 1) / pairs) *
-                                  (static_cast<double>(blocks_of(t.K)) * kBlockTime[t.b_group == 1][i] + 1.5);
+    const double time = 3.2 + static_cast<double>((tiles + pairs - 1) / pairs) *
+                                  (static_cast<double>(blocks_of(t.K)) * kBlockTime[t.b_group == 1][i] + kTileTime[i]);
     if (best.width == 0 || time < best.cost) {
       best.width = kWidths[i];
       best.cost = time;

@@ -1,9 +1,9 @@
 // fp8_rows.cu -- products of 8-bit operands with a scale for each block of 128 of K, where the outputs are too few to
 // fill the SMs with the tiles of fp8_pair.cu: single tokens, small batches, small weights.
 //
-// The rows of B (a weight's outputs) lie along the tensor core's 128 rows and the rows of A along its columns (16 to
-// 128 of them), so one token costs one pass over the weight and no more. The sum over K is split over the CTAs of a
-// cluster (up to 8). Each takes its blocks' sums out of TMEM one after another (from two or four accumulators in turn),
+// The rows of B (a weight's outputs) lie along the tensor core's 128 rows and the rows of A along its columns (16, 32
+// or 64 of them), so one token costs one pass over the weight and no more. The sum over K is split over the CTAs of a
+// cluster (up to 8). Each takes its blocks' sums out of TMEM one after another (from four accumulators in turn),
 // multiplies them by both scales and adds them in registers, then leaves its share in shared memory, and after a
 // cluster barrier every CTA adds the shares of its part of the rows in rank order through distributed shared memory and
 // stores. One launch, no workspace, the same bits every time.
@@ -33,7 +33,7 @@ constexpr int kMaxSplits = 8;
 constexpr int kMaxStages = 12;
 constexpr int kScaleBlocks = 4;  // blocks whose scales come to shared memory together
 constexpr int kScaleSlots = 2;
-constexpr int kMaxBuffers = 4;
+constexpr int kBuffers = 4;  // accumulators
 
 struct RowsParams {
   CUtensorMap w, x;
@@ -49,7 +49,6 @@ struct RowsParams {
 // TM: rows of A in a tile.
 template <int TM>
 struct Shape {
-  static constexpr int kBuffers = TM <= 64 ? 4 : 2;
   static constexpr uint32_t kColumns = kBuffers * TM;  // of TMEM
   static constexpr int kStageBytes = kWeightBytes + TM * kBlock;
   static constexpr int kBlockScales = (kTileN + TM) * 4;  // of one block
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
   const uint32_t bars = base + ring_bytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
-  const uint32_t acc_empty = bars + 16u * kMaxStages, scale_full = acc_empty + 8u * kMaxBuffers;
+  const uint32_t acc_empty = bars + 16u * kMaxStages, scale_full = acc_empty + 8u * kBuffers;
   const uint32_t scale_empty = scale_full + 8u * kScaleSlots, done = scale_empty + 8u * kScaleSlots, slot = done + 8u;
   const uint32_t scales = bars + 512u;
   unsigned* const status = p.status;
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < T::kBuffers; ++b) mbar_init(acc_empty + 8u * b, kSumWarps);
+    for (int b = 0; b < kBuffers; ++b) mbar_init(acc_empty + 8u * b, kSumWarps);
     for (int s = 0; s < kScaleSlots; ++s) {
       mbar_init(scale_full + 8u * s, 32);
       mbar_init(scale_empty + 8u * s, kSumWarps);
@@ -206,10 +205,10 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
     uint32_t use = 0;
 #pragma unroll 1
     for (int kb = kb0; kb < kb1; ++kb, ++use) {
-      const uint32_t b = use % T::kBuffers, st = base + static_cast<uint32_t>(s) * T::kStageBytes;
+      const uint32_t b = use % kBuffers, st = base + static_cast<uint32_t>(s) * T::kStageBytes;
       const uint64_t dw = ff::with_address(form, st), dx = ff::with_address(form, st + kWeightBytes);
       ok = __all_sync(0xffffffffu, wait_counted(full(s), phase, status) &&
-                                       wait_counted(acc_empty + 8u * b, (use / T::kBuffers & 1u) ^ 1u, status));
+                                       wait_counted(acc_empty + 8u * b, (use / kBuffers & 1u) ^ 1u, status));
       if (!ok) break;
       tc::tc_fence_after();
       mma_block<1>(tmem + b * TM, dw, dx, p.idesc);
@@ -254,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(const __grid_constan
       if (!ok) break;
 #pragma unroll 1
       for (int j = 0; j < kScaleBlocks && kb + j < kb1; ++j, ++use) {
-        const uint32_t b = use % T::kBuffers, of_rows = at + j * T::kBlockScales, columns = of_rows + 4u * kTileN;
+        const uint32_t b = use % kBuffers, of_rows = at + j * T::kBlockScales, columns = of_rows + 4u * kTileN;
         float w;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(of_rows + (p.b_group == 1 ? 4u * (32 * q + lane) : 0u)) : "memory");
         ok = __all_sync(0xffffffffu, wait_counted(empty(s), phase, status));
@@ -363,7 +362,7 @@ cudaError_t launch(const ProductTask& t, const RowsPlan& plan, cudaStream_t stre
   int stages = budget / T::kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages > per_cta) stages = per_cta;
-  if (stages < T::kBuffers) stages = T::kBuffers;  // empty[s] says for one block at a time that its sums are there
+  if (stages < kBuffers) stages = kBuffers;  // empty[s] says for one block at a time that its sums are there
   p.stages = stages;
   int smem = stages * T::kStageBytes;
   if (smem < T::kShareBytes) smem = T::kShareBytes;
@@ -381,21 +380,22 @@ cudaError_t launch_rows(const ProductTask& t, const RowsPlan& plan, cudaStream_t
   switch (plan.rows) {
     case 16: return launch<TYPE, 16>(t, plan, stream, status);
     case 32: return launch<TYPE, 32>(t, plan, stream, status);
-    case 64: return launch<TYPE, 64>(t, plan, stream, status);
-    default: return launch<TYPE, 128>(t, plan, stream, status);
+    default: return launch<TYPE, 64>(t, plan, stream, status);
   }
 }
 
 }  // namespace
 
-// Expected time in microseconds: what a launch takes, a CTA's blocks (0.27, 0.30, 0.36 or 0.7 each in tiles of 16, 32, 64 or
-// 128 rows, measured) and the join, in as many waves as the CTAs need; all SMs together take in at most 14 TB/s.
+// Expected time in microseconds: what a launch takes, a CTA's blocks (0.27, 0.30 or 0.36 each in tiles of 16, 32 or 64
+// rows, measured) and the join, in as many waves as the CTAs need; all SMs together take in at most 14 TB/s. Against the
+// pairs' kernel: 64 x 4096 x 4096 8.4 us here and 10.3 there, 128 x 4096 x 4096 10.3 and 10.4, 256 x 4096 x 4096 14.5 and
+// 10.5.
 RowsPlan plan_rows(const ProductTask& t, int sms) {
   RowsPlan best;
   const int64_t blocks = blocks_of(t.K), tiles_n = (t.N + kTileN - 1) / kTileN;
-  for (const int rows : {16, 32, 64, 128}) {
+  for (const int rows : {16, 32, 64}) {
     const int64_t tiles = tiles_n * ((t.M + rows - 1) / rows);
-    const double block = rows == 16 ? 0.27 : rows == 32 ? 0.30 : rows == 64 ? 0.36 : 0.7;
+    const double block = rows == 16 ? 0.27 : rows == 32 ? 0.30 : 0.36;
     for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
       if (splits > 1 && blocks < 2 * splits) break;
       // SMs that clusters reach when a CTA fills an SM.
