@@ -205,6 +205,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   const uint32_t mine = smem_u32(words) + row::place_of_thread<WIDE>(), my_sums = smem_u32(words) + threadIdx.x * 16u;
   // A sum's eight values are two places of 16 bytes.
   for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(my_sums + p.sum_first + i * kSumPitch, 0u, 0u, 0u, 0u);
+#pragma unroll 1
+  for (int i = 0; i < kPlaces; ++i)
+    if (p.at[i] >= 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c) row::clear_place<WIDE>(mine + p.at[i] + c * kPitch, left_of(c));
   ff::wait_for_earlier_kernels();
   auto fetch = [&](int place, const uint16_t* from, bool inside) {
     if (p.at[place] < 0) return;
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
     for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, from + c * stride, left_of(c));
   };
   auto get = [&](int place, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left_of(c)), f);
+    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, left_of(c)), f);
   };
   // A parameter's words, in shared memory, or read again for each row where that is full.
   int gate_row = 0;
@@ -328,21 +333,26 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         }
       }
       float rho = 1.0f, sigma = 1.0f, mean_g = 0.0f, mean_gx = 0.0f;
+      // dy weight stays in registers, but for rows off boundaries, whose code has none to spare: there it is formed again
+      // (4096 x 4095 98 us, and 103 with what the compiler then kept in memory; 8192 x 2048 with dropout 55 us and 53).
+      constexpr bool kKeepG = WIDE;
+      uint64_t g[kKeepG ? C : 1][4];
       if (has_norm || has_post) {
         float s[4] = {};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           if (has_norm) {
-            uint64_t g[4], w[4];
-            get(kDy, c, g);
+            uint64_t w[4];
+            uint64_t(&gc)[4] = g[kKeepG ? c : 0];
+            get(kDy, c, gc);
             if (p.in[kW].p != nullptr) {
               parameter(kW, c, w);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) g[i] = row::mul2(g[i], w[i]);
+              for (int i = 0; i < 4; ++i) gc[i] = row::mul2(gc[i], w[i]);
             }
             s[0] += row::dot(xh[c], xh[c]);
-            s[1] += row::dot(g, xh[c]);
-            if (layer) s[2] += row::sum(g);
+            s[1] += row::dot(gc, xh[c]);
+            if (layer) s[2] += row::sum(gc);
           }
           if (has_post) s[3] += row::dot(hh[c], hh[c]);
         }
@@ -374,21 +384,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         if (has_norm) {
           get(kDy, c, f);
           add(kBias, c, f);
-          uint64_t g[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             xh[c][i] = row::mul2(xh[c][i], row::both(rho));
-            g[i] = row::mul2(f[i], xh[c][i]);
+            w[i] = row::mul2(f[i], xh[c][i]);
           }
-          add(kWeight, c, g);
-          if (p.in[kW].p != nullptr) {
-            parameter(kW, c, w);
+          add(kWeight, c, w);
+          uint64_t(&gc)[4] = g[kKeepG ? c : 0];
+          if (!kKeepG) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
+            for (int i = 0; i < 4; ++i) gc[i] = f[i];
+            if (p.in[kW].p != nullptr) {
+              parameter(kW, c, w);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) gc[i] = row::mul2(gc[i], w[i]);
+            }
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            f[i] = row::fma2(xh[c][i], row::both(-mean_gx), f[i]);
+            f[i] = row::fma2(xh[c][i], row::both(-mean_gx), gc[i]);
             if (layer) f[i] = row::add2(f[i], row::both(-mean_g));
             d[c][i] = row::fma2(f[i], row::both(rho), d[c][i]);
           }
@@ -401,8 +415,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         }
         if (has_h) {
           row::Keep keep;
-          if (p.drop.dropped != 0)
+          if (p.drop.dropped != 0) {
             keep.draw(key, static_cast<uint64_t>(static_cast<uint32_t>(m)) * groups + static_cast<uint32_t>(first_column + c * stride) / 4u, p.drop.dropped);
+            // The kept values' factor, for everything that follows.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], row::both(p.drop.factor));
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) hh[c][i] = row::mul2(hh[c][i], row::both(sigma));
           if (p.sum_at[kGate] >= 0) {
@@ -418,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
 #pragma unroll
               for (int i = 0; i < 4; ++i) f[i] = row::add2(f[i], w[i]);
             }
-            if (p.drop.dropped != 0) keep.apply(f, p.drop.factor);
+            if (p.drop.dropped != 0) keep.apply(f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], d[c][i]);
             add(kGate, c, f);
@@ -428,7 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
           }
-          if (p.drop.dropped != 0) keep.apply(d[c], p.drop.factor);
+          if (p.drop.dropped != 0) keep.apply(d[c]);
           if (has_post) {
             add(kPostBias, c, d[c]);
 #pragma unroll

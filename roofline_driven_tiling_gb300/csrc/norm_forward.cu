@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
     for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, from + c * stride, left(c));
   };
   auto get = [&](int place, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived(mine + p.at[place] + c * kPitch, left(c)), f);
+    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, left(c)), f);
   };
 
   uint64_t v[C][4];
@@ -165,6 +165,11 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
   const uint16_t* h = p.in[kH].p + m * p.in[kH].ld + first;
   uint16_t* r = p.r.p + m * p.r.ld + first;
   uint16_t* y = p.y.p + m * p.y.ld + first;
+#pragma unroll 1
+  for (int i = 0; i < kPlaces; ++i)
+    if (p.at[i] >= 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c) row::clear_place<WIDE>(mine + p.at[i] + c * kPitch, left(c));
 #pragma unroll 1
   for (int i = kPostWeight; i < kPlaces; ++i)
     if (p.at[i] >= 0) fetch(i, p.in[i].p + first, false);

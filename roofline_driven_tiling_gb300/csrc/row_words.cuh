@@ -139,8 +139,15 @@ __device__ __forceinline__ void settle(uint32_t to, const uint16_t* p, int left)
   __syncwarp();
   if (left > 0) st_shared_v4(to, v.x, v.y, v.z, v.w);
 }
+// WIDE: threads beyond the row's end have zeros in their places (clear_place(), before the first word is fetched), so that
+// nothing is asked at each read. Otherwise the copies of the lane before may lie there.
+template <bool WIDE>
 __device__ __forceinline__ uint4 arrived(uint32_t to, int left) {
-  return left > 0 ? load_shared(to) : make_uint4(0, 0, 0, 0);
+  return WIDE || left > 0 ? load_shared(to) : make_uint4(0, 0, 0, 0);
+}
+template <bool WIDE>
+__device__ __forceinline__ void clear_place(uint32_t to, int left) {
+  if (WIDE && left <= 0) st_shared_v4(to, 0u, 0u, 0u, 0u);
 }
 
 // The same at once, where there is no place for it.
@@ -299,13 +306,19 @@ struct Keep {
       }
     }
   }
-  // Kept values times `factor`, the others 0.
-  __device__ __forceinline__ void apply(uint64_t (&f)[4], float factor) const {
+  // Kept values, the others 0.
+  __device__ __forceinline__ void apply(uint64_t (&f)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 x = halves(mul2(f[i], both(factor)));
+      const float2 x = halves(f[i]);
       f[i] = pack2(__uint_as_float(__float_as_uint(x.x) & mask[2 * i]), __uint_as_float(__float_as_uint(x.y) & mask[2 * i + 1]));
     }
+  }
+  // The same times `factor`.
+  __device__ __forceinline__ void apply(uint64_t (&f)[4], float factor) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], both(factor));
+    apply(f);
   }
 };
 

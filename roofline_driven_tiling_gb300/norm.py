@@ -202,22 +202,20 @@ def residual_norm_backward(dy, dr, r, h=None, weight=None, bias=None, gate=None,
     pb = None if post_bias is None else _vector(post_bias, "post_bias", dtype, index, N)
     dx, dxp, lddx = _output(dx, "dx", dtype, device, (M, N), stream)
     dh, dhp, lddh = (False, None, N) if h is None else _output(dh, "dh", dtype, device, (M, N), stream)
-    # The parameters' gradients side by side in one allocation, each on a 16-byte boundary.
-    wide = N + 7 & -8
-    present = (weight is not None, bias is not None, post_weight is not None, post_bias is not None)
-    vectors, grads, ptrs, ldgate = sum(present), [None] * 5, [None] * 5, N
-    rows = vectors + (gates if gate is not None else 0)
-    if rows:
-        room = _new((rows, N), (wide, 1), dtype, device, stream)
-        first, parts = room.data_ptr(), room[:vectors].unbind(0) if vectors else ()
-        i = 0
-        for j in range(4):
-            if present[j]:
-                grads[j], ptrs[j] = parts[i], first + 2 * wide * i
-                i += 1
-        if gate is not None:
-            grads[4], ptrs[4], ldgate = room[vectors] if gate.dim() == 1 else room[vectors:], first + 2 * wide * vectors, wide
+    grads, ptrs, ldgate, vectors = [None] * 5, [None] * 5, N, 0
+    for j, t in enumerate((weight, bias, post_weight, post_bias)):
+        if t is not None:
+            grads[j] = t = _new((N,), (1,), dtype, device, stream)
+            ptrs[j] = t.data_ptr()
             vectors += 1
+    if gate is not None:
+        if gate.dim() == 1:
+            grads[4] = t = _new((N,), (1,), dtype, device, stream)
+        else:
+            ldgate = N + 7 & -8  # rows on 16-byte boundaries
+            grads[4] = t = _new((gates, N), (ldgate, 1), dtype, device, stream)
+        ptrs[4] = t.data_ptr()
+        vectors += 1
     need = 0 if workspace is not None or not vectors or not M else (
         _workspace_size or _function_of_size())(M, N, gates, vectors)
     keep, ws, size = _workspace(workspace, need, device, stream)
