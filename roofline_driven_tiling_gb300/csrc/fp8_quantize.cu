@@ -19,7 +19,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Magnitudes are compared as the integers of their bits, and 16-bit ones two to a register (after unpacking to FP32, one by
+// one, both ways over 4096 x 8192 took 34.2 us, rows 19.6).
+template <int TYPE>
+constexpr int kHeld = TYPE == kF32 ? 1 : 2;  // magnitudes in a register
+template <int TYPE>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (TYPE == kF32) {
+    return max(a, b);
+  } else {
+    return __vmaxs2(a, b);
+  }
+}
+// The FP32 bits of magnitude i of a register.
+template <int TYPE>
+__device__ __forceinline__ uint32_t magnitude(uint32_t held, int i) {
+  if constexpr (TYPE == kF32) {
+    return held;
+  } else if constexpr (TYPE == kBf16) {
+    return i ? held & 0xffff0000u : held << 16;
+  } else {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(held >> 16 * i & 0xffffu))));
+  }
+}
+// The larger halves of a and of b.
+template <int TYPE>
+__device__ __forceinline__ uint32_t both_largest(uint32_t a, uint32_t b) {
+  return larger<TYPE>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+}
 
 // A block's scale and 1 / scale from the bits of its largest magnitude.
 struct Scale {
@@ -47,10 +74,13 @@ __device__ __forceinline__ uint32_t pack_fp8x2(float lo, float hi) {
 }
 
 template <int FORMAT>
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], float inverse) {
+__device__ __forceinline__ uint2 pack8(const uint64_t (&v)[4], float inverse) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack_fp8x2<FORMAT>(v[2 * i] * inverse, v[2 * i + 1] * inverse);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = ff::halves(ff::mul2(v[i], ff::both(inverse)));
+    w[i] = pack_fp8x2<FORMAT>(f.x, f.y);
+  }
   return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
@@ -66,10 +96,45 @@ __device__ __forceinline__ void store8(uint8_t* p, int64_t left, bool wide, uint
 }
 
 // The largest over a half-warp's 16 lanes, in all of them.
+template <int TYPE>
 __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+  for (int d = 8; d > 0; d >>= 1) v = larger<TYPE>(v, __shfl_xor_sync(0xffffffffu, v, d));
   return v;
+}
+// From maxima of a lane's rows (kHeld to a register) to the scales of the half-warp's: a lane first gives away half of its
+// registers at a step, until it holds one, and only it turns that into scales, its rows' `value`s. In every lane v becomes
+// the inverses, as inverse_of() reads them (powers of two and NaN, whose upper 16 bits say all).
+template <int TYPE, int FORMAT, int W>
+__device__ __forceinline__ void half_warp_scales(uint32_t (&v)[W], float (&value)[kHeld<TYPE>]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) x[i] = v[i];
+#pragma unroll
+  for (int d = W / 2; d > 0; d >>= 1) {
+    const bool high = lane & d;
+#pragma unroll
+    for (int i = 0; i < d; ++i) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + d], d);
+      x[i] = larger<TYPE>(high ? x[i + d] : x[i], other);
+    }
+  }
+  // The lane holds register lane % W.
+#pragma unroll
+  for (int d = W; d <= 8; d *= 2) x[0] = larger<TYPE>(x[0], __shfl_xor_sync(0xffffffffu, x[0], d));
+  uint32_t inverses = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld<TYPE>; ++i) {
+    const Scale s = scale_of<FORMAT>(magnitude<TYPE>(x[0], i));
+    value[i] = s.value;
+    inverses |= __float_as_uint(s.inverse) >> 16 << 16 * i;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = __shfl_sync(0xffffffffu, inverses, (lane & 16) + i);
+}
+__device__ __forceinline__ float inverse_of(uint32_t held, int i) {
+  return __uint_as_float(i ? held & 0xffff0000u : held << 16);
 }
 
 // A thread's eight consecutive values of a row as they were read (16-bit ones take half the registers), zeros beyond its
@@ -91,13 +156,17 @@ struct Eight {
       w = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  // Pairs of neighbours.
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = ff::to_f32x2<TYPE == kBf16 ? ff::kBf16 : ff::kF16>(u[i]);
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      v[i] = ff::pack2(f.x, f.y);
     }
+  }
+  __device__ __forceinline__ void magnitudes(uint32_t (&a)[4]) const {
+    a[0] = w.x & 0x7fff7fffu, a[1] = w.y & 0x7fff7fffu, a[2] = w.z & 0x7fff7fffu, a[3] = w.w & 0x7fff7fffu;
   }
 };
 template <>
@@ -113,11 +182,38 @@ struct Eight<kF32> {
       for (int i = 0; i < 8; ++i) f[i] = i < left ? p[i] : 0.0f;
     }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f[i];
+    for (int i = 0; i < 4; ++i) v[i] = ff::pack2(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ void magnitudes(uint32_t (&a)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = __float_as_uint(f[i]) & 0x7fffffffu;
   }
 };
+
+// The maxima of ROWS rows' eight values, kHeld rows to a register: magnitude<TYPE>(v[i / kHeld], i % kHeld) is row i's.
+template <int TYPE, int ROWS>
+__device__ __forceinline__ void row_maxima(const Eight<TYPE> (&x)[ROWS], uint32_t (&v)[ROWS / kHeld<TYPE>]) {
+  constexpr int kWords = 8 / kHeld<TYPE>;
+  uint32_t most[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    uint32_t a[kWords];
+    x[i].magnitudes(a);
+    most[i] = a[0];
+#pragma unroll
+    for (int j = 1; j < kWords; ++j) most[i] = larger<TYPE>(most[i], a[j]);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS / kHeld<TYPE>; ++i) {
+    if constexpr (TYPE == kF32) {
+      v[i] = most[i];
+    } else {
+      v[i] = both_largest<TYPE>(most[2 * i], most[2 * i + 1]);
+    }
+  }
+}
 
 struct QuantizeParams {
   int64_t M, N, ldx;
@@ -143,18 +239,26 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_co
   Eight<TYPE> x[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
+  uint32_t most[kAhead / kHeld<TYPE>];
+  row_maxima<TYPE, kAhead>(x, most);
+  float value[kHeld<TYPE>];
+  half_warp_scales<TYPE, FORMAT>(most, value);
+  const int lane = threadIdx.x % 16;
+  if (lane < kAhead / kHeld<TYPE> && n0 - lane * 8 < p.N) {
+#pragma unroll
+    for (int i = 0; i < kHeld<TYPE>; ++i) {
+      const int64_t m = m0 + lane * kHeld<TYPE> + i;
+      if (m < p.M) p.rows.s.p[m * p.rows.s.row + b * p.rows.s.block] = value[i];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    float v[8];
+    uint64_t v[4];
     x[i].get(v);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, magnitude(v[j]));
-    const Scale s = scale_of<FORMAT>(half_warp_max(amax));
     const int64_t m = m0 + i;
-    if (m >= p.M) continue;
-    if (left > 0) store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, s.inverse));
-    if (threadIdx.x % 16 == 0 && left > 0) p.rows.s.p[m * p.rows.s.row + b * p.rows.s.block] = s.value;
+    if (m < p.M && left > 0)
+      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide,
+             pack8<FORMAT>(v, inverse_of(most[i / kHeld<TYPE>], i % kHeld<TYPE>)));
   }
 }
 
@@ -167,32 +271,11 @@ __device__ __forceinline__ uint32_t transposed_at(int column, int word) {
   return static_cast<uint32_t>(column * kBlock + ((word ^ (column / 8)) & 15) * 8);
 }
 
-// Maxima of eight rows over a half-warp's 16 lanes, in all of them: a lane first gives away half of its rows at a
-// step, until it holds one (16 shuffles instead of 32).
-__device__ __forceinline__ void half_warp_maxima(uint32_t (&v)[8]) {
-  const int lane = threadIdx.x & 31;
-  uint32_t x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = v[i];
-#pragma unroll
-  for (int d = 4; d > 0; d >>= 1) {
-    const bool high = lane & d;
-#pragma unroll
-    for (int i = 0; i < d; ++i) {
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + d], d);
-      x[i] = max(high ? x[i + d] : x[i], other);
-    }
-  }
-  // The lane holds row lane % 8.
-  x[0] = max(x[0], __shfl_xor_sync(0xffffffffu, x[0], 8));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, x[0], (lane & 16) + i);
-}
-
 template <int TYPE, int FORMAT, bool SQUARE>
 __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_kernel(const __grid_constant__ QuantizeParams p) {
   constexpr int kWarps = kThreads / 32;
-  __shared__ __align__(16) uint32_t column_max[kWarps][kBlock];
+  constexpr int kHeldHere = kHeld<TYPE>, kWords = 8 / kHeldHere;
+  __shared__ __align__(16) uint32_t column_max[kWarps][kBlock / kHeldHere];
   __shared__ __align__(16) float column_inverse[kBlock];
   __shared__ __align__(16) uint8_t transposed[kBlock * kBlock];
   ff::wait_for_earlier_kernels();
@@ -203,44 +286,45 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_
   Eight<TYPE> x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
-  uint32_t row_max[8], amax[8] = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v[8];
-    x[i].get(v);
-    row_max[i] = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t a = magnitude(v[j]);
-      row_max[i] = max(row_max[i], a);
-      if (!SQUARE) amax[j] = max(amax[j], a);
-    }
-  }
+  uint32_t row_max[kWords];  // eight rows too
+  row_maxima<TYPE, 8>(x, row_max);
   Scale all = {};
   if (SQUARE) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) row_max[0] = max(row_max[0], row_max[i]);
-    row_max[0] = half_warp_max(row_max[0]);
+    for (int i = 1; i < kWords; ++i) row_max[0] = larger<TYPE>(row_max[0], row_max[i]);
+    row_max[0] = half_warp_max<TYPE>(row_max[0]);
     if (threadIdx.x % 16 == 0) column_max[0][threadIdx.x / 16] = row_max[0];
     __syncthreads();
-    all = scale_of<FORMAT>(half_warp_max(column_max[0][threadIdx.x % 16]));
+    uint32_t most = half_warp_max<TYPE>(column_max[0][threadIdx.x % 16]);
+    if (TYPE != kF32) most = both_largest<TYPE>(most, most);
+    all = scale_of<FORMAT>(magnitude<TYPE>(most, 0));
     if (threadIdx.x == 0) {
       if (p.rows.q != nullptr) p.rows.s.p[mb * p.rows.s.row + nb * p.rows.s.block] = all.value;
       if (columns) p.columns.s.p[nb * p.columns.s.row + mb * p.columns.s.block] = all.value;
     }
   } else if (columns) {
+    uint32_t amax[kWords];
+    x[0].magnitudes(amax);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax[j] = max(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], 16));
+    for (int i = 1; i < 8; ++i) {
+      uint32_t a[kWords];
+      x[i].magnitudes(a);
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) amax[j] = larger<TYPE>(amax[j], a[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) amax[j] = larger<TYPE>(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], 16));
     if ((threadIdx.x & 16) == 0) {
-      uint4* to = reinterpret_cast<uint4*>(&column_max[warp][c0]);
-      to[0] = make_uint4(amax[0], amax[1], amax[2], amax[3]);
-      to[1] = make_uint4(amax[4], amax[5], amax[6], amax[7]);
+#pragma unroll
+      for (int j = 0; j < kWords; j += 4)
+        *reinterpret_cast<uint4*>(&column_max[warp][c0 / kHeldHere + j]) = make_uint4(amax[j], amax[j + 1], amax[j + 2], amax[j + 3]);
     }
     __syncthreads();
     if (threadIdx.x < kBlock) {
-      uint32_t a = 0;
+      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) a = max(a, column_max[i][threadIdx.x]);
+      for (int i = 0; i < kWarps; ++i) most = larger<TYPE>(most, column_max[i][threadIdx.x / kHeldHere]);
+      const uint32_t a = magnitude<TYPE>(most, static_cast<int>(threadIdx.x) % kHeldHere);
       const Scale s = scale_of<FORMAT>(a);
       const int64_t n = nb * kBlock + threadIdx.x;
       column_inverse[threadIdx.x] = s.inverse;
@@ -249,38 +333,48 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_
     __syncthreads();
   }
   if (p.rows.q != nullptr) {
-    if (!SQUARE) half_warp_maxima(row_max);
+    if (!SQUARE) {
+      float value[kHeldHere];
+      half_warp_scales<TYPE, FORMAT>(row_max, value);
+      const int lane = threadIdx.x % 16;
+#pragma unroll
+      for (int i = 0; i < kHeldHere; ++i) {
+        const int64_t m = m0 + lane * kHeldHere + i;
+        if (lane < kWords && m < p.M) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = value[i];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t m = m0 + i;
-      const Scale s = SQUARE ? all : scale_of<FORMAT>(row_max[i]);
-      float v[8];
+      uint64_t v[4];
       x[i].get(v);
       if (m >= p.M) continue;
-      if (!SQUARE && threadIdx.x % 16 == 0) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = s.value;
-      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, s.inverse));
+      const float inverse = SQUARE ? all.inverse : inverse_of(row_max[i / kHeldHere], i % kHeldHere);
+      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, inverse));
     }
   }
   if (!columns) return;
-  float inverse[8];
+  uint64_t inverse[4];
   if (SQUARE) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) inverse[j] = all.inverse;
+    for (int j = 0; j < 4; ++j) inverse[j] = ff::both(all.inverse);
   } else {
     const float4 lo = reinterpret_cast<const float4*>(column_inverse + c0)[0], hi = reinterpret_cast<const float4*>(column_inverse + c0)[1];
-    inverse[0] = lo.x, inverse[1] = lo.y, inverse[2] = lo.z, inverse[3] = lo.w;
-    inverse[4] = hi.x, inverse[5] = hi.y, inverse[6] = hi.z, inverse[7] = hi.w;
+    inverse[0] = ff::pack2(lo.x, lo.y), inverse[1] = ff::pack2(lo.z, lo.w);
+    inverse[2] = ff::pack2(hi.x, hi.y), inverse[3] = ff::pack2(hi.z, hi.w);
   }
   uint32_t bytes[8][2];  // a column's eight rows
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    float v[8], w[8];
+    uint64_t v[4], w[4];
     x[i].get(v);
     x[i + 1].get(w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t two = pack_fp8x2<FORMAT>(v[j] * inverse[j], w[j] * inverse[j]);
-      bytes[j][i / 4] = i % 4 == 0 ? two : bytes[j][i / 4] | two << 16;
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = ff::halves(ff::mul2(v[j], inverse[j])), b = ff::halves(ff::mul2(w[j], inverse[j]));
+      const uint32_t two[2] = {pack_fp8x2<FORMAT>(a.x, b.x), pack_fp8x2<FORMAT>(a.y, b.y)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) bytes[2 * j + k][i / 4] = i % 4 == 0 ? two[k] : bytes[2 * j + k][i / 4] | two[k] << 16;
     }
   }
 #pragma unroll
