@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_co
   const int64_t tile = blockIdx.x, m0 = (tile / p.column_tiles * (16 / p.across) + down) * kAhead;
   const int64_t b = tile % p.column_tiles * p.across + (half - down * p.across), n0 = b * kBlock + threadIdx.x % 16 * 8;
   const int64_t left = p.N - n0;
+  const int64_t from = m0 * p.ldx + n0;
+  uint8_t* to = p.rows.q + m0 * p.rows.ld + n0;
   Eight<TYPE> x[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
+  for (int i = 0; i < kAhead; ++i) x[i].load(p.X, from + i * p.ldx, m0 + i < p.M ? left : 0, p.x_wide);
   uint32_t most[kAhead / kHeld<TYPE>];
   row_maxima<TYPE, kAhead>(x, most);
   float value[kHeld<TYPE>];
@@ -255,10 +257,9 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const __grid_co
   for (int i = 0; i < kAhead; ++i) {
     uint64_t v[4];
     x[i].get(v);
-    const int64_t m = m0 + i;
-    if (m < p.M && left > 0)
-      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide,
-             pack8<FORMAT>(v, inverse_of(most[i / kHeld<TYPE>], i % kHeld<TYPE>)));
+    if (m0 + i < p.M && left > 0)
+      store8(to, left, p.rows_wide, pack8<FORMAT>(v, inverse_of(most[i / kHeld<TYPE>], i % kHeld<TYPE>)));
+    to += p.rows.ld;
   }
 }
 
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_
   const bool columns = p.columns.q != nullptr;
   Eight<TYPE> x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i].load(p.X, (m0 + i) * p.ldx + n0, m0 + i < p.M ? left : 0, p.x_wide);
+  for (int i = 0; i < 8; ++i) x[i].load(p.X, m0 * p.ldx + n0 + i * p.ldx, m0 + i < p.M ? left : 0, p.x_wide);
   uint32_t row_max[kWords];  // eight rows too
   row_maxima<TYPE, 8>(x, row_max);
   Scale all = {};
@@ -343,14 +344,14 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_
         if (lane < kWords && m < p.M) p.rows.s.p[m * p.rows.s.row + nb * p.rows.s.block] = value[i];
       }
     }
+    uint8_t* to = p.rows.q + m0 * p.rows.ld + n0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t m = m0 + i;
+    for (int i = 0; i < 8; ++i, to += p.rows.ld) {
       uint64_t v[4];
       x[i].get(v);
-      if (m >= p.M) continue;
+      if (m0 + i >= p.M) continue;
       const float inverse = SQUARE ? all.inverse : inverse_of(row_max[i / kHeldHere], i % kHeldHere);
-      store8(p.rows.q + m * p.rows.ld + n0, left, p.rows_wide, pack8<FORMAT>(v, inverse));
+      store8(to, left, p.rows_wide, pack8<FORMAT>(v, inverse));
     }
   }
   if (!columns) return;
@@ -384,12 +385,12 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) quantize_tile_
   // Sixteen threads to a transposed row of 128 bytes.
   const int word = threadIdx.x % 16;
   const int64_t rows_left = p.M - mb * kBlock - word * 8;
+  uint8_t* to = p.columns.q + (nb * kBlock + threadIdx.x / 16) * p.columns.ld + mb * kBlock + word * 8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; ++i, to += 16 * p.columns.ld) {
     const int c = threadIdx.x / 16 + 16 * i;
-    const int64_t n = nb * kBlock + c;
-    if (n < p.N)
-      store8(p.columns.q + n * p.columns.ld + mb * kBlock + word * 8, rows_left, p.columns_wide,
+    if (nb * kBlock + c < p.N)
+      store8(to, rows_left, p.columns_wide,
              *reinterpret_cast<const uint2*>(transposed + transposed_at(c, word)));
   }
 }
