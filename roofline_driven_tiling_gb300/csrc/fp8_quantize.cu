@@ -5,6 +5,10 @@
 // e4m3, 57344 = 1.75 2^15 for e5m2), at least 2^-126: an exponent off the bits of amax. x / s is then exact, and
 // every value is rounded once. amax is taken over bit patterns, so that an infinity or NaN anywhere in a block
 // makes the scale NaN and with it the whole block.
+//
+// Bound by memory, near enough by instructions that those were what the steps saved: 8192 x 8192 bfloat16 along rows 33 us
+// (6.1 TB/s), 4096 x 8192 along rows 17.4 (5.8), columns 20.6 (4.9), both 27.8 (4.8; 4.5 rounds of three blocks to an SM),
+// both with squares 25.5.
 #include <cuda_runtime.h>
 
 #include <cstdint>

