@@ -50,7 +50,10 @@ int quantize(Wide type, int64_t M, int64_t N, const void* X, int64_t ldx, int fo
     return T2S_ERR_INVALID;
   if (Qt != nullptr && (bad_scales(t.columns.s, square ? nb : N, mb) || overlapping(t.columns.s, square ? nb : N, mb)))
     return T2S_ERR_INVALID;
-  if (Q != nullptr && Qt != nullptr && S == St) return T2S_ERR_INVALID;
+  const void* const scales[2] = {Q != nullptr ? S : nullptr, Qt != nullptr ? St : nullptr};
+  if (scales[0] == scales[1]) return T2S_ERR_INVALID;
+  for (const void* w : scales)
+    if (w != nullptr && (w == X || w == Q || w == Qt)) return T2S_ERR_INVALID;
   return done(run_quantize(t, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -68,7 +71,9 @@ int product(Wide type, int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_
   ProductTask t{type, M, N, K, A, B, lda, ldb, format_a, format_b, {const_cast<float*>(SA), sa_row, sa_block},
                 {const_cast<float*>(SB), sb_row, sb_block}, b_group, C, ldc};
   const int64_t kb = blocks_of(K);
-  if (bad_scales(t.sa, M, kb) || bad_scales(t.sb, (N + b_group - 1) / b_group, kb)) return T2S_ERR_INVALID;
+  if (bad_scales(t.sa, M, kb) || bad_scales(t.sb, (N + b_group - 1) / b_group, kb) ||
+      (kb > 0 && (C == SA || C == SB)))
+    return T2S_ERR_INVALID;
   return done(run_product(t, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -48,6 +48,18 @@ def test_gemm_arguments(lib):
         assert _call(lib, "t2s_gemm_fp8", a, kw) == {binding.T2S_OK}, kw
 
 
+def test_scales_are_no_other_argument(lib):
+    Q, S, Qt, St = F + (1 << 20), F + (1 << 21), F + (1 << 22), F + (1 << 23)
+    a = dict(M=256, N=300, X=F, ldx=300, format=0, square=0, Q=Q, ldq=304, S=S, s_row=1, s_block=256, Qt=Qt, ldqt=256, St=St,
+             st_row=1, st_block=300, stream=None)
+    for kw in (dict(S=F), dict(S=Q), dict(S=Qt), dict(St=F), dict(St=Q), dict(St=Qt), dict(Qt=None, S=F), dict(Q=None, St=Qt)):
+        assert _call(lib, "t2s_quantize_fp8", a, kw) == {binding.T2S_ERR_INVALID}, kw
+    a = dict(M=64, N=200, K=300, A=F, lda=304, format_a=0, SA=Q, sa_row=1, sa_block=64, B=S, ldb=304, format_b=1, SB=Qt,
+             sb_row=1, sb_block=200, group=1, C=St, ldc=200, stream=None)
+    for kw in (dict(C=Q), dict(C=Qt)):
+        assert _call(lib, "t2s_gemm_fp8", a, kw) == {binding.T2S_ERR_INVALID}, kw
+
+
 def test_python_checks():
     x = torch.zeros(4, 128)
     q = x.to(torch.float8_e4m3fn)
