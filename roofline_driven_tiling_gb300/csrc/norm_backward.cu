@@ -8,8 +8,8 @@
 // CTAs' shares in their order.
 //
 // Rows are read once (N <= 8192). Bound by instructions, not by memory (every value of a warp's word costs about 20): 8192 x
-// 2048 with a gate and dropout 52.7 us (3.8 TB/s), 8192 x 4096 without dropout 88 (4.6), layer norms before and after with all
-// sums 95; off 16-byte boundaries 4096 x 4095 98, 1300 x 1003 27 (nine rows to a block, and the second launch 4 us). Two words
+// 2048 with a gate and dropout 52.2 us (3.9 TB/s), 8192 x 4096 without dropout 87 (4.6), layer norms before and after with all
+// sums 92; off 16-byte boundaries 4096 x 4095 97, 1300 x 1003 26 (nine rows to a block, and the second launch 4 us). Two words
 // a thread with half the threads were no faster (8192 x 4096 98).
 #include <cuda_runtime.h>
 
@@ -42,6 +42,9 @@ Split split_of(int64_t M, int64_t gates, int ctas) {
   return {static_cast<int>(gates * pieces), static_cast<int>(pieces)};
 }
 
+// From one of a CTA's sums to the next: rows of 16-byte words.
+__host__ __device__ inline int64_t share_pitch(int64_t N) { return (N + 3) & ~static_cast<int64_t>(3); }
+
 struct BackwardParams {
   BackwardTask t;
   Split split;
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
   const float inv_n = 1.0f / static_cast<float>(t.N);
   const uint64_t key = t.drop.dropped != 0 ? drop_key(t.drop) : 0;
   const Rows rows = rows_of(p, blockIdx.x);
-  float* const partials = t.partials + static_cast<int64_t>(blockIdx.x) * p.slots * t.N;
+  float* const partials = t.partials + static_cast<int64_t>(blockIdx.x) * p.slots * share_pitch(t.N);
   const bool has_h = t.H.p != nullptr;
   for (int64_t m = rows.first; m < rows.last; ++m) {
     const bool first = m == rows.first, gate_first = p.split.pieces > 0 ? first : m % rows.per_gate == 0;
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
     };
     auto add = [&](int vector, int64_t n, float v, bool start) {
       if (p.slot[vector] < 0) return;
-      float* to = partials + p.slot[vector] * t.N + n;
+      float* to = partials + p.slot[vector] * share_pitch(t.N) + n;
       *to = start ? v : *to + v;
     };
     float s[2] = {};
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
       }
       add(kGate, n, d * v, gate_first);
       if (gate_last && p.slot[kGate] >= 0)
-        t.dgate.p[m / rows.per_gate * t.dgate.ld + n] = ff::from_f32<KIND>(partials[p.slot[kGate] * t.N + n]);
+        t.dgate.p[m / rows.per_gate * t.dgate.ld + n] = ff::from_f32<KIND>(partials[p.slot[kGate] * share_pitch(t.N) + n]);
       if (t.post == T2S_NORM_NONE) {
         if (t.dH.p != nullptr) t.dH.p[m * t.dH.ld + n] = ff::from_f32<KIND>(dn);
         continue;
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_backward_kernel(const __gri
   }
 }
 
-// Rows of up to 8192 values: a group of threads takes a row, C words of eight values a thread; a block holds several
+// Rows of up to 8192 values: a group of threads takes a row, a word of eight values a thread; a block holds several
 // groups. The row's r, dy, dr and h come to shared memory, r and h of the next row as soon as this row's are in
 // registers, and the parameters' words stay there. The sums over rows are added in shared memory too, each group's in its
 // own place. All of these places belong to one thread each. At the end of a block's rows (of a gate's for dgate) the
@@ -196,48 +199,37 @@ struct RowParams {
   float* partials;
 };
 
-template <int KIND, bool WIDE, int C, int THREADS>
+template <int KIND, bool WIDE, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(const __grid_constant__ RowParams p) {
   extern __shared__ uint4 words[];
   __shared__ float rooms[row::Group::kRoomFloats];
-  // In shared memory, from one of a thread's words to the next: of the inputs, and of the sums (two places each).
-  constexpr uint32_t kPitch = THREADS / 32 * row::kWarpBytes<WIDE>, kSumPitch = THREADS * 16;
+  constexpr uint32_t kSumPitch = THREADS * 16;  // in shared memory, from one of a sum's two places of a thread to the other
   row::Group group(p.threads, rooms);
-  const int n = p.N, threads = static_cast<int>(blockDim.x), rows_at_once = threads / p.threads;
-  const int first_column = group.rank * row::kWord, stride = p.threads * row::kWord;
+  const int n = p.N, rows_at_once = static_cast<int>(blockDim.x) / p.threads;
+  const int first_column = group.rank * row::kWord, left = n - first_column;
   const uint32_t first_byte = 2u * static_cast<uint32_t>(first_column);
-  auto left_of = [&](int c) { return n - first_column - c * stride; };
   const uint32_t mine = smem_u32(words) + row::place_of_thread<WIDE>(), my_sums = smem_u32(words) + threadIdx.x * 16u;
   // A sum's eight values are two places of 16 bytes.
-  for (int i = 0; i < 2 * p.sum_slots * C; ++i) st_shared_v4(my_sums + p.sum_first + i * kSumPitch, 0u, 0u, 0u, 0u);
+  for (int i = 0; i < 2 * p.sum_slots; ++i) st_shared_v4(my_sums + p.sum_first + i * kSumPitch, 0u, 0u, 0u, 0u);
 #pragma unroll 1
   for (int i = 0; i < kPlaces; ++i)
-    if (p.at[i] >= 0)
-#pragma unroll
-      for (int c = 0; c < C; ++c) row::clear_place<WIDE>(mine + p.at[i] + c * kPitch, left_of(c));
+    if (p.at[i] >= 0) row::clear_place<WIDE>(mine + p.at[i], left);
   ff::wait_for_earlier_kernels();
   auto fetch = [&](int place, const uint16_t* from, bool inside) {
-    if (p.at[place] < 0) return;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      row::fetch_word<WIDE>(mine + p.at[place] + c * kPitch, p.in[place], from + c * stride, left_of(c), inside);
+    if (p.at[place] >= 0) row::fetch_word<WIDE>(mine + p.at[place], p.in[place], from, left, inside);
   };
   auto settle = [&](int place, const uint16_t* from) {
-    if (WIDE || p.at[place] < 0) return;
-#pragma unroll
-    for (int c = 0; c < C; ++c) row::settle<WIDE>(mine + p.at[place] + c * kPitch, from + c * stride, left_of(c));
+    if (!WIDE && p.at[place] >= 0) row::settle<WIDE>(mine + p.at[place], from, left);
   };
-  auto get = [&](int place, int c, uint64_t(&f)[4]) {
-    row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place] + c * kPitch, left_of(c)), f);
-  };
+  auto get = [&](int place, uint64_t(&f)[4]) { row::unpack<KIND>(row::arrived<WIDE>(mine + p.at[place], left), f); };
   // A parameter's words, in shared memory, or read again for each row where that is full.
   int gate_row = 0;
-  auto parameter = [&](int place, int c, uint64_t(&f)[4]) {
+  auto parameter = [&](int place, uint64_t(&f)[4]) {
     if (p.at[place] >= 0) {
-      get(place, c, f);
+      get(place, f);
     } else {
       const uint16_t* from = p.in[place].row(place == kG ? gate_row : 0, first_byte);
-      row::unpack<KIND>(row::load_word<WIDE>(p.in[place], from + c * stride, left_of(c)), f);
+      row::unpack<KIND>(row::load_word<WIDE>(p.in[place], from, left), f);
     }
   };
   fetch(kW, p.in[kW].row(0, first_byte), false);
@@ -250,9 +242,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
   const bool has_h = p.in[kH].p != nullptr, has_norm = p.norm != T2S_NORM_NONE, has_post = has_h && p.post != T2S_NORM_NONE;
   const bool layer = p.norm == T2S_NORM_LAYER, post_layer = has_post && p.post == T2S_NORM_LAYER;
 
-  auto add = [&](int vector, int c, const uint64_t(&f)[4]) {
+  auto add = [&](int vector, const uint64_t(&f)[4]) {
     if (p.sum_at[vector] < 0) return;
-    const uint32_t to = my_sums + p.sum_at[vector] + 2 * c * kSumPitch;
+    const uint32_t to = my_sums + p.sum_at[vector];
     uint64_t a, b;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -261,14 +253,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
       asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(to + i * kSumPitch), "l"(a), "l"(b) : "memory");
     }
   };
-  // A sum's column i over the groups, which are cleared if `clear`.
-  auto total = [&](int sum_at, int i, bool clear) {
-    float s = 0.0f;
-    const int word = i / row::kWord, c = word < p.threads ? 0 : 1, thread = word - c * p.threads, j = i % row::kWord;
-    float* from = reinterpret_cast<float*>(words + sum_at / 16 + (2 * c + j / 4) * THREADS + thread) + j % 4;
-    for (int g = 0; g < rows_at_once; ++g, from += p.threads * 4) {
-      s += *from;
-      if (clear) *from = 0.0f;
+  // Four columns of a sum from place `q` (two places a sum) over the groups, in their order; cleared if `clear`.
+  auto total = [&](int q, bool clear) {
+    float4* from = reinterpret_cast<float4*>(words + p.sum_first / 16) + q * THREADS + group.rank;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int g = 0; g < rows_at_once; ++g, from += p.threads) {
+      const float4 v = *from;
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      if (clear) *from = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     return s;
   };
@@ -307,60 +299,47 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
           if (i <= kH || i == kG || fresh == kW) settle(i, p.in[i].row(i <= kH ? m : i == kG ? gate_row : 0, first_byte));
         fresh = kPlaces;
       }
-      uint64_t xh[C][4], hh[C][4], d[C][4];
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (has_norm) get(kR, c, xh[c]);
-        if (has_h) get(kH, c, hh[c]);
-      }
+      uint64_t xh[4], hh[4], d[4];
+      if (has_norm) get(kR, xh);
+      if (has_h) get(kH, hh);
       fetch_next(kR);
       fetch_next(kH);
       if (layer || post_layer) {
         float means[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (layer) means[0] += row::sum(xh[c]);
-          if (post_layer) means[1] += row::sum(hh[c]);
-        }
+        if (layer) means[0] = row::sum(xh);
+        if (post_layer) means[1] = row::sum(hh);
         group.sums(means);
+        if (layer) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (layer) {
+          for (int i = 0; i < 4; ++i) xh[i] = row::add2(xh[i], row::both(-means[0] * inv_n));
+          row::clear_from<WIDE>(xh, left);
+        }
+        if (post_layer) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xh[c][i] = row::add2(xh[c][i], row::both(-means[0] * inv_n));
-            row::clear_from<WIDE>(xh[c], left_of(c));
-          }
-          if (post_layer) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hh[c][i] = row::add2(hh[c][i], row::both(-means[1] * inv_n));
-            row::clear_from<WIDE>(hh[c], left_of(c));
-          }
+          for (int i = 0; i < 4; ++i) hh[i] = row::add2(hh[i], row::both(-means[1] * inv_n));
+          row::clear_from<WIDE>(hh, left);
         }
       }
       float rho = 1.0f, sigma = 1.0f, mean_g = 0.0f, mean_gx = 0.0f;
       // dy weight stays in registers, but for rows off boundaries, whose code has none to spare: there it is formed again
-      // (4096 x 4095 98 us, and 103 with what the compiler then kept in memory; 8192 x 2048 with dropout 55 us and 53).
+      // (4096 x 4095 97 us, and 103 with what the compiler then kept in memory; 8192 x 2048 with dropout 55 us and 53).
       constexpr bool kKeepG = WIDE;
-      uint64_t g[kKeepG ? C : 1][4];
+      uint64_t g[4];
       if (has_norm || has_post) {
         float s[4] = {};
+        if (has_norm) {
+          uint64_t w[4];
+          get(kDy, g);
+          if (p.in[kW].p != nullptr) {
+            parameter(kW, w);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (has_norm) {
-            uint64_t w[4];
-            uint64_t(&gc)[4] = g[kKeepG ? c : 0];
-            get(kDy, c, gc);
-            if (p.in[kW].p != nullptr) {
-              parameter(kW, c, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) gc[i] = row::mul2(gc[i], w[i]);
-            }
-            s[0] += row::dot(xh[c], xh[c]);
-            s[1] += row::dot(gc, xh[c]);
-            if (layer) s[2] += row::sum(gc);
+            for (int i = 0; i < 4; ++i) g[i] = row::mul2(g[i], w[i]);
           }
-          if (has_post) s[3] += row::dot(hh[c], hh[c]);
+          s[0] = row::dot(xh, xh);
+          s[1] = row::dot(g, xh);
+          if (layer) s[2] = row::sum(g);
         }
+        if (has_post) s[3] = row::dot(hh, hh);
         if (layer || has_post) {
           group.sums(s);
         } else {
@@ -376,95 +355,90 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
         if (has_post) sigma = rsqrtf(s[3] * inv_n + p.eps);
       }
       float q[2] = {0.0f, 0.0f};
+      uint64_t f[4], w[4];
+      if (p.at[kDr] >= 0) {
+        get(kDr, d);
+      } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int left = left_of(c);
-        uint64_t f[4], w[4];
-        if (p.at[kDr] >= 0) {
-          get(kDr, c, d[c]);
-        } else {
+        for (int i = 0; i < 4; ++i) d[i] = 0;
+      }
+      if (has_norm) {
+        get(kDy, f);
+        add(kBias, f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[c][i] = 0;
+        for (int i = 0; i < 4; ++i) {
+          xh[i] = row::mul2(xh[i], row::both(rho));
+          w[i] = row::mul2(f[i], xh[i]);
         }
-        if (has_norm) {
-          get(kDy, c, f);
-          add(kBias, c, f);
+        add(kWeight, w);
+        if (!kKeepG) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xh[c][i] = row::mul2(xh[c][i], row::both(rho));
-            w[i] = row::mul2(f[i], xh[c][i]);
+          for (int i = 0; i < 4; ++i) g[i] = f[i];
+          if (p.in[kW].p != nullptr) {
+            parameter(kW, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = row::mul2(g[i], w[i]);
           }
-          add(kWeight, c, w);
-          uint64_t(&gc)[4] = g[kKeepG ? c : 0];
-          if (!kKeepG) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) gc[i] = f[i];
-            if (p.in[kW].p != nullptr) {
-              parameter(kW, c, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) gc[i] = row::mul2(gc[i], w[i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[i] = row::fma2(xh[c][i], row::both(-mean_gx), gc[i]);
-            if (layer) f[i] = row::add2(f[i], row::both(-mean_g));
-            d[c][i] = row::fma2(f[i], row::both(rho), d[c][i]);
-          }
-          if (layer) row::clear_from<WIDE>(d[c], left);  // the mean is not for the values beyond the row's end
         }
-        if (p.dx.p != nullptr) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], row::both(p.scale));
-          row::store_word<WIDE>(p.dx, p.dx.row(m, first_byte) + c * stride, left, row::pack<KIND>(f));
+        for (int i = 0; i < 4; ++i) {
+          f[i] = row::fma2(xh[i], row::both(-mean_gx), g[i]);
+          if (layer) f[i] = row::add2(f[i], row::both(-mean_g));
+          d[i] = row::fma2(f[i], row::both(rho), d[i]);
         }
-        if (has_h) {
-          row::Keep keep;
-          if (p.drop.dropped != 0) {
-            keep.draw(key, static_cast<uint64_t>(static_cast<uint32_t>(m)) * groups + static_cast<uint32_t>(first_column + c * stride) / 4u, p.drop.dropped);
-            // The kept values' factor, for everything that follows.
+        if (layer) row::clear_from<WIDE>(d, left);  // the mean is not for the values beyond the row's end
+      }
+      if (p.dx.p != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], row::both(p.drop.factor));
+        for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[i], row::both(p.scale));
+        row::store_word<WIDE>(p.dx, p.dx.row(m, first_byte), left, row::pack<KIND>(f));
+      }
+      if (has_h) {
+        row::Keep keep;
+        if (p.drop.dropped != 0) {
+          keep.draw(key, static_cast<uint64_t>(static_cast<uint32_t>(m)) * groups + static_cast<uint32_t>(first_column) / 4u, p.drop.dropped);
+          // The kept values' factor, for everything that follows.
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = row::mul2(d[i], row::both(p.drop.factor));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hh[i] = row::mul2(hh[i], row::both(sigma));
+        if (p.sum_at[kGate] >= 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = hh[i];
+          if (p.in[kPw].p != nullptr) {
+            parameter(kPw, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
           }
+          if (p.in[kPb].p != nullptr) {
+            parameter(kPb, w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) hh[c][i] = row::mul2(hh[c][i], row::both(sigma));
-          if (p.sum_at[kGate] >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = hh[c][i];
-            if (p.in[kPw].p != nullptr) {
-              parameter(kPw, c, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], w[i]);
-            }
-            if (p.in[kPb].p != nullptr) {
-              parameter(kPb, c, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = row::add2(f[i], w[i]);
-            }
-            if (p.drop.dropped != 0) keep.apply(f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], d[c][i]);
-            add(kGate, c, f);
+            for (int i = 0; i < 4; ++i) f[i] = row::add2(f[i], w[i]);
           }
-          if (p.in[kG].p != nullptr) {
-            parameter(kG, c, w);
+          if (p.drop.dropped != 0) keep.apply(f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
+          for (int i = 0; i < 4; ++i) f[i] = row::mul2(f[i], d[i]);
+          add(kGate, f);
+        }
+        if (p.in[kG].p != nullptr) {
+          parameter(kG, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i] = row::mul2(d[i], w[i]);
+        }
+        if (p.drop.dropped != 0) keep.apply(d);
+        if (has_post) {
+          add(kPostBias, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[i], hh[i]);
+          add(kPostWeight, f);
+          if (p.in[kPw].p != nullptr) {
+            parameter(kPw, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = row::mul2(d[i], w[i]);
           }
-          if (p.drop.dropped != 0) keep.apply(d[c]);
-          if (has_post) {
-            add(kPostBias, c, d[c]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = row::mul2(d[c][i], hh[c][i]);
-            add(kPostWeight, c, f);
-            if (p.in[kPw].p != nullptr) {
-              parameter(kPw, c, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) d[c][i] = row::mul2(d[c][i], w[i]);
-            }
-            if (post_layer) q[0] += row::sum(d[c]);
-            q[1] += row::dot(d[c], hh[c]);
-          }
+          if (post_layer) q[0] = row::sum(d);
+          q[1] = row::dot(d, hh);
         }
       }
       fetch_next(kDy);
@@ -473,29 +447,38 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
       if (has_post) {
         group.sums(q);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            d[c][i] = row::fma2(hh[c][i], row::both(-q[1] * inv_n), d[c][i]);
-            if (post_layer) d[c][i] = row::add2(d[c][i], row::both(-q[0] * inv_n));
-            d[c][i] = row::mul2(d[c][i], row::both(sigma));
-          }
+        for (int i = 0; i < 4; ++i) {
+          d[i] = row::fma2(hh[i], row::both(-q[1] * inv_n), d[i]);
+          if (post_layer) d[i] = row::add2(d[i], row::both(-q[0] * inv_n));
+          d[i] = row::mul2(d[i], row::both(sigma));
+        }
       }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        row::store_word<WIDE>(p.dh, p.dh.row(m, first_byte) + c * stride, left_of(c), row::pack<KIND>(d[c]));
+      row::store_word<WIDE>(p.dh, p.dh.row(m, first_byte), left, row::pack<KIND>(d));
     }
     if (p.split.pieces == 0 && p.sum_at[kGate] >= 0) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n; i += threads)
-        p.dgate.p[static_cast<int64_t>(gate_row) * p.dgate.ld + i] = ff::from_f32<KIND>(total(p.sum_at[kGate], i, true));
+      for (int half = group.index; half < 2; half += rows_at_once) {
+        const int i = first_column + 4 * half;
+        if (i >= n) continue;
+        const float4 v = total((p.sum_at[kGate] - p.sum_first) / static_cast<int>(kSumPitch) + half, true);
+        uint16_t* to = p.dgate.p + static_cast<int64_t>(gate_row) * p.dgate.ld + i;
+        const uint2 w = make_uint2(ff::pack_f32<KIND>(v.x, v.y), ff::pack_f32<KIND>(v.z, v.w));
+        if (i + 4 <= n && (reinterpret_cast<uintptr_t>(to) & 7u) == 0) {
+          *reinterpret_cast<uint2*>(to) = w;
+        } else {
+          row::store_values(to, 0, min(4, n - i), make_uint4(w.x, w.y, 0u, 0u));
+        }
+      }
       __syncthreads();
     }
   }
   __syncthreads();
-  float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * n;
-  for (int slot = 0; slot < p.sum_slots; ++slot)
-    for (int i = threadIdx.x; i < n; i += threads) out[static_cast<int64_t>(slot) * n + i] = total(p.sum_first + 2 * slot * C * static_cast<int>(kSumPitch), i, false);
+  // The groups share out the places.
+  float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * share_pitch(n);
+  for (int q = group.index; q < 2 * p.sum_slots; q += rows_at_once) {
+    const int i = first_column + 4 * (q & 1);
+    if (i < n) *reinterpret_cast<float4*>(out + (q >> 1) * share_pitch(n) + i) = total(q, false);
+  }
 }
 
 // Adds the CTAs' shares: a block takes 32 columns of one vector (or of one row of dgate), its warps every
@@ -536,7 +519,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
   if (n < p.N)
 #pragma unroll 10
     for (int c = first + warp; c < last; c += kSumWarps)
-      sum += p.partials[(static_cast<int64_t>(c) * p.slots + p.slot[which]) * p.N + n];
+      sum += p.partials[(static_cast<int64_t>(c) * p.slots + p.slot[which]) * share_pitch(p.N) + n];
   room[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || n >= p.N) return;
@@ -544,16 +527,16 @@ __global__ void __launch_bounds__(32 * kSumWarps) share_sum_kernel(const __grid_
   p.out[which][row * p.ldgate + n] = ff::from_f32<KIND>(sum);
 }
 
-// How the row kernel takes a row: words of a thread, threads of a row, threads of a block.
+// How the row kernel takes a row: threads of a row, of a block.
 struct RowPlan {
-  int words, threads, block;  // words 0: too long
+  int threads, block;  // threads 0: too long
   int pitch() const { return block <= 512 ? 512 : 1024; }  // the kernel's THREADS
 };
 RowPlan row_plan(int64_t N) {
   const int64_t words = (N + row::kWord - 1) / row::kWord;
-  if (words > 1024) return {0, 0, 0};
+  if (words > 1024) return {0, 0};
   const int threads = static_cast<int>((words + 31) / 32 * 32);
-  return {1, threads, threads <= 512 ? 512 / threads * threads : threads};
+  return {threads, threads <= 512 ? 512 / threads * threads : threads};
 }
 
 constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
@@ -562,7 +545,7 @@ constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
 // and sums alone do not fit.
 template <bool WIDE>
 bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
-  const int word = plan.words * plan.pitch() * 16, in_word = plan.words * plan.pitch() / 32 * static_cast<int>(row::kWarpBytes<WIDE>);
+  const int word = plan.pitch() * 16, in_word = plan.pitch() / 32 * static_cast<int>(row::kWarpBytes<WIDE>);
   int ins = 0, all = 0;
   for (int i = 0; i < kPlaces; ++i) {
     const bool present = p->in[i].p != nullptr;
@@ -584,18 +567,18 @@ bool lay_out(RowParams* p, const RowPlan& plan, const int* slot, int* bytes) {
   return true;
 }
 
-template <int KIND, bool WIDE, int C, int THREADS>
+template <int KIND, bool WIDE, int THREADS>
 cudaError_t launch_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
-  cudaError_t e = prepare_smem<row_backward_kernel<KIND, WIDE, C, THREADS>>(kMostSmem);
+  cudaError_t e = prepare_smem<row_backward_kernel<KIND, WIDE, THREADS>>(kMostSmem);
   return e != cudaSuccess ? e
                           : ff::launch_early(stream, {dim3(static_cast<unsigned>(p.split.ctas)), plan.block, 1, smem},
-                                             row_backward_kernel<KIND, WIDE, C, THREADS>, p);
+                                             row_backward_kernel<KIND, WIDE, THREADS>, p);
 }
 
 template <int KIND, bool WIDE>
 cudaError_t run_rows(const RowParams& p, const RowPlan& plan, int smem, cudaStream_t stream) {
-  return plan.block <= 512 ? launch_rows<KIND, WIDE, 1, 512>(p, plan, smem, stream)
-                           : launch_rows<KIND, WIDE, 1, 1024>(p, plan, smem, stream);
+  return plan.block <= 512 ? launch_rows<KIND, WIDE, 512>(p, plan, smem, stream)
+                           : launch_rows<KIND, WIDE, 1024>(p, plan, smem, stream);
 }
 
 template <int KIND>
@@ -617,7 +600,7 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
   memset(&p, 0, sizeof(p));
   bool wide = false;
   int smem = 0;
-  if (plan.words > 0) {
+  if (plan.threads > 0) {
     const Input in[kPlaces] = {t.norm != T2S_NORM_NONE ? t.R : Input{}, t.dY, t.dR, t.H, {t.weight, 0}, t.gate,
                                {t.post_weight, 0}, {t.post_bias, 0}};
     p.dx = row::view_of(t.dX.p, t.dX.ld, t.M, t.N), p.dh = row::view_of(t.dH.p, t.dH.ld, t.M, t.N);
@@ -630,9 +613,9 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
     p.M = static_cast<int>(t.M), p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
-    if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.words = 0;
+    if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.threads = 0;
   }
-  if (plan.words > 0) {
+  if (plan.threads > 0) {
     p.split = split = split_of(t.M, t.gates, plan.block <= 512 && smem <= 112 * 1024 ? kMostCtas : kSms);
     const int parts = split.pieces > 0 ? split.pieces : split.ctas;
     const int whole = split.pieces > 0 ? p.rows_per_gate : static_cast<int>(t.gates);
@@ -663,7 +646,8 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
 
 size_t backward_workspace_bytes(int64_t M, int64_t N, int64_t gates, int vectors) {
   if (M == 0 || N == 0 || vectors == 0) return 0;
-  return static_cast<size_t>(split_of(M, gates, kMostCtas).ctas) * static_cast<size_t>(vectors) * static_cast<size_t>(N) * 4;
+  return static_cast<size_t>(split_of(M, gates, kMostCtas).ctas) * static_cast<size_t>(vectors) *
+         static_cast<size_t>(share_pitch(N)) * 4;
 }
 
 cudaError_t run_backward(const BackwardTask& t, cudaStream_t stream) {
