@@ -8,7 +8,6 @@
 namespace t2s {
 namespace fp8 {
 
-
 // The MMAs of one block of 128 values of K (four of K = 32) by one elected thread of a converged warp, from
 // 128-byte swizzled K-major rows; D starts from the first product.
 template <int G>

@@ -127,8 +127,8 @@ __device__ __forceinline__ void store_box(const PairParams& p, uint32_t box, int
 
 // Roles: warp 0 copies A and B, warps 1 and 2 issue the MMAs (rank 0 only), warps 4..11 take the sums.
 // Warp 3 holds TMEM and copies scales. full[s] / empty[s] per ring slot (empty also says that the slot's sums are in
-// TMEM: one commit for both), acc_empty[b] per accumulator, scale_full[s] / scale_empty[s] per slot of scales; a role that gives up a bounded wait records it and stops, and the
-// others' own waits end the same way.
+// TMEM: one commit for both), acc_empty[b] per accumulator, scale_full[s] / scale_empty[s] per slot of scales; a role
+// that gives up a bounded wait records it and stops, and the others' own waits end the same way.
 // CHUNKS: groups of 32 columns of each of the two warps of a row quarter. VECTOR: a scale for every row of B.
 template <int TYPE, int CHUNKS, bool VECTOR>
 __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_constant__ PairParams p) {

@@ -347,6 +347,29 @@ def test_dropout(m, n):
     assert bool((y[~keep] == 0).all()) and bool(torch.isinf(y[keep]).all())
 
 
+@pytest.mark.parametrize("n", [1, 3, 37, 1003, 2048])
+@pytest.mark.parametrize("shift,pad", [(0, 0), (1, 4), (2, 3), (4, 8)])
+def test_gate_gradients_of_any_stride(n, shift, pad):
+    """The C entry point with dgate's rows at any place: the bits of rows on 16-byte boundaries, nothing written between them."""
+    m = 6
+    mk = Maker(n, BF16)
+    dy, r, h, gate = mk.normal(m, n), mk.normal(m, n), mk.normal(m, n), mk.normal(m, n, 0.5, 0.5)
+    want = t2s.residual_norm_backward(dy, None, r, h, gate=gate, eps=1e-6)
+    frame = torch.full((m * (n + pad) + 16,), CANARY, dtype=BF16, device="cuda")
+    dgate = frame[shift:shift + m * (n + pad)].view(m, n + pad)[:, :n]
+    dx, dh = torch.empty_like(r), torch.empty_like(h)
+    size = binding.t2s_residual_norm_backward_workspace_size(m, n, m, 1)
+    workspace = torch.empty(size, dtype=torch.uint8, device="cuda")
+    rc = binding.lib().t2s_residual_norm_backward_bf16(
+        m, n, binding.T2S_NORM_RMS, binding.T2S_NORM_NONE, dy.data_ptr(), n, None, n, r.data_ptr(), n, h.data_ptr(), n, None,
+        None, None, gate.data_ptr(), n, m, 1.0, 1e-6, 0, None, 0, 0, dx.data_ptr(), n, dh.data_ptr(), n, None, None, None,
+        None, dgate.data_ptr(), n + pad, workspace.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    assert rc == binding.T2S_OK
+    assert bool((dgate == want.dgate).all()) and bool((dx == want.dx).all()) and bool((dh == want.dh).all())
+    dgate.fill_(CANARY)
+    assert bool((frame == CANARY).all()), "write outside dgate"
+
+
 def test_offsets_beyond_32_bits():
     """Rows whose offset passes 2^31 and 2^32 elements, from a tensor that spaces them so."""
     n, ld = 520, 1 << 28
