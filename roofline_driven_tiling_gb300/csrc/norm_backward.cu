@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
       __syncthreads();
     }
   }
+  row::wait_copies();  // a group without a row has waited for none: its parameters' copies land before the CTA's memory goes
   __syncthreads();
   // The groups share out the places.
   float* const out = p.partials + static_cast<int64_t>(blockIdx.x) * p.sum_slots * share_pitch(n);

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
       row::store_word<WIDE>(p.y, y + c * stride, left(c), row::pack<KIND>(v[c]));
     }
   }
+  row::wait_copies();  // a group without a row has waited for none: its parameters' copies land before the CTA's memory goes
 }
 
 constexpr int kSms = 152, kMostSmem = 226 * 1024;

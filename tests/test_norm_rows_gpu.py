@@ -1,0 +1,67 @@
+"""Norms and their gradients where rows are few or narrow for a block: groups of threads without a row, and rows of less
+than a word, whose neighbours' words reach past the matrix (GPU tests).
+
+A row's r, y, dx and dh, and dgate of a gate of its own, come from that row alone, so that they have the same bits in a
+batch of any number of rows with the same places. Bars against float64 are those of test_norm_gpu."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import roofline_driven_tiling_gb300 as t2s  # noqa: E402
+from roofline_driven_tiling_gb300 import binding  # noqa: E402
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    assert binding.device_status() == binding.T2S_OK
+
+
+def tensors(m, n, dtype, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    new = lambda *s, mean=0.0: (mean + torch.randn(*s, generator=gen, device="cuda")).to(dtype)  # noqa: E731
+    t = {name: new(m, n) for name in ("x", "h", "dy", "dr")}
+    t["gate"] = new(m, n, mean=0.5)
+    opt = dict(weight=new(n, mean=1.0), bias=new(n), norm="layer", post_norm="rms", post_weight=new(n, mean=1.0),
+               post_bias=new(n), scale=0.5, eps=1e-5, p=0.2, seed=seed, sequence=3)
+    return t, opt
+
+
+def run(t, opt, rows, stream=None):
+    """r, y and the gradients of the first rows, each with a gate of its own."""
+    gate = t["gate"][:rows]
+    r, y = t2s.residual_norm(t["x"][:rows], t["h"][:rows], gate=gate, stream=stream, **opt)
+    g = t2s.residual_norm_backward(t["dy"][:rows], t["dr"][:rows], r, t["h"][:rows], gate=gate, stream=stream, **opt)
+    return (r, y, g.dx, g.dh, g.dgate), (g.dweight, g.dbias, g.dpost_weight, g.dpost_bias)
+
+
+@pytest.mark.parametrize("n", [8, 64, 96, 256, 257, 520, 1003, 2048, 4097])
+def test_groups_without_a_row(n):
+    """Fewer rows than a block has groups of threads, call after call on two streams, so that a block's memory goes to the
+    next one at once: the bits of the same rows among many."""
+    many = 3200  # rows for every group of every block
+    t, opt = tensors(many, n, BF16, n)
+    whole, _ = run(t, opt, many)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for rows in (1, 2, 3, 5, 9, 15):
+        got = [run(t, opt, rows, s.cuda_stream) for _ in range(6) for s in streams]
+        torch.cuda.synchronize()
+        for own, sums in got:
+            for a, b in zip(own, whole):
+                assert bool((a == b[:rows]).all())
+            for a, b in zip(sums, got[0][1]):
+                assert bool((a == b).all())
+        # One row: the sums over rows are its terms.
+        if rows == 1:
+            assert bool((got[0][1][1] == t["dy"][0]).all())
+    assert binding.device_status() == binding.T2S_OK
