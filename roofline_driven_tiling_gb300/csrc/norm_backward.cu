@@ -189,7 +189,8 @@ struct RowParams {
   row::View in[kPlaces], dx, dh;
   int at[kPlaces], sum_at[kVectors];  // of their words in shared memory, in bytes; -1: absent, or no room
   int sum_slots, sum_first;
-  int M, rows_per_gate, share, longer;  // a block's rows of a gate, or its gates: one more in the first `longer` blocks
+  int rows_per_gate, share, longer;  // a block's rows of a gate, or its gates: one more in the first `longer` blocks
+  int inner_end;  // of the rows whose aligned words lie within r, dy, dr and h
   Split split;
   int N, threads;  // threads of a row
   int norm, post;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_backward_kernel(c
     for (; m < end; m += rows_at_once) {
       auto fetch_next = [&](int i) {
         const int r = m + rows_at_once;
-        if (r < end) fetch(i, p.in[i].row(r, first_byte), r < p.M - 1);
+        if (r < end) fetch(i, p.in[i].row(r, first_byte), r < p.inner_end);
       };
       row::wait_copies();
       if (!WIDE) {
@@ -610,8 +611,13 @@ cudaError_t run(const BackwardTask& t, cudaStream_t stream) {
       p.in[i] = row::view_of(in[i].p, in[i].ld, i <= kH ? t.M : i == kG ? t.gates : 1, t.N);
       wide = wide && row::whole_words(p.in[i], t.N);
     }
+    p.inner_end = static_cast<int>(t.M);
+    for (int i = kR; i <= kH; ++i) {
+      const int end = static_cast<int>(row::inner_end(p.in[i], t.M));
+      if (end < p.inner_end) p.inner_end = end;
+    }
     p.sum_slots = slots;
-    p.M = static_cast<int>(t.M), p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
+    p.rows_per_gate = static_cast<int>(t.M / t.gates), p.N = static_cast<int>(t.N), p.threads = plan.threads;
     p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
     p.dgate = t.dgate, p.partials = t.partials;
     if (!(wide ? lay_out<true>(&p, plan, slot, &smem) : lay_out<false>(&p, plan, slot, &smem))) plan.threads = 0;

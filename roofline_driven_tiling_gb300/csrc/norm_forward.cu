@@ -86,6 +86,7 @@ struct RowParams {
   row::View in[kPlaces], r, y;
   int at[kPlaces];  // of its words in shared memory, in bytes; -1: absent, or a gate that changes
   int64_t M, rows_per_gate, step;  // rows that all groups take at once
+  int64_t inner_end;  // of the rows of x and h whose aligned words lie within both
   int64_t x_step, h_step, r_step, y_step;
   int N, threads;  // threads of a row
   int norm, post;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of<C, THREADS>()) row_forward_
       if (p.at[i] >= 0) settle(i, p.in[i].p + first);
   }
   for (; m < p.M; m += p.step, x += p.x_step, h += p.h_step, r += p.r_step, y += p.y_step) {
-    const bool more = m + p.step < p.M, inside = m + p.step < p.M - 1;  // the next row, not the last one
+    const bool more = m + p.step < p.M, inside = m + p.step < p.inner_end;  // the next row
     row::wait_copies();
     settle(kX, x);
     if (has_h) {
@@ -281,6 +282,8 @@ cudaError_t run_rows(const ForwardTask& t, int threads, cudaStream_t stream) {
   }
   p.r = row::view_of(t.R.p, t.R.ld, t.M, t.N), p.y = row::view_of(t.Y.p, t.Y.ld, t.M, t.N);
   wide = wide && row::whole_words(p.r, t.N) && row::whole_words(p.y, t.N);
+  const int64_t x_end = row::inner_end(p.in[kX], t.M), h_end = row::inner_end(p.in[kH], t.M);
+  p.inner_end = x_end < h_end ? x_end : h_end;
   p.M = t.M, p.rows_per_gate = t.M / t.gates, p.N = static_cast<int>(t.N), p.threads = threads;
   p.norm = t.norm, p.post = t.post, p.scale = t.scale, p.eps = t.eps, p.drop = t.drop;
   const int block = THREADS / threads * threads;

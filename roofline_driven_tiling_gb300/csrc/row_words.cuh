@@ -34,6 +34,13 @@ inline View view_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t cols) {
   v.wide = ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(v.ld * 2)) & 15u) == 0;
   return v;
 }
+// The first row whose aligned words may reach beyond the end of a matrix of `rows` rows. A row's words hold up to seven values
+// before and after its own, which lie in the rows around it: in one, or in several rows of fewer than seven values. (At
+// the matrix's start as many rows are meant; fetch_word's `inside` says how they are kept out.)
+inline int64_t inner_end(const View& v, int64_t rows) {
+  if (v.p == nullptr || v.ld == 0) return rows;
+  return rows - (v.ld < kWord - 1 ? (kWord - 2 + v.ld) / v.ld : 1);
+}
 
 // The eight words' values from 32-bit words w[o] on: a shift by o = 1 to 7 values, the same for a whole row.
 __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
@@ -101,7 +108,8 @@ static __device__ __noinline__ void fetch_part(uint32_t to, const uint16_t* begi
   if (o + n > kWord && (threadIdx.x % 32 == 31 || left <= kWord))
     copy_async(to + 16u, from + kWord, static_cast<int>(min(static_cast<int64_t>(16), 2 * (end - from - kWord))));
 }
-// `inside`: a row with others before and after it.
+// `inside`: all of the row's aligned words lie within the matrix. The callers say so of the rows below inner_end() that a
+// group takes after its first: rows of fewer than seven values are then the 16th or a later one, longer ones the second.
 template <bool WIDE>
 __device__ __forceinline__ void fetch_word(uint32_t to, const View& v, const uint16_t* p, int left, bool inside) {
   if (left <= 0) return;

@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 
 import roofline_driven_tiling_gb300 as t2s  # noqa: E402
 from roofline_driven_tiling_gb300 import binding  # noqa: E402
+from test_norm_gpu import build, check_backward, check_forward, Maker  # noqa: E402
 
 BF16, F16 = torch.bfloat16, torch.float16
 
@@ -64,4 +65,20 @@ def test_groups_without_a_row(n):
         # One row: the sums over rows are its terms.
         if rows == 1:
             assert bool((got[0][1][1] == t["dy"][0]).all())
+    assert binding.device_status() == binding.T2S_OK
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 6, 7, 9])
+def test_many_narrow_rows(n):
+    """More rows than all groups of a launch take at once, each of less than a word and up to seven of them in one."""
+    for i, (dtype, pad, shift) in enumerate([(BF16, 0, 0), (F16, 0, 3), (BF16, 1, 5), (F16, 8, 1)]):
+        m = 11000 + i
+        mk = Maker(i, dtype, pad, shift)
+        opt, t = build(mk, 6 * n + i, m, n)
+        r, y = t2s.residual_norm(t["x"], t["h"], r=mk.empty(m, n), y=mk.empty(m, n), **opt)
+        check_forward(opt, t["x"], t["h"], r, y, dtype, str(opt.keys()))
+        dy, dr = mk.normal(m, n), mk.normal(m, n)
+        g = t2s.residual_norm_backward(dy, dr, r, t["h"], dx=mk.empty(m, n), dh=mk.empty(m, n), **opt)
+        check_backward(opt, dy, dr, r, t["h"], g, dtype, str(opt.keys()))
+        mk.check_canaries()
     assert binding.device_status() == binding.T2S_OK
