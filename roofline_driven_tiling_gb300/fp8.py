@@ -19,7 +19,9 @@ outputs weight and its gradients, with weights scaled in 128 x 128:
     dw = gemm_fp8(xt, xts, dt.t(), dts.t(), dtype=torch.float32)
 
 Sums are FP32, outputs are rounded once. The work runs on ``stream`` (the integer value of a
-cudaStream_t; default: torch's current stream). No autograd history is recorded.
+cudaStream_t; default: torch's current stream). No autograd history is recorded: tensors that require
+grad (8-bit ones do where they were cast from such a tensor, or are parameters) are refused unless
+gradients are off (``torch.no_grad()``).
 """
 from __future__ import annotations
 
@@ -161,8 +163,8 @@ def gemm_fp8(a, a_scale, b, b_scale, dtype=torch.bfloat16, out=None, stream=None
     if group == 128 and b_scale.shape != (blocks, (N + 127) // 128):
         raise ValueError("b_scale must be %d x %d or %d x %d, got %s" % (
             blocks, N, blocks, (N + 127) // 128, tuple(b_scale.shape)))
-    if _grad_enabled() and (a_scale.requires_grad or b_scale.requires_grad):
-        raise ValueError("gemm_fp8 records no autograd history, and a scale requires grad: call it under torch.no_grad()")
+    if _grad_enabled() and (a.requires_grad or b.requires_grad or a_scale.requires_grad or b_scale.requires_grad):
+        raise ValueError("gemm_fp8 records no autograd history, and an input requires grad: call it under torch.no_grad()")
     if out is None:
         out, ldc = _new((M, N), (N, 1), dtype, a.device, stream), N
     else:
