@@ -457,11 +457,15 @@ int t2s_gated_backward_f16(int64_t M, int64_t N, int64_t K, const uint16_t *dH, 
  * rows of K 8-bit values: the sum over blocks b of 128 values of K of
  *     SA[m * sa_row + b * sa_block] * SB[(n / b_group) * sb_row + b * sb_block] * (A_b B_b^T)[m, n];
  * b_group is 1 (every row of B has scales) or 128 (a scale for 128 x 128). A and B may have either
- * format each, and any scales, in any order of places (strides >= 0; a stride of 0 repeats one). The
+ * format each, and scales in any order of places (strides >= 0; a stride of 0 repeats one). The
  * tensor cores add a block's 128 products in FP32 (their additions truncate: an error below 2^-16 of
  * the block's sum of magnitudes, about 1e-7 of it on random operands); blocks are scaled and added in FP32, in an order that the sizes alone decide, and C
- * is rounded once. A scale that is not finite, or products of scales beyond FP32, give NaN or infinity
- * as FP32 arithmetic does. Rows of A and B must start on 16-byte boundaries (pointer, and lda, ldb
+ * is rounded once. Scales are FP32 numbers below 2^89 in magnitude whose products are finite. A block's
+ * sum (below 2^39 in magnitude) meets either scale first, or their product, as the sizes decide: a
+ * scale below 2^-94, or a product of scales below 2^-126, so costs up to 2^-111, or 2^-150 times the
+ * other scale; a larger scale, or product, may give an infinity or NaN where C's value is finite.
+ * A scale that is not finite gives NaN or infinity as FP32 arithmetic does.
+ * Rows of A and B must start on 16-byte boundaries (pointer, and lda, ldb
  * multiples of 16 where there is more than one row); bytes between rows are not read.
  * C's rows have ldc values. K = 0 sets C to 0. Otherwise the common contract and return codes at the
  * top apply (asynchronous on `stream`, no allocation, no workspace), with programmatic launches as above.

@@ -7,7 +7,7 @@
 // per CTA take them out, multiply them by the block's scales and add them to FP32 sums in their registers (128 a
 // thread for a 256-wide tile), while the other accumulators fill. A warp of its own brings the scales to shared
 // memory some blocks ahead: fetched by the sums' warps one block ahead, they held every block up for an L2 latency
-// (0.49 us a block whatever its width). So the scales may be any FP32 numbers, and the tensor cores' truncating additions never
+// (0.49 us a block whatever its width). So the scales need be no powers of two, and the tensor cores' truncating additions never
 // run longer than 128 products.
 //
 // Measured: 4096^3 59.5 us (2.3 PFLOP/s; copies and MMAs alone 41), with a scale for every column 87; 4096 x 8192 x 2048
@@ -324,6 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_pair_kernel(const __grid_cons
               if (lane == 0) ff::arrive_remote(acc_empty_0 + 8u * b);
             }
             uint64_t* to = sum[u];
+            // Column, then row: scale by scale first, which would take any two scales whose product is normal, a 4096^3 product
+            // takes 97 us instead of 87, and 103 to 121 with a second way that is taken for far scales only.
             if constexpr (VECTOR) {
 #pragma unroll
               for (int i = 0; i < kChunk / 2; ++i)

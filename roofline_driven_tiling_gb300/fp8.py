@@ -18,10 +18,12 @@ outputs weight and its gradients, with weights scaled in 128 x 128:
     xt, xts = quantize_fp8(x, along="columns")
     dw = gemm_fp8(xt, xts, dt.t(), dts.t(), dtype=torch.float32)
 
-Sums are FP32, outputs are rounded once. The work runs on ``stream`` (the integer value of a
-cudaStream_t; default: torch's current stream). No autograd history is recorded: tensors that require
-grad (8-bit ones do where they were cast from such a tensor, or are parameters) are refused unless
-gradients are off (``torch.no_grad()``).
+Sums are FP32, outputs are rounded once. Scales lie below 2^89 in magnitude (those of ``quantize_fp8`` do for
+values up to 2^96, with e5m2 2^103), and the products of the two that meet are finite.
+
+The work runs on ``stream`` (the integer value of a cudaStream_t; default: torch's current stream). No
+autograd history is recorded: tensors that require grad (8-bit ones do where they were cast from such a
+tensor, or are parameters) are refused unless gradients are off (``torch.no_grad()``).
 """
 from __future__ import annotations
 
