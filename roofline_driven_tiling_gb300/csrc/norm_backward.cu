@@ -541,7 +541,9 @@ RowPlan row_plan(int64_t N) {
   return {threads, threads <= 512 ? 512 / threads * threads : threads};
 }
 
-constexpr int kMostSmem = 224 * 1024;  // of a block, beside the sums' rooms
+// Of a block, beside the 1 KB of rooms: what rows of more than 4096 values off boundaries take with all four inputs and all five
+// sums, to the byte (2048 x 4097 so 120 us and 2048 x 8191 157, and 226 and 453 in passes over memory).
+constexpr int kMostSmem = 226 * 1024;
 
 // Places in shared memory: inputs, parameters (those only while there is room for them all), sums. False: the inputs
 // and sums alone do not fit.

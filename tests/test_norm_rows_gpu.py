@@ -82,3 +82,29 @@ def test_many_narrow_rows(n):
         check_backward(opt, dy, dr, r, t["h"], g, dtype, str(opt.keys()))
         mk.check_canaries()
     assert binding.device_status() == binding.T2S_OK
+
+
+@pytest.mark.parametrize("n,pad,shift", [(4097, 0, 0), (4104, 1, 3), (5001, 0, 0), (6000, 3, 1), (8191, 0, 0), (8192, 0, 1), (8192, 0, 0)])
+def test_sums_of_long_rows(n, pad, shift):
+    """Rows of 4097 to 8192 values with all inputs and all sums are read once, as with fewer: dr of zeros gives the bits of no
+    dr at all, which one reading and several passes over memory would not."""
+    m = 333
+    t, opt = tensors(m, n, BF16, n + shift)
+    mk = Maker(1, BF16, pad, shift)
+
+    def moved(v):
+        view = mk.empty(m, n)
+        view.copy_(v)
+        return view
+
+    h, dy, zero = moved(t["h"]), moved(t["dy"]), moved(torch.zeros(m, n))
+    for gate in (t["gate"][0].clone(), t["gate"][:3].clone()):
+        kw = dict(opt, gate=gate)
+        r, _ = t2s.residual_norm(t["x"], h, **kw)
+        far_r = moved(r)
+        want = t2s.residual_norm_backward(dy, None, far_r, h, **kw)
+        got = t2s.residual_norm_backward(dy, zero, far_r, h, **kw)
+        check_backward(kw, dy, zero, far_r, h, got, BF16, str(n))
+        for name, a, b in zip(got._fields, got, want):
+            assert bool((a == b).all()), name
+    assert binding.device_status() == binding.T2S_OK
