@@ -54,8 +54,8 @@ __device__ __forceinline__ bool try_barrier(uint32_t bar, uint32_t parity) {
 }
 
 // A bounded barrier wait without a call in it (a kernel that moves registers between its warps can make none): the
-// thread asks once, which answers sooner where the phase is over already (4096^3 67 -> 65 us), then sleeps in the barrier
-// hardware, up to 100 us a try, and gives up after 2^17 of them.
+// thread asks once, which answers sooner where the phase is over already (4096^3 59.4 us, 61.6 without; 512 x 4096 x 4096 12.7
+// and 13.6), then sleeps in the barrier hardware, up to 100 us a try, and gives up after 2^17 of them.
 __device__ __forceinline__ bool wait_counted(uint32_t bar, uint32_t parity, unsigned* status) {
   if (try_barrier(bar, parity)) return true;
 #pragma unroll 1

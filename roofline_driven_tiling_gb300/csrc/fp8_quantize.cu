@@ -8,7 +8,8 @@
 //
 // Bound by memory, near enough by instructions that those were what the steps saved: 8192 x 8192 bfloat16 along rows 33 us
 // (6.1 TB/s), 4096 x 8192 along rows 17.4 (5.8), columns 20.6 (4.9), both 27.8 (4.8; 4.5 rounds of three blocks to an SM),
-// both with squares 25.5.
+// both with squares 25.5. FP32 values of 4096 x 8192 25.2 along rows (6.7 TB/s), both ways 39.3 (5.1; two blocks to an SM), with
+// squares 36.4. Rows off 16-byte boundaries are loaded value by value: 4096 x 8191 bfloat16 29.3 along rows, both ways 50.
 #include <cuda_runtime.h>
 
 #include <cstdint>

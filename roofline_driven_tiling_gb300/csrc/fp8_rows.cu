@@ -9,7 +9,8 @@
 // stores. One launch, no workspace, the same bits every time.
 //
 // Measured: 1 x 4096 x 8192 (outputs last) 9.2 us, 3.7 TB/s of weights out of HBM, 64 x 4096 x 4096 8.4: about 4 us are the
-// launch, the first blocks' latency and the join. On SM pairs one row took 32 us, without a split of K 18.
+// launch, the first blocks' latency and the join; 64 x 8192 x 28672 55, in two rounds of CTAs (224 tiles, one to an SM; its
+// bytes take 35), 32 x 8192 x 28672 45. On SM pairs one row took 32 us, without a split of K 18.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -358,7 +359,8 @@ cudaError_t launch(const ProductTask& t, const RowsPlan& plan, cudaStream_t stre
       return e;
     if ((e = encode_tmap_8bit_2d(&p.x, t.A, t.K, t.M, t.lda, kBlock, TM, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
   }
-  // Half of an SM's memory where more CTAs are to come or a ring of half is deep enough, otherwise all of it.
+  // Half of an SM's memory where more CTAs are to come or a ring of half is deep enough, otherwise all of it. (Tiles of 64 rows
+  // do not come two to an SM all the same: the least share below is half of a CTA's limit, and the system takes 1 KB of each.)
   constexpr int kAround = 1024 + 512 + kScaleSlots * T::kScaleBytes;
   const int per_cta = (p.blocks + plan.splits - 1) / plan.splits;
   const int budget = (tiles * plan.splits > plan.reach || 6 * T::kStageBytes <= 112 * 1024 - kAround ? 112 : 216) * 1024 - kAround;

@@ -7,10 +7,13 @@
 // A CTA takes consecutive rows and adds its rows' share of the five sums in FP32; a second launch adds the
 // CTAs' shares in their order.
 //
-// Rows are read once (N <= 8192). Bound by instructions, not by memory (every value of a warp's word costs about 20): 8192 x
-// 2048 with a gate and dropout 52.2 us (3.9 TB/s), 8192 x 4096 without dropout 87 (4.6), layer norms before and after with all
-// sums 92; off 16-byte boundaries 4096 x 4095 97, 1300 x 1003 26 (nine rows to a block, and the second launch 4 us). Two words
-// a thread with half the threads were no faster (8192 x 4096 98).
+// Rows are read once (N <= 8192). No single limit: instructions (every value of a warp's word costs about 20, 73 % of the issue
+// slots), the sums' reads and writes of shared memory for every row, and the second launch of 4 us. With a gate: 8192 x 2048 and
+// dropout 52 us (3.9 TB/s), 8192 x 4096 87 (4.6). Layer norms before and after with all five sums: 8192 x 2048 and
+// dropout 91, 8192 x 4096 182 (one block of 512 threads to an SM, by the sums' shared memory). Off 16-byte boundaries 4096 x
+// 4095 97 (50 on them), 1300 x 1003 26 (nine rows to a block). A gate for each of 4096 rows of 2048 51 us, and one for all 27:
+// a block takes its gates one after another. Rows beyond 8192 take passes over memory of two bytes a load: 4096 x 12288 767 us
+// (0.8 TB/s). Two words a thread with half the threads were no faster (8192 x 4096 98).
 #include <cuda_runtime.h>
 
 #include <atomic>

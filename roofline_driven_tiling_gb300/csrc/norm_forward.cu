@@ -3,8 +3,9 @@
 // x and h are read once and r and y written once where a row fits the registers of a block (N <= 8192): mean first, then
 // the squares of what is left of it. A warp takes a row of up to 1024 values alone, without barriers; longer ones take two
 // words a thread. The next row's words come to shared memory behind this row's sums, also where rows start off 16-byte
-// boundaries. Bound by memory: 8192 x 4096 with a second norm 44.4 us (6.0 TB/s); one row of 4096 2.6 us (the launch);
-// 8192 x 1003 without boundaries 43 us, bound by the instructions that put words together.
+// boundaries. Bound by memory: 8192 x 4096 with a second norm 44.4 us (6.0 TB/s), 4096 x 8192 46; one row of 4096 2.6 us (the
+// launch). 8192 x 1003 off boundaries 42 us (8192 x 1000 13), bound by the instructions that put words together. Rows beyond
+// 8192 take passes over memory of two bytes a load: 4096 x 12288 225 us (1.8 TB/s), without h 71; one row of 16384 11.
 #include <cuda_runtime.h>
 
 #include <cstdint>

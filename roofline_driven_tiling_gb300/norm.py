@@ -184,7 +184,8 @@ def residual_norm_backward(dy, dr, r, h=None, weight=None, bias=None, gate=None,
     """ResidualNormGradients from dy, the gradient of y (None with ``norm`` "none"), dr, that of r's other uses
     (None for none), r as the forward pass returned it, and the forward pass's other arguments. dx and dh
     are None (allocated here), tensors that receive them, or False (not computed); every parameter that
-    is given gets its gradient."""
+    is given gets its gradient. Those of vectors are contiguous; that of a matrix of gates has rows on
+    16-byte boundaries, N rounded up to a multiple of 8 values apart."""
     code, post = _norm(norm, "norm"), _norm(post_norm, "post_norm")
     dtype, device, index, rp, ldr, M, N = _first(r, "r")
     if (dy is None) != (code == binding.T2S_NORM_NONE):

@@ -108,3 +108,12 @@ def test_sums_of_long_rows(n, pad, shift):
         for name, a, b in zip(got._fields, got, want):
             assert bool((a == b).all()), name
     assert binding.device_status() == binding.T2S_OK
+
+
+@pytest.mark.parametrize("n", [8, 20, 1003])
+def test_places_of_gate_gradients(n):
+    """A vector's gradient is contiguous, a matrix's rows start on 16-byte boundaries."""
+    t, opt = tensors(6, n, BF16, n)
+    for gate, strides in ((t["gate"][0].clone(), (1,)), (t["gate"][:3], ((n + 7) // 8 * 8, 1))):
+        g = t2s.residual_norm_backward(t["dy"], None, t["x"], t["h"], gate=gate, **opt)
+        assert g.dgate.shape == gate.shape and g.dgate.stride() == strides and g.dgate.data_ptr() % 16 == 0
