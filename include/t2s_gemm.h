@@ -459,9 +459,10 @@ int t2s_gated_backward_f16(int64_t M, int64_t N, int64_t K, const uint16_t *dH, 
  * b_group is 1 (every row of B has scales) or 128 (a scale for 128 x 128). A and B may have either
  * format each, and scales in any order of places (strides >= 0; a stride of 0 repeats one). The
  * tensor cores add a block's 128 products in FP32 (their additions truncate: an error below 2^-16 of
- * the block's sum of magnitudes, about 1e-7 of it on random operands); blocks are scaled and added in FP32, in an order that the sizes alone decide, and C
- * is rounded once. Scales are FP32 numbers below 2^89 in magnitude whose products are finite. A block's
- * sum (below 2^39 in magnitude) meets either scale first, or their product, as the sizes decide: a
+ * the block's sum of magnitudes, about 1e-7 of it on random operands); blocks are scaled and added in
+ * FP32, in an order that the sizes and b_group alone decide, and C is rounded once.
+ * Scales are FP32 numbers below 2^89 in magnitude whose products are finite. A block's
+ * sum (below 2^39 in magnitude) meets either scale first, or their product, as those decide too: a
  * scale below 2^-94, or a product of scales below 2^-126, so costs up to 2^-111, or 2^-150 times the
  * other scale; a larger scale, or product, may give an infinity or NaN where C's value is finite.
  * A scale that is not finite gives NaN or infinity as FP32 arithmetic does.
@@ -538,7 +539,7 @@ int t2s_gemm_fp8_f32(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t 
  * gradient is t2s_dropout of dY with the same seed and sequence, and no R.
  *
  * Statistics, sums and arithmetic are FP32 (squares overflow from about 1e19 on), in an order that
- * sizes, alignment and wanted outputs alone decide; every output is rounded to 16 bits once. eps and
+ * sizes, alignment and which arguments are there alone decide; every output is rounded to 16 bits once. eps and
  * scale are finite, eps >= 0 (0 with a row of zeros gives NaN). Matrices have row strides of at least N
  * values; any 2-byte alignment is taken (16-byte aligned rows are read with wide loads). Outputs equal to
  * other arguments are rejected except as said. M = 0: the sums over rows are 0. N = 0: nothing to do.
